@@ -1,7 +1,8 @@
 /*
  * dfa.h -- C ABI of libdfa: exact causal blockwise attention (forward and
  * recomputation backward), chunk-pair partials, log-sum-exp merge, sequence
- * permutes and ring schedules, for NVIDIA GB300 (sm_103a).
+ * permutes and ring schedules, rotary positions and decoding over a paged
+ * 8-bit key/value cache, for NVIDIA GB300 (sm_103a).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -60,9 +61,11 @@ typedef enum dfa_status {
     DFA_ERR_WORKSPACE = 3,   /* workspace missing or smaller than required    */
     DFA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed             */
     DFA_ERR_TIMEOUT = 5,     /* a device-side wait gave up (async, see above) */
-    DFA_ERR_BOUNDS = 6       /* a device-side index outside its tensor: only a
-                                library built with DFA_DEBUG_BOUNDS checks and
-                                reports this (async, like DFA_ERR_TIMEOUT)    */
+    DFA_ERR_BOUNDS = 6       /* a device-side index outside its tensor (async,
+                                like DFA_ERR_TIMEOUT): a bad page or length of
+                                a paged cache, in every build; the attention
+                                kernels check and report theirs only in a
+                                library built with DFA_DEBUG_BOUNDS           */
 } dfa_status;
 
 /* Sequence partitions over P logical workers (chunks). */
@@ -384,6 +387,156 @@ dfa_status dfa_permute(const dfa_attn_desc* desc, int32_t inverse, const void* i
  */
 dfa_status dfa_permute_rope(const dfa_attn_desc* desc, int32_t inverse, const void* in,
                             void* out, int64_t heads, float theta_base, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions and the paged key/value cache (serving).  The pages
+ * describe no counterpart beyond the rotation itself (Striped Attention Guide,
+ * "Preserving Rotary Position Embeddings").
+ *
+ * Strides: these calls take their row tensors [B, H, L, d] with strides in
+ * elements for batch, head and token (features are contiguous), so that the
+ * heads of a packed projection [B, L, H, d] are read where they are.  A NULL
+ * stride array means contiguous.  Strides are multiples of 16 bytes.  An
+ * output's rows must not overlap one another.
+ * ------------------------------------------------------------------------ */
+
+/* A rotary embedding.  Feature pair t < rot_dim/2 of a row at position i is
+ * turned by the angle i * f_t, f_t = theta_base^(-2t/rot_dim), and multiplied
+ * by gain: x' = gain (x cos - y sin), y' = gain (x sin + y cos).  Features
+ * [rot_dim, d) pass unchanged.  scaling changes the frequencies for contexts
+ * longer than the trained one:
+ *   DFA_ROPE_LINEAR  f_t / factor (position interpolation);
+ *   DFA_ROPE_BANDS   by the turns r = orig_len f_t / (2 pi) that a pair makes in
+ *                    the trained context: f_t / factor where r <= low, f_t where
+ *                    r >= high, and in between
+ *                    (1 - u) f_t / factor + u f_t, u = (r - low) / (high - low).
+ * Angles are reduced exactly modulo a turn: f_t / (2 pi) is held as a 64-bit
+ * fraction of a turn (from fp64) and multiplied by the integer position. */
+enum { DFA_ROPE_INTERLEAVED = 0, /* pairs (2t, 2t + 1)              */
+       DFA_ROPE_HALF = 1 };      /* pairs (t, t + rot_dim/2)        */
+enum { DFA_ROPE_PLAIN = 0, DFA_ROPE_LINEAR = 1, DFA_ROPE_BANDS = 2 };
+
+typedef struct dfa_rope_spec {
+    int32_t layout;    /* DFA_ROPE_INTERLEAVED or DFA_ROPE_HALF             */
+    int32_t rot_dim;   /* rotated features: a multiple of 16, 16..d         */
+    int32_t scaling;   /* DFA_ROPE_PLAIN, _LINEAR or _BANDS                 */
+    int32_t reserved;  /* 0                                                 */
+    double theta_base; /* > 1                                               */
+    double factor;     /* LINEAR, BANDS: > 0                                */
+    double orig_len;   /* BANDS: trained context, > 0                       */
+    double low, high;  /* BANDS: 0 <= low < high                            */
+    double gain;       /* > 0; 0 means 1                                    */
+} dfa_rope_spec;
+
+/*
+ * dfa_rope -- rotate query or key rows at their positions, out of place or in
+ * place (out == x with equal strides; any other overlap is refused).
+ *   x, out [B,H,L,d], bf16 (fp32 = 0) or fp32 (1); d 64 or 128; L may be 0.
+ *   Positions: positions[b*L + l] (device) where positions is not NULL, else
+ *   row l's position under map (host), else l.  Any int32 is a position.
+ *   inverse = 1: the transposed rotation (angle -i f_t, the same gain): given
+ *   dout it yields dx, the call's backward.
+ * Arithmetic in fp32, rounded once to the output's type.
+ */
+dfa_status dfa_rope(const dfa_rope_spec* spec, int32_t B, int32_t H, int64_t L, int32_t d,
+                    int32_t fp32, const void* x, const int64_t* x_strides, void* out,
+                    const int64_t* out_strides, const dfa_pos_map* map,
+                    const int32_t* positions, int32_t inverse, void* stream);
+
+/* A paged cache (plain data; every array is the caller's, on the device).
+ * Row j of sequence b lies in page block_table[b*max_pages + j/page], at row
+ * j % page.  seq_lens[b] counts the rows of sequence b, those that a call
+ * appends or queries among them: set it before the call.  Only table entries
+ * below ceil(seq_lens[b]/page) are read.  Sequences may share pages that are
+ * only read; a page that rows are appended to belongs to one sequence.
+ *
+ * E4M3: a cell stands for code * scale, with one fp32 scale per page and head
+ * of K and of V.  Scales are powers of two: the smallest s >= 2^-100 with
+ * |x| <= 448 s for every finite row of the page so far, so raising a scale when
+ * a louder row arrives shifts the exponents of the codes that are there and
+ * rounds only those that become subnormal (below 2^-6 of the new scale).
+ * (Pages that were filled elsewhere may have any positive normal scale.)
+ *
+ * Lengths and page numbers are checked on the device: seq_lens[b] outside
+ * [0, max_pages*page], a new or query length outside [0, T] or above the
+ * sequence's, or a page outside [0, npages) is skipped (nothing is read or
+ * written through it) and sets the workspace's status word, which
+ * dfa_stream_status reports as DFA_ERR_BOUNDS; that sequence's outputs are
+ * then invalid. */
+enum { DFA_CACHE_BF16 = 0, DFA_CACHE_E4M3 = 1 };
+
+typedef struct dfa_paged_cache {
+    int32_t dtype;       /* DFA_CACHE_BF16 or DFA_CACHE_E4M3                */
+    int32_t page;        /* rows per page: 16, 32, 64 or 128                */
+    int32_t Hkv;         /* key/value heads                                 */
+    int32_t d;           /* 64 or 128                                       */
+    int64_t npages;      /* pages of k and of v                             */
+    int64_t page_stride; /* elements from a page to the next, a multiple of
+                            16 bytes, >= Hkv*page*d; 0: Hkv*page*d          */
+    void* k;             /* [npages][Hkv][page][d], 16-byte aligned         */
+    void* v;
+    float* k_scale;      /* [npages][Hkv] (E4M3; ignored for BF16)          */
+    float* v_scale;
+    int32_t B;           /* sequences                                       */
+    int32_t max_pages;   /* width of block_table                            */
+    const int32_t* block_table; /* [B][max_pages]                           */
+    const int32_t* seq_lens;    /* [B]                                      */
+} dfa_paged_cache;
+
+/*
+ * dfa_cache_append -- store the new rows of every sequence, keys rotated on
+ * the way, and rotate the queries that go with them.  The n = new_lens[b]
+ * (NULL: T) new rows of sequence b are tokens 0..n-1 of its k and v and go to
+ * rows seq_lens[b] - n .. seq_lens[b] - 1, which are also their positions.
+ * Rows from n on are not read.  With rope, K is rotated in fp32 and rounded
+ * once to the cell's type (NULL: stored as it is); V is stored as it is.
+ * E4M3: a NaN or an infinity is stored as NaN and does not count towards the
+ * scale; rows of a touched page that were there before are requantised when its
+ * scale rises; a page whose row 0 is among the new rows starts a new scale.
+ * Storing the same rows again gives the same cells.
+ *   k, v [B,Hkv,T,d] bf16 (strided); 1 <= T < 2^30.
+ *   q, q_out [B,Hq,T,d] bf16 (strided): rows below new_lens[b] are rotated
+ *   into q_out (in place when they are one tensor), the others left as they
+ *   were; q NULL: no queries.  q needs rope.
+ *   ws: 256 bytes (the status word).
+ */
+dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,
+                            const int32_t* new_lens, const void* k, const int64_t* k_strides,
+                            const void* v, const int64_t* v_strides, int32_t Hq, const void* q,
+                            const int64_t* q_strides, void* q_out, const int64_t* q_out_strides,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dfa_cache_gather -- cached rows [pos0, pos0 + L) of every sequence as
+ * contiguous bf16, for calls that read plain tensors (a prompt's next chunk
+ * attends to them with dfa_chunk_fwd).  code * scale is exact in bf16 (except
+ * below its smallest normal number).  Rows behind a sequence's end are left as
+ * they were.
+ *   k_out, v_out [B,Hkv,L,d] bf16, 16-byte aligned; either may be NULL.
+ *   ws: 256 bytes (the status word).
+ */
+dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t L, void* k_out,
+                            void* v_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dfa_decode_paged -- attention of the last few tokens of every sequence over
+ * its paged cache (split-KV, as dfa_decode over one contiguous cache).  Sequence b
+ * has n = q_lens[b] (NULL: T) query tokens, tokens 0..n-1 of q, at positions
+ * seq_lens[b] - n + t; with desc->causal key j is visible iff j <= that
+ * position, else every row of the sequence is.  A row that sees no key gives
+ * O = 0, LSE = -inf; output rows from n on are left as they were.  What lies
+ * in a page behind the sequence's end, or in rows that a token does not see,
+ * does not reach its result, NaN and infinities included.
+ * desc supplies B, Hq, Hkv, d, causal, scale, o_fp32 (ndocs must be 0).
+ *   q [B,Hq,T,d] bf16 (strided); o [B,Hq,T,d] bf16 or fp32 (o_fp32) and
+ *   lse [B,Hq,T] fp32, contiguous.  (Hq/Hkv) * T <= 1024.
+ *   ws: dfa_decode_paged_workspace_size(desc, T) bytes (partials), whatever
+ *   the lengths and the table.
+ */
+size_t dfa_decode_paged_workspace_size(const dfa_attn_desc* desc, int32_t T);
+dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
+                            const int32_t* q_lens, const void* q, const int64_t* q_strides,
+                            void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Ring schedule (host only, no device work) for the P workers of desc's

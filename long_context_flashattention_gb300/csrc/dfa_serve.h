@@ -1,0 +1,88 @@
+// dfa_serve.h -- plain-data structures shared by the host launchers and the
+// kernels of rotary positions and of the paged key/value cache.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "dfa_params.h"
+
+namespace dfa {
+
+struct DevStatus;
+
+// A rotary embedding as the kernels use it.  turn[t] is pair t's frequency as a
+// 64-bit fraction of a full turn, so that (position * turn[t]) mod 2^64 is the
+// reduced angle: exact for every int32 position, in integer arithmetic.
+struct RopeTable {
+    uint64_t turn[64];
+    float gain;
+    int32_t half_layout;  // pairs (t, t + half) instead of (2t, 2t + 1)
+    int32_t half;         // rot_dim / 2
+    int32_t units;        // rot_dim / 16: units of 8 pairs (16 features)
+};
+
+// A row tensor [B, H, L, d] with contiguous features; strides in elements.
+struct Rows {
+    void* p;
+    int64_t sb, sh, sl;
+};
+
+struct RopeRowsParams {
+    RopeTable t;
+    Rows x, out;
+    int32_t B, H, d;
+    int64_t L;
+    int32_t inverse;
+    int32_t heads;                // heads per work item
+    const int32_t* positions;     // [B][L] or NULL
+    DevMap map;
+};
+
+// Device view of a paged cache (dfa_paged_cache).
+struct CacheView {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* table;
+    const int32_t* seq_lens;
+    int64_t npages, page_stride;  // page_stride in elements
+    int32_t B, Hkv, d, page, max_pages, e4m3;
+    DevStatus* status;
+};
+
+struct AppendParams {
+    CacheView c;
+    RopeTable t;                  // units = 0: no rotation
+    const int32_t* new_lens;      // [B] or NULL
+    Rows k, v, q, q_out;
+    int32_t T, Hq;
+    int32_t pages;                // pages a sequence's new rows may touch
+    int32_t kv_blocks;            // blocks of K and V; the rest rotate q
+};
+
+struct GatherParams {
+    CacheView c;
+    int64_t pos0, L;
+    void* k_out;
+    void* v_out;
+    int32_t page0, pages;         // pages [page0, page0 + pages) hold the rows
+};
+
+struct PagedParams {
+    CacheView c;
+    Rows q;
+    const int32_t* q_lens;        // [B] or NULL
+    int32_t Hq, G, T, causal, o_fp32;
+    float scale_log2;
+    void* o;                      // [B, Hq, T, d]
+    float* lse;                   // [B, Hq, T]
+};
+
+cudaError_t launch_rope_rows(const RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_append(const AppendParams& p, int64_t q_items, cudaStream_t stream);
+cudaError_t launch_cache_gather(const GatherParams& p, cudaStream_t stream);
+cudaError_t launch_decode_paged(const PagedParams& p, cudaStream_t stream);
+
+}  // namespace dfa

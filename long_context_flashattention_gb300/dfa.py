@@ -86,6 +86,27 @@ class Schedule(ctypes.Structure):
 TILE_SKIP, TILE_FULL, TILE_PARTIAL = 0, 1, 2
 
 
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("theta_base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("gain", ctypes.c_double)]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("npages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2}
+
+
 _lib = None
 
 
@@ -101,6 +122,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         D = ctypes.POINTER(AttnDesc)
+        C = ctypes.POINTER(PagedCacheDesc)
         sigs = {
             "dfa_attn_fwd": (i32, [D, vp, vp, vp, vp, vp, vp, sz, vp]),
             "dfa_attn_bwd": (i32, [D, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -120,6 +142,13 @@ def lib():
                                           vp]),
             "dfa_decode_workspace_size": (sz, [D, i32, i64, i32]),
             "dfa_decode": (i32, [D, i32, i64, i64, vp, vp, vp, vp, vp, i32, vp, sz, vp]),
+            "dfa_rope": (i32, [ctypes.POINTER(RopeSpec), i32, i32, i64, i32, i32, vp, vp, vp, vp,
+                               ctypes.POINTER(PosMap), vp, i32, vp]),
+            "dfa_cache_append": (i32, [C, ctypes.POINTER(RopeSpec), i32, vp, vp, vp, vp, vp, i32,
+                                       vp, vp, vp, vp, vp, sz, vp]),
+            "dfa_cache_gather": (i32, [C, i64, i64, vp, vp, vp, sz, vp]),
+            "dfa_decode_paged_workspace_size": (sz, [D, i32]),
+            "dfa_decode_paged": (i32, [D, C, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
             "dfa_make_schedule": (i32, [D, i32, i32, ctypes.POINTER(Schedule)]),
             "dfa_partition_map": (i32, [D, i32, ctypes.POINTER(PosMap)]),
             "dfa_workspace_size": (sz, [D, i32]),
@@ -518,6 +547,245 @@ def attn_steps_host(steps, causal=True, scale=None, P=1, partition="contiguous",
                                      _stream(h2d_stream) if overlap else None,
                                      _stream(d2h_stream) if overlap else None))
     return outs
+
+
+# ----------------------------------------------------------------------------
+# rotary positions and the paged key/value cache
+# ----------------------------------------------------------------------------
+def rope_spec(d, layout="interleaved", rot_dim=None, theta_base=10000.0, scaling="none",
+              factor=1.0, orig_len=0.0, low=0.0, high=0.0, gain=1.0) -> RopeSpec:
+    """A rotary embedding (dfa_rope_spec) of the first rot_dim (default: all) of
+    d features: layout "interleaved" (pairs 2t, 2t+1) or "half" (t, t +
+    rot_dim/2); scaling "none", "linear" (factor) or "bands" (factor, orig_len,
+    low, high); gain multiplies the rotated features."""
+    return RopeSpec(ROPE_LAYOUTS[layout], d if rot_dim is None else rot_dim,
+                    ROPE_SCALINGS[scaling], 0, theta_base, factor, orig_len, low, high, gain)
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _rows(t, name, dtype, device, shape=None):
+    """Pointer and strides of a [B,H,L,d] row tensor with contiguous features."""
+    if t.dim() != 4 or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} [B,H,L,d] tensor on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the features of {name} must be contiguous")
+    return t.data_ptr(), _Strides(st[0], st[1], st[2])
+
+
+def _int32(t, name, shape, device):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on {device}")
+    return t.data_ptr()
+
+
+def _on_current(device):
+    """The call's kernels run on the current device; the tensors have to be there."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, not on {device}")
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _new(stream, shape, dtype, device):
+    """Memory that the call's stream may use at once (and keeps until it is done)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def rope(x, spec: RopeSpec, positions=None, pos_map: PosMap | None = None, inverse=False,
+         out=None, stream=None):
+    """Rotate rows x [B,H,L,d] (bf16 or fp32; any strides with contiguous
+    features) at positions [B,L] int32, or at those of pos_map, or at 0..L-1
+    (dfa_rope).  inverse: the transposed rotation, for gradients.  out=x works in
+    place; without out a contiguous tensor is returned."""
+    dev = x.device
+    _on_current(dev)
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bf16 or fp32")
+    if positions is not None and pos_map is not None:
+        raise ValueError("give positions or pos_map, not both")
+    xp, xs = _rows(x, "x", x.dtype, dev)
+    B, H, L, d = x.shape
+    if out is None:
+        out = _new(stream, x.shape, x.dtype, dev)
+    op, os_ = _rows(out, "out", x.dtype, dev, x.shape)
+    _check(lib().dfa_rope(ctypes.byref(spec), B, H, L, d, int(x.dtype == torch.float32), xp, xs,
+                          op, os_, None if pos_map is None else ctypes.byref(pos_map),
+                          _int32(positions, "positions", (B, L), dev), int(inverse),
+                          _raw_stream(stream)))
+    return out
+
+
+class PagedCache:
+    """A paged key/value cache (dfa_paged_cache) over the caller's tensors, which
+    it keeps alive: k, v [npages,Hkv,page,d], bf16 or float8_e4m3fn (pages may be
+    strided: k and v can be two halves of one tensor), with k_scale and v_scale
+    [npages,Hkv] fp32 for 8 bits; block_table [B,max_pages] and seq_lens [B]
+    int32.  Change their contents freely; a new table or batch is a new
+    PagedCache."""
+
+    def __init__(self, k, v, block_table, seq_lens, k_scale=None, v_scale=None):
+        dev = k.device
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("k must be a bf16 or float8_e4m3fn [npages,Hkv,page,d] tensor")
+        if v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("k and v must agree in shape, dtype and strides")
+        npages, Hkv, page, d = k.shape
+        # (the strides of dimensions of one element say nothing)
+        inner = zip(k.shape[1:], k.stride()[1:], (page * d, d, 1))
+        if any(n > 1 and st != want for n, st, want in inner) or (
+                npages > 1 and k.stride(0) < Hkv * page * d):
+            raise ValueError("the heads, rows and features of a page must be contiguous")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        B, max_pages = block_table.shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("an 8-bit cache has k_scale and v_scale, a bf16 cache has none")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (npages, Hkv) or
+                                  not t.is_contiguous()):
+                raise ValueError("scales must be contiguous fp32 [npages, Hkv] tensors")
+        for t in (v, block_table, seq_lens, k_scale, v_scale):
+            if t is not None and t.device != dev:
+                raise ValueError("the cache's tensors must be on one device")
+        self.device, self.dtype = dev, k.dtype
+        self.B, self.Hkv, self.page, self.d = B, Hkv, page, d
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.desc = PagedCacheDesc(
+            int(e4m3), page, Hkv, d, npages, k.stride(0) if npages > 1 else 0, k.data_ptr(),
+            v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+            v_scale.data_ptr() if e4m3 else None, B, max_pages,
+            _int32(block_table, "block_table", (B, max_pages), dev),
+            _int32(seq_lens, "seq_lens", (B,), dev))
+        self._ref = ctypes.byref(self.desc)
+
+
+def paged_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:
+    """A workspace for the calls on this cache: Hq query heads, T tokens a
+    sequence at most.  It serves one call at a time."""
+    desc = make_desc(cache.B, Hq or cache.Hkv, cache.Hkv, 1, cache.d)
+    n = int(lib().dfa_decode_paged_workspace_size(ctypes.byref(desc), T))
+    # more rows than decode_paged takes: the other calls need the status word only
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.device)
+
+
+def _ws(ws, nbytes, cache, stream):
+    if ws is None:
+        return _new(stream, (nbytes,), torch.uint8, cache.device)
+    if ws.device != cache.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {cache.device}")
+    return ws
+
+
+def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens=None, q=None,
+                 q_out=None, ws=None, stream=None):
+    """Store the new rows k, v [B,Hkv,T,d] bf16 (any strides with contiguous
+    features) of every sequence at the end of its cached rows, keys rotated by
+    rope on the way (dfa_cache_append).  cache.seq_lens counts them already;
+    new_lens [B] int32: how many of the T are a sequence's (default: all).  With
+    q [B,Hq,T,d] its rows are rotated too, into q_out (default: a new contiguous
+    tensor; rows from new_lens on are not written), which is returned."""
+    dev = cache.device
+    _on_current(dev)
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hkv,T,d]")
+    T = k.shape[2]
+    shape = (cache.B, cache.Hkv, T, cache.d)
+    kp, ks = _rows(k, "k", torch.bfloat16, dev, shape)
+    vp, vs = _rows(v, "v", torch.bfloat16, dev, shape)
+    ws = _ws(ws, 256, cache, stream)
+    Hq, qp, qs, op, os_ = 0, None, None, None, None
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B,Hq,T,d]")
+        Hq = q.shape[1]
+        shape = (cache.B, Hq, T, cache.d)
+        qp, qs = _rows(q, "q", torch.bfloat16, dev, shape)
+        if q_out is None:
+            q_out = _new(stream, shape, torch.bfloat16, dev)
+        op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(lib().dfa_cache_append(cache._ref, None if rope is None else ctypes.byref(rope), T,
+                                  _int32(new_lens, "new_lens", (cache.B,), dev), kp, ks, vp, vs,
+                                  Hq, qp, qs, op, os_, ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream)))
+    return q_out
+
+
+def cache_gather(cache: PagedCache, L, pos0=0, k_out=None, v_out=None, ws=None, stream=None):
+    """Cached rows [pos0, pos0 + L) of every sequence as contiguous bf16
+    [B,Hkv,L,d] (dfa_cache_gather): returns (k_out, v_out).  Rows behind a
+    sequence's end are not written."""
+    dev = cache.device
+    _on_current(dev)
+    shape = (cache.B, cache.Hkv, L, cache.d)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = _new(stream, shape, torch.bfloat16, dev)
+        elif (t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or
+              not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bf16 {list(shape)} tensor on {dev}")
+        outs.append(t)
+    ws = _ws(ws, 256, cache, stream)
+    _check(lib().dfa_cache_gather(cache._ref, pos0, L, outs[0].data_ptr(), outs[1].data_ptr(),
+                                  ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+    return outs[0], outs[1]
+
+
+def decode_paged(cache: PagedCache, q, q_lens=None, causal=True, scale=None, out_fp32=False,
+                 ws=None, out=None, lse=None, stream=None):
+    """Attention of the last tokens of every sequence over its cached rows
+    (dfa_decode_paged): q [B,Hq,T,d] bf16 (any strides with contiguous features),
+    q_lens [B] int32 of the T tokens per sequence (default: all), the last of
+    them at position seq_lens - 1.  Returns (O [B,Hq,T,d], LSE [B,Hq,T]); rows
+    from q_lens on are not written."""
+    dev = cache.device
+    _on_current(dev)
+    if q.dim() != 4:
+        raise ValueError("q must be [B,Hq,T,d]")
+    B, Hq, T, d = q.shape
+    qp, qs = _rows(q, "q", torch.bfloat16, dev, (cache.B, Hq, T, cache.d))
+    o_dtype = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out = _new(stream, (B, Hq, T, d), o_dtype, dev)
+    elif (out.shape != q.shape or out.dtype != o_dtype or out.device != dev or
+          not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous {o_dtype} tensor of q's shape on {dev}")
+    if lse is None:
+        lse = _new(stream, (B, Hq, T), torch.float32, dev)
+    elif (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != dev or
+          not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous fp32 [B,Hq,T] tensor on {dev}")
+    desc = AttnDesc(B, Hq, cache.Hkv, 1, d, int(causal),
+                    1.0 / math.sqrt(d) if scale is None else scale, 1, 0, 1, int(out_fp32), 0,
+                    None)
+    ref = ctypes.byref(desc)
+    if ws is None:
+        ws = _new(stream, (max(256, int(lib().dfa_decode_paged_workspace_size(ref, T))),),
+                  torch.uint8, dev)
+    else:
+        ws = _ws(ws, 0, cache, stream)
+    _check(lib().dfa_decode_paged(ref, cache._ref, T, _int32(q_lens, "q_lens", (B,), dev), qp, qs,
+                                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream)))
+    return out, lse
 
 
 # ----------------------------------------------------------------------------
