@@ -1,114 +1,918 @@
-// dfa_paged.cu -- decoding attention over a paged cache, simple form: one block
-// per query row, a warp per key in turn, fp32 throughout.
+// dfa_paged.cu -- decoding attention over a paged key/value cache: the last few
+// tokens of a ragged batch of sequences against their cached rows (FlashAttention
+// glossary entry, the Flash-Decoding variant: the keys are split, partial results
+// are merged by log-sum-exp rescaling).
+//
+// Method.  For a row q of a sequence, with keys k_j = s_j c_j (codes c_j times
+// the scale s_j of their page and head) and values v_j = u_j w_j:
+//   x_j = scale log2(e) s_j (q . c_j),   O = sum_j 2^(x_j - LSE) u_j w_j.
+// The codes go into the matrix products as they are (e4m3 is exact in fp16); the
+// key's scale multiplies the score, the value's scale its weight.  Weights are
+// held as 2^(x_j + log2 u_j - M) with M the running maximum of the exponent, so
+// that they stay in fp16's range whatever the scales are, and the sum of
+// probabilities collects 2^(x_j + log2 u_j - M) / u_j in fp32.
+//
+// What bounds it: HBM.  A cached row is read once and meets G*T query rows, a
+// few operations a byte: too few rows for a 128-row tcgen05 tile, so the products
+// are the 16x8x16 warp products, with the cache in the 16-row operand and 8
+// query rows (NB = 1) or 16 (NB = 2) in the other: S^T = K Q^T, O^T = V^T P^T.
+//
+// Work.  (sequence, head, row group) segments of 64-key tiles form one line,
+// cut evenly over a persistent grid whatever the lengths: a block's range
+// covers whole segments, whose result it writes, and up to two cut ones, whose
+// partials it leaves in the workspace for merge_kernel.  The lengths are read
+// on the device, so a captured graph follows them.
+//
+// A block: warp 4 fetches pages by TMA into a ring of tiles (128- or 64-byte
+// swizzle; the page numbers and scales of 32 pages are looked up at a time);
+// warps 0-3 take 16 keys of every tile each, with a running maximum, sum and O
+// of their own, joined at the segment's end.
+//
+// Rounding: fp16 weights (half a step 2^-11) for 8-bit cells, and q as fp16
+// relative to the power of two of the row's largest element (exact but for
+// elements 2^-14 below it); for bf16 cells q as it is and the weight as two bf16
+// terms (2^-16), since one would add as much error as the rounding of O.
 #include "dfa_serve.cuh"
 
 namespace dfa {
 
-namespace {
+namespace paged {
 
-template <typename CELL, int D>
-__global__ void __launch_bounds__(256) decode_paged_kernel(const __grid_constant__ PagedParams p)
+constexpr int kWarps = 4;                  // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = kPagedTile;
+constexpr float kGrow = 8.f;               // rescale when the maximum grows by 2^8
+constexpr float kSumShift = 16.f;          // 8-bit cells: sums are kept times 2^-16, so
+                                           // that scales of 2^-100 do not overflow them
+constexpr float kNoPage = -1.f;            // in place of a key scale
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D, bool F8, int NB>
+struct Cfg {
+    static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+    static constexpr int kPlanes = kRowBytes > 128 ? 2 : 1;  // boxes side by side
+    static constexpr int kPlaneBytes = kRowBytes / kPlanes;  // 64 or 128: swizzle width
+    static constexpr int kOperand = kTile * kRowBytes;       // K or V of a tile
+    static constexpr int kStage = 2 * kOperand;
+    static constexpr int kStages = kStage >= 32768 ? 2 : 49152 / kStage;
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kPitch = D + 4;                     // floats of an O row in the join
+    static constexpr int kJoin = kWarps * kRows * kPitch * 4;
+    static constexpr int kSmem = 1024 + kStages * kStage + kJoin;
+    // blocks of an SM that are resident together (registers and shared memory)
+    static constexpr int kResident = NB == 1 && kStage < 32768 ? 3 : 2;
+    static constexpr int kSteps = D / 16;                    // products over the features
+    static constexpr int kLaneVals = kPlaneBytes / (F8 ? 8 : 16);  // V features per plane, lane
+};
+
+struct Shared {
+    uint64_t full[8], empty[8];
+    float2 scale[8][4];           // per stage and page: K and V scale (kNoPage: no page)
+    // maxima and sums of the warps at a segment's end; two sets, since a warp may
+    // end the next segment while another still reads this one's
+    float m[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
+    long long warp_sum[kThreads / 32];
+    long long w0, w1, total, base;
+    int32_t b, active;            // active: blocks that have tiles
+    uint32_t abort;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3)
 {
-    constexpr bool k8 = sizeof(CELL) == 1;
-    constexpr int C = D / 32;
-    __shared__ float s_m[8], s_l[8], s_o[8][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t i = blockIdx.x;
-    const int32_t t = (int32_t)(i % p.T);
-    i /= p.T;
-    const int32_t hq = (int32_t)(i % p.Hq), b = (int32_t)(i / p.Hq), hk = hq / p.G;
-    int32_t len, n;
-    seq_rows(p.c, p.q_lens, p.T, b, len, n);
-    if (t >= n)
-        return;
-    const int32_t keys = p.causal ? len - n + t + 1 : len;
-    float q[C], o[C], m = -INFINITY, l = 0.f;
-    const __nv_bfloat16* qr = (const __nv_bfloat16*)p.q.p + b * p.q.sb + hq * p.q.sh + t * p.q.sl;
-    for (int c = 0; c < C; ++c) {
-        q[c] = __bfloat162float(qr[lane * C + c]) * p.scale_log2;
-        o[c] = 0.f;
-    }
-    for (int32_t j = warp; j < keys; j += 8) {
-        const int32_t id = page_of(p.c, b, j / p.c.page);
-        if (id < 0)
-            continue;
-        const int64_t at = (int64_t)id * p.c.page_stride +
-                           ((int64_t)hk * p.c.page + j % p.c.page) * D + lane * C;
-        float ks = 1.f, vs = 1.f, kf[C], vf[C];
-        if (k8) {
-            ks = p.c.k_scale[(int64_t)id * p.c.Hkv + hk];
-            vs = p.c.v_scale[(int64_t)id * p.c.Hkv + hk];
-            for (int c = 0; c < C; c += 2) {
-                const float2 a = e4m3x2_float2(*(const uint16_t*)((const uint8_t*)p.c.k + at + c));
-                const float2 w = e4m3x2_float2(*(const uint16_t*)((const uint8_t*)p.c.v + at + c));
-                kf[c] = a.x, kf[c + 1] = a.y, vf[c] = w.x, vf[c + 1] = w.y;
-            }
-        } else {
-            for (int c = 0; c < C; ++c) {
-                kf[c] = __bfloat162float(((const __nv_bfloat16*)p.c.k)[at + c]);
-                vf[c] = __bfloat162float(((const __nv_bfloat16*)p.c.v)[at + c]);
-            }
-        }
-        float s = 0.f;
-        for (int c = 0; c < C; ++c)
-            s = fmaf(q[c], kf[c], s);
-        for (int off = 16; off > 0; off >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= ks;
-        const float mn = fmaxf(m, s);
-        const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float pj = mn == -INFINITY ? exp2f(s) : exp2f(s - mn);
-        l = l * alpha + pj;
-        for (int c = 0; c < C; ++c)
-            o[c] = o[c] * alpha + pj * vs * vf[c];
-        m = mn;
-    }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
-    for (int c = 0; c < C; ++c)
-        s_o[warp][lane * C + c] = o[c];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f, acc = 0.f;
-    for (int w = 0; w < 8; ++w)
-        M = fmaxf(M, s_m[w]);
-    const int f = threadIdx.x;
-    for (int w = 0; w < 8; ++w) {
-        const float e = s_m[w] == -INFINITY ? (s_l[w] == 0.f ? 0.f : 1.f) : exp2f(s_m[w] - M);
-        L += e * s_l[w];
-        if (f < D)
-            acc += e * s_o[w][f];
-    }
-    const int64_t row = ((int64_t)b * p.Hq + hq) * p.T + t;
-    if (f < D) {
-        const float r = L == 0.f ? 0.f : acc / L;
-        if (p.o_fp32)
-            ((float*)p.o)[row * D + f] = r;
-        else
-            ((__nv_bfloat16*)p.o)[row * D + f] = __float2bfloat16_rn(r);
-    }
-    if (f == 0)
-        p.lse[row] = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * 0.69314718055994531f + logf(L);
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
 }
 
-}  // namespace
-
-cudaError_t launch_decode_paged(const PagedParams& p, cudaStream_t stream)
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
 {
-    const unsigned blocks = (unsigned)((int64_t)p.c.B * p.Hq * p.T);
-    if (p.c.e4m3) {
-        if (p.c.d == 128)
-            decode_paged_kernel<uint8_t, 128><<<blocks, 256, 0, stream>>>(p);
-        else
-            decode_paged_kernel<uint8_t, 64><<<blocks, 256, 0, stream>>>(p);
-    } else {
-        if (p.c.d == 128)
-            decode_paged_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(p);
-        else
-            decode_paged_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(p);
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void consumer_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+// D (16x8, fp32) += A (16x16) B (16x8), fp16 or bf16 operands
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// transpose of an 8x8 matrix of 16-bit elements held one row per 4 lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// Byte offset of 16-byte chunk c of row r of a swizzled plane.
+template <int PB>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c)
+{
+    return PB == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+
+// Tiles of a sequence with `n` queried tokens: at least one, so that rows
+// without keys are written too.
+__device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
+{
+    return n > 0 ? max(1, ceil_div(len, kTile)) : 0;
+}
+
+// A run of tiles [tile0, tile0 + nt) of one segment of the block's range.
+struct Walk {
+    long long w, w1, base;  // next and end of the range; first tile of sequence b
+    int32_t b, len, n, tiles;
+    int32_t hr, tile0, nt;  // head * row groups + row group
+
+    __device__ __forceinline__ void start(const PagedParams& p, const Shared& sh)
+    {
+        w = sh.w0;
+        w1 = sh.w1;
+        base = sh.base;
+        b = sh.b;
+        if (w < w1) {
+            seq_rows(p.c, p.q_lens, p.T, b, len, n);
+            tiles = tiles_of(len, n);
+        }
     }
+    __device__ __forceinline__ bool next(const PagedParams& p)
+    {
+        if (w >= w1)
+            return false;
+        const int32_t per_seq = p.c.Hkv * p.row_groups;
+        while (w >= base + (long long)tiles * per_seq) {
+            base += (long long)tiles * per_seq;
+            ++b;
+            seq_rows(p.c, p.q_lens, p.T, b, len, n);
+            tiles = tiles_of(len, n);
+        }
+        const long long at = w - base;
+        hr = (int32_t)(at / tiles);
+        tile0 = (int32_t)(at - (long long)hr * tiles);
+        nt = (int32_t)min((long long)(tiles - tile0), w1 - w);
+        w += nt;
+        return true;
+    }
+};
+
+// The block's range of the line of tiles, and the sequence that it begins in.
+__device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
+{
+    const int32_t per_seq = p.c.Hkv * p.row_groups;
+    const int32_t chunk = ceil_div(p.c.B, kThreads);
+    const int32_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, p.c.B);
+    long long sum = 0;
+    for (int32_t b = b0; b < b1; ++b) {
+        int32_t len, n;
+        seq_rows(p.c, p.q_lens, p.T, b, len, n);
+        sum += (long long)tiles_of(len, n) * per_seq;
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if ((threadIdx.x & 31) >= o)
+            incl += x;
+    }
+    if ((threadIdx.x & 31) == 31)
+        sh.warp_sum[threadIdx.x >> 5] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < (threadIdx.x >> 5))
+            before += sh.warp_sum[w];
+        total += sh.warp_sum[w];
+    }
+    incl += before;
+    const int32_t active = (int32_t)min((long long)gridDim.x, total);
+    const bool mine = (int32_t)blockIdx.x < active;  // then at least one tile
+    const long long w0 = mine ? total * blockIdx.x / active : 0;
+    const long long w1 = mine ? total * (blockIdx.x + 1) / active : 0;
+    if (threadIdx.x == 0) {
+        sh.w0 = w0;
+        sh.w1 = w1;
+        sh.total = total;
+        sh.active = active;
+    }
+    if (w0 < w1 && incl - sum <= w0 && w0 < incl) {
+        long long base = incl - sum;
+        for (int32_t b = b0; b < b1; ++b) {
+            int32_t len, n;
+            seq_rows(p.c, p.q_lens, p.T, b, len, n);
+            const long long t = (long long)tiles_of(len, n) * per_seq;
+            if (w0 < base + t) {
+                sh.b = b;
+                sh.base = base;
+                break;
+            }
+            base += t;
+        }
+    }
+    __syncthreads();
+}
+
+template <int D, bool F8, int NB>
+__device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32_t ring,
+                                        const CUtensorMap& tk, const CUtensorMap& tv,
+                                        const WaitCtx& wctx)
+{
+    using C = Cfg<D, F8, NB>;
+    const int lane = threadIdx.x & 31;
+    const int32_t page = p.c.page;
+    const int32_t box_rows = min(page, kTile);
+    const int32_t per_tile = kTile / box_rows;  // boxes of a tile
+    uint32_t it = 0;
+    Walk wk;
+    wk.start(p, sh);
+    while (wk.next(p)) {
+        const int32_t h = wk.hr / p.row_groups;
+        const int32_t pages_end =
+            ceil_div(min(wk.len, (wk.tile0 + wk.nt) * kTile), page);  // of this run
+        int32_t win = -64, id = -1;  // first page of the 32 looked up; this lane's
+        float ks = 1.f, vs = 1.f;
+        for (int32_t i = 0; i < wk.nt; ++i, ++it) {
+            const int32_t key0 = (wk.tile0 + i) * kTile;
+            const int32_t p0 = key0 / page;
+            if (p0 >= win + 32) {
+                win = p0;
+                id = -1;
+                if (win + lane < pages_end) {
+                    id = page_of(p.c, wk.b, win + lane);
+                    if (F8 && id >= 0) {
+                        const int64_t at = (int64_t)id * p.c.Hkv + h;
+                        ks = __ldg(p.c.k_scale + at);
+                        vs = __ldg(p.c.v_scale + at);
+                    }
+                }
+            }
+            const uint32_t st = it % C::kStages;
+            if (it >= C::kStages) {
+                const bool ok = mbar_wait(&sh.empty[st], (it / C::kStages - 1) & 1, wctx, 50);
+                if (!__all_sync(0xffffffffu, ok))
+                    return;
+            }
+            const int src = p0 - win + lane;  // lanes below per_tile: their box's page
+            const int32_t my = __shfl_sync(0xffffffffu, id, src & 31);
+            const float my_ks = __shfl_sync(0xffffffffu, ks, src & 31);
+            const float my_vs = __shfl_sync(0xffffffffu, vs, src & 31);
+            const bool load = lane < per_tile && p0 + lane < pages_end && my >= 0;
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
+            if (lane == 0)
+                mbar_expect(&sh.full[st], boxes * (2 * box_rows * C::kRowBytes));
+            __syncwarp();
+            if (load) {
+                const uint32_t dst = ring + st * C::kStage + lane * box_rows * C::kPlaneBytes;
+                const int row = key0 & (page - 1);  // 0 unless a page holds several tiles
+#pragma unroll
+                for (int pl = 0; pl < C::kPlanes; ++pl) {
+                    const uint32_t d2 = dst + pl * kTile * C::kPlaneBytes;
+                    tma_load_4d(d2, &tk, &sh.full[st], pl * 64, row, h, my);
+                    tma_load_4d(d2 + C::kOperand, &tv, &sh.full[st], pl * 64, row, h, my);
+                }
+            }
+            if (lane < per_tile)
+                sh.scale[st][lane] = load ? make_float2(my_ks, my_vs) : make_float2(kNoPage, 0.f);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.full[st]);
+        }
+    }
+}
+
+// Four keys' V features of one lane as stored: keys 2t, 2t+1, 2t+8, 2t+9.
+template <int W>
+struct Vals {
+    uint32_t w[4][W];
+};
+
+template <bool F8>
+__device__ __forceinline__ bool not_finite(uint32_t w)
+{
+    if (F8)
+        return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+}
+
+// The 16x16 operand V^T of features 2j, 2j+1 of a plane (lane g: rows g and
+// g + 8) and the group's 16 keys.
+template <bool F8, int W>
+__device__ __forceinline__ void value_frag(const Vals<W>& v, int j, uint32_t (&a)[4])
+{
+    if (F8) {
+        const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;  // features 2j, 2j+1 of two keys
+        const uint32_t x = __byte_perm(v.w[0][j / 2], v.w[1][j / 2], sel);
+        const uint32_t y = __byte_perm(v.w[2][j / 2], v.w[3][j / 2], sel);
+        a[0] = e4m3x2_half2(x & 0xffffu);
+        a[1] = e4m3x2_half2(x >> 16);
+        a[2] = e4m3x2_half2(y & 0xffffu);
+        a[3] = e4m3x2_half2(y >> 16);
+    } else {
+        a[0] = __byte_perm(v.w[0][j], v.w[1][j], 0x5410);
+        a[1] = __byte_perm(v.w[0][j], v.w[1][j], 0x7632);
+        a[2] = __byte_perm(v.w[2][j], v.w[3][j], 0x5410);
+        a[3] = __byte_perm(v.w[2][j], v.w[3][j], 0x7632);
+    }
+}
+
+// Features f..f+3 of an output row, and its LSE: o and L are relative to 2^mx
+// (L also to 2^kSumShift for 8-bit cells).
+template <int D, bool F8>
+__device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int f, float mx,
+                                          float L, float4 o)
+{
+    const float inv = L == 0.f ? 0.f : (F8 ? 1.f / 65536.f : 1.f) / L;  // (NaN stays NaN)
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    if (p.o_fp32)
+        *reinterpret_cast<float4*>((float*)p.o + at * D + f) = o;
+    else
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + at * D + f) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    if (f == 0)
+        p.lse[at] = L == 0.f ? -INFINITY
+                             : ((mx == -INFINITY ? 0.f : mx) + (F8 ? kSumShift : 0.f) + log2f(L)) *
+                                   kLn2;
+}
+
+template <int D, bool F8, int NB>
+__device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32_t ring,
+                                        float* join, const WaitCtx& wctx)
+{
+    using C = Cfg<D, F8, NB>;
+    constexpr int kWords = C::kLaneVals / (F8 ? 4 : 2);  // V words per key and plane
+    constexpr int kMt = C::kPlanes * C::kLaneVals / 2;   // O^T tiles of 16 features
+    constexpr int kChunks = C::kPlaneBytes / 64;         // K chunks per lane and plane
+    static_assert(kMt == D / 16, "features");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int32_t page = p.c.page;
+    const int sc_at = page < kTile ? warp * 16 / page : 0;
+    const int32_t R = p.G * p.T;
+    uint32_t it = 0;
+    int par = 0;
+    bool dead = false;  // a wait gave up: keep the barriers' count, compute nothing
+    int4 info = make_int4(0, 0, 0, 0);
+    Walk wk;
+    wk.start(p, sh);
+    while (wk.next(p)) {
+        const int32_t h = wk.hr / p.row_groups;
+        const int32_t r0 = (wk.hr - h * p.row_groups) * C::kRows;
+        const int32_t len = wk.len, n = wk.n;
+        // ---- queries: rows g of each block of 8, this lane's features
+        uint32_t q[NB][C::kSteps][2];
+        float rf[NB][2];       // score factor of rows 2t, 2t+1
+        int32_t lim[NB][2];    // last visible key of rows 2t, 2t+1
+        int32_t tok[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int32_t r = r0 + nb * 8 + g;
+            const int32_t gh = r / p.T, tq = r - gh * p.T;
+            const bool there = r < R && tq < n;
+            const __nv_bfloat16* row = (const __nv_bfloat16*)p.q.p + wk.b * p.q.sb +
+                                       (int64_t)(h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl;
+#pragma unroll
+            for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                for (int i = 0; i < C::kSteps / C::kPlanes; i += 2) {
+                    // two steps: 8 features
+                    const int f = pl * 64 + t * (D / C::kPlanes / 4) + 4 * i;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (there)
+                        x = __ldg(reinterpret_cast<const uint4*>(row + f));
+                    const int s = pl * (C::kSteps / C::kPlanes) + i;
+                    q[nb][s][0] = x.x;
+                    q[nb][s][1] = x.y;
+                    q[nb][s + 1][0] = x.z;
+                    q[nb][s + 1][1] = x.w;
+                }
+            float f = p.scale_log2;
+            if (F8) {
+                float amax = 0.f;
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[nb][s][k])),
+                                                 fabsf(bf16hi(q[nb][s][k]))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                f *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        q[nb][s][k] =
+                            pack_half2(bf16lo(q[nb][s][k]) * inv, bf16hi(q[nb][s][k]) * inv);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                rf[nb][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
+                const int32_t rr = r0 + nb * 8 + 2 * t + k;
+                tok[nb][k] = rr < R ? rr % p.T : n;
+                lim[nb][k] = p.causal ? len - n + min(tok[nb][k], n - 1) : len - 1;
+            }
+        }
+        // keys up to all_see are visible to every row, keys from len on to none
+        const int32_t all_see = p.causal ? len - n : len - 1;
+        float O[NB][kMt][4], M[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                M[nb][k] = -INFINITY;
+                l[nb][k] = 0.f;
+            }
+#pragma unroll
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    O[nb][m][k] = 0.f;
+        }
+        // ---- the run's tiles
+        for (int32_t i = 0; i < wk.nt; ++i, ++it) {
+            const uint32_t st = it % C::kStages;
+            if (!dead) {
+                const bool ok = mbar_wait(&sh.full[st], (it / C::kStages) & 1, wctx, 60);
+                dead = !__all_sync(0xffffffffu, ok);
+            }
+            const int32_t base = (wk.tile0 + i) * kTile + warp * 16;  // the warp's 16 keys
+            const float2 sc = sh.scale[st][sc_at];
+            if (!dead && base < len && sc.x != kNoPage) {
+                const uint32_t kt = ring + st * C::kStage;
+                const uint32_t vt = kt + C::kOperand;
+                const uint32_t row = warp * 16;
+                // S^T = K Q^T; two sums, so that half the products are independent
+                float acc[NB][2][4];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[nb][0][k] = acc[nb][1][k] = 0.f;
+#pragma unroll
+                for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        const uint32_t plane = kt + pl * kTile * C::kPlaneBytes;
+                        const uint4 x =
+                            lds128(plane + chunk_at<C::kPlaneBytes>(row + g, t * kChunks + c));
+                        const uint4 y =
+                            lds128(plane + chunk_at<C::kPlaneBytes>(row + g + 8, t * kChunks + c));
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+                        constexpr int kPer = F8 ? 4 : 2;  // steps of a chunk
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) {
+                            const int s = (pl * kChunks + c) * kPer + j;
+                            uint32_t a0, a1, a2, a3;
+                            if (F8) {
+                                a0 = e4m3x2_half2(xw[j] & 0xffffu);
+                                a2 = e4m3x2_half2(xw[j] >> 16);
+                                a1 = e4m3x2_half2(yw[j] & 0xffffu);
+                                a3 = e4m3x2_half2(yw[j] >> 16);
+                            } else {
+                                a0 = xw[2 * j], a2 = xw[2 * j + 1];
+                                a1 = yw[2 * j], a3 = yw[2 * j + 1];
+                            }
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, q[nb][s][0],
+                                             q[nb][s][1]);
+                        }
+                    }
+                Vals<kWords> v[C::kPlanes];
+#pragma unroll
+                for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t r = row + 2 * t + (k & 1) + (k >> 1) * 8;
+                        const uint32_t plane = vt + pl * kTile * C::kPlaneBytes;
+                        if (kWords == 4) {
+                            const uint4 x = lds128(plane + chunk_at<C::kPlaneBytes>(r, g));
+                            v[pl].w[k][0] = x.x, v[pl].w[k][1] = x.y;
+                            v[pl].w[k][kWords - 2] = x.z, v[pl].w[k][kWords - 1] = x.w;
+                        } else {
+                            const uint2 x = lds64(plane + chunk_at<C::kPlaneBytes>(r, g >> 1) +
+                                                  (g & 1) * 8);
+                            v[pl].w[k][0] = x.x, v[pl].w[k][1] = x.y;
+                        }
+                    }
+                // value scale = vm 2^ve, vm in [1, 2) (1 for the powers of two that
+                // the append writes)
+                float ve = 0.f, vm = 1.f;
+                if (F8) {
+                    const int e = (int)(__float_as_uint(sc.y) >> 23);  // sign bit clear
+                    const bool normal = e > 0 && e < 255;
+                    ve = normal ? (float)(e - 127) : 0.f;
+                    vm = normal ? __uint_as_float((__float_as_uint(sc.y) & 0x7fffffu) |
+                                                  (127u << 23))
+                                : (e == 255 ? sc.y : 0.f);
+                }
+                const bool masked = base + 15 > all_see;  // some row does not see some key
+                bool apart = false;  // non-finite V that some rows do not see
+                if (masked) {
+                    // V of keys behind the end is not ours
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (base + 2 * t + (k & 1) + (k >> 1) * 8 >= len)
+#pragma unroll
+                            for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w)
+                                    v[pl].w[k][w] = 0u;
+                    if (p.causal && n > 1) {
+#pragma unroll
+                        for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w)
+                                    apart |= not_finite<F8>(v[pl].w[k][w]);
+                        apart = __any_sync(0xffffffffu, apart);
+                    }
+                }
+                uint32_t pt[NB][2], pr[NB][2];  // P^T (and its bf16 remainder)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // exponents of the weights: row 2t + (k & 1), key g + 8 (k >> 1)
+                        const float s = (acc[nb][0][k] + acc[nb][1][k]) * (rf[nb][k & 1] * sc.x);
+                        x[k] = F8 ? s + ve : s;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = base + g + 8 * (k >> 1) <= lim[nb][k & 1] ? x[k] : -INFINITY;
+                    }
+                    const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
+                    if (__any_sync(0xffffffffu,
+                                   x0 > M[nb][0] + kGrow || x1 > M[nb][1] + kGrow)) {
+                        float mx[2] = {x0, x1}, f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+                            const float mn = fmaxf(M[nb][k], mx[k]);
+                            f[k] = M[nb][k] == -INFINITY ? 0.f : ex2(M[nb][k] - mn);
+                            M[nb][k] = mn;
+                            l[nb][k] *= f[k];
+                        }
+#pragma unroll
+                        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                O[nb][m][k] *= f[k & 1];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float m = M[nb][k & 1];
+                        x[k] -= m == -INFINITY ? 0.f : m;
+                        // an exponential of its own: with value scales far apart the
+                        // weight may vanish where the probability does not
+                        const float prob = ex2(F8 ? x[k] - (ve + kSumShift) : x[k]);
+                        l[nb][k & 1] += prob;
+                        x[k] = F8 ? ex2(x[k]) * vm : prob;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (F8) {
+                            pt[nb][k] = transpose8(pack_half2(x[2 * k], x[2 * k + 1]));
+                        } else {
+                            const uint32_t hi = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                            const uint32_t lo =
+                                pack_bf16x2(x[2 * k] - bf16lo(hi), x[2 * k + 1] - bf16hi(hi));
+                            pt[nb][k] = transpose8(hi);
+                            pr[nb][k] = transpose8(lo);
+                        }
+                    }
+                }
+                if (!apart) {
+                    // O^T += V^T P^T
+#pragma unroll
+                    for (int m = 0; m < kMt; ++m) {
+                        uint32_t a[4];
+                        value_frag<F8>(v[m * C::kPlanes / kMt], m % (kMt / C::kPlanes), a);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                            if (!F8)
+                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
+                                             pr[nb][1]);
+                        }
+                    }
+                } else {
+                    // a NaN or an infinity times a weight of zero would reach rows
+                    // that do not see it: one token at a time, with the values
+                    // behind its position taken out
+                    for (int32_t tt = 0; tt < n; ++tt) {
+                        Vals<kWords> u[C::kPlanes];
+#pragma unroll
+                        for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w)
+                                    u[pl].w[k][w] =
+                                        base + 2 * t + (k & 1) + (k >> 1) * 8 <= len - n + tt
+                                            ? v[pl].w[k][w]
+                                            : 0u;
+#pragma unroll
+                        for (int m = 0; m < kMt; ++m) {
+                            uint32_t a[4];
+                            value_frag<F8>(u[m * C::kPlanes / kMt], m % (kMt / C::kPlanes), a);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2], O[nb][m][3]};
+                                mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                                if (!F8)
+                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (tok[nb][k & 1] == tt)
+                                        O[nb][m][k] = d[k];
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[st]);
+        }
+        // ---- join the warps: largest maximum, rescaled sums and O
+        par ^= 1;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    l[nb][k] += __shfl_xor_sync(0xffffffffu, l[nb][k], o);
+                if (g == 0) {
+                    sh.m[par][warp][nb * 8 + 2 * t + k] = M[nb][k];
+                    sh.l[par][warp][nb * 8 + 2 * t + k] = l[nb][k];
+                }
+            }
+        consumer_sync();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = nb * 8 + 2 * t + k;
+                float mx = sh.m[par][0][r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w)
+                    mx = fmaxf(mx, sh.m[par][w][r]);
+                // a warp without a maximum has O = 0, or only NaN
+                const float f = M[nb][k] == -INFINITY ? 1.f : ex2(M[nb][k] - mx);
+                if (r0 + r < R) {
+                    float* dst = join + (warp * C::kRows + r) * C::kPitch;
+#pragma unroll
+                    for (int pl = 0; pl < C::kPlanes; ++pl)
+#pragma unroll
+                        for (int j = 0; j < C::kLaneVals / 4; ++j) {
+                            const int m = pl * C::kLaneVals / 2 + 2 * j;
+                            *reinterpret_cast<float4*>(dst + pl * 64 + g * C::kLaneVals + 4 * j) =
+                                make_float4(O[nb][m][k] * f, O[nb][m][2 + k] * f,
+                                            O[nb][m + 1][k] * f, O[nb][m + 1][2 + k] * f);
+                        }
+                }
+            }
+        consumer_sync();
+        // ---- rows of the segment: D/4 threads each
+        constexpr int kPerRow = D / 4;
+        const bool whole = wk.nt == wk.tiles;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (wk.tile0 == 0 ? 1 : 0);
+        for (int r = threadIdx.x / kPerRow; r < C::kRows && r0 + r < R;
+             r += 32 * kWarps / kPerRow) {
+            const int f = threadIdx.x % kPerRow * 4;
+            float mx = sh.m[par][0][r], L = 0.f;
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w)
+                mx = fmaxf(mx, sh.m[par][w][r]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = sh.m[par][w][r];
+                L += sh.l[par][w][r] * (mw == -INFINITY ? 1.f : ex2(mw - mx));
+                const float4 y = *reinterpret_cast<const float4*>(
+                    join + (w * C::kRows + r) * C::kPitch + f);
+                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            }
+            if (!whole) {
+                if (f == 0)
+                    p.part_ml[slot * C::kRows + r] = make_float2(mx, L);
+                *reinterpret_cast<float4*>(p.part_o + (slot * C::kRows + r) * D + f) = o;
+                continue;
+            }
+            const int32_t gh = (r0 + r) / p.T, tq = r0 + r - gh * p.T;
+            if (tq >= n)
+                continue;
+            const int64_t at = ((int64_t)wk.b * p.Hq + h * p.G + gh) * p.T + tq;
+            write_row<D, F8>(p, at, f, mx, L, o);
+        }
+        if (!whole && wk.tile0 == 0) {
+            // blocks after this one that hold the rest of the segment
+            const long long end = wk.w - wk.nt + wk.tiles;
+            info = make_int4(wk.b, wk.hr, (int)((end * sh.active - 1) / sh.total) - (int)blockIdx.x,
+                             n);
+        }
+    }
+    if (threadIdx.x == 0)
+        p.info[blockIdx.x] = info;
+}
+
+template <int D, bool F8, int NB>
+__global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
+    decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                  const __grid_constant__ PagedParams p)
+{
+    using C = Cfg<D, F8, NB>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
+    float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
+                                           C::kStages * C::kStage);
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], kWarps);
+        }
+        fence_barrier_init();
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    find_range(p, sh);  // also orders the barriers' initialisation
+    const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
+    if (threadIdx.x >= 32 * kWarps) {
+        produce<D, F8, NB>(p, sh, ring, tk, tv, wctx);
+        if (*wctx.abort_flag) {
+            // let copies in flight land before the block's shared memory goes
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000ull) {
+            }
+        }
+    } else {
+        consume<D, F8, NB>(p, sh, ring, join, wctx);
+    }
+}
+
+// One row of a segment that several blocks share: block c holds its beginning,
+// the info[c].z blocks after it the rest.
+template <int D, bool F8, int ROWS>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedParams p)
+{
+    __shared__ float wt[kPagedMaxCtas], red[8];
+    __shared__ float4 acc[256];
+    const int4 info = p.info[blockIdx.x];
+    const int k = info.z + 1, r = blockIdx.y;
+    if (info.z <= 0)
+        return;
+    const int32_t h = info.y / p.row_groups;
+    const int32_t rr = (info.y - h * p.row_groups) * ROWS + r;
+    if (rr >= p.G * p.T)
+        return;
+    const int32_t gh = rr / p.T, tq = rr - gh * p.T;
+    if (tq >= info.w)
+        return;
+    auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1
+                                           : 2 * ((int64_t)blockIdx.x + i); };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float mx = -INFINITY;
+    for (int i = threadIdx.x; i < k; i += 256)
+        mx = fmaxf(mx, p.part_ml[slot(i) * ROWS + r].x);
+    for (int o = 16; o > 0; o >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0)
+        red[warp] = mx;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w)
+        mx = fmaxf(mx, red[w]);
+    __syncthreads();
+    float L = 0.f;
+    for (int i = threadIdx.x; i < k; i += 256) {
+        const float2 ml = p.part_ml[slot(i) * ROWS + r];
+        wt[i] = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+        L += ml.y * wt[i];
+    }
+    for (int o = 16; o > 0; o >>= 1)
+        L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0)
+        red[warp] = L;
+    __syncthreads();
+    L = 0.f;
+    for (int w = 0; w < 8; ++w)
+        L += red[w];
+    constexpr int kPerRow = D / 4, kGroups = 256 / kPerRow;
+    const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < k; i += kGroups) {
+        const float4 y =
+            *reinterpret_cast<const float4*>(p.part_o + (slot(i) * ROWS + r) * D + f * 4);
+        const float w = wt[i];
+        o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y);
+        o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+    }
+    acc[threadIdx.x] = o;
+    __syncthreads();
+    if (grp != 0)
+        return;
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 y = acc[i * kPerRow + f];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+    }
+    write_row<D, F8>(p, ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq, f * 4, mx, L, o);
+}
+
+template <int D, bool F8, int NB>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                   int num_sms, cudaStream_t stream)
+{
+    using C = Cfg<D, F8, NB>;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F8, NB>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    // as many blocks as are resident at once, no more than there can be tiles
+    const int64_t tiles = (int64_t)p.c.B * p.c.Hkv * p.row_groups *
+                          max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
+    const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), tiles);
+    decode_kernel<D, F8, NB><<<grid, kThreads, C::kSmem, stream>>>(tk, tv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    merge_kernel<D, F8, C::kRows><<<dim3(grid, C::kRows), 256, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, bool F8>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                        int num_sms, cudaStream_t stream)
+{
+    return p.G * p.T <= kPagedRows ? launch<D, F8, 1>(tk, tv, p, num_sms, stream)
+                                   : launch<D, F8, 2>(tk, tv, p, num_sms, stream);
+}
+
+}  // namespace paged
+
+cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedParams& p, int num_sms, cudaStream_t stream)
+{
+    if (p.c.e4m3)
+        return p.c.d == 128 ? paged::launch_rows<128, true>(tk, tv, p, num_sms, stream)
+                            : paged::launch_rows<64, true>(tk, tv, p, num_sms, stream);
+    return p.c.d == 128 ? paged::launch_rows<128, false>(tk, tv, p, num_sms, stream)
+                        : paged::launch_rows<64, false>(tk, tv, p, num_sms, stream);
 }
 
 }  // namespace dfa

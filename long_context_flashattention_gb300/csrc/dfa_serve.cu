@@ -4,7 +4,9 @@
 #include <cmath>
 #include <cstring>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include "../../include/dfa.h"
 #include "dfa_serve.h"
@@ -19,6 +21,7 @@ namespace {
 
 constexpr size_t kStatusBytes = 256;
 constexpr int64_t kMaxBlocks = INT32_MAX;
+constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;  // 4 s per wait
 
 int num_sms()
 {
@@ -200,6 +203,62 @@ dfa_status make_cache(CacheView* v, const dfa_paged_cache* c, void* ws, const ch
     return DFA_OK;
 }
 
+// Pages as a tensor map [npages][Hkv][page][d] with boxes of up to 128 bytes of
+// features by up to 64 rows, swizzled by the box's width.
+dfa_status make_page_map(CUtensorMap* out, const CacheView& c, const void* ptr, const char* name)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)p;
+    }();
+    if (!fn)
+        return set_error(DFA_ERR_CUDA, "dfa_decode_paged: cuTensorMapEncodeTiled unavailable");
+    const int es = c.e4m3 ? 1 : 2;
+    const int box_bytes = std::min(128, c.d * es);
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.Hkv,
+                          (cuuint64_t)c.npages};
+    cuuint64_t strides[3] = {(cuuint64_t)c.d * es, (cuuint64_t)c.page * c.d * es,
+                             (cuuint64_t)c.page_stride * es};
+    cuuint32_t box[4] = {(cuuint32_t)(box_bytes / es),
+                         (cuuint32_t)std::min(c.page, kPagedTile), 1, 1};
+    cuuint32_t step[4] = {1, 1, 1, 1};
+    const CUresult r =
+        fn(out, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+           const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(DFA_ERR_CUDA, "dfa_decode_paged: tensor map for %s failed (CUresult %d)",
+                         name, (int)r);
+    return DFA_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Query rows of a block: 8, or 16 where a key/value head has more.
+int paged_rows(int64_t rows_per_head)
+{
+    return rows_per_head <= kPagedRows ? kPagedRows : kPagedMaxRows;
+}
+
+// Workspace of dfa_decode_paged: status word, one record per block, two partial
+// results (maximum and sum, O) per block.
+struct PagedWs {
+    size_t info, ml, o, bytes;
+    PagedWs(int rows, int d)
+    {
+        info = kStatusBytes;
+        ml = info + align256((size_t)kPagedMaxCtas * sizeof(int4));
+        o = ml + align256((size_t)2 * kPagedMaxCtas * rows * sizeof(float2));
+        bytes = o + align256((size_t)2 * kPagedMaxCtas * rows * d * 4);
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -367,7 +426,7 @@ size_t dfa_decode_paged_workspace_size(const dfa_attn_desc* desc, int32_t T)
     if (!desc || T < 1 || desc->Hkv < 1 || desc->Hq < 1 || desc->Hq % desc->Hkv != 0 ||
         (desc->d != 64 && desc->d != 128) || (int64_t)(desc->Hq / desc->Hkv) * T > 1024)
         return 0;
-    return kStatusBytes;
+    return PagedWs(paged_rows((int64_t)(desc->Hq / desc->Hkv) * T), desc->d).bytes;
 }
 
 dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
@@ -412,8 +471,6 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     const size_t need = dfa_decode_paged_workspace_size(desc, T);
     if ((s = check_ws(ws, ws_bytes, need, "dfa_decode_paged")) != DFA_OK)
         return s;
-    if ((int64_t)p.c.B * desc->Hq * T > kMaxBlocks)
-        return set_error(DFA_ERR_UNSUPPORTED, "dfa_decode_paged: too many query rows");
     p.q_lens = q_lens;
     p.Hq = desc->Hq;
     p.G = G;
@@ -423,7 +480,20 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     p.scale_log2 = desc->scale * 1.4426950408889634f;
     p.o = o;
     p.lse = lse;
-    return launch_status(launch_decode_paged(p, (cudaStream_t)stream), "dfa_decode_paged");
+    const int rows = paged_rows((int64_t)G * T);
+    const PagedWs w(rows, p.c.d);
+    p.row_groups = (G * T + rows - 1) / rows;
+    p.info = (int4*)((char*)ws + w.info);
+    p.part_ml = (float2*)((char*)ws + w.ml);
+    p.part_o = (float*)((char*)ws + w.o);
+    p.timeout_ns = kDefaultTimeoutNs;
+    CUtensorMap tk, tv;
+    if ((s = make_page_map(&tk, p.c, p.c.k, "k")) != DFA_OK)
+        return s;
+    if ((s = make_page_map(&tv, p.c, p.c.v, "v")) != DFA_OK)
+        return s;
+    return launch_status(launch_decode_paged(tk, tv, p, num_sms(), (cudaStream_t)stream),
+                         "dfa_decode_paged");
 }
 
 }  // extern "C"

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "dfa_params.h"
@@ -75,14 +76,24 @@ struct PagedParams {
     Rows q;
     const int32_t* q_lens;        // [B] or NULL
     int32_t Hq, G, T, causal, o_fp32;
+    int32_t row_groups;           // blocks of query rows per key/value head
     float scale_log2;
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]
+    int4* info;                   // [CTAs]: sequence, head and row group, CTAs that continue it
+    float2* part_ml;              // [2 CTAs][rows]: maximum (log2), sum
+    float* part_o;                // [2 CTAs][rows][d]
+    uint64_t timeout_ns;
 };
+
+// Query rows that a decoding block works on at a time, and the most blocks.
+constexpr int kPagedRows = 8, kPagedMaxRows = 16, kPagedMaxCtas = 512;
+constexpr int kPagedTile = 64;    // keys per tile
 
 cudaError_t launch_rope_rows(const RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const AppendParams& p, int64_t q_items, cudaStream_t stream);
 cudaError_t launch_cache_gather(const GatherParams& p, cudaStream_t stream);
-cudaError_t launch_decode_paged(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace dfa
