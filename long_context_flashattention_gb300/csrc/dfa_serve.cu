@@ -133,11 +133,20 @@ dfa_status make_table(RopeTable* t, const dfa_rope_spec* s, int d)
          !(s->high > s->low) || !std::isfinite(s->high)))
         return set_error(DFA_ERR_INVALID_ARG,
                          "rope: bands need orig_len > 0 and 0 <= low < high, all finite");
+    // The frequencies take longer than a launch, and calls repeat their spec.
+    thread_local struct {
+        dfa_rope_spec spec;
+        RopeTable table;
+        bool valid = false;
+    } last;
+    if (last.valid && memcmp(&last.spec, s, sizeof *s) == 0) {
+        *t = last.table;
+        return DFA_OK;
+    }
     constexpr double kTwoPi = 6.283185307179586;
     t->gain = (float)gain;
     t->half_layout = s->layout == DFA_ROPE_HALF;
     t->half = s->rot_dim / 2;
-    t->units = s->rot_dim / 16;
     for (int i = 0; i < t->half; ++i) {
         double f = std::pow(s->theta_base, -2.0 * i / s->rot_dim);
         if (s->scaling == DFA_ROPE_LINEAR) {
@@ -152,6 +161,9 @@ dfa_status make_table(RopeTable* t, const dfa_rope_spec* s, int d)
         turn -= std::floor(turn);
         t->turn[i] = (uint64_t)std::ldexp(turn, 64);  // turn < 1: below 2^64
     }
+    last.spec = *s;
+    last.table = *t;
+    last.valid = true;
     return DFA_OK;
 }
 
@@ -272,8 +284,10 @@ dfa_status dfa_rope(const dfa_rope_spec* spec, int32_t B, int32_t H, int64_t L, 
         return set_error(DFA_ERR_INVALID_ARG, "dfa_rope: spec is NULL");
     if (B < 1 || H < 1 || L < 0)
         return set_error(DFA_ERR_INVALID_ARG, "dfa_rope: need B, H >= 1 and L >= 0");
-    if (B > (1 << 20) || H > (1 << 20) || L >= (1 << 30))
-        return set_error(DFA_ERR_UNSUPPORTED, "dfa_rope: B and H up to 2^20, L below 2^30");
+    if (B > (1 << 20) || H > (1 << 20) || L >= (1 << 30) ||
+        (int64_t)B * H >= kMaxBlocks || (int64_t)B * H * L >= kMaxBlocks)
+        return set_error(DFA_ERR_UNSUPPORTED, "dfa_rope: B and H up to 2^20, L below 2^30, "
+                         "B * H * L below 2^31");
     if (d != 64 && d != 128)
         return set_error(DFA_ERR_UNSUPPORTED, "dfa_rope: head dimension %d not supported "
                          "(64 or 128)", d);
@@ -327,14 +341,7 @@ dfa_status dfa_rope(const dfa_rope_spec* spec, int32_t B, int32_t H, int64_t L, 
     p.d = d;
     p.inverse = inverse;
     p.positions = positions;
-    // Heads per warp: a warp computes its token's angles once for all of them,
-    // but short inputs need the warps.
-    const int sms = num_sms();
-    const int step = 32 / (d / 16);
-    p.heads = 4 * step;
-    while (p.heads > step && (int64_t)B * L * ((H + p.heads - 1) / p.heads) < sms * 32)
-        p.heads /= 2;
-    return launch_status(launch_rope_rows(p, fp32, sms, (cudaStream_t)stream), "dfa_rope");
+    return launch_status(launch_rope_rows(p, fp32, num_sms(), (cudaStream_t)stream), "dfa_rope");
 }
 
 dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,
@@ -359,7 +366,6 @@ dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* r
     if ((s = make_rows(&p.v, v, v_strides, B, Hkv, T, d, 2, false, "dfa_cache_append: v")) !=
         DFA_OK)
         return s;
-    int64_t q_items = 0;
     if (q) {
         if (!rope)
             return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_append: queries without a rotation");
@@ -374,21 +380,17 @@ dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* r
         if ((s = check_apart(p.q, p.q_out, B, Hq, T, d, 2, "dfa_cache_append: q and q_out")) !=
             DFA_OK)
             return s;
-        const int per = 32 / (d / 16);
-        q_items = (int64_t)B * T * ((Hq + per - 1) / per);
+        p.Hq = Hq;
     }
     if ((s = check_ws(ws, ws_bytes, kStatusBytes, "dfa_cache_append")) != DFA_OK)
         return s;
     p.new_lens = new_lens;
     p.T = T;
-    p.Hq = Hq;
     // T rows touch at most this many pages, and never more than a sequence has
     p.pages = std::min(p.c.max_pages, (int32_t)(((int64_t)T + page - 2) / page + 1));
-    const int64_t kv_blocks = (int64_t)B * 2 * Hkv * p.pages;
-    if (kv_blocks + q_items > kMaxBlocks)
-        return set_error(DFA_ERR_UNSUPPORTED, "dfa_cache_append: too many rows for one call");
-    p.kv_blocks = (int32_t)kv_blocks;
-    return launch_status(launch_cache_append(p, q_items, (cudaStream_t)stream),
+    if ((int64_t)B * T * (p.Hq + 2 * Hkv) >= kMaxBlocks)
+        return set_error(DFA_ERR_UNSUPPORTED, "dfa_cache_append: B * T * heads above 2^31");
+    return launch_status(launch_cache_append(p, num_sms(), (cudaStream_t)stream),
                          "dfa_cache_append");
 }
 

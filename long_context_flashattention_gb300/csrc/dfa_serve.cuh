@@ -52,60 +52,108 @@ __device__ __forceinline__ int32_t page_of(const CacheView& c, int32_t b, int32_
 }
 
 // ---------------------------------------------------------------------------
-// rotation: a unit is 8 feature pairs (16 features); unit u < units holds the
-// pairs 8u..8u+7.  Its features are two runs of 8: in the half layout 8u.. and
-// half + 8u.., else 16u.. and 16u + 8...
+// rotation: a unit is V feature pairs (V features are 16 bytes), held by one lane
+// as two runs of V features so that the lanes of a row load and store 16
+// neighbouring bytes each.  Unit u of the U = rot_dim / 2V turned ones holds
+// features Vu.. and rot_dim/2 + Vu..: in the half layout these are the two
+// sides of pairs Vu.., in the interleaved one the pairs Vu/2.. and
+// (rot_dim/2 + Vu)/2...  The other units split [rot_dim, d) likewise.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void unit_runs(const RopeTable& t, int u, int& f0, int& f1)
+template <int V>
+__device__ __forceinline__ bool unit_runs(const RopeTable& t, int d, int u, int& f0, int& f1)
 {
-    const bool apart = t.half_layout && u < t.units;
-    f0 = apart ? 8 * u : 16 * u;
-    f1 = apart ? t.half + 8 * u : 16 * u + 8;
+    const int units = t.half / V;  // turned units
+    const bool turned = u < units;
+    f0 = turned ? V * u : 2 * t.half + V * (u - units);
+    f1 = f0 + (turned ? t.half : d / 2 - t.half);
+    return turned;
 }
 
-// cos and sin (gain included) of the unit's pairs at a position.  The top 32
-// bits of the phase are the angle in half turns times 2^31.
-__device__ __forceinline__ void unit_angles(const RopeTable& t, int u, int32_t pos, float sign,
-                                            float (&cs)[8], float (&sn)[8])
+// Pair i (of V) of unit u.
+template <int V>
+__device__ __forceinline__ int unit_pair(const RopeTable& t, int u, int i)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t ph = (uint64_t)(int64_t)pos * t.turn[8 * u + i];
-        sincospif((float)(int32_t)(ph >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);
-        cs[i] *= t.gain;
-        sn[i] *= t.gain * sign;
-    }
+    if (t.half_layout)
+        return V * u + i;
+    return V / 2 * u + i + (i < V / 2 ? 0 : t.half / 2 - V / 2);
 }
+
+// cos and sin (gain included) of a pair at a position.  The top 32 bits of the
+// phase are the angle in half turns times 2^31.
+__device__ __forceinline__ void pair_angle(uint64_t turn, float gain, int32_t pos, float sign,
+                                           float& cs, float& sn)
+{
+    const uint64_t ph = (uint64_t)(int64_t)pos * turn;
+    sincospif((float)(int32_t)(ph >> 32) * 4.656612873077393e-10f, &sn, &cs);
+    cs *= gain;
+    sn *= gain * sign;
+}
+
+// cos and sin of the unit's pairs where the whole warp is at one position, lane =
+// head * UNITS + unit: the 32 / UNITS lanes of a unit compute some pairs each
+// and pass them around.
+template <int V, int UNITS>
+struct WarpAngles {
+    static constexpr int kOwn = V * UNITS / 32;
+    uint64_t turn[kOwn];  // this lane's pairs
+    float gain;
+
+    __device__ __forceinline__ explicit WarpAngles(const RopeTable& t) : gain(t.gain)
+    {
+        const int lane = threadIdx.x & 31, u = lane & (UNITS - 1);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int pair = unit_pair<V>(t, u, lane / UNITS * kOwn + i);
+            turn[i] = u < t.half / V ? t.turn[pair] : 0;
+        }
+    }
+    __device__ __forceinline__ void at(int32_t pos, float sign, float (&cs)[V],
+                                       float (&sn)[V]) const
+    {
+        const int u = threadIdx.x & (UNITS - 1);
+        float c[kOwn], s[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            pair_angle(turn[i], gain, pos, sign, c[i], s[i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            cs[i] = __shfl_sync(0xffffffffu, c[i % kOwn], (i / kOwn) * UNITS + u);
+            sn[i] = __shfl_sync(0xffffffffu, s[i % kOwn], (i / kOwn) * UNITS + u);
+        }
+    }
+};
 
 // a, b: the unit's two runs
-__device__ __forceinline__ void unit_rotate(const RopeTable& t, const float (&cs)[8],
-                                            const float (&sn)[8], float (&a)[8], float (&b)[8])
+template <int V>
+__device__ __forceinline__ void unit_rotate(const RopeTable& t, const float (&cs)[V],
+                                            const float (&sn)[V], float (&a)[V], float (&b)[V])
 {
     if (t.half_layout) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
             const float x = a[i], y = b[i];
             a[i] = x * cs[i] - y * sn[i];
             b[i] = x * sn[i] + y * cs[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
             const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];
             a[2 * i] = x * cs[i] - y * sn[i];
             a[2 * i + 1] = x * sn[i] + y * cs[i];
-            b[2 * i] = z * cs[i + 4] - w * sn[i + 4];
-            b[2 * i + 1] = z * sn[i + 4] + w * cs[i + 4];
+            b[2 * i] = z * cs[i + V / 2] - w * sn[i + V / 2];
+            b[2 * i + 1] = z * sn[i + V / 2] + w * cs[i + V / 2];
         }
     }
 }
 
-// Eight features: as they lie in memory, and as fp32.  (Plain loads: a call may
+// A run of 16 bytes: as it lies in memory, and as fp32.  (Plain loads: a call may
 // work in place.)
 template <typename E>
-struct Raw8;
+struct Run;
 template <>
-struct Raw8<__nv_bfloat16> {
+struct Run<__nv_bfloat16> {
+    static constexpr int V = 8;
     uint4 w;
     __device__ __forceinline__ void load(const __nv_bfloat16* p)
     {
@@ -127,63 +175,20 @@ struct Raw8<__nv_bfloat16> {
     }
 };
 template <>
-struct Raw8<float> {
-    float4 x, y;
-    __device__ __forceinline__ void load(const float* p)
-    {
-        x = reinterpret_cast<const float4*>(p)[0];
-        y = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void store(float* p) const
-    {
-        reinterpret_cast<float4*>(p)[0] = x;
-        reinterpret_cast<float4*>(p)[1] = y;
-    }
-    __device__ __forceinline__ void get(float (&f)[8]) const
+struct Run<float> {
+    static constexpr int V = 4;
+    float4 x;
+    __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = x; }
+    __device__ __forceinline__ void get(float (&f)[4]) const
     {
         f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
-        f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
     }
-    __device__ __forceinline__ void set(const float (&f)[8])
+    __device__ __forceinline__ void set(const float (&f)[4])
     {
         x = make_float4(f[0], f[1], f[2], f[3]);
-        y = make_float4(f[4], f[5], f[6], f[7]);
     }
 };
-
-// The rows of heads h, h + step, ... below h1 of one token: BATCH rows' loads
-// are issued before the first is turned and stored.  x and out point at the
-// token's row of head 0.
-template <int BATCH, typename E>
-__device__ __forceinline__ void rotate_heads(const RopeTable& t, bool turned, const float (&cs)[8],
-                                             const float (&sn)[8], const E* x, int64_t x_sh,
-                                             E* out, int64_t out_sh, int f0, int f1, int32_t h,
-                                             int32_t h1, int32_t step)
-{
-    for (; h < h1; h += BATCH * step) {
-        Raw8<E> r[BATCH][2];
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            if (h + k * step < h1) {
-                r[k][0].load(x + (h + k * step) * x_sh + f0);
-                r[k][1].load(x + (h + k * step) * x_sh + f1);
-            }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            if (h + k * step < h1) {
-                if (turned) {
-                    float a[8], b[8];
-                    r[k][0].get(a);
-                    r[k][1].get(b);
-                    unit_rotate(t, cs, sn, a, b);
-                    r[k][0].set(a);
-                    r[k][1].set(b);
-                }
-                r[k][0].store(out + (h + k * step) * out_sh + f0);
-                r[k][1].store(out + (h + k * step) * out_sh + f1);
-            }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // 8-bit cells (e4m3) with power-of-two scales

@@ -19,8 +19,7 @@ struct RopeTable {
     uint64_t turn[64];
     float gain;
     int32_t half_layout;  // pairs (t, t + half) instead of (2t, 2t + 1)
-    int32_t half;         // rot_dim / 2
-    int32_t units;        // rot_dim / 16: units of 8 pairs (16 features)
+    int32_t half;         // rot_dim / 2; 0: no rotation
 };
 
 // A row tensor [B, H, L, d] with contiguous features; strides in elements.
@@ -55,12 +54,19 @@ struct CacheView {
 
 struct AppendParams {
     CacheView c;
-    RopeTable t;                  // units = 0: no rotation
+    RopeTable t;
     const int32_t* new_lens;      // [B] or NULL
     Rows k, v, q, q_out;
     int32_t T, Hq;
     int32_t pages;                // pages a sequence's new rows may touch
-    int32_t kv_blocks;            // blocks of K and V; the rest rotate q
+    // E4M3, page jobs: K or V rows of one page and `job_heads` heads, by
+    // `job_threads` threads each
+    int32_t job_heads, job_threads;
+    uint32_t jobs;
+    int32_t job_blocks;           // blocks with page jobs; the rest have row items
+    // row items: one token, `item_heads` of its rows (q; and k, v of a bf16 cache)
+    int32_t item_heads;
+    uint32_t items;
 };
 
 struct GatherParams {
@@ -90,8 +96,8 @@ struct PagedParams {
 constexpr int kPagedRows = 8, kPagedMaxRows = 16, kPagedMaxCtas = 512;
 constexpr int kPagedTile = 64;    // keys per tile
 
-cudaError_t launch_rope_rows(const RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream);
-cudaError_t launch_cache_append(const AppendParams& p, int64_t q_items, cudaStream_t stream);
+cudaError_t launch_rope_rows(RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedParams& p, int num_sms, cudaStream_t stream);

@@ -8,6 +8,7 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -562,19 +563,26 @@ def rope_spec(d, layout="interleaved", rot_dim=None, theta_base=10000.0, scaling
                     ROPE_SCALINGS[scaling], 0, theta_base, factor, orig_len, low, high, gain)
 
 
+# The calls below are made once per layer and decoded token, so their Python
+# part is kept short: descriptors and stride arrays are made once per value, and
+# the stream and device are asked for without building objects.
 _Strides = ctypes.c_int64 * 3
 
 
-def _rows(t, name, dtype, device, shape=None):
+@functools.lru_cache(maxsize=4096)
+def _strides(st):
+    return _Strides(st[0], st[1], st[2]) if st[3] == 1 else None
+
+
+def _rows(t, name, dtype, device, shape):
     """Pointer and strides of a [B,H,L,d] row tensor with contiguous features."""
-    if t.dim() != 4 or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} [B,H,L,d] tensor on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on {device}, not "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    st = _strides(t.stride())
+    if st is None:
         raise ValueError(f"the features of {name} must be contiguous")
-    return t.data_ptr(), _Strides(st[0], st[1], st[2])
+    return t.data_ptr(), st
 
 
 def _int32(t, name, shape, device):
@@ -585,14 +593,14 @@ def _int32(t, name, shape, device):
     return t.data_ptr()
 
 
-def _on_current(device):
-    """The call's kernels run on the current device; the tensors have to be there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+def _raw_stream(device, stream):
+    """The call's stream; its kernels run on the current device, so the tensors
+    have to be there."""
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors must be on the current CUDA device, not on {device}")
-
-
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _new(stream, shape, dtype, device):
@@ -611,21 +619,22 @@ def rope(x, spec: RopeSpec, positions=None, pos_map: PosMap | None = None, inver
     features) at positions [B,L] int32, or at those of pos_map, or at 0..L-1
     (dfa_rope).  inverse: the transposed rotation, for gradients.  out=x works in
     place; without out a contiguous tensor is returned."""
-    dev = x.device
-    _on_current(dev)
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("x must be bf16 or fp32")
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    raw = _raw_stream(dev, stream)
+    if dtype is not torch.bfloat16 and dtype is not torch.float32 or len(shape) != 4:
+        raise ValueError("x must be a bf16 or fp32 [B,H,L,d] tensor")
     if positions is not None and pos_map is not None:
         raise ValueError("give positions or pos_map, not both")
-    xp, xs = _rows(x, "x", x.dtype, dev)
-    B, H, L, d = x.shape
+    xp, xs = _rows(x, "x", dtype, dev, shape)
+    B, H, L, d = shape
     if out is None:
-        out = _new(stream, x.shape, x.dtype, dev)
-    op, os_ = _rows(out, "out", x.dtype, dev, x.shape)
-    _check(lib().dfa_rope(ctypes.byref(spec), B, H, L, d, int(x.dtype == torch.float32), xp, xs,
-                          op, os_, None if pos_map is None else ctypes.byref(pos_map),
-                          _int32(positions, "positions", (B, L), dev), int(inverse),
-                          _raw_stream(stream)))
+        out = _new(stream, shape, dtype, dev)
+    op, os_ = (xp, xs) if out is x else _rows(out, "out", dtype, dev, shape)
+    code = lib().dfa_rope(ctypes.byref(spec), B, H, L, d, dtype is torch.float32, xp, xs, op, os_,
+                          None if pos_map is None else ctypes.byref(pos_map),
+                          _int32(positions, "positions", (B, L), dev), inverse, raw)
+    if code:
+        _check(code)
     return out
 
 
@@ -678,18 +687,32 @@ class PagedCache:
 def paged_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:
     """A workspace for the calls on this cache: Hq query heads, T tokens a
     sequence at most.  It serves one call at a time."""
-    desc = make_desc(cache.B, Hq or cache.Hkv, cache.Hkv, 1, cache.d)
-    n = int(lib().dfa_decode_paged_workspace_size(ctypes.byref(desc), T))
     # more rows than decode_paged takes: the other calls need the status word only
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.device)
+    n = _paged_desc(cache.B, Hq or cache.Hkv, cache.Hkv, T, cache.d, True, 1.0, False)[1]
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
 def _ws(ws, nbytes, cache, stream):
     if ws is None:
         return _new(stream, (nbytes,), torch.uint8, cache.device)
-    if ws.device != cache.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.dtype is not torch.uint8 or ws.device != cache.device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {cache.device}")
     return ws
+
+
+def _plain(t, name, dtype, device, shape):
+    if (t.dtype is not dtype or t.device != device or t.shape != shape or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_desc(B, Hq, Hkv, T, d, causal, scale, fp32):
+    """dfa_decode_paged's descriptor (by reference) and workspace bytes (256 at
+    least: an invalid one is for the call to refuse)."""
+    ref = ctypes.byref(AttnDesc(B, Hq, Hkv, 1, d, causal, scale, 1, 0, 1, fp32, 0, None))
+    return ref, max(256, int(lib().dfa_decode_paged_workspace_size(ref, T)))
 
 
 def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens=None, q=None,
@@ -701,9 +724,9 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
     q [B,Hq,T,d] its rows are rotated too, into q_out (default: a new contiguous
     tensor; rows from new_lens on are not written), which is returned."""
     dev = cache.device
-    _on_current(dev)
-    if k.dim() != 4:
-        raise ValueError("k must be [B,Hkv,T,d]")
+    raw = _raw_stream(dev, stream)
+    if k.dim() != 4 or q is not None and q.dim() != 4:
+        raise ValueError("k, v and q must be [B,H,T,d]")
     T = k.shape[2]
     shape = (cache.B, cache.Hkv, T, cache.d)
     kp, ks = _rows(k, "k", torch.bfloat16, dev, shape)
@@ -711,8 +734,6 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
     ws = _ws(ws, 256, cache, stream)
     Hq, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
-        if q.dim() != 4:
-            raise ValueError("q must be [B,Hq,T,d]")
         Hq = q.shape[1]
         shape = (cache.B, Hq, T, cache.d)
         qp, qs = _rows(q, "q", torch.bfloat16, dev, shape)
@@ -721,10 +742,11 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
         op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(lib().dfa_cache_append(cache._ref, None if rope is None else ctypes.byref(rope), T,
+    code = lib().dfa_cache_append(cache._ref, None if rope is None else ctypes.byref(rope), T,
                                   _int32(new_lens, "new_lens", (cache.B,), dev), kp, ks, vp, vs,
-                                  Hq, qp, qs, op, os_, ws.data_ptr(), ws.numel(),
-                                  _raw_stream(stream)))
+                                  Hq, qp, qs, op, os_, ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
     return q_out
 
 
@@ -733,20 +755,20 @@ def cache_gather(cache: PagedCache, L, pos0=0, k_out=None, v_out=None, ws=None, 
     [B,Hkv,L,d] (dfa_cache_gather): returns (k_out, v_out).  Rows behind a
     sequence's end are not written."""
     dev = cache.device
-    _on_current(dev)
+    raw = _raw_stream(dev, stream)
     shape = (cache.B, cache.Hkv, L, cache.d)
-    outs = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = _new(stream, shape, torch.bfloat16, dev)
-        elif (t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or
-              not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bf16 {list(shape)} tensor on {dev}")
-        outs.append(t)
+    if k_out is None:
+        k_out = _new(stream, shape, torch.bfloat16, dev)
+    if v_out is None:
+        v_out = _new(stream, shape, torch.bfloat16, dev)
     ws = _ws(ws, 256, cache, stream)
-    _check(lib().dfa_cache_gather(cache._ref, pos0, L, outs[0].data_ptr(), outs[1].data_ptr(),
-                                  ws.data_ptr(), ws.numel(), _raw_stream(stream)))
-    return outs[0], outs[1]
+    code = lib().dfa_cache_gather(cache._ref, pos0, L,
+                                  _plain(k_out, "k_out", torch.bfloat16, dev, shape),
+                                  _plain(v_out, "v_out", torch.bfloat16, dev, shape),
+                                  ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
+    return k_out, v_out
 
 
 def decode_paged(cache: PagedCache, q, q_lens=None, causal=True, scale=None, out_fp32=False,
@@ -757,34 +779,26 @@ def decode_paged(cache: PagedCache, q, q_lens=None, causal=True, scale=None, out
     them at position seq_lens - 1.  Returns (O [B,Hq,T,d], LSE [B,Hq,T]); rows
     from q_lens on are not written."""
     dev = cache.device
-    _on_current(dev)
-    if q.dim() != 4:
+    raw = _raw_stream(dev, stream)
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B,Hq,T,d]")
-    B, Hq, T, d = q.shape
+    B, Hq, T, d = shape
     qp, qs = _rows(q, "q", torch.bfloat16, dev, (cache.B, Hq, T, cache.d))
     o_dtype = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = _new(stream, (B, Hq, T, d), o_dtype, dev)
-    elif (out.shape != q.shape or out.dtype != o_dtype or out.device != dev or
-          not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous {o_dtype} tensor of q's shape on {dev}")
+        out = _new(stream, shape, o_dtype, dev)
     if lse is None:
         lse = _new(stream, (B, Hq, T), torch.float32, dev)
-    elif (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != dev or
-          not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous fp32 [B,Hq,T] tensor on {dev}")
-    desc = AttnDesc(B, Hq, cache.Hkv, 1, d, int(causal),
-                    1.0 / math.sqrt(d) if scale is None else scale, 1, 0, 1, int(out_fp32), 0,
-                    None)
-    ref = ctypes.byref(desc)
-    if ws is None:
-        ws = _new(stream, (max(256, int(lib().dfa_decode_paged_workspace_size(ref, T))),),
-                  torch.uint8, dev)
-    else:
-        ws = _ws(ws, 0, cache, stream)
-    _check(lib().dfa_decode_paged(ref, cache._ref, T, _int32(q_lens, "q_lens", (B,), dev), qp, qs,
-                                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                                  _raw_stream(stream)))
+    desc, need = _paged_desc(B, Hq, cache.Hkv, T, d, bool(causal),
+                             1.0 / math.sqrt(d) if scale is None else scale, bool(out_fp32))
+    ws = _ws(ws, need, cache, stream)
+    code = lib().dfa_decode_paged(desc, cache._ref, T, _int32(q_lens, "q_lens", (B,), dev), qp, qs,
+                                  _plain(out, "out", o_dtype, dev, shape),
+                                  _plain(lse, "lse", torch.float32, dev, (B, Hq, T)),
+                                  ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
     return out, lse
 
 
