@@ -9,9 +9,9 @@
 //
 // Page jobs (8-bit cells).  A page's scale needs the largest value of all its
 // new rows before the first is stored, so a group of threads takes the rows of one
-// page and head and holds their features in registers in between: every row is
-// read once.  The group keeps its rows' cos and sin in registers and goes
-// through several heads with them.
+// page and head, a 16-feature unit of a row each, and holds them in registers
+// in between: every row is read once.  The group keeps its rows' cos and sin and
+// goes through several heads with them.
 //
 // Row items (queries; K and V too in a bf16 cache, where rows are independent).
 // A warp takes one token and several heads; its lanes compute the token's
@@ -22,24 +22,28 @@ namespace dfa {
 
 namespace {
 
-constexpr int kJobUnits = 1;  // 16-feature units of a page that a thread holds
 constexpr int kBatch = 2;     // rows of an item in flight per lane
 
-// codes of x / s; an infinity becomes NaN like a NaN, rather than the largest
-// finite cell
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
+// codes of x / s.  An infinity (which the conversion would store as the largest
+// finite cell) becomes NaN like a NaN; `inf`: there may be one.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv, bool inf)
 {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        y[i] = fabsf(x[i]) < INFINITY ? x[i] * inv : NAN;
+        y[i] = inf && fabsf(x[i]) == INFINITY ? NAN : x[i] * inv;
     return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
-__device__ __forceinline__ float finite_abs(float x)
+// Largest |x|, NaN left out (fmaxf does); `finite`: infinities too.
+__device__ __forceinline__ float abs_max8(float m, const float (&x)[8], bool finite)
 {
-    const float y = fabsf(x);
-    return y < INFINITY ? y : 0.f;  // NaN compares false
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float u = fabsf(x[i]), v = fabsf(x[i + 1]);
+        m = fmaxf(m, fmaxf(finite && u == INFINITY ? 0.f : u, finite && v == INFINITY ? 0.f : v));
+    }
+    return m;
 }
 
 // Row items of a block.  Rows of a token: Hq queries, then (bf16 cache) Hkv keys
@@ -65,47 +69,36 @@ __device__ __forceinline__ void row_items(const AppendParams& p, uint32_t item, 
         if (t >= n)
             continue;
         const int32_t pos = len - n + t;
-        int64_t cell = -1;  // first feature of the token's row of head 0
-        if (!F8 && h1 > p.Hq) {
-            const int32_t id = page_of(p.c, b, pos / p.c.page);
-            if (id >= 0)
-                cell = (int64_t)id * p.c.page_stride + (pos % p.c.page) * D;
-        }
+        const bool stores = !F8 && h1 > p.Hq;
+        int32_t id = stores ? page_entry(p.c, b, pos >> p.c.page_log2) : 0;
         float cs[8], sn[8];
         for (int32_t h = h0; h < h1; h += kBatch * kStep) {
             Run<__nv_bfloat16> r[kBatch][2];
-            __nv_bfloat16* to[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int32_t hk = h + h_lane + k * kStep;
-                to[k] = nullptr;
                 if (hk >= h1)
                     continue;
-                const __nv_bfloat16* from;
-                if (F8 || hk < p.Hq) {
-                    from = (const __nv_bfloat16*)p.q.p + b * p.q.sb + hk * p.q.sh + t * p.q.sl;
-                    to[k] = (__nv_bfloat16*)p.q_out.p + b * p.q_out.sb + hk * p.q_out.sh +
-                            t * p.q_out.sl;
-                } else {
-                    if (cell < 0)
-                        continue;
-                    const bool is_v = hk >= p.Hq + Hk;
-                    const int32_t hc = hk - p.Hq - (is_v ? Hk : 0);
-                    const Rows& src = is_v ? p.v : p.k;
-                    from = (const __nv_bfloat16*)src.p + b * src.sb + hc * src.sh + t * src.sl;
-                    to[k] = (__nv_bfloat16*)(is_v ? p.c.v : p.c.k) + cell +
-                            (int64_t)hc * p.c.page * D;
-                }
+                const bool is_v = hk >= p.Hq + Hk;
+                const Rows& src = F8 || hk < p.Hq ? p.q : is_v ? p.v : p.k;
+                const int32_t hs = F8 || hk < p.Hq ? hk : hk - p.Hq - (is_v ? Hk : 0);
+                const __nv_bfloat16* from =
+                    (const __nv_bfloat16*)src.p + b * src.sb + hs * src.sh + t * src.sl;
                 r[k][0].load(from + f0);
                 r[k][1].load(from + f1);
             }
-            if (h == h0 && p.t.half && h0 < p.Hq + Hk)  // not for values alone
-                angles.at(pos, 1.f, cs, sn);
+            if (h == h0) {  // while the first rows are on their way
+                if (p.t.half && h0 < p.Hq + Hk)  // (not for values alone)
+                    angles.at(pos, 1.f, cs, sn);
+                if (stores && !is_page(p.c, b, id))
+                    id = -1;
+            }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                if (!to[k])
+                const int32_t hk = h + h_lane + k * kStep;
+                if (hk >= h1)
                     continue;
-                if (turned && h + h_lane + k * kStep < p.Hq + Hk) {
+                if (turned && hk < p.Hq + Hk) {
                     float a[8], c[8];
                     r[k][0].get(a);
                     r[k][1].get(c);
@@ -113,8 +106,20 @@ __device__ __forceinline__ void row_items(const AppendParams& p, uint32_t item, 
                     r[k][0].set(a);
                     r[k][1].set(c);
                 }
-                r[k][0].store(to[k] + f0);
-                r[k][1].store(to[k] + f1);
+                __nv_bfloat16* to;
+                if (F8 || hk < p.Hq) {
+                    to = (__nv_bfloat16*)p.q_out.p + b * p.q_out.sb + hk * p.q_out.sh +
+                         t * p.q_out.sl;
+                } else {
+                    if (id < 0)
+                        continue;
+                    const bool is_v = hk >= p.Hq + Hk;
+                    const int32_t hc = hk - p.Hq - (is_v ? Hk : 0);
+                    to = (__nv_bfloat16*)(is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride +
+                         (((int64_t)hc << p.c.page_log2) + (pos & (p.c.page - 1))) * D;
+                }
+                r[k][0].store(to + f0);
+                r[k][1].store(to + f1);
             }
         }
     }
@@ -129,11 +134,32 @@ __device__ __forceinline__ void group_sync(int group, int threads)
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
+// Largest value of the group; `set` alternates between two sets of smem words,
+// so that one barrier is enough.
+__device__ __forceinline__ float group_max(float m, int group, int thread, int threads,
+                                           float (*words)[32], int& set)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threads > 32) {
+        set ^= 16;
+        float* w = words[set + group];
+        if ((thread & 31) == 0)
+            w[thread >> 5] = m;
+        group_sync(group, threads);
+        for (int i = 0; i < threads / 32; ++i)
+            m = fmaxf(m, w[i]);
+    }
+    return m;
+}
+
 // One page job: K or V rows of one page, job_heads heads.  Every thread of the
 // group takes the same way through it.
 template <int D>
 __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, int group,
-                                         int thread, const uint64_t* turn, float (*warp_max)[32])
+                                         int thread, const uint64_t* turn, float (*words)[32],
+                                         int& set)
 {
     constexpr int UNITS = D / 16;
     const uint32_t head_jobs = (p.c.Hkv + p.job_heads - 1) / p.job_heads;
@@ -146,109 +172,92 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
     const int32_t h0 = (i - is_v * head_jobs) * p.job_heads;
     int32_t len, n;
     seq_rows(p.c, p.new_lens, p.T, b, len, n);
-    const int32_t first = len - n;                 // first new row
-    const int32_t pg = first / p.c.page + ip;      // page of the sequence
-    const int32_t lo = max(first, pg * p.c.page);  // rows [lo, hi) are new
-    const int32_t hi = min(len, (pg + 1) * p.c.page);
+    const int32_t first = len - n;                          // first new row
+    const int32_t pg = (first >> p.c.page_log2) + ip;       // page of the sequence
+    const int32_t start = pg << p.c.page_log2;
+    const int32_t lo = max(first, start);                   // rows [lo, hi) are new
+    const int32_t hi = min(len, start + p.c.page);
     if (lo >= hi)
         return;
-    const int32_t id = page_of(p.c, b, pg);
-    if (id < 0)
-        return;
-    const int threads = p.job_threads, warps = threads / 32;
+    const int32_t id = page_entry(p.c, b, pg);
+    const int threads = p.job_threads;
     const Rows& src = is_v ? p.v : p.k;
-    float* scales = (is_v ? p.c.v_scale : p.c.k_scale) + (int64_t)id * p.c.Hkv;
-    const int32_t there = lo - pg * p.c.page;  // rows of the page stored before
-    const int32_t u = thread & (UNITS - 1);    // threads is a multiple of UNITS
+    const int32_t there = lo - start;        // rows of the page stored before
+    const int32_t u = thread & (UNITS - 1);  // threads is a multiple of UNITS
+    const int32_t row = lo + thread / UNITS;
+    const bool mine = row < hi;
     int f0, f1;
     const bool turned = unit_runs<8>(p.t, D, u, f0, f1) && !is_v;
-    float cs[kJobUnits][8], sn[kJobUnits][8];
+    float cs[8], sn[8];
+    const __nv_bfloat16* x = (const __nv_bfloat16*)src.p + b * src.sb + h0 * src.sh +
+                             (row - first) * src.sl;
     const int32_t h1 = min(h0 + p.job_heads, p.c.Hkv);
-    for (int32_t h = h0; h < h1; ++h) {
-        const __nv_bfloat16* x =
-            (const __nv_bfloat16*)src.p + b * src.sb + h * src.sh - (int64_t)first * src.sl;
-        uint8_t* cells = (uint8_t*)(is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride +
-                         (int64_t)h * p.c.page * D;
-        Run<__nv_bfloat16> raw[kJobUnits][2];
-#pragma unroll
-        for (int k = 0; k < kJobUnits; ++k) {
-            const int32_t row = lo + (thread + k * threads) / UNITS;
-            if (row < hi) {
-                raw[k][0].load(x + row * src.sl + f0);
-                raw[k][1].load(x + row * src.sl + f1);
-            }
-        }
+    Run<__nv_bfloat16> r0, r1;
+    if (mine) {
+        r0.load(x + f0);
+        r1.load(x + f1);
+    }
+    if (!is_page(p.c, b, id))
+        return;
+    float* scales = (is_v ? p.c.v_scale : p.c.k_scale) + (int64_t)id * p.c.Hkv;
+    uint8_t* cells = (uint8_t*)(is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride +
+                     ((int64_t)h0 << p.c.page_log2) * D;
+    for (int32_t h = h0; h < h1; ++h, cells += p.c.page * D) {
         const float old = there > 0 ? scales[h] : 0.f;
-        if (h == h0 && turned)
-#pragma unroll
-            for (int k = 0; k < kJobUnits; ++k) {
-                const int32_t row = lo + (thread + k * threads) / UNITS;
-                if (row < hi)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        pair_angle(turn[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[k][j],
-                                   sn[k][j]);
-            }
-        float a[kJobUnits][8], c[kJobUnits][8], amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < kJobUnits; ++k) {
-            if (lo + (thread + k * threads) / UNITS >= hi)
-                continue;
-            raw[k][0].get(a[k]);
-            raw[k][1].get(c[k]);
-            if (turned)
-                unit_rotate<8>(p.t, cs[k], sn[k], a[k], c[k]);
+        if (h == h0 && turned && mine)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                amax = fmaxf(amax, fmaxf(finite_abs(a[k][j]), finite_abs(c[k][j])));
+                pair_angle(turn[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[j], sn[j]);
+        float a[8], c[8], amax = 0.f;
+        if (mine) {
+            r0.get(a);
+            r1.get(c);
+            if (turned)
+                unit_rotate<8>(p.t, cs, sn, a, c);
+            amax = abs_max8(abs_max8(0.f, a, false), c, false);
+            x += src.sh;
+            if (h + 1 < h1) {  // the next head's rows, ahead of the barrier
+                r0.load(x + f0);
+                r1.load(x + f1);
+            }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (warps > 1) {
-            // two sets of maxima, so that one barrier a head is enough
-            float* wm = warp_max[(h & 1) * 16 + group];
-            if ((thread & 31) == 0)
-                wm[thread >> 5] = amax;
-            group_sync(group, threads);
-            for (int w = 0; w < warps; ++w)
-                amax = fmaxf(amax, wm[w]);
+        amax = group_max(amax, group, thread, threads, words, set);
+        const bool inf = amax == INFINITY;  // once more, over finite values
+        if (inf) {
+            amax = mine ? abs_max8(abs_max8(0.f, a, true), c, true) : 0.f;
+            amax = group_max(amax, group, thread, threads, words, set);
         }
         const float s = fmaxf(old, pow2_scale(amax));
         const float inv = 1.f / s;  // exact: a power of two (or a scale of the caller's)
-        if (s > old && there > 0) {
-            // raise the rows that are there to the new scale: exact but for
-            // cells that become subnormal
-            const float f = old * inv;
-            for (int32_t v = thread; v < there * D / 16; v += threads) {
-                uint4* cell = reinterpret_cast<uint4*>(cells) + v;
-                const uint4 w = *cell;
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                uint32_t out[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 q0 = e4m3x2_float2(in[j] & 0xffffu);
-                    const float2 q1 = e4m3x2_float2(in[j] >> 16);
-                    out[j] = e4m3x4(q0.x * f, q0.y * f, q1.x * f, q1.y * f);
-                }
-                *cell = make_uint4(out[0], out[1], out[2], out[3]);
-            }
-        }
         if (s != old) {
+            if (there > 0) {
+                // raise the rows that are there to the new scale: exact but for
+                // cells that become subnormal
+                const float f = old * inv;
+                for (int32_t v = thread; v < there * D / 16; v += threads) {
+                    uint4* cell = reinterpret_cast<uint4*>(cells) + v;
+                    const uint4 w = *cell;
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t out[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 q0 = e4m3x2_float2(in[j] & 0xffffu);
+                        const float2 q1 = e4m3x2_float2(in[j] >> 16);
+                        out[j] = e4m3x4(q0.x * f, q0.y * f, q1.x * f, q1.y * f);
+                    }
+                    *cell = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+            }
             // everyone has read the old scale (the barrier, or the warp's shuffles)
-            if (warps <= 1)
+            if (threads <= 32)
                 __syncwarp();
             if (thread == 0)
                 scales[h] = s;
         }
-#pragma unroll
-        for (int k = 0; k < kJobUnits; ++k) {
-            const int32_t row = lo + (thread + k * threads) / UNITS;
-            if (row < hi) {
-                uint8_t* cell = cells + (row - pg * p.c.page) * D;
-                *reinterpret_cast<uint2*>(cell + f0) = codes8(a[k], inv);
-                *reinterpret_cast<uint2*>(cell + f1) = codes8(c[k], inv);
-            }
+        if (mine) {
+            uint8_t* cell = cells + (row - start) * D;
+            *reinterpret_cast<uint2*>(cell + f0) = codes8(a, inv, inf);
+            *reinterpret_cast<uint2*>(cell + f1) = codes8(c, inv, inf);
         }
     }
 }
@@ -258,16 +267,17 @@ __global__ void __launch_bounds__(F8 ? 1024 : 256, F8 ? 1 : 3)
     cache_append_kernel(const __grid_constant__ AppendParams p)
 {
     if (F8 && (int32_t)blockIdx.x < p.job_blocks) {
-        __shared__ float warp_max[32][32];
+        __shared__ float words[32][32];
         __shared__ uint64_t turn[64];  // lanes read different entries: not from the parameters
         if (threadIdx.x < 64)
             turn[threadIdx.x] = p.t.turn[threadIdx.x];
         __syncthreads();
         const int groups = blockDim.x / p.job_threads;
         const int group = threadIdx.x / p.job_threads;
-        const uint32_t job = blockIdx.x * groups + group;
-        if (job < p.jobs)
-            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turn, warp_max);
+        int set = 0;
+        for (uint32_t job = blockIdx.x * groups + group; job < p.jobs;
+             job += p.job_blocks * groups)
+            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turn, words, set);
         return;
     }
     const int warps = blockDim.x >> 5;
@@ -324,9 +334,12 @@ __global__ void __launch_bounds__(128) cache_gather_kernel(const __grid_constant
 
 }  // namespace
 
-// Blocks that have work at once are some 8 an SM; below that a job or an item
-// takes as few heads as it can, above it as many as pay (angles are computed
-// once per job or item).
+// Work per job, item and block.  Angles are computed once per job or item, so
+// each takes as many heads as leave enough threads to fill the SMs; blocks take
+// several, a grid's worth at a time.  Measured (ragged chunks of 0..1000 tokens
+// of 16 sequences, 8-bit, d 64): jobs filling 1024 threads an SM 12.3 us, 512
+// 12.1, 2048 14.5; a 32K bf16 prompt of 32 heads: blocks for 4096 threads an SM
+// 242 us, 2048 249.
 cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t stream)
 {
     const int units = p.c.d / 16, step = 32 / units;
@@ -335,18 +348,18 @@ cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t strea
     if (p.c.e4m3) {
         const int rows = min(p.T, p.c.page);
         p.job_threads = 32;
-        while (p.job_threads * kJobUnits < rows * units)
+        while (p.job_threads < rows * units)
             p.job_threads *= 2;
         threads = max(threads, p.job_threads);
         const int64_t pages = (int64_t)p.c.B * 2 * p.pages;  // of one head
         p.job_heads = 8;
         while (p.job_heads > 1 &&
                pages * ((p.c.Hkv + p.job_heads - 1) / p.job_heads) * p.job_threads <
-                   (int64_t)num_sms * 2048)
+                   (int64_t)num_sms * 1024)
             p.job_heads /= 2;
         p.jobs = (uint32_t)(pages * ((p.c.Hkv + p.job_heads - 1) / p.job_heads));
         const int groups = threads / p.job_threads;
-        p.job_blocks = (int32_t)((p.jobs + groups - 1) / groups);
+        p.job_blocks = (int32_t)min((p.jobs + groups - 1) / groups, num_sms * 2048u / threads);
     }
     const int rows = p.Hq + (p.c.e4m3 ? 0 : 2 * p.c.Hkv);
     int64_t item_blocks = 0;
@@ -356,7 +369,8 @@ cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t strea
                tokens * ((rows + p.item_heads - 1) / p.item_heads) < (int64_t)num_sms * 64)
             p.item_heads /= 2;
         p.items = (uint32_t)(tokens * ((rows + p.item_heads - 1) / p.item_heads));
-        item_blocks = min((p.items + threads / 32 - 1) / (threads / 32), num_sms * 64u);
+        item_blocks = min((p.items + threads / 32 - 1) / (threads / 32),
+                          num_sms * (p.c.e4m3 ? 2048u : 4096u) / threads);
     }
     const unsigned blocks = (unsigned)(p.job_blocks + item_blocks);
     if (p.c.e4m3) {

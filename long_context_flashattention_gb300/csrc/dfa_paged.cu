@@ -58,7 +58,9 @@ struct Cfg {
     static constexpr int kRows = 8 * NB;
     static constexpr int kPitch = D + 4;                     // floats of an O row in the join
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
-    static constexpr int kSmem = 1024 + kStages * kStage + kJoin;
+    // 16 query rows take their operand from shared memory: O takes its registers
+    static constexpr int kQ = NB > 1 ? NB * (D / 16) * 32 * 8 : 0;
+    static constexpr int kSmem = 1024 + kStages * kStage + kJoin + kQ;
     // blocks of an SM that are resident together (registers and shared memory)
     static constexpr int kResident = NB == 1 && kStage < 32768 ? 3 : 2;
     static constexpr int kSteps = D / 16;                    // products over the features
@@ -71,6 +73,7 @@ struct Shared {
     // maxima and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
     float m[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
+    float qf[2][8];               // NB = 2: score factors of the query rows
     long long warp_sum[kThreads / 32];
     long long w0, w1, total, base;
     int32_t b, active;            // active: blocks that have tiles
@@ -359,6 +362,70 @@ __device__ __forceinline__ void value_frag(const Vals<W>& v, int j, uint32_t (&a
     }
 }
 
+// V of plane pl for the group's 16 keys, whose tile rows begin at `row`; zero
+// for keys from `upto` on (the group's first key is `base`).
+template <typename C, int W>
+__device__ __forceinline__ void load_values(Vals<W>& v, uint32_t vt, uint32_t row, int pl, int g,
+                                            int t, int32_t base, int32_t upto)
+{
+    const uint32_t plane = vt + pl * kTile * C::kPlaneBytes;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t key = 2 * t + (k & 1) + (k >> 1) * 8, r = row + key;
+        if (W == 4) {
+            const uint4 x = lds128(plane + chunk_at<C::kPlaneBytes>(r, g));
+            v.w[k][0] = x.x, v.w[k][1] = x.y;
+            v.w[k][W - 2] = x.z, v.w[k][W - 1] = x.w;
+        } else {
+            const uint2 x = lds64(plane + chunk_at<C::kPlaneBytes>(r, g >> 1) + (g & 1) * 8);
+            v.w[k][0] = x.x, v.w[k][1] = x.y;
+        }
+        if (upto != INT32_MAX && base + (int32_t)key >= upto)
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                v.w[k][w] = 0u;
+    }
+}
+
+// One query row's features for this lane (t of 4) as the products' operand; with
+// 8-bit cells as fp16 relative to the power of two of the row's largest.
+// Returns the factor of the row's scores.
+template <int D, bool F8, int PLANES>
+__device__ __forceinline__ float load_queries(const __nv_bfloat16* row, bool there, int t,
+                                              float scale_log2, uint32_t (&q)[D / 16][2])
+{
+    constexpr int kPer = D / 16 / PLANES;  // steps of a plane
+#pragma unroll
+    for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            uint4 x = make_uint4(0, 0, 0, 0);  // two steps: 8 features
+            if (there)
+                x = __ldg(reinterpret_cast<const uint4*>(row + pl * 64 + t * 4 * kPer + 4 * i));
+            const int s = pl * kPer + i;
+            q[s][0] = x.x, q[s][1] = x.y;
+            q[s + 1][0] = x.z, q[s + 1][1] = x.w;
+        }
+    if (!F8)
+        return scale_log2;
+    float amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[s][k])), fabsf(bf16hi(q[s][k]))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            q[s][k] = pack_half2(bf16lo(q[s][k]) * inv, bf16hi(q[s][k]) * inv);
+    return scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 // Features f..f+3 of an output row, and its LSE: o and L are relative to 2^mx
 // (L also to 2^kSumShift for 8-bit cells).
 template <int D, bool F8>
@@ -380,7 +447,7 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int 
 
 template <int D, bool F8, int NB>
 __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32_t ring,
-                                        float* join, const WaitCtx& wctx)
+                                        float* join, uint2* qs, const WaitCtx& wctx)
 {
     using C = Cfg<D, F8, NB>;
     constexpr int kWords = C::kLaneVals / (F8 ? 4 : 2);  // V words per key and plane
@@ -403,61 +470,41 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         const int32_t r0 = (wk.hr - h * p.row_groups) * C::kRows;
         const int32_t len = wk.len, n = wk.n;
         // ---- queries: rows g of each block of 8, this lane's features
-        uint32_t q[NB][C::kSteps][2];
-        float rf[NB][2];       // score factor of rows 2t, 2t+1
-        int32_t lim[NB][2];    // last visible key of rows 2t, 2t+1
+        uint32_t q[C::kSteps][2];  // NB = 1: the operand itself
+        float rf[NB][2];           // score factor of rows 2t, 2t+1
+        int32_t lim[NB][2];        // last visible key of rows 2t, 2t+1
         int32_t tok[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        if (NB == 1 || warp < NB) {
+            const int nb = NB == 1 ? 0 : warp;
             const int32_t r = r0 + nb * 8 + g;
             const int32_t gh = r / p.T, tq = r - gh * p.T;
             const bool there = r < R && tq < n;
             const __nv_bfloat16* row = (const __nv_bfloat16*)p.q.p + wk.b * p.q.sb +
                                        (int64_t)(h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl;
-#pragma unroll
-            for (int pl = 0; pl < C::kPlanes; ++pl)
-#pragma unroll
-                for (int i = 0; i < C::kSteps / C::kPlanes; i += 2) {
-                    // two steps: 8 features
-                    const int f = pl * 64 + t * (D / C::kPlanes / 4) + 4 * i;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (there)
-                        x = __ldg(reinterpret_cast<const uint4*>(row + f));
-                    const int s = pl * (C::kSteps / C::kPlanes) + i;
-                    q[nb][s][0] = x.x;
-                    q[nb][s][1] = x.y;
-                    q[nb][s + 1][0] = x.z;
-                    q[nb][s + 1][1] = x.w;
-                }
-            float f = p.scale_log2;
-            if (F8) {
-                float amax = 0.f;
+            const float f = load_queries<D, F8, C::kPlanes>(row, there, t, p.scale_log2, q);
+            if (NB == 1) {
+                rf[0][0] = __shfl_sync(0xffffffffu, f, 2 * t * 4);
+                rf[0][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
+            } else {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[nb][s][k])),
-                                                 fabsf(bf16hi(q[nb][s][k]))));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                f *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int s = 0; s < C::kSteps; ++s)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        q[nb][s][k] =
-                            pack_half2(bf16lo(q[nb][s][k]) * inv, bf16hi(q[nb][s][k]) * inv);
+                    qs[(nb * C::kSteps + s) * 32 + lane] = make_uint2(q[s][0], q[s][1]);
+                if (t == 0)
+                    sh.qf[nb][g] = f;
             }
+        }
+        if (NB > 1)
+            consumer_sync();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                rf[nb][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
+                if (NB > 1)
+                    rf[nb][k] = sh.qf[nb][2 * t + k];
                 const int32_t rr = r0 + nb * 8 + 2 * t + k;
                 tok[nb][k] = rr < R ? rr % p.T : n;
                 lim[nb][k] = p.causal ? len - n + min(tok[nb][k], n - 1) : len - 1;
             }
-        }
         // keys up to all_see are visible to every row, keys from len on to none
         const int32_t all_see = p.causal ? len - n : len - 1;
         float O[NB][kMt][4], M[NB][2], l[NB][2];
@@ -520,26 +567,11 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                                 a1 = yw[2 * j], a3 = yw[2 * j + 1];
                             }
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-                                mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, q[nb][s][0],
-                                             q[nb][s][1]);
-                        }
-                    }
-                Vals<kWords> v[C::kPlanes];
-#pragma unroll
-                for (int pl = 0; pl < C::kPlanes; ++pl)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t r = row + 2 * t + (k & 1) + (k >> 1) * 8;
-                        const uint32_t plane = vt + pl * kTile * C::kPlaneBytes;
-                        if (kWords == 4) {
-                            const uint4 x = lds128(plane + chunk_at<C::kPlaneBytes>(r, g));
-                            v[pl].w[k][0] = x.x, v[pl].w[k][1] = x.y;
-                            v[pl].w[k][kWords - 2] = x.z, v[pl].w[k][kWords - 1] = x.w;
-                        } else {
-                            const uint2 x = lds64(plane + chunk_at<C::kPlaneBytes>(r, g >> 1) +
-                                                  (g & 1) * 8);
-                            v[pl].w[k][0] = x.x, v[pl].w[k][1] = x.y;
+                            for (int nb = 0; nb < NB; ++nb) {
+                                const uint2 b = NB == 1 ? make_uint2(q[s][0], q[s][1])
+                                                        : qs[(nb * C::kSteps + s) * 32 + lane];
+                                mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
+                            }
                         }
                     }
                 // value scale = vm 2^ve, vm in [1, 2) (1 for the powers of two that
@@ -555,26 +587,18 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 }
                 const bool masked = base + 15 > all_see;  // some row does not see some key
                 bool apart = false;  // non-finite V that some rows do not see
-                if (masked) {
-                    // V of keys behind the end is not ours
+                if (masked && p.causal && n > 1) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (base + 2 * t + (k & 1) + (k >> 1) * 8 >= len)
+                    for (int pl = 0; pl < C::kPlanes; ++pl) {
+                        Vals<kWords> v;
+                        load_values<C, kWords>(v, vt, row, pl, g, t, base, len);
 #pragma unroll
-                            for (int pl = 0; pl < C::kPlanes; ++pl)
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
-                                for (int w = 0; w < kWords; ++w)
-                                    v[pl].w[k][w] = 0u;
-                    if (p.causal && n > 1) {
-#pragma unroll
-                        for (int pl = 0; pl < C::kPlanes; ++pl)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int w = 0; w < kWords; ++w)
-                                    apart |= not_finite<F8>(v[pl].w[k][w]);
-                        apart = __any_sync(0xffffffffu, apart);
+                            for (int w = 0; w < kWords; ++w)
+                                apart |= not_finite<F8>(v.w[k][w]);
                     }
+                    apart = __any_sync(0xffffffffu, apart);
                 }
                 uint32_t pt[NB][2], pr[NB][2];  // P^T (and its bf16 remainder)
 #pragma unroll
@@ -634,18 +658,26 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                         }
                     }
                 }
+                // O^T += V^T P^T; V of keys behind the end is not ours
+                const int32_t upto = masked ? len : INT32_MAX;
                 if (!apart) {
-                    // O^T += V^T P^T
 #pragma unroll
-                    for (int m = 0; m < kMt; ++m) {
-                        uint32_t a[4];
-                        value_frag<F8>(v[m * C::kPlanes / kMt], m % (kMt / C::kPlanes), a);
+                    for (int pl = 0; pl < C::kPlanes; ++pl) {
+                        Vals<kWords> v;
+                        load_values<C, kWords>(v, vt, row, pl, g, t, base, upto);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                            if (!F8)
-                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
-                                             pr[nb][1]);
+                        for (int j = 0; j < kMt / C::kPlanes; ++j) {
+                            const int m = pl * (kMt / C::kPlanes) + j;
+                            uint32_t a[4];
+                            value_frag<F8>(v, j, a);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0],
+                                             pt[nb][1]);
+                                if (!F8)
+                                    mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
+                                                 pr[nb][1]);
+                            }
                         }
                     }
                 } else {
@@ -653,31 +685,28 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     // that do not see it: one token at a time, with the values
                     // behind its position taken out
                     for (int32_t tt = 0; tt < n; ++tt) {
-                        Vals<kWords> u[C::kPlanes];
 #pragma unroll
-                        for (int pl = 0; pl < C::kPlanes; ++pl)
+                        for (int pl = 0; pl < C::kPlanes; ++pl) {
+                            Vals<kWords> v;
+                            load_values<C, kWords>(v, vt, row, pl, g, t, base, len - n + tt + 1);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
+                            for (int j = 0; j < kMt / C::kPlanes; ++j) {
+                                const int m = pl * (kMt / C::kPlanes) + j;
+                                uint32_t a[4];
+                                value_frag<F8>(v, j, a);
 #pragma unroll
-                                for (int w = 0; w < kWords; ++w)
-                                    u[pl].w[k][w] =
-                                        base + 2 * t + (k & 1) + (k >> 1) * 8 <= len - n + tt
-                                            ? v[pl].w[k][w]
-                                            : 0u;
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2],
+                                                  O[nb][m][3]};
+                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                                    if (!F8)
+                                        mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0],
+                                                     pr[nb][1]);
 #pragma unroll
-                        for (int m = 0; m < kMt; ++m) {
-                            uint32_t a[4];
-                            value_frag<F8>(u[m * C::kPlanes / kMt], m % (kMt / C::kPlanes), a);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2], O[nb][m][3]};
-                                mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                                if (!F8)
-                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (tok[nb][k & 1] == tt)
-                                        O[nb][m][k] = d[k];
+                                    for (int k = 0; k < 4; ++k)
+                                        if (tok[nb][k & 1] == tt)
+                                            O[nb][m][k] = d[k];
+                                }
                             }
                         }
                     }
@@ -791,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
     }
+    cudaTriggerProgrammaticLaunchCompletion();  // merge_kernel's blocks may be launched
     find_range(p, sh);  // also orders the barriers' initialisation
     const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
     if (threadIdx.x >= 32 * kWarps) {
@@ -802,76 +832,131 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
             }
         }
     } else {
-        consume<D, F8, NB>(p, sh, ring, join, wctx);
+        consume<D, F8, NB>(p, sh, ring, join, reinterpret_cast<uint2*>(join + C::kJoin / 4), wctx);
     }
 }
 
-// One row of a segment that several blocks share: block c holds its beginning,
-// the info[c].z blocks after it the rest.
+// Rows of the segments that several blocks share: block c holds such a segment's
+// beginning, the info[c].z blocks after it the rest.  Few partials: one warp a
+// row; many (a long sequence with few heads): the block's 8 warps share a row's.
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedParams p)
 {
     __shared__ float wt[kPagedMaxCtas], red[8];
     __shared__ float4 acc[256];
+    cudaGridDependencySynchronize();  // the blocks' partials
     const int4 info = p.info[blockIdx.x];
-    const int k = info.z + 1, r = blockIdx.y;
+    const int k = info.z + 1;
     if (info.z <= 0)
         return;
     const int32_t h = info.y / p.row_groups;
-    const int32_t rr = (info.y - h * p.row_groups) * ROWS + r;
-    if (rr >= p.G * p.T)
-        return;
-    const int32_t gh = rr / p.T, tq = rr - gh * p.T;
-    if (tq >= info.w)
-        return;
+    const int32_t r0 = (info.y - h * p.row_groups) * ROWS;
     auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1
                                            : 2 * ((int64_t)blockIdx.x + i); };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float mx = -INFINITY;
-    for (int i = threadIdx.x; i < k; i += 256)
-        mx = fmaxf(mx, p.part_ml[slot(i) * ROWS + r].x);
-    for (int o = 16; o > 0; o >>= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0)
-        red[warp] = mx;
-    __syncthreads();
-    for (int w = 0; w < 8; ++w)
-        mx = fmaxf(mx, red[w]);
-    __syncthreads();
-    float L = 0.f;
-    for (int i = threadIdx.x; i < k; i += 256) {
-        const float2 ml = p.part_ml[slot(i) * ROWS + r];
-        wt[i] = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
-        L += ml.y * wt[i];
-    }
-    for (int o = 16; o > 0; o >>= 1)
-        L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0)
-        red[warp] = L;
-    __syncthreads();
-    L = 0.f;
-    for (int w = 0; w < 8; ++w)
-        L += red[w];
-    constexpr int kPerRow = D / 4, kGroups = 256 / kPerRow;
-    const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // row r of the group -> output row, or -1
+    auto target = [&](int r) -> int64_t {
+        const int32_t rr = r0 + r, gh = rr / p.T, tq = rr - gh * p.T;
+        if (rr >= p.G * p.T || tq >= info.w)
+            return -1;
+        return ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq;
+    };
+    constexpr int kPerRow = D / 4;  // lanes of 4 features
+    if (k <= 16) {
+        constexpr int kGroups = 32 / kPerRow;
+        const int grp = lane / kPerRow, f = lane % kPerRow;
+        for (int r = blockIdx.y * 8 + warp; r < ROWS; r += 8 * gridDim.y) {
+            const int64_t at = target(r);
+            if (at < 0)
+                continue;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < k)
+                ml = p.part_ml[slot(lane) * ROWS + r];
+            float mx = ml.x;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+            mx = __shfl_sync(0xffffffffu, mx, 0);
+            // a block without a maximum has O = 0, or only NaN
+            const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+            float L = ml.y * w;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, o, 16);
+            L = __shfl_sync(0xffffffffu, L, 0);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = grp; i < k; i += kGroups) {
-        const float4 y =
-            *reinterpret_cast<const float4*>(p.part_o + (slot(i) * ROWS + r) * D + f * 4);
-        const float w = wt[i];
-        o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y);
-        o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
-    }
-    acc[threadIdx.x] = o;
-    __syncthreads();
-    if (grp != 0)
+            for (int i = 0; i < k; i += kGroups) {
+                const float wi = __shfl_sync(0xffffffffu, w, i + grp);
+                if (i + grp >= k)
+                    continue;
+                const float4 y = *reinterpret_cast<const float4*>(
+                    p.part_o + (slot(i + grp) * ROWS + r) * D + f * 4);
+                o.x = fmaf(wi, y.x, o.x), o.y = fmaf(wi, y.y, o.y);
+                o.z = fmaf(wi, y.z, o.z), o.w = fmaf(wi, y.w, o.w);
+            }
+            if (kGroups == 2) {
+                o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+                o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+                o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+                o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+            }
+            if (grp == 0)
+                write_row<D, F8>(p, at, f * 4, mx, L, o);
+        }
         return;
-    for (int i = 1; i < kGroups; ++i) {
-        const float4 y = acc[i * kPerRow + f];
-        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
     }
-    write_row<D, F8>(p, ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq, f * 4, mx, L, o);
+    constexpr int kGroups = 256 / kPerRow;
+    const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
+    for (int r = blockIdx.y; r < ROWS; r += gridDim.y) {
+        const int64_t at = target(r);
+        if (at < 0)
+            continue;
+        float mx = -INFINITY;
+        for (int i = threadIdx.x; i < k; i += 256)
+            mx = fmaxf(mx, p.part_ml[slot(i) * ROWS + r].x);
+        for (int o = 16; o > 0; o >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        __syncthreads();  // the row before has been read
+        if (lane == 0)
+            red[warp] = mx;
+        __syncthreads();
+        for (int w = 0; w < 8; ++w)
+            mx = fmaxf(mx, red[w]);
+        __syncthreads();
+        float L = 0.f;
+        for (int i = threadIdx.x; i < k; i += 256) {
+            const float2 ml = p.part_ml[slot(i) * ROWS + r];
+            wt[i] = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+            L += ml.y * wt[i];
+        }
+        for (int o = 16; o > 0; o >>= 1)
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0)
+            red[warp] = L;
+        __syncthreads();
+        L = 0.f;
+        for (int w = 0; w < 8; ++w)
+            L += red[w];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = grp; i < k; i += kGroups) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(p.part_o + (slot(i) * ROWS + r) * D + f * 4);
+            const float w = wt[i];
+            o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y);
+            o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+        }
+        acc[threadIdx.x] = o;
+        __syncthreads();
+        if (grp == 0) {
+            for (int i = 1; i < kGroups; ++i) {
+                const float4 y = acc[i * kPerRow + f];
+                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            }
+            write_row<D, F8>(p, at, f * 4, mx, L, o);
+        }
+    }
 }
 
 template <int D, bool F8, int NB>
@@ -891,8 +976,19 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedPara
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    merge_kernel<D, F8, C::kRows><<<dim3(grid, C::kRows), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    // The merge's blocks may start while the decode's end, and wait there.  With
+    // few segments each is cut into many partials: a block a row.
+    const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, segments * 8 >= grid ? 1 : C::kRows);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel<D, F8, C::kRows>, p);
 }
 
 template <int D, bool F8>

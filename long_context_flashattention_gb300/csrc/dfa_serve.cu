@@ -209,6 +209,7 @@ dfa_status make_cache(CacheView* v, const dfa_paged_cache* c, void* ws, const ch
     v->Hkv = c->Hkv;
     v->d = c->d;
     v->page = c->page;
+    v->page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
     v->max_pages = c->max_pages;
     v->e4m3 = e4m3;
     v->status = (DevStatus*)ws;

@@ -39,16 +39,27 @@ __device__ __forceinline__ void seq_rows(const CacheView& c, const int32_t* new_
     }
 }
 
-// Page number of rows [i*page, (i+1)*page) of sequence b; -1 (reported) when
-// it is out of range.  i < max_pages.
+// Table entry of rows [i*page, (i+1)*page) of sequence b, i < max_pages; and
+// whether it is a page (if not, that is reported).  Apart, so that other loads
+// can be on their way before the entry is looked at.
+__device__ __forceinline__ int32_t page_entry(const CacheView& c, int32_t b, int32_t i)
+{
+    return __ldg(c.table + (int64_t)b * c.max_pages + i);
+}
+
+__device__ __forceinline__ bool is_page(const CacheView& c, int32_t b, int32_t id)
+{
+    if (id >= 0 && id < c.npages)
+        return true;
+    cache_fault(c.status, kSitePage, b);
+    return false;
+}
+
+// The page, or -1.
 __device__ __forceinline__ int32_t page_of(const CacheView& c, int32_t b, int32_t i)
 {
-    const int32_t id = __ldg(c.table + (int64_t)b * c.max_pages + i);
-    if (id < 0 || id >= c.npages) {
-        cache_fault(c.status, kSitePage, b);
-        return -1;
-    }
-    return id;
+    const int32_t id = page_entry(c, b, i);
+    return is_page(c, b, id) ? id : -1;
 }
 
 // ---------------------------------------------------------------------------

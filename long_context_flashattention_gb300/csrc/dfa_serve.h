@@ -48,7 +48,7 @@ struct CacheView {
     const int32_t* table;
     const int32_t* seq_lens;
     int64_t npages, page_stride;  // page_stride in elements
-    int32_t B, Hkv, d, page, max_pages, e4m3;
+    int32_t B, Hkv, d, page, page_log2, max_pages, e4m3;
     DevStatus* status;
 };
 
