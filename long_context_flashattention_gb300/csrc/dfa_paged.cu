@@ -41,6 +41,7 @@ namespace paged {
 constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = kPagedTile;
+constexpr int kSegment = 2;                // cost of a segment beside its tiles, in tiles
 constexpr float kGrow = 8.f;               // rescale when the maximum grows by 2^8
 constexpr float kSumShift = 16.f;          // 8-bit cells: sums are kept times 2^-16, so
                                            // that scales of 2^-100 do not overflow them
@@ -58,17 +59,18 @@ struct Cfg {
     static constexpr int kRows = 8 * NB;
     static constexpr int kPitch = D + 4;                     // floats of an O row in the join
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
+    static constexpr int kQRows = kRows * D * 2;  // a segment's queries, two segments
     // 16 query rows take their operand from shared memory: O takes its registers
     static constexpr int kQ = NB > 1 ? NB * (D / 16) * 32 * 8 : 0;
-    static constexpr int kSmem = 1024 + kStages * kStage + kJoin + kQ;
+    static constexpr int kSmem = 1024 + kStages * kStage + kJoin + 2 * kQRows + kQ;
     // blocks of an SM that are resident together (registers and shared memory)
     static constexpr int kResident = NB == 1 && kStage < 32768 ? 3 : 2;
     static constexpr int kSteps = D / 16;                    // products over the features
-    static constexpr int kLaneVals = kPlaneBytes / (F8 ? 8 : 16);  // V features per plane, lane
 };
 
 struct Shared {
-    uint64_t full[8], empty[8];
+    uint64_t full[8], empty[8];   // tiles
+    uint64_t q_full[2], q_empty[2];
     float2 scale[8][4];           // per stage and page: K and V scale (kNoPage: no page)
     // maxima and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
@@ -88,6 +90,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
         "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_load_u32(uint32_t dst, const void* src, uint32_t bytes,
+                                              uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -159,6 +171,13 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c)
     return PB == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
 
+// Query row r of a key/value head: head of the group and token.
+__device__ __forceinline__ void split_row(const PagedParams& p, int32_t r, int32_t& gh, int32_t& tq)
+{
+    gh = (int32_t)(((uint32_t)r * p.inv_T) >> 21);  // r / T: r below 2^11
+    tq = r - gh * p.T;
+}
+
 // Tiles of a sequence with `n` queried tokens: at least one, so that rows
 // without keys are written too.
 __device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
@@ -166,40 +185,59 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
     return n > 0 ? max(1, ceil_div(len, kTile)) : 0;
 }
 
+// The line that is cut: every segment takes kSegment units (its queries, the join
+// and the rows' output cost a block about that many tiles' time), then one unit
+// per tile.  A cut inside the former puts the whole segment behind it.
+//
 // A run of tiles [tile0, tile0 + nt) of one segment of the block's range.
 struct Walk {
-    long long w, w1, base;  // next and end of the range; first tile of sequence b
+    long long w, w1;  // next unit and end of the range
     int32_t b, len, n, tiles;
-    int32_t hr, tile0, nt;  // head * row groups + row group
+    int32_t h, rg;    // key/value head, row group
+    int32_t tile0, nt;
+    bool fresh;       // tile0 is where the range begins
 
     __device__ __forceinline__ void start(const PagedParams& p, const Shared& sh)
     {
         w = sh.w0;
         w1 = sh.w1;
-        base = sh.base;
         b = sh.b;
-        if (w < w1) {
-            seq_rows(p.c, p.q_lens, p.T, b, len, n);
-            tiles = tiles_of(len, n);
-        }
+        fresh = true;
+        if (w >= w1)
+            return;
+        seq_rows(p.c, p.q_lens, p.T, b, len, n);
+        tiles = tiles_of(len, n);
+        const long long at = w - sh.base, unit = tiles + kSegment;
+        const long long hr = at / unit;
+        h = (int32_t)(hr / p.row_groups);
+        rg = (int32_t)(hr - (long long)h * p.row_groups);
+        tile0 = max(0, (int32_t)(at - hr * unit) - kSegment);
+        w -= at - hr * unit;  // the segment's first unit
     }
     __device__ __forceinline__ bool next(const PagedParams& p)
     {
-        if (w >= w1)
+        if (!fresh) {
+            w += tiles + kSegment;
+            if (w >= w1)
+                return false;
+            tile0 = 0;
+            if (++rg == p.row_groups) {
+                rg = 0;
+                if (++h == p.c.Hkv) {
+                    h = 0;
+                    do {
+                        ++b;
+                        seq_rows(p.c, p.q_lens, p.T, b, len, n);
+                        tiles = tiles_of(len, n);
+                    } while (tiles == 0);
+                }
+            }
+        } else if (w >= w1) {
             return false;
-        const int32_t per_seq = p.c.Hkv * p.row_groups;
-        while (w >= base + (long long)tiles * per_seq) {
-            base += (long long)tiles * per_seq;
-            ++b;
-            seq_rows(p.c, p.q_lens, p.T, b, len, n);
-            tiles = tiles_of(len, n);
         }
-        const long long at = w - base;
-        hr = (int32_t)(at / tiles);
-        tile0 = (int32_t)(at - (long long)hr * tiles);
-        nt = (int32_t)min((long long)(tiles - tile0), w1 - w);
-        w += nt;
-        return true;
+        fresh = false;
+        nt = (int32_t)min((long long)tiles, w1 - w - kSegment) - tile0;
+        return nt > 0;  // (the last segment's beginning may lie in the range, its tiles behind)
     }
 };
 
@@ -213,7 +251,8 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
     for (int32_t b = b0; b < b1; ++b) {
         int32_t len, n;
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
-        sum += (long long)tiles_of(len, n) * per_seq;
+        const int32_t tiles = tiles_of(len, n);
+        sum += tiles ? (long long)(tiles + kSegment) * per_seq : 0;
     }
     long long incl = sum;
 #pragma unroll
@@ -247,7 +286,8 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
         for (int32_t b = b0; b < b1; ++b) {
             int32_t len, n;
             seq_rows(p.c, p.q_lens, p.T, b, len, n);
-            const long long t = (long long)tiles_of(len, n) * per_seq;
+            const int32_t tiles = tiles_of(len, n);
+            const long long t = tiles ? (long long)(tiles + kSegment) * per_seq : 0;
             if (w0 < base + t) {
                 sh.b = b;
                 sh.base = base;
@@ -259,39 +299,79 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
     __syncthreads();
 }
 
+// The producer warp: queries of a segment, then its tiles.  Every wait it has for
+// itself (lengths, page numbers, scales of the next segment) begins while tiles
+// of this one are still to be fetched.
 template <int D, bool F8, int NB>
 __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32_t ring,
-                                        const CUtensorMap& tk, const CUtensorMap& tv,
-                                        const WaitCtx& wctx)
+                                        uint32_t q_rows, const CUtensorMap& tk,
+                                        const CUtensorMap& tv, const WaitCtx& wctx)
 {
     using C = Cfg<D, F8, NB>;
     const int lane = threadIdx.x & 31;
     const int32_t page = p.c.page;
     const int32_t box_rows = min(page, kTile);
     const int32_t per_tile = kTile / box_rows;  // boxes of a tile
-    uint32_t it = 0;
+    uint32_t it = 0, seg = 0;
     Walk wk;
     wk.start(p, sh);
-    while (wk.next(p)) {
-        const int32_t h = wk.hr / p.row_groups;
+    bool more = wk.next(p);
+    // Table entry of this lane's page of the 32 from page `win` on; -1: none.
+    auto entry = [&](const Walk& x, int32_t win) {
+        const int32_t end = ceil_div(min(x.len, (x.tile0 + x.nt) * kTile), page);
+        return win + lane < end ? page_entry(p.c, x.b, win + lane) : -1;
+    };
+    int32_t next_id = more ? entry(wk, (wk.tile0 * kTile) >> p.c.page_log2) : -1;
+    for (; more; ++seg) {
+        const int32_t h = wk.h;
         const int32_t pages_end =
             ceil_div(min(wk.len, (wk.tile0 + wk.nt) * kTile), page);  // of this run
-        int32_t win = -64, id = -1;  // first page of the 32 looked up; this lane's
+        int32_t win = (wk.tile0 * kTile) >> p.c.page_log2, id = next_id;
         float ks = 1.f, vs = 1.f;
+        auto check_window = [&] {  // the lane's page, and its scales on their way
+            if (win + lane >= pages_end || !is_page(p.c, wk.b, id)) {
+                id = -1;
+            } else if (F8) {
+                const int64_t at = (int64_t)id * p.c.Hkv + h;
+                ks = __ldg(p.c.k_scale + at);
+                vs = __ldg(p.c.v_scale + at);
+            }
+        };
+        check_window();
+        {
+            const uint32_t qb = seg & 1;
+            if (seg >= 2) {
+                const bool ok = mbar_wait(&sh.q_empty[qb], (seg / 2 - 1) & 1, wctx, 51);
+                if (!__all_sync(0xffffffffu, ok))
+                    return;
+            }
+            const int32_t r = wk.rg * C::kRows + lane;
+            int32_t gh, tq;
+            split_row(p, r, gh, tq);
+            const bool there = lane < C::kRows && r < p.G * p.T && tq < wk.n;
+            const uint32_t rows = __popc(__ballot_sync(0xffffffffu, there));
+            if (lane == 0)
+                mbar_expect(&sh.q_full[qb], rows * (D * 2));
+            __syncwarp();
+            if (there)
+                bulk_load_u32(q_rows + qb * C::kQRows + lane * (D * 2),
+                              (const __nv_bfloat16*)p.q.p + wk.b * p.q.sb +
+                                  (int64_t)(h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl,
+                              D * 2, &sh.q_full[qb]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.q_full[qb]);
+        }
+        Walk nx = wk;
+        bool more_next = false;
+        const int32_t look = min(wk.nt - 1, C::kStages - 1);
         for (int32_t i = 0; i < wk.nt; ++i, ++it) {
             const int32_t key0 = (wk.tile0 + i) * kTile;
-            const int32_t p0 = key0 / page;
+            const int32_t p0 = key0 >> p.c.page_log2;
             if (p0 >= win + 32) {
                 win = p0;
-                id = -1;
-                if (win + lane < pages_end) {
-                    id = page_of(p.c, wk.b, win + lane);
-                    if (F8 && id >= 0) {
-                        const int64_t at = (int64_t)id * p.c.Hkv + h;
-                        ks = __ldg(p.c.k_scale + at);
-                        vs = __ldg(p.c.v_scale + at);
-                    }
-                }
+                id = entry(wk, win);
+                check_window();
             }
             const uint32_t st = it % C::kStages;
             if (it >= C::kStages) {
@@ -301,8 +381,6 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
             }
             const int src = p0 - win + lane;  // lanes below per_tile: their box's page
             const int32_t my = __shfl_sync(0xffffffffu, id, src & 31);
-            const float my_ks = __shfl_sync(0xffffffffu, ks, src & 31);
-            const float my_vs = __shfl_sync(0xffffffffu, vs, src & 31);
             const bool load = lane < per_tile && p0 + lane < pages_end && my >= 0;
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
             if (lane == 0)
@@ -318,96 +396,152 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
                     tma_load_4d(d2 + C::kOperand, &tv, &sh.full[st], pl * 64, row, h, my);
                 }
             }
+            // the scales last: they may still be on their way
+            const float my_ks = __shfl_sync(0xffffffffu, ks, src & 31);
+            const float my_vs = __shfl_sync(0xffffffffu, vs, src & 31);
             if (lane < per_tile)
-                sh.scale[st][lane] = load ? make_float2(my_ks, my_vs) : make_float2(kNoPage, 0.f);
+                sh.scale[st][lane] =
+                    load ? make_float2(my_ks, my_vs) : make_float2(kNoPage, 0.f);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.full[st]);
+            if (i == look) {
+                more_next = nx.next(p);
+                next_id = more_next ? entry(nx, (nx.tile0 * kTile) >> p.c.page_log2) : -1;
+            }
         }
+        wk = nx;
+        more = more_next;
     }
 }
 
-// Four keys' V features of one lane as stored: keys 2t, 2t+1, 2t+8, 2t+9.
-template <int W>
-struct Vals {
-    uint32_t w[4][W];
-};
-
-template <bool F8>
-__device__ __forceinline__ bool not_finite(uint32_t w)
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
 {
-    if (F8)
-        return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-    return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
 }
 
-// The 16x16 operand V^T of features 2j, 2j+1 of a plane (lane g: rows g and
-// g + 8) and the group's 16 keys.
-template <bool F8, int W>
-__device__ __forceinline__ void value_frag(const Vals<W>& v, int j, uint32_t (&a)[4])
-{
-    if (F8) {
-        const uint32_t sel = (j & 1) ? 0x7362 : 0x5140;  // features 2j, 2j+1 of two keys
-        const uint32_t x = __byte_perm(v.w[0][j / 2], v.w[1][j / 2], sel);
-        const uint32_t y = __byte_perm(v.w[2][j / 2], v.w[3][j / 2], sel);
+// V of a warp's 16 keys as 16x16 operands V^T (a0, a1: keys 2t, 2t+1; a2, a3: keys
+// 2t+8, 2t+9), tile by tile of 16 features.  `upto`: keys from that group-relative
+// one on are zero.
+//
+// bf16: the matrix loads transpose; tile m has features 16m + g (a0, a2) and
+// 16m + 8 + g (a1, a3).
+template <typename C, bool F8>
+struct Values {
+    uint32_t base;
+    uint32_t keep[2];
+
+    __device__ __forceinline__ void load(uint32_t vt, uint32_t row, int upto)
+    {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+        base = vt;
+        key_ = row + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            keep[i] = (2 * t + 8 * i < upto ? 0xffffu : 0u) |
+                      (2 * t + 8 * i + 1 < upto ? 0xffff0000u : 0u);
+    }
+    __device__ __forceinline__ void tile(int m, bool whole, uint32_t (&a)[4]) const
+    {
+        const uint32_t c = 2 * m + ((threadIdx.x >> 3) & 1);  // 16-byte chunk of the row
+        const uint32_t plane = base + (c >> 3) * kTile * C::kPlaneBytes;
+        ldmatrix4<true>(plane + chunk_at<128>(key_, c & 7), a);
+        if (!whole) {
+            a[0] &= keep[0], a[1] &= keep[0];
+            a[2] &= keep[1], a[3] &= keep[1];
+        }
+    }
+    static __device__ __forceinline__ bool not_finite(uint32_t w)
+    {
+        return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
+    }
+
+  private:
+    uint32_t key_;
+};
+
+// e4m3: a lane reads 16 (d = 128) or 8 features of four keys and turns them to
+// fp16; tile m has its features 2m (a0, a2) and 2m + 1 (a1, a3).
+template <typename C>
+struct Values<C, true> {
+    static constexpr int W = C::kPlaneBytes / 32;  // words per key
+    uint32_t w[4][W];
+
+    __device__ __forceinline__ void load(uint32_t vt, uint32_t row, int upto)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int key = 2 * t + (k & 1) + (k >> 1) * 8;
+            if (W == 4) {
+                const uint4 x = lds128(vt + chunk_at<C::kPlaneBytes>(row + key, g));
+                w[k][0] = x.x, w[k][1] = x.y;
+                w[k][W - 2] = x.z, w[k][W - 1] = x.w;
+            } else {
+                const uint2 x =
+                    lds64(vt + chunk_at<C::kPlaneBytes>(row + key, g >> 1) + (g & 1) * 8);
+                w[k][0] = x.x, w[k][1] = x.y;
+            }
+            if (key >= upto)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    w[k][i] = 0u;
+        }
+    }
+    __device__ __forceinline__ void tile(int m, bool, uint32_t (&a)[4]) const
+    {
+        const uint32_t sel = (m & 1) ? 0x7362 : 0x5140;  // features 2m, 2m+1 of two keys
+        const uint32_t x = __byte_perm(w[0][m / 2], w[1][m / 2], sel);
+        const uint32_t y = __byte_perm(w[2][m / 2], w[3][m / 2], sel);
         a[0] = e4m3x2_half2(x & 0xffffu);
         a[1] = e4m3x2_half2(x >> 16);
         a[2] = e4m3x2_half2(y & 0xffffu);
         a[3] = e4m3x2_half2(y >> 16);
-    } else {
-        a[0] = __byte_perm(v.w[0][j], v.w[1][j], 0x5410);
-        a[1] = __byte_perm(v.w[0][j], v.w[1][j], 0x7632);
-        a[2] = __byte_perm(v.w[2][j], v.w[3][j], 0x5410);
-        a[3] = __byte_perm(v.w[2][j], v.w[3][j], 0x7632);
     }
-}
-
-// V of plane pl for the group's 16 keys, whose tile rows begin at `row`; zero
-// for keys from `upto` on (the group's first key is `base`).
-template <typename C, int W>
-__device__ __forceinline__ void load_values(Vals<W>& v, uint32_t vt, uint32_t row, int pl, int g,
-                                            int t, int32_t base, int32_t upto)
-{
-    const uint32_t plane = vt + pl * kTile * C::kPlaneBytes;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t key = 2 * t + (k & 1) + (k >> 1) * 8, r = row + key;
-        if (W == 4) {
-            const uint4 x = lds128(plane + chunk_at<C::kPlaneBytes>(r, g));
-            v.w[k][0] = x.x, v.w[k][1] = x.y;
-            v.w[k][W - 2] = x.z, v.w[k][W - 1] = x.w;
-        } else {
-            const uint2 x = lds64(plane + chunk_at<C::kPlaneBytes>(r, g >> 1) + (g & 1) * 8);
-            v.w[k][0] = x.x, v.w[k][1] = x.y;
-        }
-        if (upto != INT32_MAX && base + (int32_t)key >= upto)
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                v.w[k][w] = 0u;
+    static __device__ __forceinline__ bool not_finite(uint32_t h)  // of a pair of fp16
+    {
+        return (h & 0x7c000000u) == 0x7c000000u || (h & 0x7c00u) == 0x7c00u;
     }
-}
+};
 
-// One query row's features for this lane (t of 4) as the products' operand; with
-// 8-bit cells as fp16 relative to the power of two of the row's largest.
-// Returns the factor of the row's scores.
-template <int D, bool F8, int PLANES>
-__device__ __forceinline__ float load_queries(const __nv_bfloat16* row, bool there, int t,
-                                              float scale_log2, uint32_t (&q)[D / 16][2])
+// 8 query rows in shared memory as the products' operand (16 features a step, two
+// words a lane), rows that are not `there` (lane: row g) as zeros.  Returns the
+// factor of row g's scores.  e4m3: as fp16 relative to the power of two of the
+// row's largest element, in the order in which the lanes hold K's features.
+template <int D, bool F8>
+__device__ __forceinline__ float load_queries(uint32_t rows, bool there, float scale_log2,
+                                              uint32_t (&q)[D / 16][2])
 {
-    constexpr int kPer = D / 16 / PLANES;  // steps of a plane
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (!F8) {
 #pragma unroll
-    for (int pl = 0; pl < PLANES; ++pl)
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-            uint4 x = make_uint4(0, 0, 0, 0);  // two steps: 8 features
-            if (there)
-                x = __ldg(reinterpret_cast<const uint4*>(row + pl * 64 + t * 4 * kPer + 4 * i));
-            const int s = pl * kPer + i;
-            q[s][0] = x.x, q[s][1] = x.y;
-            q[s + 1][0] = x.z, q[s + 1][1] = x.w;
+        for (int s = 0; s < D / 16; s += 2) {
+            // chunks 2s .. 2s+3 of the rows
+            uint32_t r[4];
+            ldmatrix4<false>(rows + (lane & 7) * (D * 2) + (2 * s + (lane >> 3)) * 16, r);
+            q[s][0] = there ? r[0] : 0u, q[s][1] = there ? r[1] : 0u;
+            q[s + 1][0] = there ? r[2] : 0u, q[s + 1][1] = there ? r[3] : 0u;
         }
-    if (!F8)
         return scale_log2;
+    }
+#pragma unroll
+    for (int s = 0; s < D / 16; s += 2) {
+        uint4 x = lds128(rows + g * (D * 2) + t * (D / 2) + s * 8);
+        if (!there)
+            x = make_uint4(0, 0, 0, 0);
+        q[s][0] = x.x, q[s][1] = x.y;
+        q[s + 1][0] = x.z, q[s + 1][1] = x.w;
+    }
     float amax = 0.f;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
@@ -447,41 +581,42 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int 
 
 template <int D, bool F8, int NB>
 __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32_t ring,
-                                        float* join, uint2* qs, const WaitCtx& wctx)
+                                        float* join, uint32_t q_rows, uint2* qs,
+                                        const WaitCtx& wctx)
 {
     using C = Cfg<D, F8, NB>;
-    constexpr int kWords = C::kLaneVals / (F8 ? 4 : 2);  // V words per key and plane
-    constexpr int kMt = C::kPlanes * C::kLaneVals / 2;   // O^T tiles of 16 features
-    constexpr int kChunks = C::kPlaneBytes / 64;         // K chunks per lane and plane
-    static_assert(kMt == D / 16, "features");
+    constexpr int kMt = D / 16;                   // O^T tiles of 16 features
+    constexpr int kChunks = C::kPlaneBytes / 64;  // e4m3: K chunks per lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int32_t page = p.c.page;
     const int sc_at = page < kTile ? warp * 16 / page : 0;
     const int32_t R = p.G * p.T;
-    uint32_t it = 0;
+    uint32_t it = 0, seg = 0;
     int par = 0;
     bool dead = false;  // a wait gave up: keep the barriers' count, compute nothing
     int4 info = make_int4(0, 0, 0, 0);
     Walk wk;
     wk.start(p, sh);
-    while (wk.next(p)) {
-        const int32_t h = wk.hr / p.row_groups;
-        const int32_t r0 = (wk.hr - h * p.row_groups) * C::kRows;
+    for (; wk.next(p); ++seg) {
+        const int32_t h = wk.h, r0 = wk.rg * C::kRows;
         const int32_t len = wk.len, n = wk.n;
         // ---- queries: rows g of each block of 8, this lane's features
         uint32_t q[C::kSteps][2];  // NB = 1: the operand itself
         float rf[NB][2];           // score factor of rows 2t, 2t+1
         int32_t lim[NB][2];        // last visible key of rows 2t, 2t+1
         int32_t tok[NB][2];
+        if (!dead) {
+            const bool ok = mbar_wait(&sh.q_full[seg & 1], (seg / 2) & 1, wctx, 61);
+            dead = !__all_sync(0xffffffffu, ok);
+        }
         if (NB == 1 || warp < NB) {
             const int nb = NB == 1 ? 0 : warp;
-            const int32_t r = r0 + nb * 8 + g;
-            const int32_t gh = r / p.T, tq = r - gh * p.T;
-            const bool there = r < R && tq < n;
-            const __nv_bfloat16* row = (const __nv_bfloat16*)p.q.p + wk.b * p.q.sb +
-                                       (int64_t)(h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl;
-            const float f = load_queries<D, F8, C::kPlanes>(row, there, t, p.scale_log2, q);
+            int32_t gh, tq;
+            split_row(p, r0 + nb * 8 + g, gh, tq);
+            const float f =
+                load_queries<D, F8>(q_rows + (seg & 1) * C::kQRows + nb * 8 * (D * 2),
+                                    r0 + nb * 8 + g < R && tq < n, p.scale_log2, q);
             if (NB == 1) {
                 rf[0][0] = __shfl_sync(0xffffffffu, f, 2 * t * 4);
                 rf[0][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
@@ -493,6 +628,9 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     sh.qf[nb][g] = f;
             }
         }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.q_empty[seg & 1]);
         if (NB > 1)
             consumer_sync();
 #pragma unroll
@@ -502,7 +640,9 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 if (NB > 1)
                     rf[nb][k] = sh.qf[nb][2 * t + k];
                 const int32_t rr = r0 + nb * 8 + 2 * t + k;
-                tok[nb][k] = rr < R ? rr % p.T : n;
+                int32_t gh, tq;
+                split_row(p, rr, gh, tq);
+                tok[nb][k] = rr < R ? tq : n;
                 lim[nb][k] = p.causal ? len - n + min(tok[nb][k], n - 1) : len - 1;
             }
         // keys up to all_see are visible to every row, keys from len on to none
@@ -541,39 +681,40 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         acc[nb][0][k] = acc[nb][1][k] = 0.f;
+                auto product = [&](int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-                for (int pl = 0; pl < C::kPlanes; ++pl)
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const uint2 b = NB == 1 ? make_uint2(q[s][0], q[s][1])
+                                                : qs[(nb * C::kSteps + s) * 32 + lane];
+                        mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
+                    }
+                };
+                if (F8) {
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
-                        const uint32_t plane = kt + pl * kTile * C::kPlaneBytes;
                         const uint4 x =
-                            lds128(plane + chunk_at<C::kPlaneBytes>(row + g, t * kChunks + c));
+                            lds128(kt + chunk_at<C::kPlaneBytes>(row + g, t * kChunks + c));
                         const uint4 y =
-                            lds128(plane + chunk_at<C::kPlaneBytes>(row + g + 8, t * kChunks + c));
+                            lds128(kt + chunk_at<C::kPlaneBytes>(row + g + 8, t * kChunks + c));
                         const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
                         const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-                        constexpr int kPer = F8 ? 4 : 2;  // steps of a chunk
 #pragma unroll
-                        for (int j = 0; j < kPer; ++j) {
-                            const int s = (pl * kChunks + c) * kPer + j;
-                            uint32_t a0, a1, a2, a3;
-                            if (F8) {
-                                a0 = e4m3x2_half2(xw[j] & 0xffffu);
-                                a2 = e4m3x2_half2(xw[j] >> 16);
-                                a1 = e4m3x2_half2(yw[j] & 0xffffu);
-                                a3 = e4m3x2_half2(yw[j] >> 16);
-                            } else {
-                                a0 = xw[2 * j], a2 = xw[2 * j + 1];
-                                a1 = yw[2 * j], a3 = yw[2 * j + 1];
-                            }
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                const uint2 b = NB == 1 ? make_uint2(q[s][0], q[s][1])
-                                                        : qs[(nb * C::kSteps + s) * 32 + lane];
-                                mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
-                            }
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            product(c * 4 + j, e4m3x2_half2(xw[j] & 0xffffu),
+                                    e4m3x2_half2(yw[j] & 0xffffu), e4m3x2_half2(xw[j] >> 16),
+                                    e4m3x2_half2(yw[j] >> 16));
                     }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < C::kSteps; ++s) {
+                        const uint32_t plane = kt + (s / 4) * kTile * C::kPlaneBytes;
+                        uint32_t a[4];
+                        ldmatrix4<false>(plane + chunk_at<128>(row + (lane & 15),
+                                                               (2 * s + (lane >> 4)) & 7),
+                                         a);
+                        product(s, a[0], a[1], a[2], a[3]);
+                    }
+                }
                 // value scale = vm 2^ve, vm in [1, 2) (1 for the powers of two that
                 // the append writes)
                 float ve = 0.f, vm = 1.f;
@@ -587,16 +728,16 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 }
                 const bool masked = base + 15 > all_see;  // some row does not see some key
                 bool apart = false;  // non-finite V that some rows do not see
+                Values<C, F8> v;
                 if (masked && p.causal && n > 1) {
+                    v.load(vt, row, len - base);
 #pragma unroll
-                    for (int pl = 0; pl < C::kPlanes; ++pl) {
-                        Vals<kWords> v;
-                        load_values<C, kWords>(v, vt, row, pl, g, t, base, len);
+                    for (int m = 0; m < kMt; ++m) {
+                        uint32_t a[4];
+                        v.tile(m, false, a);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w)
-                                apart |= not_finite<F8>(v.w[k][w]);
+                            apart |= v.not_finite(a[k]);
                     }
                     apart = __any_sync(0xffffffffu, apart);
                 }
@@ -659,25 +800,18 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     }
                 }
                 // O^T += V^T P^T; V of keys behind the end is not ours
-                const int32_t upto = masked ? len : INT32_MAX;
                 if (!apart) {
+                    v.load(vt, row, masked ? len - base : 16);
 #pragma unroll
-                    for (int pl = 0; pl < C::kPlanes; ++pl) {
-                        Vals<kWords> v;
-                        load_values<C, kWords>(v, vt, row, pl, g, t, base, upto);
+                    for (int m = 0; m < kMt; ++m) {
+                        uint32_t a[4];
+                        v.tile(m, !masked, a);
 #pragma unroll
-                        for (int j = 0; j < kMt / C::kPlanes; ++j) {
-                            const int m = pl * (kMt / C::kPlanes) + j;
-                            uint32_t a[4];
-                            value_frag<F8>(v, j, a);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0],
-                                             pt[nb][1]);
-                                if (!F8)
-                                    mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
-                                                 pr[nb][1]);
-                            }
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                            if (!F8)
+                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
+                                             pr[nb][1]);
                         }
                     }
                 } else {
@@ -685,28 +819,21 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     // that do not see it: one token at a time, with the values
                     // behind its position taken out
                     for (int32_t tt = 0; tt < n; ++tt) {
+                        v.load(vt, row, len - n + tt + 1 - base);
 #pragma unroll
-                        for (int pl = 0; pl < C::kPlanes; ++pl) {
-                            Vals<kWords> v;
-                            load_values<C, kWords>(v, vt, row, pl, g, t, base, len - n + tt + 1);
+                        for (int m = 0; m < kMt; ++m) {
+                            uint32_t a[4];
+                            v.tile(m, false, a);
 #pragma unroll
-                            for (int j = 0; j < kMt / C::kPlanes; ++j) {
-                                const int m = pl * (kMt / C::kPlanes) + j;
-                                uint32_t a[4];
-                                value_frag<F8>(v, j, a);
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2], O[nb][m][3]};
+                                mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                                if (!F8)
+                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
 #pragma unroll
-                                for (int nb = 0; nb < NB; ++nb) {
-                                    float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2],
-                                                  O[nb][m][3]};
-                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                                    if (!F8)
-                                        mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0],
-                                                     pr[nb][1]);
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        if (tok[nb][k & 1] == tt)
-                                            O[nb][m][k] = d[k];
-                                }
+                                for (int k = 0; k < 4; ++k)
+                                    if (tok[nb][k & 1] == tt)
+                                        O[nb][m][k] = d[k];
                             }
                         }
                     }
@@ -745,14 +872,17 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 if (r0 + r < R) {
                     float* dst = join + (warp * C::kRows + r) * C::kPitch;
 #pragma unroll
-                    for (int pl = 0; pl < C::kPlanes; ++pl)
-#pragma unroll
-                        for (int j = 0; j < C::kLaneVals / 4; ++j) {
-                            const int m = pl * C::kLaneVals / 2 + 2 * j;
-                            *reinterpret_cast<float4*>(dst + pl * 64 + g * C::kLaneVals + 4 * j) =
-                                make_float4(O[nb][m][k] * f, O[nb][m][2 + k] * f,
-                                            O[nb][m + 1][k] * f, O[nb][m + 1][2 + k] * f);
+                    for (int m = 0; m < kMt; ++m) {
+                        if (F8) {  // features 2m, 2m + 1 of the lane's kMt * 2
+                            if (m % 2 == 0)
+                                *reinterpret_cast<float4*>(dst + g * (2 * kMt) + 2 * m) =
+                                    make_float4(O[nb][m][k] * f, O[nb][m][2 + k] * f,
+                                                O[nb][m + 1][k] * f, O[nb][m + 1][2 + k] * f);
+                        } else {
+                            dst[16 * m + g] = O[nb][m][k] * f;
+                            dst[16 * m + 8 + g] = O[nb][m][2 + k] * f;
                         }
+                    }
                 }
             }
         consumer_sync();
@@ -782,17 +912,18 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 *reinterpret_cast<float4*>(p.part_o + (slot * C::kRows + r) * D + f) = o;
                 continue;
             }
-            const int32_t gh = (r0 + r) / p.T, tq = r0 + r - gh * p.T;
+            int32_t gh, tq;
+            split_row(p, r0 + r, gh, tq);
             if (tq >= n)
                 continue;
             const int64_t at = ((int64_t)wk.b * p.Hq + h * p.G + gh) * p.T + tq;
             write_row<D, F8>(p, at, f, mx, L, o);
         }
         if (!whole && wk.tile0 == 0) {
-            // blocks after this one that hold the rest of the segment
-            const long long end = wk.w - wk.nt + wk.tiles;
-            info = make_int4(wk.b, wk.hr, (int)((end * sh.active - 1) / sh.total) - (int)blockIdx.x,
-                             n);
+            // blocks after this one that hold the rest: up to the last tile's
+            const long long last = wk.w + kSegment + wk.tiles - 1;
+            info = make_int4(wk.b, wk.h * p.row_groups + wk.rg,
+                             (int)(((last + 1) * sh.active - 1) / sh.total) - (int)blockIdx.x, n);
         }
     }
     if (threadIdx.x == 0)
@@ -810,11 +941,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
     const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
     float* join = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
                                            C::kStages * C::kStage);
+    const uint32_t q_rows = smem_u32(join) + C::kJoin;
+    uint2* qs = reinterpret_cast<uint2*>(join + (C::kJoin + 2 * C::kQRows) / 4);
     if (threadIdx.x == 0) {
         sh.abort = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], kWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.q_full[s], 1);
+            mbar_init(&sh.q_empty[s], kWarps);
         }
         fence_barrier_init();
         prefetch_tmap(&tk);
@@ -824,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
     find_range(p, sh);  // also orders the barriers' initialisation
     const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
     if (threadIdx.x >= 32 * kWarps) {
-        produce<D, F8, NB>(p, sh, ring, tk, tv, wctx);
+        produce<D, F8, NB>(p, sh, ring, q_rows, tk, tv, wctx);
         if (*wctx.abort_flag) {
             // let copies in flight land before the block's shared memory goes
             const uint64_t t0 = globaltimer_ns();
@@ -832,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
             }
         }
     } else {
-        consume<D, F8, NB>(p, sh, ring, join, reinterpret_cast<uint2*>(join + C::kJoin / 4), wctx);
+        consume<D, F8, NB>(p, sh, ring, join, q_rows, qs, wctx);
     }
 }
 
@@ -856,7 +993,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // row r of the group -> output row, or -1
     auto target = [&](int r) -> int64_t {
-        const int32_t rr = r0 + r, gh = rr / p.T, tq = rr - gh * p.T;
+        const int32_t rr = r0 + r;
+        int32_t gh, tq;
+        split_row(p, rr, gh, tq);
         if (rr >= p.G * p.T || tq >= info.w)
             return -1;
         return ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq;

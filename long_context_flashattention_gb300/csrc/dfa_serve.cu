@@ -478,6 +478,7 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     p.Hq = desc->Hq;
     p.G = G;
     p.T = T;
+    p.inv_T = ((1u << 21) + T - 1) / T;
     p.causal = desc->causal;
     p.o_fp32 = desc->o_fp32;
     p.scale_log2 = desc->scale * 1.4426950408889634f;

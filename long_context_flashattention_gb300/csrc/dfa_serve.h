@@ -82,6 +82,7 @@ struct PagedParams {
     Rows q;
     const int32_t* q_lens;        // [B] or NULL
     int32_t Hq, G, T, causal, o_fp32;
+    uint32_t inv_T;               // 2^21 / T, rounded up
     int32_t row_groups;           // blocks of query rows per key/value head
     float scale_log2;
     void* o;                      // [B, Hq, T, d]
