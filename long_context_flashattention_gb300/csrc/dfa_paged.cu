@@ -41,8 +41,8 @@ namespace paged {
 constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = kPagedTile;
-constexpr int kSegment = 2;                // cost of a segment beside its tiles, in tiles
 constexpr float kGrow = 8.f;               // rescale when the maximum grows by 2^8
+constexpr float kNone = -1e30f;            // running maximum before the first key
 constexpr float kSumShift = 16.f;          // 8-bit cells: sums are kept times 2^-16, so
                                            // that scales of 2^-100 do not overflow them
 constexpr float kNoPage = -1.f;            // in place of a key scale
@@ -60,6 +60,10 @@ struct Cfg {
     static constexpr int kPitch = D + 4;                     // floats of an O row in the join
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kQRows = kRows * D * 2;  // a segment's queries, two segments
+    // What a segment costs a block beside its tiles, in tiles.  Measured (64 ragged
+    // sequences to 8K, 8 heads; 1, 2, 3, 4): e4m3 92.6, 91.9, 92.8, 93.9 us, with
+    // 16 query rows 130, 126, 119, 115 us; bf16 with 16 rows 178, 176, 176, 177.
+    static constexpr int kSegmentCost = F8 && NB == 2 ? 4 : 2;
     // 16 query rows take their operand from shared memory: O takes its registers
     static constexpr int kQ = NB > 1 ? NB * (D / 16) * 32 * 8 : 0;
     static constexpr int kSmem = 1024 + kStages * kStage + kJoin + 2 * kQRows + kQ;
@@ -71,7 +75,7 @@ struct Cfg {
 struct Shared {
     uint64_t full[8], empty[8];   // tiles
     uint64_t q_full[2], q_empty[2];
-    float2 scale[8][4];           // per stage and page: K and V scale (kNoPage: no page)
+    float4 scale[8][4];           // per stage and page: see page_scale
     // maxima and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
     float m[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
@@ -132,6 +136,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B
+template <bool F16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // transpose of an 8x8 matrix of 16-bit elements held one row per 4 lanes
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
@@ -185,7 +206,7 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
     return n > 0 ? max(1, ceil_div(len, kTile)) : 0;
 }
 
-// The line that is cut: every segment takes kSegment units (its queries, the join
+// The line that is cut: every segment takes p.segment_cost units (its queries, the join
 // and the rows' output cost a block about that many tiles' time), then one unit
 // per tile.  A cut inside the former puts the whole segment behind it.
 //
@@ -207,17 +228,17 @@ struct Walk {
             return;
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
         tiles = tiles_of(len, n);
-        const long long at = w - sh.base, unit = tiles + kSegment;
+        const long long at = w - sh.base, unit = tiles + p.segment_cost;
         const long long hr = at / unit;
         h = (int32_t)(hr / p.row_groups);
         rg = (int32_t)(hr - (long long)h * p.row_groups);
-        tile0 = max(0, (int32_t)(at - hr * unit) - kSegment);
+        tile0 = max(0, (int32_t)(at - hr * unit) - p.segment_cost);
         w -= at - hr * unit;  // the segment's first unit
     }
     __device__ __forceinline__ bool next(const PagedParams& p)
     {
         if (!fresh) {
-            w += tiles + kSegment;
+            w += tiles + p.segment_cost;
             if (w >= w1)
                 return false;
             tile0 = 0;
@@ -236,7 +257,7 @@ struct Walk {
             return false;
         }
         fresh = false;
-        nt = (int32_t)min((long long)tiles, w1 - w - kSegment) - tile0;
+        nt = (int32_t)min((long long)tiles, w1 - w - p.segment_cost) - tile0;
         return nt > 0;  // (the last segment's beginning may lie in the range, its tiles behind)
     }
 };
@@ -252,7 +273,7 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
         int32_t len, n;
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
         const int32_t tiles = tiles_of(len, n);
-        sum += tiles ? (long long)(tiles + kSegment) * per_seq : 0;
+        sum += tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
     }
     long long incl = sum;
 #pragma unroll
@@ -287,7 +308,7 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
             int32_t len, n;
             seq_rows(p.c, p.q_lens, p.T, b, len, n);
             const int32_t tiles = tiles_of(len, n);
-            const long long t = tiles ? (long long)(tiles + kSegment) * per_seq : 0;
+            const long long t = tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
             if (w0 < base + t) {
                 sh.b = b;
                 sh.base = base;
@@ -297,6 +318,23 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
         }
     }
     __syncthreads();
+}
+
+// What a group of 16 keys needs of its page's scales s (K) and u (V): s, log2 u,
+// 2^-kSumShift / u, and whether the latter is safe to multiply with.
+template <bool F8>
+__device__ __forceinline__ float4 page_scale(bool there, float s, float u)
+{
+    if (!there)
+        return make_float4(kNoPage, 0.f, 0.f, 0.f);
+    if (!F8)
+        return make_float4(1.f, 0.f, 1.f, 0.f);
+    // exponent and significand apart: exact for a power of two
+    const uint32_t bits = __float_as_uint(u);
+    const int e = (int)((bits >> 23) & 0xffu);
+    const float lu = e == 255 ? u : (float)max(e - 127, -126) +
+                                        log2f(__uint_as_float((bits & 0x7fffffu) | (127u << 23)));
+    return make_float4(s, lu, ex2(-kSumShift - lu), 0.f);
 }
 
 // The producer warp: queries of a segment, then its tiles.  Every wait it has for
@@ -312,7 +350,7 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
     const int32_t page = p.c.page;
     const int32_t box_rows = min(page, kTile);
     const int32_t per_tile = kTile / box_rows;  // boxes of a tile
-    uint32_t it = 0, seg = 0;
+    uint32_t st = 0, phase = 0, seg = 0;
     Walk wk;
     wk.start(p, sh);
     bool more = wk.next(p);
@@ -338,12 +376,12 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
             }
         };
         check_window();
-        {
+        auto fetch_queries = [&] {
             const uint32_t qb = seg & 1;
             if (seg >= 2) {
                 const bool ok = mbar_wait(&sh.q_empty[qb], (seg / 2 - 1) & 1, wctx, 51);
                 if (!__all_sync(0xffffffffu, ok))
-                    return;
+                    return false;
             }
             const int32_t r = wk.rg * C::kRows + lane;
             int32_t gh, tq;
@@ -361,11 +399,12 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.q_full[qb]);
-        }
+            return true;
+        };
         Walk nx = wk;
         bool more_next = false;
         const int32_t look = min(wk.nt - 1, C::kStages - 1);
-        for (int32_t i = 0; i < wk.nt; ++i, ++it) {
+        for (int32_t i = 0; i < wk.nt; ++i) {
             const int32_t key0 = (wk.tile0 + i) * kTile;
             const int32_t p0 = key0 >> p.c.page_log2;
             if (p0 >= win + 32) {
@@ -373,12 +412,10 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
                 id = entry(wk, win);
                 check_window();
             }
-            const uint32_t st = it % C::kStages;
-            if (it >= C::kStages) {
-                const bool ok = mbar_wait(&sh.empty[st], (it / C::kStages - 1) & 1, wctx, 50);
-                if (!__all_sync(0xffffffffu, ok))
-                    return;
-            }
+            // (passes at once in the first round: the phase before the barrier's first)
+            const bool ok = mbar_wait(&sh.empty[st], phase ^ 1, wctx, 50);
+            if (!__all_sync(0xffffffffu, ok))
+                return;
             const int src = p0 - win + lane;  // lanes below per_tile: their box's page
             const int32_t my = __shfl_sync(0xffffffffu, id, src & 31);
             const bool load = lane < per_tile && p0 + lane < pages_end && my >= 0;
@@ -400,11 +437,16 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
             const float my_ks = __shfl_sync(0xffffffffu, ks, src & 31);
             const float my_vs = __shfl_sync(0xffffffffu, vs, src & 31);
             if (lane < per_tile)
-                sh.scale[st][lane] =
-                    load ? make_float2(my_ks, my_vs) : make_float2(kNoPage, 0.f);
+                sh.scale[st][lane] = page_scale<F8>(load, my_ks, my_vs);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.full[st]);
+            if (++st == C::kStages) {
+                st = 0;
+                phase ^= 1;
+            }
+            if (i == 0 && !fetch_queries())
+                return;
             if (i == look) {
                 more_next = nx.next(p);
                 next_id = more_next ? entry(nx, (nx.tile0 * kTile) >> p.c.page_log2) : -1;
@@ -431,32 +473,36 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4])
 }
 
 // V of a warp's 16 keys as 16x16 operands V^T (a0, a1: keys 2t, 2t+1; a2, a3: keys
-// 2t+8, 2t+9), tile by tile of 16 features.  `upto`: keys from that group-relative
-// one on are zero.
+// 2t+8, 2t+9), tile by tile of 16 features.  clip(n): the keys from the group's
+// n-th on are zero.
 //
 // bf16: the matrix loads transpose; tile m has features 16m + g (a0, a2) and
 // 16m + 8 + g (a1, a3).
 template <typename C, bool F8>
 struct Values {
-    uint32_t base;
-    uint32_t keep[2];
+    uint32_t base, key_, keep[2];
 
-    __device__ __forceinline__ void load(uint32_t vt, uint32_t row, int upto)
+    __device__ __forceinline__ void load(uint32_t vt, uint32_t row)
     {
-        const int lane = threadIdx.x & 31, t = lane & 3;
+        const int lane = threadIdx.x & 31;
         base = vt;
         key_ = row + (lane & 7) + (lane >> 4) * 8;
+    }
+    __device__ __forceinline__ void clip(int upto)
+    {
+        const int t = threadIdx.x & 3;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             keep[i] = (2 * t + 8 * i < upto ? 0xffffu : 0u) |
                       (2 * t + 8 * i + 1 < upto ? 0xffff0000u : 0u);
     }
-    __device__ __forceinline__ void tile(int m, bool whole, uint32_t (&a)[4]) const
+    template <bool CLIPPED>
+    __device__ __forceinline__ void tile(int m, uint32_t (&a)[4]) const
     {
         const uint32_t c = 2 * m + ((threadIdx.x >> 3) & 1);  // 16-byte chunk of the row
         const uint32_t plane = base + (c >> 3) * kTile * C::kPlaneBytes;
         ldmatrix4<true>(plane + chunk_at<128>(key_, c & 7), a);
-        if (!whole) {
+        if (CLIPPED) {
             a[0] &= keep[0], a[1] &= keep[0];
             a[2] &= keep[1], a[3] &= keep[1];
         }
@@ -465,9 +511,6 @@ struct Values {
     {
         return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
     }
-
-  private:
-    uint32_t key_;
 };
 
 // e4m3: a lane reads 16 (d = 128) or 8 features of four keys and turns them to
@@ -477,7 +520,7 @@ struct Values<C, true> {
     static constexpr int W = C::kPlaneBytes / 32;  // words per key
     uint32_t w[4][W];
 
-    __device__ __forceinline__ void load(uint32_t vt, uint32_t row, int upto)
+    __device__ __forceinline__ void load(uint32_t vt, uint32_t row)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -492,13 +535,20 @@ struct Values<C, true> {
                     lds64(vt + chunk_at<C::kPlaneBytes>(row + key, g >> 1) + (g & 1) * 8);
                 w[k][0] = x.x, w[k][1] = x.y;
             }
-            if (key >= upto)
+        }
+    }
+    __device__ __forceinline__ void clip(int upto)
+    {
+        const int t = threadIdx.x & 3;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (2 * t + (k & 1) + (k >> 1) * 8 >= upto)
 #pragma unroll
                 for (int i = 0; i < W; ++i)
                     w[k][i] = 0u;
-        }
     }
-    __device__ __forceinline__ void tile(int m, bool, uint32_t (&a)[4]) const
+    template <bool CLIPPED>
+    __device__ __forceinline__ void tile(int m, uint32_t (&a)[4]) const
     {
         const uint32_t sel = (m & 1) ? 0x7362 : 0x5140;  // features 2m, 2m+1 of two keys
         const uint32_t x = __byte_perm(w[0][m / 2], w[1][m / 2], sel);
@@ -575,8 +625,7 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int 
             make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     if (f == 0)
         p.lse[at] = L == 0.f ? -INFINITY
-                             : ((mx == -INFINITY ? 0.f : mx) + (F8 ? kSumShift : 0.f) + log2f(L)) *
-                                   kLn2;
+                             : (mx + (F8 ? kSumShift : 0.f) + log2f(L)) * kLn2;
 }
 
 template <int D, bool F8, int NB>
@@ -592,7 +641,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
     const int32_t page = p.c.page;
     const int sc_at = page < kTile ? warp * 16 / page : 0;
     const int32_t R = p.G * p.T;
-    uint32_t it = 0, seg = 0;
+    uint32_t st = 0, phase = 0, seg = 0;
     int par = 0;
     bool dead = false;  // a wait gave up: keep the barriers' count, compute nothing
     int4 info = make_int4(0, 0, 0, 0);
@@ -603,7 +652,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         const int32_t len = wk.len, n = wk.n;
         // ---- queries: rows g of each block of 8, this lane's features
         uint32_t q[C::kSteps][2];  // NB = 1: the operand itself
-        float rf[NB][2];           // score factor of rows 2t, 2t+1
+        uint64_t rf[NB];           // score factors of rows 2t, 2t+1
         int32_t lim[NB][2];        // last visible key of rows 2t, 2t+1
         int32_t tok[NB][2];
         if (!dead) {
@@ -618,8 +667,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 load_queries<D, F8>(q_rows + (seg & 1) * C::kQRows + nb * 8 * (D * 2),
                                     r0 + nb * 8 + g < R && tq < n, p.scale_log2, q);
             if (NB == 1) {
-                rf[0][0] = __shfl_sync(0xffffffffu, f, 2 * t * 4);
-                rf[0][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
+                rf[0] = f2pack(__shfl_sync(0xffffffffu, f, 2 * t * 4),
+                               __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4));
             } else {
 #pragma unroll
                 for (int s = 0; s < C::kSteps; ++s)
@@ -634,25 +683,26 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         if (NB > 1)
             consumer_sync();
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+            if (NB > 1)
+                rf[nb] = f2pack(sh.qf[nb][2 * t], sh.qf[nb][2 * t + 1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (NB > 1)
-                    rf[nb][k] = sh.qf[nb][2 * t + k];
                 const int32_t rr = r0 + nb * 8 + 2 * t + k;
                 int32_t gh, tq;
                 split_row(p, rr, gh, tq);
                 tok[nb][k] = rr < R ? tq : n;
                 lim[nb][k] = p.causal ? len - n + min(tok[nb][k], n - 1) : len - 1;
             }
+        }
         // keys up to all_see are visible to every row, keys from len on to none
         const int32_t all_see = p.causal ? len - n : len - 1;
-        float O[NB][kMt][4], M[NB][2], l[NB][2];
+        float O[NB][kMt][4], M[NB][2], l[NB][2], lu_max = -INFINITY;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                M[nb][k] = -INFINITY;
+                M[nb][k] = kNone;
                 l[nb][k] = 0.f;
             }
 #pragma unroll
@@ -662,31 +712,28 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     O[nb][m][k] = 0.f;
         }
         // ---- the run's tiles
-        for (int32_t i = 0; i < wk.nt; ++i, ++it) {
-            const uint32_t st = it % C::kStages;
+        for (int32_t i = 0; i < wk.nt; ++i) {
             if (!dead) {
-                const bool ok = mbar_wait(&sh.full[st], (it / C::kStages) & 1, wctx, 60);
+                const bool ok = mbar_wait(&sh.full[st], phase, wctx, 60);
                 dead = !__all_sync(0xffffffffu, ok);
             }
             const int32_t base = (wk.tile0 + i) * kTile + warp * 16;  // the warp's 16 keys
-            const float2 sc = sh.scale[st][sc_at];
+            const float4 sc = sh.scale[st][sc_at];
             if (!dead && base < len && sc.x != kNoPage) {
                 const uint32_t kt = ring + st * C::kStage;
                 const uint32_t vt = kt + C::kOperand;
                 const uint32_t row = warp * 16;
                 // S^T = K Q^T; two sums, so that half the products are independent
                 float acc[NB][2][4];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[nb][0][k] = acc[nb][1][k] = 0.f;
                 auto product = [&](int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         const uint2 b = NB == 1 ? make_uint2(q[s][0], q[s][1])
                                                 : qs[(nb * C::kSteps + s) * 32 + lane];
-                        mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
+                        if (s < 2)
+                            mma16816_first<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
+                        else
+                            mma16816<F8>(acc[nb][s & 1], a0, a1, a2, a3, b.x, b.y);
                     }
                 };
                 if (F8) {
@@ -715,58 +762,61 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                         product(s, a[0], a[1], a[2], a[3]);
                     }
                 }
-                // value scale = vm 2^ve, vm in [1, 2) (1 for the powers of two that
-                // the append writes)
-                float ve = 0.f, vm = 1.f;
-                if (F8) {
-                    const int e = (int)(__float_as_uint(sc.y) >> 23);  // sign bit clear
-                    const bool normal = e > 0 && e < 255;
-                    ve = normal ? (float)(e - 127) : 0.f;
-                    vm = normal ? __uint_as_float((__float_as_uint(sc.y) & 0x7fffffu) |
-                                                  (127u << 23))
-                                : (e == 255 ? sc.y : 0.f);
-                }
                 const bool masked = base + 15 > all_see;  // some row does not see some key
                 bool apart = false;  // non-finite V that some rows do not see
                 Values<C, F8> v;
                 if (masked && p.causal && n > 1) {
-                    v.load(vt, row, len - base);
+                    v.load(vt, row);
+                    v.clip(len - base);
 #pragma unroll
                     for (int m = 0; m < kMt; ++m) {
                         uint32_t a[4];
-                        v.tile(m, false, a);
+                        v.template tile<true>(m, a);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             apart |= v.not_finite(a[k]);
                     }
                     apart = __any_sync(0xffffffffu, apart);
                 }
+                // The sum of probabilities from the weights, which are u times as
+                // large: not where u is so far below an earlier page's that the
+                // weight may vanish where the probability does not.
+                lu_max = fmaxf(lu_max, sc.y);
+                const bool far = F8 && !(lu_max - sc.y <= 60.f && sc.y <= 80.f);
                 uint32_t pt[NB][2], pr[NB][2];  // P^T (and its bf16 remainder)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
+                    // Exponents of the weights less the running maximum, rows 2t and
+                    // 2t+1 of a pair, key g in x[0], x[1], key g + 8 in x[2], x[3].
+                    const uint64_t factor = F8 ? f2mul(rf[nb], f2pack(sc.x, sc.x)) : rf[nb];
+                    uint64_t dot[2];
                     float x[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // exponents of the weights: row 2t + (k & 1), key g + 8 (k >> 1)
-                        const float s = (acc[nb][0][k] + acc[nb][1][k]) * (rf[nb][k & 1] * sc.x);
-                        x[k] = F8 ? s + ve : s;
-                    }
-                    if (masked) {
+                    for (int k = 0; k < 2; ++k)
+                        dot[k] = f2add(f2pack(acc[nb][0][2 * k], acc[nb][0][2 * k + 1]),
+                                       f2pack(acc[nb][1][2 * k], acc[nb][1][2 * k + 1]));
+                    auto exponents = [&](float m0, float m1) {
+                        const uint64_t off = f2pack((F8 ? sc.y : 0.f) - m0, (F8 ? sc.y : 0.f) - m1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            x[k] = base + g + 8 * (k >> 1) <= lim[nb][k & 1] ? x[k] : -INFINITY;
-                    }
-                    const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
-                    if (__any_sync(0xffffffffu,
-                                   x0 > M[nb][0] + kGrow || x1 > M[nb][1] + kGrow)) {
-                        float mx[2] = {x0, x1}, f[2];
+                        for (int k = 0; k < 2; ++k)
+                            f2unpack(f2fma(dot[k], factor, off), x[2 * k], x[2 * k + 1]);
+                        if (masked)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (base + g + 8 * (k >> 1) > lim[nb][k & 1])
+                                    x[k] = -INFINITY;
+                    };
+                    exponents(M[nb][0], M[nb][1]);
+                    if (__any_sync(0xffffffffu, fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kGrow)) {
+                        exponents(0.f, 0.f);
+                        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, f[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
                             const float mn = fmaxf(M[nb][k], mx[k]);
-                            f[k] = M[nb][k] == -INFINITY ? 0.f : ex2(M[nb][k] - mn);
+                            f[k] = ex2(M[nb][k] - mn);
                             M[nb][k] = mn;
                             l[nb][k] *= f[k];
                         }
@@ -775,64 +825,69 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 O[nb][m][k] *= f[k & 1];
+                        exponents(M[nb][0], M[nb][1]);
                     }
+                    float w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float m = M[nb][k & 1];
-                        x[k] -= m == -INFINITY ? 0.f : m;
-                        // an exponential of its own: with value scales far apart the
-                        // weight may vanish where the probability does not
-                        const float prob = ex2(F8 ? x[k] - (ve + kSumShift) : x[k]);
-                        l[nb][k & 1] += prob;
-                        x[k] = F8 ? ex2(x[k]) * vm : prob;
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = ex2(x[k]);
+                    if (far) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            l[nb][k & 1] += ex2(x[k] - sc.y - kSumShift);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            l[nb][k & 1] = F8 ? fmaf(w[k], sc.z, l[nb][k & 1]) : l[nb][k & 1] + w[k];
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         if (F8) {
-                            pt[nb][k] = transpose8(pack_half2(x[2 * k], x[2 * k + 1]));
+                            pt[nb][k] = transpose8(pack_half2(w[2 * k], w[2 * k + 1]));
                         } else {
-                            const uint32_t hi = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                            const uint32_t hi = pack_bf16x2(w[2 * k], w[2 * k + 1]);
                             const uint32_t lo =
-                                pack_bf16x2(x[2 * k] - bf16lo(hi), x[2 * k + 1] - bf16hi(hi));
+                                pack_bf16x2(w[2 * k] - bf16lo(hi), w[2 * k + 1] - bf16hi(hi));
                             pt[nb][k] = transpose8(hi);
                             pr[nb][k] = transpose8(lo);
                         }
                     }
                 }
-                // O^T += V^T P^T; V of keys behind the end is not ours
-                if (!apart) {
-                    v.load(vt, row, masked ? len - base : 16);
+                // O^T += V^T P^T
+                auto weigh = [&](int nb, float(&d)[4], const uint32_t(&a)[4]) {
+                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
+                    if (!F8)
+                        mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
+                };
+                if (!masked) {
+                    v.load(vt, row);
 #pragma unroll
                     for (int m = 0; m < kMt; ++m) {
                         uint32_t a[4];
-                        v.tile(m, !masked, a);
+                        v.template tile<false>(m, a);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                            if (!F8)
-                                mma16816<F8>(O[nb][m], a[0], a[1], a[2], a[3], pr[nb][0],
-                                             pr[nb][1]);
-                        }
+                        for (int nb = 0; nb < NB; ++nb)
+                            weigh(nb, O[nb][m], a);
                     }
                 } else {
-                    // a NaN or an infinity times a weight of zero would reach rows
-                    // that do not see it: one token at a time, with the values
-                    // behind its position taken out
-                    for (int32_t tt = 0; tt < n; ++tt) {
-                        v.load(vt, row, len - n + tt + 1 - base);
+                    // V of keys behind the end is not ours.  And a NaN or an infinity
+                    // times a weight of zero would reach rows that do not see it:
+                    // then one token at a time, with the values behind its position
+                    // taken out.
+                    for (int32_t tt = apart ? 0 : n - 1; tt < n; ++tt) {
+                        v.load(vt, row);
+                        v.clip((apart ? len - n + tt + 1 : len) - base);
 #pragma unroll
                         for (int m = 0; m < kMt; ++m) {
                             uint32_t a[4];
-                            v.tile(m, false, a);
+                            v.template tile<true>(m, a);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
                                 float d[4] = {O[nb][m][0], O[nb][m][1], O[nb][m][2], O[nb][m][3]};
-                                mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                                if (!F8)
-                                    mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
+                                weigh(nb, d, a);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    if (tok[nb][k & 1] == tt)
+                                    if (!apart || tok[nb][k & 1] == tt)
                                         O[nb][m][k] = d[k];
                             }
                         }
@@ -842,6 +897,10 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.empty[st]);
+            if (++st == C::kStages) {
+                st = 0;
+                phase ^= 1;
+            }
         }
         // ---- join the warps: largest maximum, rescaled sums and O
         par ^= 1;
@@ -867,8 +926,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w)
                     mx = fmaxf(mx, sh.m[par][w][r]);
-                // a warp without a maximum has O = 0, or only NaN
-                const float f = M[nb][k] == -INFINITY ? 1.f : ex2(M[nb][k] - mx);
+                const float f = ex2(M[nb][k] - mx);
                 if (r0 + r < R) {
                     float* dst = join + (warp * C::kRows + r) * C::kPitch;
 #pragma unroll
@@ -901,7 +959,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float mw = sh.m[par][w][r];
-                L += sh.l[par][w][r] * (mw == -INFINITY ? 1.f : ex2(mw - mx));
+                L += sh.l[par][w][r] * ex2(mw - mx);
                 const float4 y = *reinterpret_cast<const float4*>(
                     join + (w * C::kRows + r) * C::kPitch + f);
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
@@ -921,7 +979,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         }
         if (!whole && wk.tile0 == 0) {
             // blocks after this one that hold the rest: up to the last tile's
-            const long long last = wk.w + kSegment + wk.tiles - 1;
+            const long long last = wk.w + p.segment_cost + wk.tiles - 1;
             info = make_int4(wk.b, wk.h * p.row_groups + wk.rg,
                              (int)(((last + 1) * sh.active - 1) / sh.total) - (int)blockIdx.x, n);
         }
@@ -1008,7 +1066,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
             const int64_t at = target(r);
             if (at < 0)
                 continue;
-            float2 ml = make_float2(-INFINITY, 0.f);
+            float4 y[16 / kGroups];  // all on their way at once
+#pragma unroll
+            for (int i = 0; i < 16; i += kGroups)
+                if (i + grp < k)
+                    y[i / kGroups] = *reinterpret_cast<const float4*>(
+                        p.part_o + (slot(i + grp) * ROWS + r) * D + f * 4);
+            float2 ml = make_float2(kNone, 0.f);
             if (lane < k)
                 ml = p.part_ml[slot(lane) * ROWS + r];
             float mx = ml.x;
@@ -1016,23 +1080,20 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
             for (int o = 8; o > 0; o >>= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
             mx = __shfl_sync(0xffffffffu, mx, 0);
-            // a block without a maximum has O = 0, or only NaN
-            const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+            const float w = ex2(ml.x - mx);
             float L = ml.y * w;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, o, 16);
             L = __shfl_sync(0xffffffffu, L, 0);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < k; i += kGroups) {
+#pragma unroll
+            for (int i = 0; i < 16; i += kGroups) {
                 const float wi = __shfl_sync(0xffffffffu, w, i + grp);
-                if (i + grp >= k)
-                    continue;
-                const float4 y = *reinterpret_cast<const float4*>(
-                    p.part_o + (slot(i + grp) * ROWS + r) * D + f * 4);
-                o.x = fmaf(wi, y.x, o.x), o.y = fmaf(wi, y.y, o.y);
-                o.z = fmaf(wi, y.z, o.z), o.w = fmaf(wi, y.w, o.w);
+                if (i + grp < k) {
+                    o.x = fmaf(wi, y[i / kGroups].x, o.x), o.y = fmaf(wi, y[i / kGroups].y, o.y);
+                    o.z = fmaf(wi, y[i / kGroups].z, o.z), o.w = fmaf(wi, y[i / kGroups].w, o.w);
+                }
             }
             if (kGroups == 2) {
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
@@ -1051,7 +1112,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         const int64_t at = target(r);
         if (at < 0)
             continue;
-        float mx = -INFINITY;
+        float mx = kNone;
         for (int i = threadIdx.x; i < k; i += 256)
             mx = fmaxf(mx, p.part_ml[slot(i) * ROWS + r].x);
         for (int o = 16; o > 0; o >>= 1)
@@ -1066,7 +1127,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         float L = 0.f;
         for (int i = threadIdx.x; i < k; i += 256) {
             const float2 ml = p.part_ml[slot(i) * ROWS + r];
-            wt[i] = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+            wt[i] = ex2(ml.x - mx);
             L += ml.y * wt[i];
         }
         for (int o = 16; o > 0; o >>= 1)
@@ -1099,7 +1160,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
 }
 
 template <int D, bool F8, int NB>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                    int num_sms, cudaStream_t stream)
 {
     using C = Cfg<D, F8, NB>;
@@ -1111,12 +1172,16 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedPara
     const int64_t tiles = (int64_t)p.c.B * p.c.Hkv * p.row_groups *
                           max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
     const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), tiles);
+    p.segment_cost = C::kSegmentCost;
     decode_kernel<D, F8, NB><<<grid, kThreads, C::kSmem, stream>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    // The merge's blocks may start while the decode's end, and wait there.  With
-    // few segments each is cut into many partials: a block a row.
+    // The merge's blocks may start while the decode's end, and wait there.  (The
+    // decode itself starts on empty SMs: its blocks are as many as fit, and where a
+    // kernel before it still held some SMs they would be dealt out unevenly; 64
+    // ragged sequences then took 104 us instead of 91.)  With few segments each is
+    // cut into many partials: a block a row.
     const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1131,7 +1196,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedPara
 }
 
 template <int D, bool F8>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                         int num_sms, cudaStream_t stream)
 {
     return p.G * p.T <= kPagedRows ? launch<D, F8, 1>(tk, tv, p, num_sms, stream)
@@ -1141,7 +1206,7 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
 }  // namespace paged
 
 cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv,
-                                const PagedParams& p, int num_sms, cudaStream_t stream)
+                                PagedParams& p, int num_sms, cudaStream_t stream)
 {
     if (p.c.e4m3)
         return p.c.d == 128 ? paged::launch_rows<128, true>(tk, tv, p, num_sms, stream)

@@ -84,6 +84,7 @@ struct PagedParams {
     int32_t Hq, G, T, causal, o_fp32;
     uint32_t inv_T;               // 2^21 / T, rounded up
     int32_t row_groups;           // blocks of query rows per key/value head
+    int32_t segment_cost;         // in tiles
     float scale_log2;
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]
@@ -101,6 +102,6 @@ cudaError_t launch_rope_rows(RopeRowsParams& p, int fp32, int num_sms, cudaStrea
 cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_decode_paged(const CUtensorMap& tk, const CUtensorMap& tv,
-                                const PagedParams& p, int num_sms, cudaStream_t stream);
+                                PagedParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace dfa
