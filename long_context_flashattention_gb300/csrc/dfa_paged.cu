@@ -81,8 +81,9 @@ struct Shared {
     float m[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
     float qf[2][8];               // NB = 2: score factors of the query rows
     long long warp_sum[kThreads / 32];
-    long long w0, w1, total, base;
-    int32_t b, active;            // active: blocks that have tiles
+    long long w0, w1, base;       // the block's range; first unit of sequence b
+    long long each, rest;         // units of a block; the first `rest` blocks have one more
+    int32_t b;
     uint32_t abort;
 };
 
@@ -206,6 +207,19 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
     return n > 0 ? max(1, ceil_div(len, kTile)) : 0;
 }
 
+// a / b for a >= 0, b > 0, the short way where a has 32 bits
+__device__ __forceinline__ long long divide(long long a, int32_t b)
+{
+    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// The block whose range has this unit.
+__device__ __forceinline__ int block_of(const Shared& sh, long long unit)
+{
+    const long long longer = sh.rest * (sh.each + 1);
+    return (int)(unit < longer ? unit / (sh.each + 1) : sh.rest + (unit - longer) / sh.each);
+}
+
 // The line that is cut: every segment takes p.segment_cost units (its queries, the join
 // and the rows' output cost a block about that many tiles' time), then one unit
 // per tile.  A cut inside the former puts the whole segment behind it.
@@ -229,7 +243,7 @@ struct Walk {
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
         tiles = tiles_of(len, n);
         const long long at = w - sh.base, unit = tiles + p.segment_cost;
-        const long long hr = at / unit;
+        const long long hr = divide(at, (int32_t)unit);
         h = (int32_t)(hr / p.row_groups);
         rg = (int32_t)(hr - (long long)h * p.row_groups);
         tile0 = max(0, (int32_t)(at - hr * unit) - p.segment_cost);
@@ -294,13 +308,14 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
     incl += before;
     const int32_t active = (int32_t)min((long long)gridDim.x, total);
     const bool mine = (int32_t)blockIdx.x < active;  // then at least one tile
-    const long long w0 = mine ? total * blockIdx.x / active : 0;
-    const long long w1 = mine ? total * (blockIdx.x + 1) / active : 0;
+    const long long each = divide(total, max(active, 1)), rest = total - each * active;
+    const long long w0 = mine ? each * blockIdx.x + min((long long)blockIdx.x, rest) : 0;
+    const long long w1 = mine ? w0 + each + ((long long)blockIdx.x < rest ? 1 : 0) : 0;
     if (threadIdx.x == 0) {
         sh.w0 = w0;
         sh.w1 = w1;
-        sh.total = total;
-        sh.active = active;
+        sh.each = each;
+        sh.rest = rest;
     }
     if (w0 < w1 && incl - sum <= w0 && w0 < incl) {
         long long base = incl - sum;
@@ -981,7 +996,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             // blocks after this one that hold the rest: up to the last tile's
             const long long last = wk.w + p.segment_cost + wk.tiles - 1;
             info = make_int4(wk.b, wk.h * p.row_groups + wk.rg,
-                             (int)(((last + 1) * sh.active - 1) / sh.total) - (int)blockIdx.x, n);
+                             block_of(sh, last) - (int)blockIdx.x, n);
         }
     }
     if (threadIdx.x == 0)
