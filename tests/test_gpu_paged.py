@@ -454,6 +454,88 @@ def test_decode_many_query_heads_of_one_cache_head():
     check_decode(c, c.cuda(), randn(2, 48, 2, 64, seed=68))
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("B,lens", [(1, [20000]), (32, [9 + i for i in range(31)] + [20000])])
+def test_decode_one_long_sequence(dtype, B, lens):
+    """One sequence cut over most of the grid: hundreds of partial results a row."""
+    c = ref.Cache(dtype, B, 2, 64, 128, 157, lens, seed=86, extra=0)
+    check_decode(c, c.cuda(), randn(B, 6, 1, 64, seed=87))
+
+
+def test_decode_mostly_idle_batch():
+    """A padded batch: slots without queries, some of them without rows, between the
+    others and at both ends; their outputs are left as they were."""
+    g = torch.Generator().manual_seed(88)
+    lens = torch.randint(0, 200, (400,), generator=g).tolist()
+    q_lens = [min(2, n) if i % 7 == 3 else 0 for i, n in enumerate(lens)]
+    c = ref.Cache(E4M3, 400, 1, 64, 16, 13, lens, seed=89)
+    check_decode(c, c.cuda(), randn(400, 2, 2, 64, seed=90), q_lens)
+    check_decode(c, c.cuda(), randn(400, 2, 2, 64, seed=90), [0] * 400)
+
+
+def test_workspace_of_other_shapes_and_captured_without_one():
+    """One workspace, sized for the largest call, serves calls of every shape in
+    turn; and a call without one can be captured."""
+    c = ref.Cache(E4M3, 2, 2, 128, 32, 8, [200, 131], seed=91)
+    dev = c.cuda()
+    ws = dfa.paged_workspace(dev, 8, 4)
+    for T in (4, 1, 3, 1):
+        q = randn(2, 8, T, 128, seed=92 + T)
+        o, lse = dfa.decode_paged(dev, q.cuda(), ws=ws)
+        dfa.cache_gather(dev, 7, ws=ws)
+        dfa.stream_status(ws)
+        O, LSE, tO, tL = ref.attention(c, q)
+        ref.check(o, O, tO, BF16)
+        ref.check(lse, LSE, tL, torch.float32)
+    g, qg = torch.cuda.CUDAGraph(), q.cuda()
+    with torch.cuda.graph(g):
+        o, lse = dfa.decode_paged(dev, qg)
+        r = dfa.rope(qg, dfa.rope_spec(128, layout="half"))
+        k, v = dfa.cache_gather(dev, 200)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    ref.check(o, O, tO, BF16)
+    check_rope(r, q, torch.arange(1), "half", 128, False, {})
+    assert torch.equal(k[0].cpu().double(), c.rows("k", 0, 200))
+
+
+def test_binding_refuses_on_the_gpu():
+    """What only tensors on the device can show."""
+    c = ref.Cache(E4M3, 2, 2, 64, 16, 2, [5, 17], seed=93)
+    dev = c.cuda()
+    x = randn(2, 2, 3, 64, seed=94).cuda()
+    spec = dfa.rope_spec(64)
+    pos = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: dfa.rope(x.half(), spec), lambda: dfa.rope(x[0], spec),
+        lambda: dfa.rope(x, spec, positions=pos.long()),
+        lambda: dfa.rope(x, spec, positions=pos[:, :2]),
+        lambda: dfa.rope(x, spec, positions=pos, pos_map=dfa.pos_map(1, (3, 0))),
+        lambda: dfa.rope(x.transpose(2, 3), spec), lambda: dfa.rope(x, spec, out=x[:1]),
+        lambda: dfa.rope(x, spec, out=x.float()),
+        lambda: dfa.cache_append(dev, x.float(), x), lambda: dfa.cache_append(dev, x, x[:1]),
+        lambda: dfa.cache_append(dev, x, x, q_out=x),
+        lambda: dfa.cache_append(dev, x, x, new_lens=torch.ones(2, device="cuda")),
+        lambda: dfa.cache_append(dev, x, x, ws=torch.zeros(256, device="cuda")),
+        lambda: dfa.cache_gather(dev, 4, k_out=x), lambda: dfa.decode_paged(dev, x[0]),
+        lambda: dfa.decode_paged(dev, x[:1]), lambda: dfa.decode_paged(dev, x.float()),
+        lambda: dfa.decode_paged(dev, x, out=x.float()),
+        lambda: dfa.decode_paged(dev, x, lse=torch.zeros(2, 2, 2, device="cuda")),
+        lambda: dfa.decode_paged(dev, x, q_lens=torch.ones(3, dtype=torch.int32, device="cuda")),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: dfa.rope(x, spec, out=x.as_strided((2, 2, 3, 64), (384, 0, 64, 1))),
+              lambda: dfa.decode_paged(dev, x[:, :1]),                # 1 head over 2
+              lambda: dfa.decode_paged(dev, x, ws=torch.zeros(256, dtype=torch.uint8,
+                                                              device="cuda")),
+              lambda: dfa.cache_append(dev, x, x, q=x, q_out=torch.empty_like(x))):
+        with pytest.raises(dfa.DfaError):
+            f()
+
+
 def test_shared_pages_are_read_by_both():
     """Two sequences with a common prefix in the same pages."""
     c = ref.Cache(E4M3, 2, 1, 64, 16, 4, [50, 50], seed=69)
