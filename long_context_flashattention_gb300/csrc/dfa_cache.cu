@@ -24,32 +24,37 @@ namespace {
 
 constexpr int kBatch = 2;     // rows of an item in flight per lane
 
-// codes of x / s.  An infinity (which the conversion would store as the largest
-// finite cell) becomes NaN like a NaN; `inf`: there may be one.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv, bool inf)
+// codes of x / s; a NaN stays one
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
 {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y[i] = inf && fabsf(x[i]) == INFINITY ? NAN : x[i] * inv;
-    return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+    return make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                      e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
-// Largest |x|, NaN left out (fmaxf does); `finite`: infinities too.
-__device__ __forceinline__ float abs_max8(float m, const float (&x)[8], bool finite)
+// Infinities become NaN (the conversion would store them as the largest finite
+// cell).
+__device__ __forceinline__ void no_infinities(float (&x)[8])
 {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float u = fabsf(x[i]), v = fabsf(x[i + 1]);
-        m = fmaxf(m, fmaxf(finite && u == INFINITY ? 0.f : u, finite && v == INFINITY ? 0.f : v));
-    }
+    for (int i = 0; i < 8; ++i)
+        if (fabsf(x[i]) == INFINITY)
+            x[i] = NAN;
+}
+
+// Largest |x|, NaN left out (fmaxf does)
+__device__ __forceinline__ float abs_max8(float m, const float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
     return m;
 }
 
 // Row items of a block.  Rows of a token: Hq queries, then (bf16 cache) Hkv keys
 // and Hkv values.
 template <bool F8, int D>
-__device__ __forceinline__ void row_items(const AppendParams& p, uint32_t item, uint32_t stride)
+__device__ __forceinline__ void row_items(const AppendParams& p, const uint64_t* turns,
+                                          uint32_t item, uint32_t stride)
 {
     constexpr int UNITS = D / 16, kStep = 32 / UNITS;
     const int lane = threadIdx.x & 31;
@@ -58,7 +63,7 @@ __device__ __forceinline__ void row_items(const AppendParams& p, uint32_t item, 
     const uint32_t per_token = (rows + p.item_heads - 1) / p.item_heads;
     int f0, f1;
     const bool turned = unit_runs<8>(p.t, D, u, f0, f1);
-    const WarpAngles<8, UNITS> angles(p.t);
+    const WarpAngles<8, UNITS> angles(p.t, turns);
     for (; item < p.items; item += stride) {
         const uint32_t token = item / per_token;
         const int32_t h0 = (int32_t)(item - token * per_token) * p.item_heads;
@@ -137,28 +142,27 @@ __device__ __forceinline__ void group_sync(int group, int threads)
 // Largest value of the group; `set` alternates between two sets of smem words,
 // so that one barrier is enough.
 __device__ __forceinline__ float group_max(float m, int group, int thread, int threads,
-                                           float (*words)[32], int& set)
+                                           uint32_t (*words)[32], int& set)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // (the bits of floats that are not negative are ordered as they are)
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     if (threads > 32) {
         set ^= 16;
-        float* w = words[set + group];
+        uint32_t* w = words[set + group];
         if ((thread & 31) == 0)
-            w[thread >> 5] = m;
+            w[thread >> 5] = bits;
         group_sync(group, threads);
-        for (int i = 0; i < threads / 32; ++i)
-            m = fmaxf(m, w[i]);
+        const int lane = thread & 31;
+        bits = __reduce_max_sync(0xffffffffu, lane < threads / 32 ? w[lane] : 0u);
     }
-    return m;
+    return __uint_as_float(bits);
 }
 
 // One page job: K or V rows of one page, job_heads heads.  Every thread of the
 // group takes the same way through it.
 template <int D>
 __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, int group,
-                                         int thread, const uint64_t* turn, float (*words)[32],
+                                         int thread, const uint64_t* turns, uint32_t (*words)[32],
                                          int& set)
 {
     constexpr int UNITS = D / 16;
@@ -207,14 +211,14 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
         if (h == h0 && turned && mine)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                pair_angle(turn[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[j], sn[j]);
+                pair_angle(turns[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[j], sn[j]);
         float a[8], c[8], amax = 0.f;
         if (mine) {
             r0.get(a);
             r1.get(c);
             if (turned)
                 unit_rotate<8>(p.t, cs, sn, a, c);
-            amax = abs_max8(abs_max8(0.f, a, false), c, false);
+            amax = abs_max8(abs_max8(0.f, a), c);
             x += src.sh;
             if (h + 1 < h1) {  // the next head's rows, ahead of the barrier
                 r0.load(x + f0);
@@ -222,10 +226,13 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
             }
         }
         amax = group_max(amax, group, thread, threads, words, set);
-        const bool inf = amax == INFINITY;  // once more, over finite values
-        if (inf) {
-            amax = mine ? abs_max8(abs_max8(0.f, a, true), c, true) : 0.f;
-            amax = group_max(amax, group, thread, threads, words, set);
+        if (amax == INFINITY) {  // (rare) once more, over finite values
+            if (mine) {
+                no_infinities(a);
+                no_infinities(c);
+            }
+            amax = group_max(mine ? abs_max8(abs_max8(0.f, a), c) : 0.f, group, thread, threads,
+                             words, set);
         }
         const float s = fmaxf(old, pow2_scale(amax));
         const float inv = 1.f / s;  // exact: a power of two (or a scale of the caller's)
@@ -256,8 +263,8 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
         }
         if (mine) {
             uint8_t* cell = cells + (row - start) * D;
-            *reinterpret_cast<uint2*>(cell + f0) = codes8(a, inv, inf);
-            *reinterpret_cast<uint2*>(cell + f1) = codes8(c, inv, inf);
+            *reinterpret_cast<uint2*>(cell + f0) = codes8(a, inv);
+            *reinterpret_cast<uint2*>(cell + f1) = codes8(c, inv);
         }
     }
 }
@@ -266,22 +273,22 @@ template <bool F8, int D>
 __global__ void __launch_bounds__(F8 ? 1024 : 256, F8 ? 1 : 3)
     cache_append_kernel(const __grid_constant__ AppendParams p)
 {
+    __shared__ uint64_t turns[64];  // lanes read different entries: not from the parameters
+    if (threadIdx.x < 64)
+        turns[threadIdx.x] = p.t.turn[threadIdx.x];
+    __syncthreads();
     if (F8 && (int32_t)blockIdx.x < p.job_blocks) {
-        __shared__ float words[32][32];
-        __shared__ uint64_t turn[64];  // lanes read different entries: not from the parameters
-        if (threadIdx.x < 64)
-            turn[threadIdx.x] = p.t.turn[threadIdx.x];
-        __syncthreads();
+        __shared__ uint32_t words[32][32];
         const int groups = blockDim.x / p.job_threads;
         const int group = threadIdx.x / p.job_threads;
         int set = 0;
         for (uint32_t job = blockIdx.x * groups + group; job < p.jobs;
              job += p.job_blocks * groups)
-            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turn, words, set);
+            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turns, words, set);
         return;
     }
     const int warps = blockDim.x >> 5;
-    row_items<F8, D>(p, (blockIdx.x - p.job_blocks) * warps + (threadIdx.x >> 5),
+    row_items<F8, D>(p, turns, (blockIdx.x - p.job_blocks) * warps + (threadIdx.x >> 5),
                      (gridDim.x - p.job_blocks) * warps);
 }
 

@@ -13,11 +13,14 @@ namespace dfa {
 
 namespace {
 
-constexpr int kBatch = 4;  // rows in flight per lane
+// Rows in flight per lane.  Measured (bf16 32 heads x 32768 x 128, fp32 2 x 8 x
+// 16381 x 128, us; blocks an SM by registers): 4 rows and 3 blocks 84.4, 42.8;
+// 4 and 2 82.1, 45.1; 2 and 4 87.6, 43.8.
+constexpr int kBatch = 4;
 
 // One warp per item = (batch, token, `heads` heads); lane = (head, unit).
 template <typename E, int D>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, sizeof(E) == 2 ? 2 : 3)
     rope_rows_kernel(const __grid_constant__ RopeRowsParams p, uint32_t items, uint32_t head_items)
 {
     constexpr int V = Run<E>::V, UNITS = D / (2 * V), kStep = 32 / UNITS;
@@ -27,7 +30,11 @@ __global__ void __launch_bounds__(256, 3)
     const bool turned = unit_runs<V>(p.t, D, u, f0, f1);
     // features that pass through are already there when the call works in place
     const bool move = turned || p.x.p != p.out.p;
-    const WarpAngles<V, UNITS> angles(p.t);
+    __shared__ uint64_t turns[64];
+    if (threadIdx.x < 64)
+        turns[threadIdx.x] = p.t.turn[threadIdx.x];
+    __syncthreads();
+    const WarpAngles<V, UNITS> angles(p.t, turns);
     for (uint32_t it = blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += gridDim.x * 8) {
         const uint32_t row = it / head_items;
         const int32_t h0 = (int32_t)(it - row * head_items) * p.heads;

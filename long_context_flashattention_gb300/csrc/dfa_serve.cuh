@@ -109,13 +109,15 @@ struct WarpAngles {
     uint64_t turn[kOwn];  // this lane's pairs
     float gain;
 
-    __device__ __forceinline__ explicit WarpAngles(const RopeTable& t) : gain(t.gain)
+    // turns: the table's, in shared memory (the lanes read different entries)
+    __device__ __forceinline__ WarpAngles(const RopeTable& t, const uint64_t* turns)
+        : gain(t.gain)
     {
         const int lane = threadIdx.x & 31, u = lane & (UNITS - 1);
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             const int pair = unit_pair<V>(t, u, lane / UNITS * kOwn + i);
-            turn[i] = u < t.half / V ? t.turn[pair] : 0;
+            turn[i] = u < t.half / V ? turns[pair] : 0;
         }
     }
     __device__ __forceinline__ void at(int32_t pos, float sign, float (&cs)[V],
