@@ -174,8 +174,23 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
     i /= (uint32_t)p.pages;
     const int32_t is_v = i >= head_jobs;
     const int32_t h0 = (i - is_v * head_jobs) * p.job_heads;
+    // One look at the lengths for the whole group, whose barriers everyone has to
+    // reach.
+    const int threads = p.job_threads;
     int32_t len, n;
-    seq_rows(p.c, p.new_lens, p.T, b, len, n);
+    if (thread < 32)
+        seq_rows(p.c, p.new_lens, p.T, b, len, n);
+    if (threads > 32) {
+        set ^= 16;
+        uint32_t* w = words[set + group];
+        if (thread == 0) {
+            w[0] = len;
+            w[1] = n;
+        }
+        group_sync(group, threads);
+        len = w[0];
+        n = w[1];
+    }
     const int32_t first = len - n;                          // first new row
     const int32_t pg = (first >> p.c.page_log2) + ip;       // page of the sequence
     const int32_t start = pg << p.c.page_log2;
@@ -183,8 +198,7 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
     const int32_t hi = min(len, start + p.c.page);
     if (lo >= hi)
         return;
-    const int32_t id = page_entry(p.c, b, pg);
-    const int threads = p.job_threads;
+    int32_t id = page_entry(p.c, b, pg);
     const Rows& src = is_v ? p.v : p.k;
     const int32_t there = lo - start;        // rows of the page stored before
     const int32_t u = thread & (UNITS - 1);  // threads is a multiple of UNITS
@@ -201,13 +215,14 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
         r0.load(x + f0);
         r1.load(x + f1);
     }
-    if (!is_page(p.c, b, id))
-        return;
+    const bool stores = is_page(p.c, b, id);  // if not, on to the barriers all the same
+    if (!stores)
+        id = 0;
     float* scales = (is_v ? p.c.v_scale : p.c.k_scale) + (int64_t)id * p.c.Hkv;
     uint8_t* cells = (uint8_t*)(is_v ? p.c.v : p.c.k) + (int64_t)id * p.c.page_stride +
                      ((int64_t)h0 << p.c.page_log2) * D;
     for (int32_t h = h0; h < h1; ++h, cells += p.c.page * D) {
-        const float old = there > 0 ? scales[h] : 0.f;
+        const float old = there > 0 && stores ? scales[h] : 0.f;
         if (h == h0 && turned && mine)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -236,7 +251,7 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
         }
         const float s = fmaxf(old, pow2_scale(amax));
         const float inv = 1.f / s;  // exact: a power of two (or a scale of the caller's)
-        if (s != old) {
+        if (s != old && stores) {
             if (there > 0) {
                 // raise the rows that are there to the new scale: exact but for
                 // cells that become subnormal
@@ -261,7 +276,7 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
             if (thread == 0)
                 scales[h] = s;
         }
-        if (mine) {
+        if (mine && stores) {
             uint8_t* cell = cells + (row - start) * D;
             *reinterpret_cast<uint2*>(cell + f0) = codes8(a, inv);
             *reinterpret_cast<uint2*>(cell + f1) = codes8(c, inv);

@@ -72,9 +72,19 @@ struct Cfg {
     static constexpr int kSteps = D / 16;                    // products over the features
 };
 
+// A run of tiles [tile0, tile0 + nt) of one segment: key/value head h, row group
+// rg of sequence b, which has len rows, n queries and that many tiles.
+struct Piece {
+    int32_t b, h, rg, len, n;
+    int32_t tile0, nt, tiles;
+    long long w;      // the segment's first unit on the line
+};
+
 struct Shared {
     uint64_t full[8], empty[8];   // tiles
     uint64_t q_full[2], q_empty[2];
+    uint64_t meet;                // of the consumer warps
+    Piece run[2];                   // of the segments whose queries are there
     float4 scale[8][4];           // per stage and page: see page_scale
     // maxima and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
@@ -86,6 +96,18 @@ struct Shared {
     int32_t b;
     uint32_t abort;
 };
+
+// A barrier of the consumer warps whose wait is bounded like the others; false:
+// the block is giving up.
+__device__ __forceinline__ bool meet(Shared& sh, uint32_t& phase, const WaitCtx& wctx)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(&sh.meet);
+    const bool ok = mbar_wait(&sh.meet, phase, wctx, 62);
+    phase ^= 1;
+    return __all_sync(0xffffffffu, ok);
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2, int c3)
@@ -113,11 +135,6 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
                  "r"(bytes)
                  : "memory");
-}
-
-__device__ __forceinline__ void consumer_sync()
-{
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
 
 // D (16x8, fp32) += A (16x16) B (16x8), fp16 or bf16 operands
@@ -217,19 +234,19 @@ __device__ __forceinline__ long long divide(long long a, int32_t b)
 __device__ __forceinline__ int block_of(const Shared& sh, long long unit)
 {
     const long long longer = sh.rest * (sh.each + 1);
-    return (int)(unit < longer ? unit / (sh.each + 1) : sh.rest + (unit - longer) / sh.each);
+    const long long c = unit < longer ? unit / (sh.each + 1) : sh.rest + (unit - longer) / sh.each;
+    return (int)min(c, (long long)gridDim.x - 1);
 }
 
 // The line that is cut: every segment takes p.segment_cost units (its queries, the join
 // and the rows' output cost a block about that many tiles' time), then one unit
 // per tile.  A cut inside the former puts the whole segment behind it.
 //
-// A run of tiles [tile0, tile0 + nt) of one segment of the block's range.
-struct Walk {
-    long long w, w1;  // next unit and end of the range
-    int32_t b, len, n, tiles;
-    int32_t h, rg;    // key/value head, row group
-    int32_t tile0, nt;
+// The producer's way along the block's range.  (Lengths that change while the
+// kernel runs give results without meaning, but nothing worse: only this one
+// warp goes by them, and every index that comes of them is checked.)
+struct Walk : Piece {
+    long long w1;     // end of the range
     bool fresh;       // tile0 is where the range begins
 
     __device__ __forceinline__ void start(const PagedParams& p, const Shared& sh)
@@ -243,11 +260,13 @@ struct Walk {
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
         tiles = tiles_of(len, n);
         const long long at = w - sh.base, unit = tiles + p.segment_cost;
-        const long long hr = divide(at, (int32_t)unit);
+        const long long hr =
+            min(divide(at, (int32_t)unit), (long long)p.c.Hkv * p.row_groups - 1);
         h = (int32_t)(hr / p.row_groups);
         rg = (int32_t)(hr - (long long)h * p.row_groups);
-        tile0 = max(0, (int32_t)(at - hr * unit) - p.segment_cost);
-        w -= at - hr * unit;  // the segment's first unit
+        const int32_t within = (int32_t)min(at - hr * unit, unit - 1);
+        tile0 = max(0, within - p.segment_cost);
+        w -= within;  // the segment's first unit
     }
     __device__ __forceinline__ bool next(const PagedParams& p)
     {
@@ -261,7 +280,8 @@ struct Walk {
                 if (++h == p.c.Hkv) {
                     h = 0;
                     do {
-                        ++b;
+                        if (++b >= p.c.B)
+                            return false;
                         seq_rows(p.c, p.q_lens, p.T, b, len, n);
                         tiles = tiles_of(len, n);
                     } while (tiles == 0);
@@ -281,6 +301,10 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
 {
     const int32_t per_seq = p.c.Hkv * p.row_groups;
     const int32_t chunk = ceil_div(p.c.B, kThreads);
+    if (threadIdx.x == 0) {
+        sh.b = 0;
+        sh.base = 0;
+    }
     const int32_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, p.c.B);
     long long sum = 0;
     for (int32_t b = b0; b < b1; ++b) {
@@ -393,18 +417,18 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
         check_window();
         auto fetch_queries = [&] {
             const uint32_t qb = seg & 1;
-            if (seg >= 2) {
-                const bool ok = mbar_wait(&sh.q_empty[qb], (seg / 2 - 1) & 1, wctx, 51);
-                if (!__all_sync(0xffffffffu, ok))
-                    return false;
-            }
+            const bool ok = mbar_wait(&sh.q_empty[qb], (seg / 2 + 1) & 1, wctx, 51);
+            if (!__all_sync(0xffffffffu, ok))
+                return false;
             const int32_t r = wk.rg * C::kRows + lane;
             int32_t gh, tq;
             split_row(p, r, gh, tq);
             const bool there = lane < C::kRows && r < p.G * p.T && tq < wk.n;
             const uint32_t rows = __popc(__ballot_sync(0xffffffffu, there));
-            if (lane == 0)
+            if (lane == 0) {
+                sh.run[qb] = wk;
                 mbar_expect(&sh.q_full[qb], rows * (D * 2));
+            }
             __syncwarp();
             if (there)
                 bulk_load_u32(q_rows + qb * C::kQRows + lane * (D * 2),
@@ -469,6 +493,12 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
         }
         wk = nx;
         more = more_next;
+    }
+    // no more runs
+    const bool ok = mbar_wait(&sh.q_empty[seg & 1], (seg / 2 + 1) & 1, wctx, 52);
+    if (__all_sync(0xffffffffu, ok) && lane == 0) {
+        sh.run[seg & 1].nt = 0;
+        mbar_arrive(&sh.q_full[seg & 1]);
     }
 }
 
@@ -588,7 +618,7 @@ __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float s
                                               uint32_t (&q)[D / 16][2])
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if (!F8) {
+    if constexpr (!F8) {
 #pragma unroll
         for (int s = 0; s < D / 16; s += 2) {
             // chunks 2s .. 2s+3 of the rows
@@ -598,31 +628,32 @@ __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float s
             q[s + 1][0] = there ? r[2] : 0u, q[s + 1][1] = there ? r[3] : 0u;
         }
         return scale_log2;
+    } else {
+#pragma unroll
+        for (int s = 0; s < D / 16; s += 2) {
+            uint4 x = lds128(rows + g * (D * 2) + t * (D / 2) + s * 8);
+            if (!there)
+                x = make_uint4(0, 0, 0, 0);
+            q[s][0] = x.x, q[s][1] = x.y;
+            q[s + 1][0] = x.z, q[s + 1][1] = x.w;
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[s][k])), fabsf(bf16hi(q[s][k]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                q[s][k] = pack_half2(bf16lo(q[s][k]) * inv, bf16hi(q[s][k]) * inv);
+        return scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
     }
-#pragma unroll
-    for (int s = 0; s < D / 16; s += 2) {
-        uint4 x = lds128(rows + g * (D * 2) + t * (D / 2) + s * 8);
-        if (!there)
-            x = make_uint4(0, 0, 0, 0);
-        q[s][0] = x.x, q[s][1] = x.y;
-        q[s + 1][0] = x.z, q[s + 1][1] = x.w;
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[s][k])), fabsf(bf16hi(q[s][k]))));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            q[s][k] = pack_half2(bf16lo(q[s][k]) * inv, bf16hi(q[s][k]) * inv);
-    return scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // Features f..f+3 of an output row, and its LSE: o and L are relative to 2^mx
@@ -656,13 +687,16 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
     const int32_t page = p.c.page;
     const int sc_at = page < kTile ? warp * 16 / page : 0;
     const int32_t R = p.G * p.T;
-    uint32_t st = 0, phase = 0, seg = 0;
+    uint32_t st = 0, phase = 0, met = 0;
     int par = 0;
-    bool dead = false;  // a wait gave up: keep the barriers' count, compute nothing
     int4 info = make_int4(0, 0, 0, 0);
-    Walk wk;
-    wk.start(p, sh);
-    for (; wk.next(p); ++seg) {
+    for (uint32_t seg = 0;; ++seg) {
+        bool ok = mbar_wait(&sh.q_full[seg & 1], (seg / 2) & 1, wctx, 61);
+        if (!__all_sync(0xffffffffu, ok))
+            return;
+        const Piece wk = sh.run[seg & 1];
+        if (wk.nt == 0)
+            break;
         const int32_t h = wk.h, r0 = wk.rg * C::kRows;
         const int32_t len = wk.len, n = wk.n;
         // ---- queries: rows g of each block of 8, this lane's features
@@ -670,10 +704,6 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         uint64_t rf[NB];           // score factors of rows 2t, 2t+1
         int32_t lim[NB][2];        // last visible key of rows 2t, 2t+1
         int32_t tok[NB][2];
-        if (!dead) {
-            const bool ok = mbar_wait(&sh.q_full[seg & 1], (seg / 2) & 1, wctx, 61);
-            dead = !__all_sync(0xffffffffu, ok);
-        }
         if (NB == 1 || warp < NB) {
             const int nb = NB == 1 ? 0 : warp;
             int32_t gh, tq;
@@ -695,8 +725,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.q_empty[seg & 1]);
-        if (NB > 1)
-            consumer_sync();
+        if (NB > 1 && !meet(sh, met, wctx))
+            return;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             if (NB > 1)
@@ -728,13 +758,12 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         }
         // ---- the run's tiles
         for (int32_t i = 0; i < wk.nt; ++i) {
-            if (!dead) {
-                const bool ok = mbar_wait(&sh.full[st], phase, wctx, 60);
-                dead = !__all_sync(0xffffffffu, ok);
-            }
+            ok = mbar_wait(&sh.full[st], phase, wctx, 60);
+            if (!__all_sync(0xffffffffu, ok))
+                return;
             const int32_t base = (wk.tile0 + i) * kTile + warp * 16;  // the warp's 16 keys
             const float4 sc = sh.scale[st][sc_at];
-            if (!dead && base < len && sc.x != kNoPage) {
+            if (base < len && sc.x != kNoPage) {
                 const uint32_t kt = ring + st * C::kStage;
                 const uint32_t vt = kt + C::kOperand;
                 const uint32_t row = warp * 16;
@@ -931,7 +960,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     sh.l[par][warp][nb * 8 + 2 * t + k] = l[nb][k];
                 }
             }
-        consumer_sync();
+        if (!meet(sh, met, wctx))
+            return;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -958,7 +988,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     }
                 }
             }
-        consumer_sync();
+        if (!meet(sh, met, wctx))
+            return;
         // ---- rows of the segment: D/4 threads each
         constexpr int kPerRow = D / 4;
         const bool whole = wk.nt == wk.tiles;
@@ -1026,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
             mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.q_empty[s], kWarps);
         }
+        mbar_init(&sh.meet, kWarps);
         fence_barrier_init();
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
