@@ -63,7 +63,7 @@ __device__ __forceinline__ void row_items(const AppendParams& p, const uint64_t*
     const uint32_t per_token = (rows + p.item_heads - 1) / p.item_heads;
     int f0, f1;
     const bool turned = unit_runs<8>(p.t, D, u, f0, f1);
-    const WarpAngles<8, UNITS> angles(p.t, turns);
+    const SharedAngles<8, UNITS, kStep> angles(p.t, turns);
     for (; item < p.items; item += stride) {
         const uint32_t token = item / per_token;
         const int32_t h0 = (int32_t)(item - token * per_token) * p.item_heads;

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256, sizeof(E) == 2 ? 2 : 3)
     if (threadIdx.x < 64)
         turns[threadIdx.x] = p.t.turn[threadIdx.x];
     __syncthreads();
-    const WarpAngles<V, UNITS> angles(p.t, turns);
+    const SharedAngles<V, UNITS, kStep> angles(p.t, turns);
     for (uint32_t it = blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += gridDim.x * 8) {
         const uint32_t row = it / head_items;
         const int32_t h0 = (int32_t)(it - row * head_items) * p.heads;
@@ -77,34 +77,90 @@ __global__ void __launch_bounds__(256, sizeof(E) == 2 ? 2 : 3)
 }
 
 template <typename E>
-void launch(const RopeRowsParams& p, int blocks, uint32_t items, uint32_t head_items,
-            cudaStream_t stream)
+struct RopeRows {
+    const RopeRowsParams& p;
+    struct Token {
+        uint32_t b, l;
+        int32_t pos;
+        bool ok;
+    };
+    __device__ __forceinline__ Token token(uint32_t i) const
+    {
+        const uint32_t b = i / (uint32_t)p.L, l = i - b * (uint32_t)p.L;
+        return {b, l, p.positions ? __ldg(p.positions + i) : map_pos(p.map, (int32_t)l), true};
+    }
+    __device__ __forceinline__ const E* from(const Token& k, int32_t h) const
+    {
+        return (const E*)p.x.p + k.b * p.x.sb + k.l * p.x.sl + h * p.x.sh;
+    }
+    __device__ __forceinline__ E* to(const Token& k, int32_t h) const
+    {
+        return (E*)p.out.p + k.b * p.out.sb + k.l * p.out.sl + h * p.out.sh;
+    }
+    __device__ __forceinline__ bool turns(int32_t) const { return true; }
+};
+
+// Few heads: the lanes that heads do not take go to other tokens.  Measured (bf16,
+// d 128, 2^20 rows of 1, 2, 4, 8 heads, us): 140, 100, 89, 86, where a warp a
+// token takes 515, 272, 146, 101.  Two rows a lane and 4 blocks an SM; 2 and 3: 129,
+// 101, 98, 95; 2 and 5 (spills): 168, 123, 113, 111; 4 and 2: 160, 129, 112, 106.
+// One head is bound by its own angles, 64 sincospif a row.
+constexpr int kFewBatch = 2;
+
+template <typename E, int D, int G>
+__global__ void __launch_bounds__(256, 4)
+    rope_few_kernel(const __grid_constant__ RopeRowsParams p, uint32_t tokens)
 {
-    if (p.d == 128)
-        rope_rows_kernel<E, 128><<<blocks, 256, 0, stream>>>(p, items, head_items);
-    else
-        rope_rows_kernel<E, 64><<<blocks, 256, 0, stream>>>(p, items, head_items);
+    __shared__ uint64_t turns[64];
+    if (threadIdx.x < 64)
+        turns[threadIdx.x] = p.t.turn[threadIdx.x];
+    __syncthreads();
+    few_heads<E, D, G, kFewBatch>(p.t, turns, RopeRows<E>{p}, p.H, tokens,
+                                  p.inverse ? -1.f : 1.f, blockIdx.x * 8 + (threadIdx.x >> 5),
+                                  gridDim.x * 8);
 }
 
-}  // namespace
-
-// Heads per warp: a warp computes its token's angles once for all of them, but
-// short inputs need the warps.  (B * H * L is below 2^31.)
-cudaError_t launch_rope_rows(RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream)
+template <typename E, int D>
+cudaError_t launch(RopeRowsParams& p, int num_sms, cudaStream_t stream)
 {
-    const int step = 32 / (p.d / (fp32 ? 8 : 16));
+    constexpr int kStep = 32 / (D / (2 * Run<E>::V));
     const uint32_t rows = (uint32_t)(p.B * p.L);
-    p.heads = 4 * kBatch * step;
-    while (p.heads > step && rows * ((p.H + p.heads - 1) / p.heads) < num_sms * 32u)
+    if (p.H <= 2 * kStep) {
+        const int g = few_heads_group(p.H, kStep);
+        const uint32_t each = (p.H > g ? kFewBatch / 2 : kFewBatch) * (kStep / g);
+        const int blocks = (int)min((rows + 8 * each - 1) / (8 * each), num_sms * 8u);
+        if (g == 1)
+            rope_few_kernel<E, D, 1><<<blocks, 256, 0, stream>>>(p, rows);
+        else if (g == 2)
+            rope_few_kernel<E, D, kStep < 2 ? 1 : 2><<<blocks, 256, 0, stream>>>(p, rows);
+        else if (g == 4)
+            rope_few_kernel<E, D, kStep < 4 ? 1 : 4><<<blocks, 256, 0, stream>>>(p, rows);
+        else
+            rope_few_kernel<E, D, kStep < 8 ? 1 : 8><<<blocks, 256, 0, stream>>>(p, rows);
+        return cudaGetLastError();
+    }
+    // Heads per warp: a warp computes its token's angles once for all of them, but
+    // short inputs need the warps.
+    p.heads = 4 * kBatch * kStep;
+    while (p.heads > kStep && rows * ((p.H + p.heads - 1) / p.heads) < num_sms * 32u)
         p.heads /= 2;
     const uint32_t head_items = (p.H + p.heads - 1) / p.heads;
     const uint32_t items = rows * head_items;
     const int blocks = (int)min((items + 7) / 8, num_sms * 8u);
-    if (fp32)
-        launch<float>(p, blocks, items, head_items, stream);
-    else
-        launch<__nv_bfloat16>(p, blocks, items, head_items, stream);
+    rope_rows_kernel<E, D><<<blocks, 256, 0, stream>>>(p, items, head_items);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+// (B * H * L is below 2^31.)
+cudaError_t launch_rope_rows(RopeRowsParams& p, int fp32, int num_sms, cudaStream_t stream)
+{
+    if (fp32)
+        return p.d == 128 ? launch<float, 128>(p, num_sms, stream)
+                          : launch<float, 64>(p, num_sms, stream);
+    return p.d == 128 ? launch<__nv_bfloat16, 128>(p, num_sms, stream)
+                      : launch<__nv_bfloat16, 64>(p, num_sms, stream);
 }
 
 }  // namespace dfa

@@ -100,38 +100,39 @@ __device__ __forceinline__ void pair_angle(uint64_t turn, float gain, int32_t po
     sn *= gain * sign;
 }
 
-// cos and sin of the unit's pairs where the whole warp is at one position, lane =
-// head * UNITS + unit: the 32 / UNITS lanes of a unit compute some pairs each
-// and pass them around.
-template <int V, int UNITS>
-struct WarpAngles {
-    static constexpr int kOwn = V * UNITS / 32;
+// cos and sin of a unit's pairs where G * UNITS lanes are at one position, lane =
+// (token * G + head) * UNITS + unit: the G lanes of a unit compute V / G pairs
+// each and pass them around.
+template <int V, int UNITS, int G>
+struct SharedAngles {
+    static constexpr int kOwn = V / G;
     uint64_t turn[kOwn];  // this lane's pairs
     float gain;
 
     // turns: the table's, in shared memory (the lanes read different entries)
-    __device__ __forceinline__ WarpAngles(const RopeTable& t, const uint64_t* turns)
+    __device__ __forceinline__ SharedAngles(const RopeTable& t, const uint64_t* turns)
         : gain(t.gain)
     {
         const int lane = threadIdx.x & 31, u = lane & (UNITS - 1);
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
-            const int pair = unit_pair<V>(t, u, lane / UNITS * kOwn + i);
+            const int pair = unit_pair<V>(t, u, lane / UNITS % G * kOwn + i);
             turn[i] = u < t.half / V ? turns[pair] : 0;
         }
     }
     __device__ __forceinline__ void at(int32_t pos, float sign, float (&cs)[V],
                                        float (&sn)[V]) const
     {
-        const int u = threadIdx.x & (UNITS - 1);
+        const int lane = threadIdx.x & 31;
+        const int first = lane & ~(G * UNITS - 1), u = lane & (UNITS - 1);
         float c[kOwn], s[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; ++i)
             pair_angle(turn[i], gain, pos, sign, c[i], s[i]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            cs[i] = __shfl_sync(0xffffffffu, c[i % kOwn], (i / kOwn) * UNITS + u);
-            sn[i] = __shfl_sync(0xffffffffu, s[i % kOwn], (i / kOwn) * UNITS + u);
+            cs[i] = __shfl_sync(0xffffffffu, c[i % kOwn], first + (i / kOwn) * UNITS + u);
+            sn[i] = __shfl_sync(0xffffffffu, s[i % kOwn], first + (i / kOwn) * UNITS + u);
         }
     }
 };
@@ -202,6 +203,72 @@ struct Run<float> {
         x = make_float4(f[0], f[1], f[2], f[3]);
     }
 };
+
+// Rows of tokens with few heads: lane = (token, head of G, unit), H <= G or, where
+// the G heads take the whole warp, H <= 2 G.  A warp has BATCH rows a lane in
+// flight, of as many tokens as that takes.  Rows: token(i) -> what is known
+// of a token (pos; ok: there is such a row to move), from(token, h), to(token, h)
+// (NULL: nowhere) and turns(h).
+template <typename E, int D, int G, int BATCH, typename Rows>
+__device__ __forceinline__ void few_heads(const RopeTable& t, const uint64_t* turns,
+                                          const Rows& rows, int32_t H, uint32_t tokens, float sign,
+                                          uint32_t warp, uint32_t warps)
+{
+    constexpr int V = Run<E>::V, UNITS = D / (2 * V), kTokens = 32 / UNITS / G;
+    const int lane = threadIdx.x & 31, u = lane & (UNITS - 1);
+    const int32_t h = lane / UNITS % G;
+    const uint32_t mine = lane / UNITS / G;  // token of the kTokens at a time
+    const int twice = H > G ? 1 : 0;         // two heads of a token a lane
+    const uint32_t each = (BATCH >> twice) * kTokens;
+    int f0, f1;
+    const bool turned = unit_runs<V>(t, D, u, f0, f1);
+    const SharedAngles<V, UNITS, G> angles(t, turns);
+    for (uint32_t first = warp * each; first < tokens; first += warps * each) {
+        typename Rows::Token tok[BATCH];
+        Run<E> r[BATCH][2];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const uint32_t i = first + (k >> twice) * kTokens + mine;
+            const int32_t hk = h + (k & twice) * G;
+            tok[k] = rows.token(min(i, tokens - 1));
+            tok[k].ok = tok[k].ok && i < tokens && hk < H;
+            if (tok[k].ok) {
+                const E* x = rows.from(tok[k], hk);
+                r[k][0].load(x + f0);
+                r[k][1].load(x + f1);
+            }
+        }
+        float cs[V], sn[V];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int32_t hk = h + (k & twice) * G;
+            if (!(k & twice))
+                angles.at(tok[k].pos, sign, cs, sn);
+            E* to = tok[k].ok ? rows.to(tok[k], hk) : nullptr;
+            if (!to)
+                continue;
+            if (turned && rows.turns(hk)) {
+                float a[V], c[V];
+                r[k][0].get(a);
+                r[k][1].get(c);
+                unit_rotate<V>(t, cs, sn, a, c);
+                r[k][0].set(a);
+                r[k][1].set(c);
+            }
+            r[k][0].store(to + f0);
+            r[k][1].store(to + f1);
+        }
+    }
+}
+
+// Heads a step of `step` that few_heads takes H of: the power of two.
+inline int few_heads_group(int H, int step)
+{
+    int g = 1;
+    while (g < H && g < step)
+        g *= 2;
+    return g;
+}
 
 // ---------------------------------------------------------------------------
 // 8-bit cells (e4m3) with power-of-two scales

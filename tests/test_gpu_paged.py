@@ -76,6 +76,23 @@ def test_rope_positions_far_and_negative(layout):
     ref.check(got, want, tol, x.dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (128, 32)])
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 6, 8, 9, 16, 17])
+def test_rope_few_heads_at_positions_of_their_own(H, d, rot, dtype):
+    """Lanes that heads do not take go to other tokens, whose positions differ; an
+    odd number of tokens, input and output strided differently."""
+    B, L = 3, 67
+    x = randn(B, L, H, d, seed=H, dtype=dtype).transpose(1, 2)
+    pos = torch.randint(-1000, 100000, (B, L), generator=torch.Generator().manual_seed(H),
+                        dtype=torch.int32)
+    out = torch.full((B, H + 1, L, d), 7.0, dtype=dtype, device="cuda")
+    dfa.rope(x.cuda(), dfa.rope_spec(d, layout="half", rot_dim=rot, **BANDS), positions=pos.cuda(),
+             out=out[:, :H])
+    check_rope(out[:, :H], x, pos[:, None], "half", rot, False, BANDS)
+    assert (out[:, H] == 7).all()
+
+
 @pytest.mark.parametrize("kind,P,stripe", [("striped", 8, 1), ("striped", 4, 16),
                                            ("balanced", 4, 1), ("contiguous", 4, 1)])
 def test_rope_at_a_workers_positions(orc, kind, P, stripe):
