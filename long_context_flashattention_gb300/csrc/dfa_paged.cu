@@ -9,8 +9,11 @@
 // The codes go into the matrix products as they are (e4m3 is exact in fp16); the
 // key's scale multiplies the score, the value's scale its weight.  Weights are
 // held as 2^(x_j + log2 u_j - M) with M the running maximum of the exponent, so
-// that they stay in fp16's range whatever the scales are, and the sum of
-// probabilities collects 2^(x_j + log2 u_j - M) / u_j in fp32.
+// that they stay in fp16's range whatever the scales are.  The sum of
+// probabilities collects 2^(x_j - N) in fp32: N = M, and the weights over u_j are
+// its terms, as long as u_j is in [2^-40, 2^40]; from the first page on whose
+// scale is not (values near the type's ends, pages of zeros) N is the running
+// maximum of x_j itself.  O = 2^(M - N) (weighted sum) / (sum).
 //
 // What bounds it: HBM.  A cached row is read once and meets G*T query rows, a
 // few operations a byte: too few rows for a 128-row tcgen05 tile, so the products
@@ -43,8 +46,9 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = kPagedTile;
 constexpr float kGrow = 8.f;               // rescale when the maximum grows by 2^8
 constexpr float kNone = -1e30f;            // running maximum before the first key
-constexpr float kSumShift = 16.f;          // 8-bit cells: sums are kept times 2^-16, so
-                                           // that scales of 2^-100 do not overflow them
+constexpr float kNear = 40.f;              // N = M while |log2 u_j| is at most this: the
+                                           // terms are then 2^-80 or more of one another's
+                                           // weights, far from fp32's ends
 constexpr float kNoPage = -1.f;            // in place of a key scale
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -88,7 +92,8 @@ struct Shared {
     float4 scale[8][4];           // per stage and page: see page_scale
     // maxima and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
-    float m[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
+    // (n: while it differs from m, a warp's entry is also where it is kept)
+    float m[2][kWarps][kPagedMaxRows], n[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
     float qf[2][8];               // NB = 2: score factors of the query rows
     long long warp_sum[kThreads / 32];
     long long w0, w1, base;       // the block's range; first unit of sequence b
@@ -359,8 +364,7 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
     __syncthreads();
 }
 
-// What a group of 16 keys needs of its page's scales s (K) and u (V): s, log2 u,
-// 2^-kSumShift / u, and whether the latter is safe to multiply with.
+// What a group of 16 keys needs of its page's scales s (K) and u (V): s, log2 u, 1 / u.
 template <bool F8>
 __device__ __forceinline__ float4 page_scale(bool there, float s, float u)
 {
@@ -373,7 +377,7 @@ __device__ __forceinline__ float4 page_scale(bool there, float s, float u)
     const int e = (int)((bits >> 23) & 0xffu);
     const float lu = e == 255 ? u : (float)max(e - 127, -126) +
                                         log2f(__uint_as_float((bits & 0x7fffffu) | (127u << 23)));
-    return make_float4(s, lu, ex2(-kSumShift - lu), 0.f);
+    return make_float4(s, lu, ex2(-lu), 0.f);
 }
 
 // The producer warp: queries of a segment, then its tiles.  Every wait it has for
@@ -656,13 +660,12 @@ __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float s
     }
 }
 
-// Features f..f+3 of an output row, and its LSE: o and L are relative to 2^mx
-// (L also to 2^kSumShift for 8-bit cells).
+// Features f..f+3 of an output row, and its LSE: o is relative to 2^mx, L to 2^nx.
 template <int D, bool F8>
 __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int f, float mx,
-                                          float L, float4 o)
+                                          float nx, float L, float4 o)
 {
-    const float inv = L == 0.f ? 0.f : (F8 ? 1.f / 65536.f : 1.f) / L;  // (NaN stays NaN)
+    const float inv = L == 0.f ? 0.f : (F8 ? ex2(mx - nx) : 1.f) / L;  // (NaN stays NaN)
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
     if (p.o_fp32)
         *reinterpret_cast<float4*>((float*)p.o + at * D + f) = o;
@@ -670,8 +673,7 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int 
         *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + at * D + f) =
             make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     if (f == 0)
-        p.lse[at] = L == 0.f ? -INFINITY
-                             : (mx + (F8 ? kSumShift : 0.f) + log2f(L)) * kLn2;
+        p.lse[at] = L == 0.f ? -INFINITY : (nx + log2f(L)) * kLn2;
 }
 
 template <int D, bool F8, int NB>
@@ -688,7 +690,6 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
     const int sc_at = page < kTile ? warp * 16 / page : 0;
     const int32_t R = p.G * p.T;
     uint32_t st = 0, phase = 0, met = 0;
-    int par = 0;
     int4 info = make_int4(0, 0, 0, 0);
     for (uint32_t seg = 0;; ++seg) {
         bool ok = mbar_wait(&sh.q_full[seg & 1], (seg / 2) & 1, wctx, 61);
@@ -742,7 +743,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         }
         // keys up to all_see are visible to every row, keys from len on to none
         const int32_t all_see = p.causal ? len - n : len - 1;
-        float O[NB][kMt][4], M[NB][2], l[NB][2], lu_max = -INFINITY;
+        float O[NB][kMt][4], M[NB][2], l[NB][2];
+        bool wide = false;  // N has left M
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -822,11 +824,16 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     }
                     apart = __any_sync(0xffffffffu, apart);
                 }
-                // The sum of probabilities from the weights, which are u times as
-                // large: not where u is so far below an earlier page's that the
-                // weight may vanish where the probability does not.
-                lu_max = fmaxf(lu_max, sc.y);
-                const bool far = F8 && !(lu_max - sc.y <= 60.f && sc.y <= 80.f);
+                float* own_n = sh.n[seg & 1][warp];
+                if (F8 && __builtin_expect(!wide && !(fabsf(sc.y) <= kNear), 0)) {
+                    wide = true;
+                    if (g == 0)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            *reinterpret_cast<float2*>(own_n + nb * 8 + 2 * t) =
+                                make_float2(M[nb][0], M[nb][1]);
+                    __syncwarp();
+                }
                 uint32_t pt[NB][2], pr[NB][2];  // P^T (and its bf16 remainder)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
@@ -839,8 +846,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                     for (int k = 0; k < 2; ++k)
                         dot[k] = f2add(f2pack(acc[nb][0][2 * k], acc[nb][0][2 * k + 1]),
                                        f2pack(acc[nb][1][2 * k], acc[nb][1][2 * k + 1]));
-                    auto exponents = [&](float m0, float m1) {
-                        const uint64_t off = f2pack((F8 ? sc.y : 0.f) - m0, (F8 ? sc.y : 0.f) - m1);
+                    auto exponents = [&](float lu, float m0, float m1) {
+                        const uint64_t off = f2pack((F8 ? lu : 0.f) - m0, (F8 ? lu : 0.f) - m1);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             f2unpack(f2fma(dot[k], factor, off), x[2 * k], x[2 * k + 1]);
@@ -850,9 +857,9 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                                 if (base + g + 8 * (k >> 1) > lim[nb][k & 1])
                                     x[k] = -INFINITY;
                     };
-                    exponents(M[nb][0], M[nb][1]);
+                    exponents(sc.y, M[nb][0], M[nb][1]);
                     if (__any_sync(0xffffffffu, fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kGrow)) {
-                        exponents(0.f, 0.f);
+                        exponents(sc.y, 0.f, 0.f);
                         float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, f[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -862,23 +869,45 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                             const float mn = fmaxf(M[nb][k], mx[k]);
                             f[k] = ex2(M[nb][k] - mn);
                             M[nb][k] = mn;
-                            l[nb][k] *= f[k];
+                            if (!F8 || !wide)
+                                l[nb][k] *= f[k];
                         }
 #pragma unroll
                         for (int m = 0; m < kMt; ++m)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 O[nb][m][k] *= f[k & 1];
-                        exponents(M[nb][0], M[nb][1]);
+                        exponents(sc.y, M[nb][0], M[nb][1]);
                     }
                     float w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         w[k] = ex2(x[k]);
-                    if (far) {
+                    if (F8 && __builtin_expect(wide, 0)) {
+                        float2* at = reinterpret_cast<float2*>(own_n + nb * 8 + 2 * t);
+                        float2 N = *at;
+                        exponents(0.f, N.x, N.y);
+                        if (__any_sync(0xffffffffu,
+                                       fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kGrow)) {
+                            exponents(0.f, 0.f, 0.f);
+                            float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) {
+                                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+                                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+                            }
+                            mx[0] = fmaxf(N.x, mx[0]), mx[1] = fmaxf(N.y, mx[1]);
+                            l[nb][0] *= ex2(N.x - mx[0]), l[nb][1] *= ex2(N.y - mx[1]);
+                            N = make_float2(mx[0], mx[1]);
+                            __syncwarp();
+                            if (g == 0)
+                                *at = N;
+                            exponents(0.f, N.x, N.y);
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            l[nb][k & 1] += ex2(x[k] - sc.y - kSumShift);
+                            l[nb][k & 1] += ex2(x[k]);
+                        __syncwarp();
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -947,7 +976,6 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             }
         }
         // ---- join the warps: largest maximum, rescaled sums and O
-        par ^= 1;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -956,8 +984,10 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 for (int o = 4; o < 32; o <<= 1)
                     l[nb][k] += __shfl_xor_sync(0xffffffffu, l[nb][k], o);
                 if (g == 0) {
-                    sh.m[par][warp][nb * 8 + 2 * t + k] = M[nb][k];
-                    sh.l[par][warp][nb * 8 + 2 * t + k] = l[nb][k];
+                    sh.m[seg & 1][warp][nb * 8 + 2 * t + k] = M[nb][k];
+                    sh.l[seg & 1][warp][nb * 8 + 2 * t + k] = l[nb][k];
+                    if (F8 && !wide)
+                        sh.n[seg & 1][warp][nb * 8 + 2 * t + k] = M[nb][k];
                 }
             }
         if (!meet(sh, met, wctx))
@@ -967,10 +997,10 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int r = nb * 8 + 2 * t + k;
-                float mx = sh.m[par][0][r];
+                float mx = sh.m[seg & 1][0][r];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w)
-                    mx = fmaxf(mx, sh.m[par][w][r]);
+                    mx = fmaxf(mx, sh.m[seg & 1][w][r]);
                 const float f = ex2(M[nb][k] - mx);
                 if (r0 + r < R) {
                     float* dst = join + (warp * C::kRows + r) * C::kPitch;
@@ -997,22 +1027,24 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         for (int r = threadIdx.x / kPerRow; r < C::kRows && r0 + r < R;
              r += 32 * kWarps / kPerRow) {
             const int f = threadIdx.x % kPerRow * 4;
-            float mx = sh.m[par][0][r], L = 0.f;
+            const auto& ns = F8 ? sh.n[seg & 1] : sh.m[seg & 1];
+            float mx = sh.m[seg & 1][0][r], nx = ns[0][r], L = 0.f;
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w)
-                mx = fmaxf(mx, sh.m[par][w][r]);
+            for (int w = 1; w < kWarps; ++w) {
+                mx = fmaxf(mx, sh.m[seg & 1][w][r]);
+                nx = fmaxf(nx, ns[w][r]);
+            }
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw = sh.m[par][w][r];
-                L += sh.l[par][w][r] * ex2(mw - mx);
+                L += sh.l[seg & 1][w][r] * ex2(ns[w][r] - nx);
                 const float4 y = *reinterpret_cast<const float4*>(
                     join + (w * C::kRows + r) * C::kPitch + f);
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
             }
             if (!whole) {
                 if (f == 0)
-                    p.part_ml[slot * C::kRows + r] = make_float2(mx, L);
+                    p.part_mnl[slot * C::kRows + r] = make_float4(mx, nx, L, 0.f);
                 *reinterpret_cast<float4*>(p.part_o + (slot * C::kRows + r) * D + f) = o;
                 continue;
             }
@@ -1021,7 +1053,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             if (tq >= n)
                 continue;
             const int64_t at = ((int64_t)wk.b * p.Hq + h * p.G + gh) * p.T + tq;
-            write_row<D, F8>(p, at, f, mx, L, o);
+            write_row<D, F8>(p, at, f, mx, nx, L, o);
         }
         if (!whole && wk.tile0 == 0) {
             // blocks after this one that hold the rest: up to the last tile's
@@ -1048,6 +1080,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
     const uint32_t q_rows = smem_u32(join) + C::kJoin;
     uint2* qs = reinterpret_cast<uint2*>(join + (C::kJoin + 2 * C::kQRows) / 4);
     if (threadIdx.x == 0) {
+        p.info[blockIdx.x] = make_int4(0, 0, 0, 0);  // for a block that gives up
         sh.abort = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -1084,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedParams p)
 {
-    __shared__ float wt[kPagedMaxCtas], red[8];
+    __shared__ float wt[kPagedMaxCtas], red[8], red_n[8];
     __shared__ float4 acc[256];
     cudaGridDependencySynchronize();  // the blocks' partials
     const int4 info = p.info[blockIdx.x];
@@ -1119,16 +1152,19 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 if (i + grp < k)
                     y[i / kGroups] = *reinterpret_cast<const float4*>(
                         p.part_o + (slot(i + grp) * ROWS + r) * D + f * 4);
-            float2 ml = make_float2(kNone, 0.f);
+            float4 mnl = make_float4(kNone, kNone, 0.f, 0.f);
             if (lane < k)
-                ml = p.part_ml[slot(lane) * ROWS + r];
-            float mx = ml.x;
+                mnl = p.part_mnl[slot(lane) * ROWS + r];
+            float mx = mnl.x, nx = mnl.y;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
+            for (int o = 8; o > 0; o >>= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+                nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o, 16));
+            }
             mx = __shfl_sync(0xffffffffu, mx, 0);
-            const float w = ex2(ml.x - mx);
-            float L = ml.y * w;
+            nx = __shfl_sync(0xffffffffu, nx, 0);
+            const float w = ex2(mnl.x - mx);
+            float L = mnl.z * ex2(mnl.y - nx);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, o, 16);
@@ -1149,7 +1185,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
             }
             if (grp == 0)
-                write_row<D, F8>(p, at, f * 4, mx, L, o);
+                write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
         }
         return;
     }
@@ -1159,23 +1195,27 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         const int64_t at = target(r);
         if (at < 0)
             continue;
-        float mx = kNone;
-        for (int i = threadIdx.x; i < k; i += 256)
-            mx = fmaxf(mx, p.part_ml[slot(i) * ROWS + r].x);
-        for (int o = 16; o > 0; o >>= 1)
+        float mx = kNone, nx = kNone;
+        for (int i = threadIdx.x; i < k; i += 256) {
+            const float4 mnl = p.part_mnl[slot(i) * ROWS + r];
+            mx = fmaxf(mx, mnl.x), nx = fmaxf(nx, mnl.y);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
+        }
         __syncthreads();  // the row before has been read
         if (lane == 0)
-            red[warp] = mx;
+            red[warp] = mx, red_n[warp] = nx;
         __syncthreads();
         for (int w = 0; w < 8; ++w)
-            mx = fmaxf(mx, red[w]);
+            mx = fmaxf(mx, red[w]), nx = fmaxf(nx, red_n[w]);
         __syncthreads();
         float L = 0.f;
         for (int i = threadIdx.x; i < k; i += 256) {
-            const float2 ml = p.part_ml[slot(i) * ROWS + r];
-            wt[i] = ex2(ml.x - mx);
-            L += ml.y * wt[i];
+            const float4 mnl = p.part_mnl[slot(i) * ROWS + r];
+            wt[i] = ex2(mnl.x - mx);
+            L += mnl.z * ex2(mnl.y - nx);
         }
         for (int o = 16; o > 0; o >>= 1)
             L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -1201,7 +1241,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 const float4 y = acc[i * kPerRow + f];
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
             }
-            write_row<D, F8>(p, at, f * 4, mx, L, o);
+            write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
         }
     }
 }
@@ -1216,7 +1256,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     if (e != cudaSuccess)
         return e;
     // as many blocks as are resident at once, no more than there can be tiles
-    const int64_t tiles = (int64_t)p.c.B * p.c.Hkv * p.row_groups *
+    const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
+    const int64_t tiles = min(segments, (int64_t)kPagedMaxCtas) *
                           max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
     const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), tiles);
     p.segment_cost = C::kSegmentCost;
@@ -1229,7 +1270,6 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     // kernel before it still held some SMs they would be dealt out unevenly; 64
     // ragged sequences then took 104 us instead of 91.)  With few segments each is
     // cut into many partials: a block a row.
-    const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

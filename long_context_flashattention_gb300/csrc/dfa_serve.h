@@ -89,7 +89,7 @@ struct PagedParams {
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]
     int4* info;                   // [CTAs]: sequence, head and row group, CTAs that continue it
-    float2* part_ml;              // [2 CTAs][rows]: maximum (log2), sum
+    float4* part_mnl;             // [2 CTAs][rows]: what O and the sum are relative to (log2), sum
     float* part_o;                // [2 CTAs][rows][d]
     uint64_t timeout_ns;
 };

@@ -422,6 +422,35 @@ def test_decode_value_scales_far_apart():
     check_decode(c, c.cuda(), randn(1, 2, 1, 64, seed=59))
 
 
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("exps", [[115], [-100], [0, 115], [115, 0], [-100, 115], [115, -100, 0],
+                                  [-100, 0], [0, -100], [41, 39, -41], [-126, 3]])
+def test_decode_value_scales_at_the_ends_of_their_range(exps, T):
+    """Pages of zeros (the smallest scale) and of values near the type's largest,
+    alone and together: neither the weights nor the sum of probabilities leave
+    fp32's range."""
+    for split in (16, 40):
+        c = ref.Cache(E4M3, 1, 1, 128, 16, split, [16 * split - 3], seed=158)
+        order = c.table[0].long()
+        e = torch.tensor([float(exps[i % len(exps)]) for i in range(split)])
+        c.scales["v"][order, 0] = torch.exp2(e)
+        check_decode(c, c.cuda(), randn(1, 2, T, 128, seed=159))
+
+
+def test_decode_of_appended_values_near_the_largest():
+    dev, q = None, randn(1, 2, 1, 64, seed=160)
+    x = torch.randn(1, 1, 40, 64, generator=torch.Generator().manual_seed(161))
+    for gain in (1e38, 1e-38):
+        k, v = randn(1, 1, 40, 64, seed=162), (x * gain / 4.2).to(BF16)
+        c = ref.Cache(E4M3, 1, 1, 64, 16, 3, [40], seed=163)
+        dev = c.cuda()
+        dfa.cache_append(dev, k.cuda(), v.cuda())
+        for name, got in (("k", dev.k), ("v", dev.v)):
+            c.cells[name] = got.cpu()
+        c.scales = {"k": dev.k_scale.cpu(), "v": dev.v_scale.cpu()}
+        check_decode(c, dev, q)
+
+
 @pytest.mark.parametrize("dtype", [E4M3, BF16])
 def test_decode_nan_where_a_row_does_not_look(dtype):
     """Drafted tokens: the last token's K and V are NaN, which only that token
