@@ -430,7 +430,8 @@ typedef struct dfa_rope_spec {
 
 /*
  * dfa_rope -- rotate query or key rows at their positions, out of place or in
- * place (out == x with equal strides; any other overlap is refused).
+ * place (out == x with equal strides; tensors whose memory ranges overlap in any
+ * other way are refused, even where their rows lie between one another's).
  *   x, out [B,H,L,d], bf16 (fp32 = 0) or fp32 (1); d 64 or 128; L may be 0.
  *   Positions: positions[b*L + l] (device) where positions is not NULL, else
  *   row l's position under map (host), else l.  Any int32 is a position.
@@ -448,7 +449,8 @@ dfa_status dfa_rope(const dfa_rope_spec* spec, int32_t B, int32_t H, int64_t L, 
  * j % page.  seq_lens[b] counts the rows of sequence b, those that a call
  * appends or queries among them: set it before the call.  Only table entries
  * below ceil(seq_lens[b]/page) are read.  Sequences may share pages that are
- * only read; a page that rows are appended to belongs to one sequence.
+ * only read; a page that rows are appended to belongs to one sequence and
+ * stands in its table once.
  *
  * E4M3: a cell stands for code * scale, with one fp32 scale per page and head
  * of K and of V.  Scales are powers of two: the smallest s >= 2^-100 with
@@ -496,8 +498,9 @@ typedef struct dfa_paged_cache {
  * Storing the same rows again gives the same cells.
  *   k, v [B,Hkv,T,d] bf16 (strided); 1 <= T < 2^30.
  *   q, q_out [B,Hq,T,d] bf16 (strided): rows below new_lens[b] are rotated
- *   into q_out (in place when they are one tensor), the others left as they
- *   were; q NULL: no queries.  q needs rope.
+ *   into q_out (in place when they are one tensor; as with dfa_rope no other
+ *   overlap), the others left as they were; q NULL: no queries.  q needs rope.
+ *   q_out's rows are none of k's and v's (they may be heads of one buffer).
  *   ws: 256 bytes (the status word).
  */
 dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,

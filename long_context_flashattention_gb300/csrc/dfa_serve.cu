@@ -122,8 +122,8 @@ dfa_status make_table(RopeTable* t, const dfa_rope_spec* s, int d)
     if (!(s->theta_base > 1.0) || !std::isfinite(s->theta_base))
         return set_error(DFA_ERR_INVALID_ARG, "rope: theta_base must be finite and > 1");
     const double gain = s->gain == 0.0 ? 1.0 : s->gain;
-    if (!(gain > 0.0) || !std::isfinite(gain))
-        return set_error(DFA_ERR_INVALID_ARG, "rope: gain must be positive and finite");
+    if (!((float)gain > 0.f) || !std::isfinite((float)gain))
+        return set_error(DFA_ERR_INVALID_ARG, "rope: gain must be positive and finite in fp32");
     if (s->scaling < DFA_ROPE_PLAIN || s->scaling > DFA_ROPE_BANDS)
         return set_error(DFA_ERR_INVALID_ARG, "rope: unknown scaling %d", s->scaling);
     if (s->scaling != DFA_ROPE_PLAIN && (!(s->factor > 0.0) || !std::isfinite(s->factor)))
@@ -157,6 +157,8 @@ dfa_status make_table(RopeTable* t, const dfa_rope_spec* s, int d)
                 std::min(1.0, std::max(0.0, (turns - s->low) / (s->high - s->low)));
             f = (1.0 - u) * f / s->factor + u * f;
         }
+        if (!std::isfinite(f))
+            return set_error(DFA_ERR_INVALID_ARG, "rope: a frequency is not finite");
         double turn = f / kTwoPi;  // whole turns of an integer position drop out
         turn -= std::floor(turn);
         t->turn[i] = (uint64_t)std::ldexp(turn, 64);  // turn < 1: below 2^64
@@ -449,9 +451,10 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     if (desc->Hq < 1 || desc->Hq % desc->Hkv != 0)
         return set_error(DFA_ERR_INVALID_ARG, "dfa_decode_paged: Hq (%d) must be a positive "
                          "multiple of Hkv (%d)", desc->Hq, desc->Hkv);
-    if (!(desc->scale > 0.f) || !std::isfinite(desc->scale))
+    const float scale_log2 = desc->scale * 1.4426950408889634f;
+    if (!(scale_log2 > 0.f) || !std::isfinite(scale_log2))
         return set_error(DFA_ERR_INVALID_ARG, "dfa_decode_paged: scale must be positive and "
-                         "finite");
+                         "finite, and so must scale * log2(e)");
     if (desc->causal != 0 && desc->causal != 1)
         return set_error(DFA_ERR_INVALID_ARG, "dfa_decode_paged: causal must be 0 or 1");
     if (desc->o_fp32 != 0 && desc->o_fp32 != 1)
@@ -481,7 +484,7 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     p.inv_T = ((1u << 21) + T - 1) / T;
     p.causal = desc->causal;
     p.o_fp32 = desc->o_fp32;
-    p.scale_log2 = desc->scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.o = o;
     p.lse = lse;
     const int rows = paged_rows((int64_t)G * T);

@@ -643,8 +643,8 @@ class PagedCache:
     it keeps alive: k, v [npages,Hkv,page,d], bf16 or float8_e4m3fn (pages may be
     strided: k and v can be two halves of one tensor), with k_scale and v_scale
     [npages,Hkv] fp32 for 8 bits; block_table [B,max_pages] and seq_lens [B]
-    int32.  Change their contents freely; a new table or batch is a new
-    PagedCache."""
+    int32.  Change their contents freely (cache.seq_lens += 1); a new table or
+    batch is a new PagedCache: the calls go by the tensors it was made with."""
 
     def __init__(self, k, v, block_table, seq_lens, k_scale=None, v_scale=None):
         dev = k.device
@@ -682,6 +682,15 @@ class PagedCache:
             _int32(block_table, "block_table", (B, max_pages), dev),
             _int32(seq_lens, "seq_lens", (B,), dev))
         self._ref = ctypes.byref(self.desc)
+
+    def __setattr__(self, name, value):
+        if self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} of a PagedCache stays: change its contents, or make a "
+                                 "new PagedCache")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a PagedCache stays: change its contents")
 
 
 def paged_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:

@@ -192,6 +192,29 @@ def test_binding_refuses():
         dfa.rope_spec(64, layout="thirds")
 
 
+def test_rope_refuses_what_fp32_cannot_hold(L):
+    """A gain that is zero or infinite in fp32, frequencies that are not finite."""
+    for kw in (dict(gain=1e-60), dict(gain=1e60), dict(scaling="linear", factor=1e-310),
+               dict(scaling="bands", factor=1e-316, orig_len=512.0, low=1.0, high=4.0)):
+        assert rope(L, spec(**kw)) == 1, kw
+    assert decode(L, scale=3e38) == 1                         # times log2(e) is not finite
+
+
+def test_a_cache_keeps_its_tensors():
+    """Rebinding a cache's tensor would leave the calls with the old memory."""
+    e4 = torch.zeros(8, 2, 16, 64).to(torch.bfloat16)
+    table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    c = dfa.PagedCache(e4, e4, table, lens)
+    with pytest.raises(AttributeError, match="contents"):
+        c.seq_lens = lens + 1
+    with pytest.raises(AttributeError, match="contents"):
+        c.k = e4.clone()
+    with pytest.raises(AttributeError, match="contents"):
+        del c.block_table
+    c.seq_lens += 1                                           # in place
+    assert lens.tolist() == [1, 1] and c.desc.seq_lens == lens.data_ptr()
+
+
 def test_plain_forms_of_the_tests():
     """The tests' own fp64 forms: rotation keeps lengths, its inverse undoes it,
     the two layouts are one map under a reordering, scales are tight."""
