@@ -13,6 +13,14 @@
 // in between: every row is read once.  The group keeps its rows' cos and sin and
 // goes through several heads with them.
 //
+// Measured: a 32K bf16 prompt of 3 x 32 heads of 128, 239 us, 6.7 TB/s; into 8 bits
+// with 8 heads, no queries, 140 us, 5.2 TB/s (a job waits for its rows, then for
+// the group's largest value: rows in flight, not the rate, bound it); ragged chunks of
+// 0..1000 tokens into 16-row pages, 28 MB, 12.7 us (instruction issue 61 % while it
+// runs, the launch and the chain of loads the rest); one token of 64 sequences 4.1 us.
+// Gather of two sequences of up to 64K rows of 8 heads, 604 MB: 81.5 us (part of what it
+// writes is still in L2 when it ends).
+//
 // Row items (queries; K and V too in a bf16 cache, where rows are independent).
 // A warp takes one token and several heads; its lanes compute the token's
 // cos and sin once between them.

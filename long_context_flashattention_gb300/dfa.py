@@ -629,7 +629,9 @@ def rope(x, spec: RopeSpec, positions=None, pos_map: PosMap | None = None, inver
     B, H, L, d = shape
     if out is None:
         out = _new(stream, shape, dtype, dev)
-    op, os_ = (xp, xs) if out is x else _rows(out, "out", dtype, dev, shape)
+        op, os_ = out.data_ptr(), None
+    else:
+        op, os_ = (xp, xs) if out is x else _rows(out, "out", dtype, dev, shape)
     code = lib().dfa_rope(ctypes.byref(spec), B, H, L, d, dtype is torch.float32, xp, xs, op, os_,
                           None if pos_map is None else ctypes.byref(pos_map),
                           _int32(positions, "positions", (B, L), dev), inverse, raw)
@@ -748,7 +750,9 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
         qp, qs = _rows(q, "q", torch.bfloat16, dev, shape)
         if q_out is None:
             q_out = _new(stream, shape, torch.bfloat16, dev)
-        op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
+            op = q_out.data_ptr()
+        else:
+            op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     code = lib().dfa_cache_append(cache._ref, None if rope is None else ctypes.byref(rope), T,
