@@ -451,6 +451,27 @@ def test_decode_of_appended_values_near_the_largest():
         check_decode(c, dev, q)
 
 
+@pytest.mark.parametrize("d,Hq", [(64, 1), (128, 12)])
+def test_decode_extreme_scales_joined_from_many_blocks(d, Hq):
+    """A long sequence cut into more partial results than one warp joins; whole
+    stretches of it quiet, loud or in between."""
+    n = 700
+    c = ref.Cache(E4M3, 1, 1, d, 16, n, [16 * n - 5], seed=164)
+    e = torch.tensor([(-100.0, 0.0, 115.0, 60.0, -40.0)[i // 140] for i in range(n)])
+    c.scales["v"][c.table[0].long(), 0] = torch.exp2(e)
+    check_decode(c, c.cuda(), randn(1, Hq, 1, d, seed=165))
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("Hq,T,q_lens,causal", [(32, 32, None, True), (2, 512, [300, 512], True),
+                                                (4, 3, [0, 2], False), (17, 1, None, False)])
+def test_decode_most_rows_and_unmasked_ragged(dtype, Hq, T, q_lens, causal):
+    """1024 query rows of a head, more tokens than a page; and ragged queries that
+    see every key."""
+    c = ref.Cache(dtype, 2, 1, 64, 16, 40, [300, 530], seed=166)
+    check_decode(c, c.cuda(), randn(2, Hq, T, 64, seed=167), q_lens, causal)
+
+
 @pytest.mark.parametrize("dtype", [E4M3, BF16])
 def test_decode_nan_where_a_row_does_not_look(dtype):
     """Drafted tokens: the last token's K and V are NaN, which only that token
