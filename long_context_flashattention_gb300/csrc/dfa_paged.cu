@@ -56,6 +56,12 @@ constexpr float kNone = -1e30f;            // running maximum before the first k
 constexpr float kNear = 40.f;              // N = M while |log2 u_j| is at most this: the
                                            // terms are then 2^-80 or more of one another's
                                            // weights, far from fp32's ends
+// Where no sequence can be longer than so many tiles, segments are not cut and
+// there is nothing to merge.  Measured (GPU us cut, and whole; 1, 4, 8, 16 tiles): one
+// sequence of 8 heads, 8-bit 7.8 7.0, 9.8 8.6, 9.4 10.7, 9.8 14.8; 64 sequences 10.7
+// 9.9, 14.8 13.9, 18.5 20.1, 30.2 34.0; 16 of bf16 with 16 rows (2, 4, 8, 16 tiles)
+// 11.5 9.9, 14.0 11.1, 15.6 13.7, 19.3 19.7.
+constexpr int kWhole = 4;
 constexpr float kNoPage = -1.f;            // in place of a key scale
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -279,6 +285,7 @@ struct Walk : Piece {
         const int32_t within = (int32_t)min(at - hr * unit, unit - 1);
         tile0 = max(0, within - p.segment_cost);
         w -= within;  // the segment's first unit
+        fresh = !p.whole || within == 0;  // else: begin with the next segment
     }
     __device__ __forceinline__ bool next(const PagedParams& p)
     {
@@ -303,7 +310,7 @@ struct Walk : Piece {
             return false;
         }
         fresh = false;
-        nt = (int32_t)min((long long)tiles, w1 - w - p.segment_cost) - tile0;
+        nt = (int32_t)(p.whole ? tiles : min((long long)tiles, w1 - w - p.segment_cost)) - tile0;
         return nt > 0;  // (the last segment's beginning may lie in the range, its tiles behind)
     }
 };
@@ -1262,15 +1269,16 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess)
         return e;
-    // as many blocks as are resident at once, no more than there can be tiles
+    // as many blocks as are resident at once, no more than there can be pieces
     const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
-    const int64_t tiles = min(segments, (int64_t)kPagedMaxCtas) *
-                          max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
-    const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), tiles);
+    const int32_t longest = max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
+    p.whole = longest <= kWhole;
+    const int64_t pieces = min(segments, (int64_t)kPagedMaxCtas) * (p.whole ? 1 : longest);
+    const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), pieces);
     p.segment_cost = C::kSegmentCost;
     decode_kernel<D, F8, NB><<<grid, kThreads, C::kSmem, stream>>>(tk, tv, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess)
+    if (e != cudaSuccess || p.whole)
         return e;
     // The merge's blocks may start while the decode's end, and wait there.  (The
     // decode itself starts on empty SMs: its blocks are as many as fit, and where a

@@ -85,6 +85,7 @@ struct PagedParams {
     uint32_t inv_T;               // 2^21 / T, rounded up
     int32_t row_groups;           // blocks of query rows per key/value head
     int32_t segment_cost;         // in tiles
+    int32_t whole;                // segments are not cut
     float scale_log2;
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]

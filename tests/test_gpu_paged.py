@@ -516,6 +516,20 @@ def test_decode_ragged_batch_of_many():
     check_decode(c, c.cuda(), randn(300, 2, 1, 64, seed=66))
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("T", [1, 3])
+def test_decode_ragged_batch_of_short_sequences(dtype, T):
+    """Tables of a few tiles, whose segments are not cut: many more of them than
+    blocks, idle sequences between, at the end and at the beginning."""
+    g = torch.Generator().manual_seed(168)
+    lens = torch.randint(T, 140, (400,), generator=g).tolist()
+    q_lens = torch.randint(0, T + 1, (400,), generator=g).tolist()
+    for b in (0, 1, 50, 51, 52, 399):
+        lens[b] = q_lens[b] = 0
+    c = ref.Cache(dtype, 400, 2, 64, 16, 9, lens, seed=169)
+    check_decode(c, c.cuda(), randn(400, 8, T, 64, seed=170), q_lens)
+
+
 def test_decode_many_query_heads_of_one_cache_head():
     c = ref.Cache(E4M3, 2, 1, 64, 32, 4, [100, 128], seed=67)
     check_decode(c, c.cuda(), randn(2, 48, 2, 64, seed=68))
