@@ -11,13 +11,15 @@
 // new rows before the first is stored, so a group of threads takes the rows of one
 // page and head, a 16-feature unit of a row each, and holds them in registers
 // in between: every row is read once.  The group keeps its rows' cos and sin and
-// goes through several heads with them.
+// goes through several heads with them, the next two heads' rows on their way into
+// shared memory (one head ahead in registers, which then spill: 143 and 302 us for the
+// 32K prompts below; three, four and six heads: 133, 137, 164 where two took 132).
 //
 // Measured: a 32K bf16 prompt of 3 x 32 heads of 128, 239 us, 6.7 TB/s; into 8 bits
-// with 8 heads, no queries, 140 us, 5.2 TB/s (a job waits for its rows, then for
-// the group's largest value: rows in flight, not the rate, bound it); ragged chunks of
-// 0..1000 tokens into 16-row pages, 28 MB, 12.7 us (instruction issue 61 % while it
-// runs, the launch and the chain of loads the rest); one token of 64 sequences 4.1 us.
+// with 8 key/value heads 129 us, 5.7 TB/s, with 32 253 us, 5.3 TB/s (a group waits for
+// its largest value between loads and stores); ragged chunks of 0..1000 tokens into
+// 16-row pages, 28 MB, 12.3 us (instruction issue 61 % while it runs, the launch and
+// the chain of loads the rest); one token of 64 sequences 3.9 us.
 // Gather of two sequences of up to 64K rows of 8 heads, 604 MB: 81.5 us (part of what it
 // writes is still in L2 when it ends).
 //
@@ -31,6 +33,23 @@ namespace dfa {
 namespace {
 
 constexpr int kBatch = 2;     // rows of an item in flight per lane
+constexpr int kSlots = 64;    // shared memory of a thread of a page job: two heads' units
+
+// 16 bytes into the thread's own slot of shared memory
+__device__ __forceinline__ void copy16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ uint4 load16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
 
 // codes of x / s; a NaN stays one
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
@@ -171,7 +190,7 @@ __device__ __forceinline__ float group_max(float m, int group, int thread, int t
 template <int D>
 __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, int group,
                                          int thread, const uint64_t* turns, uint32_t (*words)[32],
-                                         int& set)
+                                         int& set, uint32_t slots)
 {
     constexpr int UNITS = D / 16;
     const uint32_t head_jobs = (p.c.Hkv + p.job_heads - 1) / p.job_heads;
@@ -216,13 +235,24 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
     const bool turned = unit_runs<8>(p.t, D, u, f0, f1) && !is_v;
     float cs[8], sn[8];
     const __nv_bfloat16* x = (const __nv_bfloat16*)src.p + b * src.sb + h0 * src.sh +
-                             (row - first) * src.sl;
+                             (row - first) * src.sl + f0;
+    const int32_t run1 = f1 - f0;                  // from the first run to the second
+    const int32_t at0 = (row - start) * D + f0;    // the first run's cells
     const int32_t h1 = min(h0 + p.job_heads, p.c.Hkv);
-    Run<__nv_bfloat16> r0, r1;
-    if (mine) {
-        r0.load(x + f0);
-        r1.load(x + f1);
-    }
+    // rows of the next heads, in slots of the thread's own
+    const uint32_t half = blockDim.x * 16;
+    uint32_t slot = slots + threadIdx.x * 16;
+    int32_t step = 2 * half;  // to the other slot
+    auto fetch = [&](uint32_t at, bool there) {
+        if (mine && there) {
+            copy16(at, x);
+            copy16(at + half, x + run1);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        x += src.sh;
+    };
+    fetch(slot, true);
+    fetch(slot + step, h0 + 1 < h1);
     const bool stores = is_page(p.c, b, id);  // if not, on to the barriers all the same
     if (!stores)
         id = 0;
@@ -236,18 +266,20 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
             for (int j = 0; j < 8; ++j)
                 pair_angle(turns[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[j], sn[j]);
         float a[8], c[8], amax = 0.f;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         if (mine) {
+            Run<__nv_bfloat16> r0, r1;
+            r0.w = load16(slot);
+            r1.w = load16(slot + half);
             r0.get(a);
             r1.get(c);
             if (turned)
                 unit_rotate<8>(p.t, cs, sn, a, c);
             amax = abs_max8(abs_max8(0.f, a), c);
-            x += src.sh;
-            if (h + 1 < h1) {  // the next head's rows, ahead of the barrier
-                r0.load(x + f0);
-                r1.load(x + f1);
-            }
         }
+        fetch(slot, h + 2 < h1);
+        slot += step;
+        step = -step;
         amax = group_max(amax, group, thread, threads, words, set);
         if (amax == INFINITY) {  // (rare) once more, over finite values
             if (mine) {
@@ -285,9 +317,8 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
                 scales[h] = s;
         }
         if (mine && stores) {
-            uint8_t* cell = cells + (row - start) * D;
-            *reinterpret_cast<uint2*>(cell + f0) = codes8(a, inv);
-            *reinterpret_cast<uint2*>(cell + f1) = codes8(c, inv);
+            *reinterpret_cast<uint2*>(cells + at0) = codes8(a, inv);
+            *reinterpret_cast<uint2*>(cells + at0 + run1) = codes8(c, inv);
         }
     }
 }
@@ -302,12 +333,14 @@ __global__ void __launch_bounds__(F8 ? 1024 : 256, F8 ? 1 : 3)
     __syncthreads();
     if (F8 && (int32_t)blockIdx.x < p.job_blocks) {
         __shared__ uint32_t words[32][32];
+        extern __shared__ uint4 slots[];
         const int groups = blockDim.x / p.job_threads;
         const int group = threadIdx.x / p.job_threads;
         int set = 0;
         for (uint32_t job = blockIdx.x * groups + group; job < p.jobs;
              job += p.job_blocks * groups)
-            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turns, words, set);
+            page_job<D>(p, job, group, threadIdx.x - group * p.job_threads, turns, words, set,
+                        smem_u32(slots));
         return;
     }
     const int warps = blockDim.x >> 5;
@@ -403,17 +436,17 @@ cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t strea
                           num_sms * (p.c.e4m3 ? 2048u : 4096u) / threads);
     }
     const unsigned blocks = (unsigned)(p.job_blocks + item_blocks);
-    if (p.c.e4m3) {
-        if (units == 8)
-            cache_append_kernel<true, 128><<<blocks, threads, 0, stream>>>(p);
-        else
-            cache_append_kernel<true, 64><<<blocks, threads, 0, stream>>>(p);
-    } else {
-        if (units == 8)
-            cache_append_kernel<false, 128><<<blocks, threads, 0, stream>>>(p);
-        else
-            cache_append_kernel<false, 64><<<blocks, threads, 0, stream>>>(p);
+    if (!p.c.e4m3) {
+        auto* kernel = units == 8 ? cache_append_kernel<false, 128> : cache_append_kernel<false, 64>;
+        kernel<<<blocks, threads, 0, stream>>>(p);
+        return cudaGetLastError();
     }
+    auto* kernel = units == 8 ? cache_append_kernel<true, 128> : cache_append_kernel<true, 64>;
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlots * 1024);
+    if (e != cudaSuccess)
+        return e;
+    kernel<<<blocks, threads, kSlots * threads, stream>>>(p);
     return cudaGetLastError();
 }
 
