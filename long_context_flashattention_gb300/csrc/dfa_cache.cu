@@ -399,10 +399,13 @@ __global__ void __launch_bounds__(128) cache_gather_kernel(const __grid_constant
 
 // Work per job, item and block.  Angles are computed once per job or item, so
 // each takes as many heads as leave enough threads to fill the SMs; blocks take
-// several, a grid's worth at a time.  Measured (ragged chunks of 0..1000 tokens
-// of 16 sequences, 8-bit, d 64): jobs filling 1024 threads an SM 12.3 us, 512
-// 12.1, 2048 14.5; a 32K bf16 prompt of 32 heads: blocks for 4096 threads an SM
-// 242 us, 2048 249.
+// several, a grid's worth at a time.  Measured (8-bit, 32 and 8 heads; jobs for 1024
+// threads and items for 64 warps an SM, 512 and 32, 384 and 24, 256 and 8; us): 1024
+// tokens 10.3, 10.3, 7.6, 7.8, 2048 17.3, 12.3, 10.3, 10.3, 4096 23.3, 18.6, 18.0;
+// ragged chunks of 0..1000 tokens of 16 sequences (d 64) 13.1, 11.1, 11.1, 11.5.
+// bf16, items for 24 and 12 warps: 512 tokens 6.1, 4.9, 2048 11.1, 8.6.  Item blocks
+// for 4096 threads an SM (a 32K bf16 prompt of 32 heads) 242 us, 2048 249; job blocks
+// for 1024 and 2048: 128.7, 129.4.
 cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t stream)
 {
     const int units = p.c.d / 16, step = 32 / units;
@@ -418,18 +421,18 @@ cudaError_t launch_cache_append(AppendParams& p, int num_sms, cudaStream_t strea
         p.job_heads = 8;
         while (p.job_heads > 1 &&
                pages * ((p.c.Hkv + p.job_heads - 1) / p.job_heads) * p.job_threads <
-                   (int64_t)num_sms * 1024)
+                   (int64_t)num_sms * 384)
             p.job_heads /= 2;
         p.jobs = (uint32_t)(pages * ((p.c.Hkv + p.job_heads - 1) / p.job_heads));
         const int groups = threads / p.job_threads;
-        p.job_blocks = (int32_t)min((p.jobs + groups - 1) / groups, num_sms * 2048u / threads);
+        p.job_blocks = (int32_t)min((p.jobs + groups - 1) / groups, num_sms * 1024u / threads);
     }
     const int rows = p.Hq + (p.c.e4m3 ? 0 : 2 * p.c.Hkv);
     int64_t item_blocks = 0;
     if (rows > 0) {
         p.item_heads = 16 * kBatch * step;
         while (p.item_heads > step &&
-               tokens * ((rows + p.item_heads - 1) / p.item_heads) < (int64_t)num_sms * 64)
+               tokens * ((rows + p.item_heads - 1) / p.item_heads) < (int64_t)num_sms * (p.c.e4m3 ? 24 : 12))
             p.item_heads /= 2;
         p.items = (uint32_t)(tokens * ((rows + p.item_heads - 1) / p.item_heads));
         item_blocks = min((p.items + threads / 32 - 1) / (threads / 32),

@@ -141,9 +141,12 @@ cudaError_t launch(RopeRowsParams& p, int num_sms, cudaStream_t stream)
         return cudaGetLastError();
     }
     // Heads per warp: a warp computes its token's angles once for all of them, but
-    // short inputs need the warps.
-    p.heads = 4 * kBatch * kStep;
-    while (p.heads > kStep && rows * ((p.H + p.heads - 1) / p.heads) < num_sms * 32u)
+    // short inputs need the warps.  Measured (warps an SM to reach, 32 and 8; us): bf16
+    // 32 heads x 512 4.9 3.7, x 2048 8.2 5.7, x 4096 10.2 9.4; 9 heads x 4096 7.8
+    // 5.7; fp32 16 heads x 1024 5.8 4.1.  Twice as many heads a warp: 128 x 4096 bf16
+    // 44.6 for 43.0, 32 x 4096 fp32 22.8 for 20.6; half as many: 32 x 2048 bf16 6.6.
+    p.heads = 2 * kBatch * kStep;
+    while (p.heads > kStep && rows * ((p.H + p.heads - 1) / p.heads) < num_sms * 8u)
         p.heads /= 2;
     const uint32_t head_items = (p.H + p.heads - 1) / p.heads;
     const uint32_t items = rows * head_items;
