@@ -715,6 +715,62 @@ def test_streams_and_workspaces_of_two_calls_at_once():
             ref.check(lse[b, :, :n], LSE[b, :, :n], tL[b, :, :n], torch.float32)
 
 
+@pytest.mark.parametrize("before", ["nothing", "copy", "memset", "join", "decode", "copies"])
+def test_captured_behind(before):
+    """A decode of few blocks captured as the first node of a graph, behind copies,
+    behind a join of two streams, and behind another decode on one workspace; what
+    came before it is seen."""
+    c = ref.Cache(E4M3, 1, 2, 128, 16, 40, [600], seed=180)
+    q, q0 = randn(1, 8, 1, 128, seed=181), randn(1, 8, 1, 128, seed=182)
+    dev, src = c.cuda(), q.cuda()
+    q_dev = q0.cuda()
+    staging = torch.empty_like(q_dev)
+    scratch = torch.ones(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = dfa.paged_workspace(dev, 8)
+    out, lse = torch.empty_like(q_dev), torch.empty(1, 8, 1, device="cuda")
+    o2, l2 = torch.empty_like(q_dev), torch.empty(1, 8, 1, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step():
+        main = torch.cuda.current_stream()
+        if before == "copy":
+            q_dev.copy_(src)
+        elif before == "copies":
+            staging.copy_(src)
+            q_dev.copy_(staging)
+        elif before == "memset":
+            q_dev.copy_(src)
+            scratch.zero_()
+        elif before == "join":
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                q_dev.copy_(src)
+                q_dev.mul_(1)
+            scratch.add_(1)
+            main.wait_stream(side)
+        elif before == "decode":
+            dfa.decode_paged(dev, q_dev, out=o2, lse=l2, ws=ws)
+            q_dev.copy_(src)
+        dfa.decode_paged(dev, q_dev, out=out, lse=lse, ws=ws)
+
+    if before == "nothing":
+        q_dev.copy_(src)
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    O, LSE, tO, tL = ref.attention(c, q)
+    for _ in range(50):
+        if before != "nothing":
+            q_dev.copy_(q0)
+        out.fill_(7.0)
+        g.replay()
+        ref.check(out, O, tO, BF16)
+        ref.check(lse, LSE, tL, torch.float32)
+    dfa.stream_status(ws)
+
+
 def test_same_call_twice_gives_the_same_bits():
     c = ref.Cache(E4M3, 3, 2, 128, 16, 64, [1000, 3, 500], seed=84)
     dev, q = c.cuda(), randn(3, 8, 2, 128, seed=85).cuda()
