@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(F8 ? 1024 : 256, F8 ? 1 : 3)
     cache_append_kernel(const __grid_constant__ AppendParams p)
 {
     __shared__ uint64_t turns[64];  // lanes read different entries: not from the parameters
+    // A decode of few blocks behind this kernel may be launched already, and waits (the
+    // two, one sequence of 1000 rows, in a graph: 12.7 -> 12.3 us).
+    cudaTriggerProgrammaticLaunchCompletion();
     if (threadIdx.x < 64)
         turns[threadIdx.x] = p.t.turn[threadIdx.x];
     __syncthreads();
