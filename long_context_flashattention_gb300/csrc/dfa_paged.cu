@@ -20,11 +20,16 @@
 // are the 16x8x16 warp products, with the cache in the 16-row operand and 8
 // query rows (NB = 1) or 16 (NB = 2) in the other: S^T = K Q^T, O^T = V^T P^T.
 //
-// Work.  (sequence, head, row group) segments of 64-key tiles form one line,
-// cut evenly over a persistent grid whatever the lengths: a block's range
-// covers whole segments, whose result it writes, and up to two cut ones, whose
-// partials it leaves in the workspace for merge_kernel.  The lengths are read
-// on the device, so a captured graph follows them.
+// Work.  (sequence, head) segments of 64-key tiles form one line, cut by cost over
+// a persistent grid whatever the lengths: a block's range covers whole segments,
+// whose result it writes, and up to two cut ones, whose partials it leaves in the
+// workspace for merge_kernel.  The lengths are read on the device, so a captured
+// graph follows them.  A head with more than 16 query rows has several groups of
+// them, and each group blocks of its own, cut alike: the groups' blocks read the same
+// tiles at about the same time, out of L2.  Measured (4 sequences of 32K rows, 8 heads,
+// bf16; 16, 32, 64, 128, 256 query rows, us): 92, 113, 195, 366, 709, where groups one
+// behind the other on the line took 92, 162, 310, 604, 1182.  In 8 bits the products
+// bound it, 61, 102, 191, 369, 725 either way.
 //
 // A block: warp 4 fetches pages by TMA into a ring of tiles (128- or 64-byte
 // swizzle; the page numbers and scales of 32 pages are looked up at a time);
@@ -111,7 +116,7 @@ struct Shared {
     long long warp_sum[kThreads / 32];
     long long w0, w1, base;       // the block's range; first unit of sequence b
     long long each, rest;         // units of a block; the first `rest` blocks have one more
-    int32_t b;
+    int32_t b, block;             // ..., and the block's place in its group
     uint32_t abort;
 };
 
@@ -248,12 +253,12 @@ __device__ __forceinline__ long long divide(long long a, int32_t b)
     return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-// The block whose range has this unit.
-__device__ __forceinline__ int block_of(const Shared& sh, long long unit)
+// The block of the group whose range has this unit.
+__device__ __forceinline__ int block_of(const PagedParams& p, const Shared& sh, long long unit)
 {
     const long long longer = sh.rest * (sh.each + 1);
     const long long c = unit < longer ? unit / (sh.each + 1) : sh.rest + (unit - longer) / sh.each;
-    return (int)min(c, (long long)gridDim.x - 1);
+    return (int)min(c, (long long)p.line_blocks - 1);
 }
 
 // The line that is cut: every segment takes p.segment_cost units (its queries, the join
@@ -267,7 +272,7 @@ struct Walk : Piece {
     long long w1;     // end of the range
     bool fresh;       // tile0 is where the range begins
 
-    __device__ __forceinline__ void start(const PagedParams& p, const Shared& sh)
+    __device__ __forceinline__ void start(const PagedParams& p, const Shared& sh, int32_t group)
     {
         w = sh.w0;
         w1 = sh.w1;
@@ -278,11 +283,9 @@ struct Walk : Piece {
         seq_rows(p.c, p.q_lens, p.T, b, len, n);
         tiles = tiles_of(len, n);
         const long long at = w - sh.base, unit = tiles + p.segment_cost;
-        const long long hr =
-            min(divide(at, (int32_t)unit), (long long)p.c.Hkv * p.row_groups - 1);
-        h = (int32_t)(hr / p.row_groups);
-        rg = (int32_t)(hr - (long long)h * p.row_groups);
-        const int32_t within = (int32_t)min(at - hr * unit, unit - 1);
+        h = (int32_t)min(divide(at, (int32_t)unit), (long long)p.c.Hkv - 1);
+        rg = group;
+        const int32_t within = (int32_t)min(at - h * unit, unit - 1);
         tile0 = max(0, within - p.segment_cost);
         w -= within;  // the segment's first unit
         fresh = !p.whole || within == 0;  // else: begin with the next segment
@@ -294,17 +297,14 @@ struct Walk : Piece {
             if (w >= w1)
                 return false;
             tile0 = 0;
-            if (++rg == p.row_groups) {
-                rg = 0;
-                if (++h == p.c.Hkv) {
-                    h = 0;
-                    do {
-                        if (++b >= p.c.B)
-                            return false;
-                        seq_rows(p.c, p.q_lens, p.T, b, len, n);
-                        tiles = tiles_of(len, n);
-                    } while (tiles == 0);
-                }
+            if (++h == p.c.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= p.c.B)
+                        return false;
+                    seq_rows(p.c, p.q_lens, p.T, b, len, n);
+                    tiles = tiles_of(len, n);
+                } while (tiles == 0);
             }
         } else if (w >= w1) {
             return false;
@@ -316,12 +316,16 @@ struct Walk : Piece {
 };
 
 // The block's range of the line of tiles, and the sequence that it begins in.
+template <int NB>
 __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
 {
-    const int32_t per_seq = p.c.Hkv * p.row_groups;
+    const int32_t per_seq = p.c.Hkv;
     const int32_t chunk = ceil_div(p.c.B, kThreads);
+    // (up to 8 query rows are one group)
+    const int32_t block = NB == 1 ? blockIdx.x : blockIdx.x / p.row_groups;
     if (threadIdx.x == 0) {
         sh.b = 0;
+        sh.block = block;
         sh.base = 0;
     }
     const int32_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, p.c.B);
@@ -349,11 +353,11 @@ __device__ __forceinline__ void find_range(const PagedParams& p, Shared& sh)
         total += sh.warp_sum[w];
     }
     incl += before;
-    const int32_t active = (int32_t)min((long long)gridDim.x, total);
-    const bool mine = (int32_t)blockIdx.x < active;  // then at least one tile
+    const int32_t active = (int32_t)min((long long)p.line_blocks, total);
+    const bool mine = block < active;  // then at least one unit
     const long long each = divide(total, max(active, 1)), rest = total - each * active;
-    const long long w0 = mine ? each * blockIdx.x + min((long long)blockIdx.x, rest) : 0;
-    const long long w1 = mine ? w0 + each + ((long long)blockIdx.x < rest ? 1 : 0) : 0;
+    const long long w0 = mine ? each * block + min((long long)block, rest) : 0;
+    const long long w1 = mine ? w0 + each + (block < rest ? 1 : 0) : 0;
     if (threadIdx.x == 0) {
         sh.w0 = w0;
         sh.w1 = w1;
@@ -409,7 +413,7 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
     const int32_t per_tile = kTile / box_rows;  // boxes of a tile
     uint32_t st = 0, phase = 0, seg = 0;
     Walk wk;
-    wk.start(p, sh);
+    wk.start(p, sh, NB == 1 ? 0 : blockIdx.x - sh.block * p.row_groups);
     bool more = wk.next(p);
     // Table entry of this lane's page of the 32 from page `win` on; -1: none.
     auto entry = [&](const Walk& x, int32_t win) {
@@ -712,7 +716,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         const Piece wk = sh.run[seg & 1];
         if (wk.nt == 0)
             break;
-        const int32_t h = wk.h, r0 = wk.rg * C::kRows;
+        const int32_t h = wk.h, r0 = NB == 1 ? 0 : wk.rg * C::kRows;
         const int32_t len = wk.len, n = wk.n;
         // ---- queries: rows g of each block of 8, this lane's features
         uint32_t q[C::kSteps][2];  // NB = 1: the operand itself
@@ -1070,10 +1074,10 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             write_row<D, F8>(p, at, f, mx, nx, L, o);
         }
         if (!whole && wk.tile0 == 0) {
-            // blocks after this one that hold the rest: up to the last tile's
+            // the group's blocks after this one that hold the rest: up to the last tile's
             const long long last = wk.w + p.segment_cost + wk.tiles - 1;
-            info = make_int4(wk.b, wk.h * p.row_groups + wk.rg,
-                             block_of(sh, last) - (int)blockIdx.x, n);
+            info = make_int4(wk.b, NB == 1 ? wk.h : wk.h * p.row_groups + wk.rg,
+                             block_of(p, sh, last) - sh.block, n);
         }
     }
     if (threadIdx.x == 0)
@@ -1112,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
     cudaTriggerProgrammaticLaunchCompletion();  // merge_kernel's blocks may be launched
     if (threadIdx.x == 0)
         p.info[blockIdx.x] = make_int4(0, 0, 0, 0);  // for a block that gives up
-    find_range(p, sh);  // also orders the barriers' initialisation
+    find_range<NB>(p, sh);  // also orders the barriers' initialisation
     const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
     if (threadIdx.x >= 32 * kWarps) {
         produce<D, F8, NB>(p, sh, ring, q_rows, tk, tv, wctx);
@@ -1128,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
 }
 
 // Rows of the segments that several blocks share: block c holds such a segment's
-// beginning, the info[c].z blocks after it the rest.  Few partials: one warp a
+// beginning, the info[c].z blocks of its group after it the rest.  Few partials: one warp a
 // row; many (a long sequence with few heads): the block's 8 warps share a row's.
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedParams p)
@@ -1140,10 +1144,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     const int k = info.z + 1;
     if (info.z <= 0)
         return;
-    const int32_t h = info.y / p.row_groups;
-    const int32_t r0 = (info.y - h * p.row_groups) * ROWS;
-    auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1
-                                           : 2 * ((int64_t)blockIdx.x + i); };
+    const int32_t h = ROWS == kPagedRows ? info.y : info.y / p.row_groups;
+    const int32_t r0 = ROWS == kPagedRows ? 0 : (info.y - h * p.row_groups) * ROWS;
+    const int own = 2 * blockIdx.x, step = 2 * (ROWS == kPagedRows ? 1 : p.row_groups);
+    auto slot = [&](int i) { return i == 0 ? own + 1 : own + i * step; };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // row r of the group -> output row, or -1
     auto target = [&](int r) -> int64_t {
@@ -1272,11 +1276,13 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     if (e != cudaSuccess)
         return e;
     // as many blocks as are resident at once, no more than there can be pieces
-    const int64_t segments = (int64_t)p.c.B * p.c.Hkv * p.row_groups;
+    const int64_t segments = (int64_t)p.c.B * p.c.Hkv;  // of one row group
     const int32_t longest = max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
     p.whole = longest <= kWhole;
     const int64_t pieces = min(segments, (int64_t)kPagedMaxCtas) * (p.whole ? 1 : longest);
-    const int grid = (int)min((int64_t)min(kPagedMaxCtas, C::kResident * num_sms), pieces);
+    const int resident = min(kPagedMaxCtas, C::kResident * num_sms);
+    p.line_blocks = (int)min((int64_t)max(1, resident / p.row_groups), pieces);
+    const int grid = p.line_blocks * p.row_groups;
     p.segment_cost = C::kSegmentCost;
     // A grid of at most one block an SM may be launched while the kernel before it ends
     // (its blocks wait at their beginning): one sequence of 1000 rows, called one after
@@ -1301,7 +1307,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     // segments each is cut into many partials: a block a row.
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(grid, segments * 8 >= grid ? 1 : C::kRows);
+    cfg.gridDim = dim3(grid, segments * 8 >= p.line_blocks ? 1 : C::kRows);
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, merge_kernel<D, F8, C::kRows>, p);
 }

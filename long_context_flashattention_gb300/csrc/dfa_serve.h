@@ -83,7 +83,8 @@ struct PagedParams {
     const int32_t* q_lens;        // [B] or NULL
     int32_t Hq, G, T, causal, o_fp32;
     uint32_t inv_T;               // 2^21 / T, rounded up
-    int32_t row_groups;           // blocks of query rows per key/value head
+    int32_t row_groups;           // groups of query rows per key/value head
+    int32_t line_blocks;          // blocks of a group; block c of group rg: c * row_groups + rg
     int32_t segment_cost;         // in tiles
     int32_t whole;                // segments are not cut
     float scale_log2;

@@ -543,6 +543,13 @@ def test_decode_one_long_sequence(dtype, B, lens):
     check_decode(c, c.cuda(), randn(B, 6, 1, 64, seed=87))
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+def test_decode_long_sequences_of_several_row_groups(dtype):
+    """40 query rows of a head: three groups, each cut over its own blocks."""
+    c = ref.Cache(dtype, 2, 1, 64, 32, 330, [9000, 10500], seed=183)
+    check_decode(c, c.cuda(), randn(2, 10, 4, 64, seed=184), [4, 3])
+
+
 def test_decode_mostly_idle_batch():
     """A padded batch: slots without queries, some of them without rows, between the
     others and at both ends; their outputs are left as they were."""
