@@ -38,7 +38,7 @@
 //
 // Measured (64 ragged sequences of up to 8192 rows, 8 heads of 128, 1.12 GB in
 // bf16): bf16 168 us, 6.7 TB/s, 8-bit 92 us, 6.1 TB/s; with 16 query rows a head
-// 175 and 117 us (twice the products for the bytes).  One 128K sequence of 32
+// 175 and 115 us (twice the products for the bytes).  One 128K sequence of 32
 // heads, 8-bit: 162 us, 6.6 TB/s.  About 10 us of each are fixed: the launch, the way to
 // the first tile (lengths, page number, page), the last blocks' tail and the
 // merge, which make up all of the 9.4 us of one sequence of 1000 rows.
@@ -83,9 +83,11 @@ struct Cfg {
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kQRows = kRows * D * 2;  // a segment's queries, two segments
     // What a segment costs a block beside its tiles, in tiles.  Measured (the batch
-    // above; 1, 2, 3, 4): e4m3 92.6, 91.9, 92.8, 93.9 us, with 16 query rows 130, 126,
-    // 119, 115 us (117 now); bf16 with 16 rows 178, 176, 176, 177.
-    static constexpr int kSegmentCost = F8 && NB == 2 ? 4 : 2;
+    // above; 1, 2, 3, 4, 5, 6): e4m3 91.4, 90.8, 90.9, 91.7 us; with 16 query rows 136,
+    // 129, 126, 118, 115, 115; bf16 with 16 rows 177, 174, 174, 175.  256 sequences to
+    // 1024 rows: 56.3, 52.6, 52.7, 54.4; 121, 106, 97.8, 89.9, 87.2, 87.7; 110, 99.7, 97.7,
+    // 100.
+    static constexpr int kSegmentCost = F8 && NB == 2 ? 5 : 2;
     // 16 query rows take their operand from shared memory: O takes its registers
     static constexpr int kQ = NB > 1 ? NB * (D / 16) * 32 * 8 : 0;
     static constexpr int kSmem = 1024 + kStages * kStage + kJoin + 2 * kQRows + kQ;
