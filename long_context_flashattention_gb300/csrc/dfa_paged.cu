@@ -1134,13 +1134,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
 }
 
 // Rows of the segments that several blocks share: block c holds such a segment's
-// beginning, the info[c].z blocks of its group after it the rest.  Few partials: one warp a
-// row; many (a long sequence with few heads): the block's 8 warps share a row's.
-template <int D, bool F8, int ROWS>
+// beginning, the info[c].z blocks of its group after it the rest.  One warp a row; where most
+// segments have many partials (a long sequence with few heads) a block a row.
+template <int D, bool F8, int ROWS, bool BLOCK_A_ROW>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedParams p)
 {
-    __shared__ float wt[kPagedMaxCtas], red[8], red_n[8];
-    __shared__ float4 acc[256];
     cudaGridDependencySynchronize();  // the blocks' partials
     const int4 info = p.info[blockIdx.x];
     const int k = info.z + 1;
@@ -1161,45 +1159,62 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         return ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq;
     };
     constexpr int kPerRow = D / 4;  // lanes of 4 features
-    if (k <= 16) {
+    if constexpr (!BLOCK_A_ROW) {
         constexpr int kGroups = 32 / kPerRow;
         const int grp = lane / kPerRow, f = lane % kPerRow;
-        for (int r = blockIdx.y * 8 + warp; r < ROWS; r += 8 * gridDim.y) {
+        for (int r = warp; r < ROWS; r += 8) {
             const int64_t at = target(r);
             if (at < 0)
                 continue;
-            float4 y[16 / kGroups];  // all on their way at once
+            float4 y[16 / kGroups];  // of 16 partials, all on their way at once
+            auto fetch = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < 16; i += kGroups)
-                if (i + grp < k)
-                    y[i / kGroups] = *reinterpret_cast<const float4*>(
-                        p.part_o + (slot(i + grp) * ROWS + r) * D + f * 4);
-            float4 mnl = make_float4(kNone, kNone, 0.f, 0.f);
-            if (lane < k)
-                mnl = p.part_mnl[slot(lane) * ROWS + r];
+                for (int i = 0; i < 16; i += kGroups)
+                    if (c + i + grp < k)
+                        y[i / kGroups] = *reinterpret_cast<const float4*>(
+                            p.part_o + (slot(c + i + grp) * ROWS + r) * D + f * 4);
+            };
+            auto maxima = [&](int i) {
+                return i < k ? p.part_mnl[slot(i) * ROWS + r]
+                             : make_float4(kNone, kNone, 0.f, 0.f);
+            };
+            fetch(0);
+            float4 mnl = maxima(lane);
             float mx = mnl.x, nx = mnl.y;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
-                nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o, 16));
+            for (int i = lane + 32; i < k; i += 32) {
+                const float4 more = maxima(i);
+                mx = fmaxf(mx, more.x), nx = fmaxf(nx, more.y);
             }
-            mx = __shfl_sync(0xffffffffu, mx, 0);
-            nx = __shfl_sync(0xffffffffu, nx, 0);
-            const float w = ex2(mnl.x - mx);
-            float L = mnl.z * ex2(mnl.y - nx);
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                L += __shfl_xor_sync(0xffffffffu, L, o, 16);
-            L = __shfl_sync(0xffffffffu, L, 0);
+            for (int o = 16; o > 0; o >>= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
+            }
+            float L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0;;) {
+                const float w = ex2(mnl.x - mx);
+                if (lane < 16)
+                    L += mnl.z * ex2(mnl.y - nx);
 #pragma unroll
-            for (int i = 0; i < 16; i += kGroups) {
-                const float wi = __shfl_sync(0xffffffffu, w, i + grp);
-                if (i + grp < k) {
-                    o.x = fmaf(wi, y[i / kGroups].x, o.x), o.y = fmaf(wi, y[i / kGroups].y, o.y);
-                    o.z = fmaf(wi, y[i / kGroups].z, o.z), o.w = fmaf(wi, y[i / kGroups].w, o.w);
+                for (int i = 0; i < 16; i += kGroups) {
+                    const float wi = __shfl_sync(0xffffffffu, w, i + grp);
+                    if (c + i + grp < k) {
+                        const float4 x = y[i / kGroups];
+                        o.x = fmaf(wi, x.x, o.x), o.y = fmaf(wi, x.y, o.y);
+                        o.z = fmaf(wi, x.z, o.z), o.w = fmaf(wi, x.w, o.w);
+                    }
                 }
+                c += 16;
+                if (c >= k)
+                    break;
+                fetch(c);
+                mnl = maxima(c + (lane & 15));
             }
+#pragma unroll
+            for (int i = 8; i > 0; i >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, i, 16);
+            L = __shfl_sync(0xffffffffu, L, 0);
             if (kGroups == 2) {
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
                 o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
@@ -1209,59 +1224,75 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
             if (grp == 0)
                 write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
         }
-        return;
-    }
-    constexpr int kGroups = 256 / kPerRow;
-    const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
-    for (int r = blockIdx.y; r < ROWS; r += gridDim.y) {
+    } else {
+        constexpr int kGroups = 256 / kPerRow, kAhead = 4;
+        __shared__ float wt[kPagedMaxCtas], red_m[8], red_n[8], red_l[8];
+        __shared__ float4 acc[256];
+        const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
+        const int r = blockIdx.y;
         const int64_t at = target(r);
         if (at < 0)
-            continue;
+            return;
+        auto partial = [&](int i) {
+            return *reinterpret_cast<const float4*>(p.part_o + (slot(i) * ROWS + r) * D + f * 4);
+        };
+        float4 y[kAhead];  // on their way while the weights are made
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (grp + i * kGroups < k)
+                y[i] = partial(grp + i * kGroups);
+        float4 mnl[kPagedMaxCtas / 256];
         float mx = kNone, nx = kNone;
-        for (int i = threadIdx.x; i < k; i += 256) {
-            const float4 mnl = p.part_mnl[slot(i) * ROWS + r];
-            mx = fmaxf(mx, mnl.x), nx = fmaxf(nx, mnl.y);
+#pragma unroll
+        for (int i = 0; i < kPagedMaxCtas / 256; ++i) {
+            const int at_i = threadIdx.x + i * 256;
+            mnl[i] = at_i < k ? p.part_mnl[slot(at_i) * ROWS + r]
+                              : make_float4(kNone, kNone, 0.f, 0.f);
+            mx = fmaxf(mx, mnl[i].x), nx = fmaxf(nx, mnl[i].y);
         }
+#pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
         }
-        __syncthreads();  // the row before has been read
         if (lane == 0)
-            red[warp] = mx, red_n[warp] = nx;
+            red_m[warp] = mx, red_n[warp] = nx;
         __syncthreads();
         for (int w = 0; w < 8; ++w)
-            mx = fmaxf(mx, red[w]), nx = fmaxf(nx, red_n[w]);
-        __syncthreads();
+            mx = fmaxf(mx, red_m[w]), nx = fmaxf(nx, red_n[w]);
         float L = 0.f;
-        for (int i = threadIdx.x; i < k; i += 256) {
-            const float4 mnl = p.part_mnl[slot(i) * ROWS + r];
-            wt[i] = ex2(mnl.x - mx);
-            L += mnl.z * ex2(mnl.y - nx);
+#pragma unroll
+        for (int i = 0; i < kPagedMaxCtas / 256; ++i) {
+            wt[threadIdx.x + i * 256] = ex2(mnl[i].x - mx);
+            L += mnl[i].z * ex2(mnl[i].y - nx);
         }
+#pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             L += __shfl_xor_sync(0xffffffffu, L, o);
         if (lane == 0)
-            red[warp] = L;
+            red_l[warp] = L;
         __syncthreads();
-        L = 0.f;
-        for (int w = 0; w < 8; ++w)
-            L += red[w];
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float w, const float4& x) {
+            o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (grp + i * kGroups < k)
+                add(wt[grp + i * kGroups], y[i]);
 #pragma unroll 4
-        for (int i = grp; i < k; i += kGroups) {
-            const float4 y =
-                *reinterpret_cast<const float4*>(p.part_o + (slot(i) * ROWS + r) * D + f * 4);
-            const float w = wt[i];
-            o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y);
-            o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
-        }
+        for (int i = grp + kAhead * kGroups; i < k; i += kGroups)
+            add(wt[i], partial(i));
         acc[threadIdx.x] = o;
         __syncthreads();
         if (grp == 0) {
+            L = 0.f;
+            for (int w = 0; w < 8; ++w)
+                L += red_l[w];
             for (int i = 1; i < kGroups; ++i) {
-                const float4 y = acc[i * kPerRow + f];
-                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+                const float4 x = acc[i * kPerRow + f];
+                o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             }
             write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
         }
@@ -1305,13 +1336,17 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     e = cudaLaunchKernelEx(&cfg, decode_kernel<D, F8, NB>, tk, tv, p);
     if (e != cudaSuccess || p.whole)
         return e;
-    // The merge's blocks may start while the decode's end, and wait there.  With few
-    // segments each is cut into many partials: a block a row.
+    // The merge's blocks may start while the decode's end, and wait there.  With so few
+    // segments that each is cut into more partials than a warp takes at once, a block
+    // a row.  Measured (8 bits, 8K rows; a block a row, a warp a row): 2, 3, 5 sequences of 8
+    // heads 13.1 14.4, 14.9 15.5, 18.4 18.2 us; one of 1 head 13.5 22.1 (20K rows).
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(grid, segments * 8 >= p.line_blocks ? 1 : C::kRows);
+    const bool block_a_row = segments * 15 < p.line_blocks;
+    cfg.gridDim = dim3(grid, block_a_row ? C::kRows : 1);
     cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, merge_kernel<D, F8, C::kRows>, p);
+    return cudaLaunchKernelEx(&cfg, block_a_row ? merge_kernel<D, F8, C::kRows, true>
+                                                : merge_kernel<D, F8, C::kRows, false>, p);
 }
 
 template <int D, bool F8>
