@@ -685,8 +685,12 @@ template <int D, bool F8>
 __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int f, float mx,
                                           float nx, float L, float4 o)
 {
-    const float inv = L == 0.f ? 0.f : (F8 ? ex2(mx - nx) : 1.f) / L;  // (NaN stays NaN)
+    // 2^(mx - nx) in two halves: it may be below fp32's range where o makes up for it
+    const float half = F8 ? ex2(0.5f * (mx - nx)) : 1.f;
+    const float inv = L == 0.f ? 0.f : half / L;  // (NaN stays NaN)
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    if (F8)
+        o.x *= half, o.y *= half, o.z *= half, o.w *= half;
     if (p.o_fp32)
         *reinterpret_cast<float4*>((float*)p.o + at * D + f) = o;
     else

@@ -437,6 +437,25 @@ def test_decode_value_scales_at_the_ends_of_their_range(exps, T):
         check_decode(c, c.cuda(), randn(1, 2, T, 128, seed=159))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_results_at_the_end_of_fp32(d):
+    """Outputs next to fp32's smallest normal numbers: the quietest page has the
+    loudest scores, by a little more than 2^8, so that what the weighted sum is
+    relative to lies more than 2^126 below what the sum of probabilities is."""
+    c = ref.Cache(E4M3, 1, 1, d, 16, 8, [128], seed=185)
+    order = c.table[0].long()
+    k = torch.zeros(c.npages, 1, 16, d)
+    k[..., 0] = -96.0
+    k[order[0], ..., 0], k[order[4], ..., 0] = 0.0, 7.0
+    c.cells["k"] = k.to(E4M3)
+    c.scales["k"][:] = 1.0
+    c.scales["v"][:] = 2.0 ** -118
+    c.scales["v"][order[4]] = 2.0 ** -126
+    q = torch.zeros(1, 2, 1, d, dtype=BF16)
+    q[..., 0] = 1.0
+    check_decode(c, c.cuda(), q, scale=1.0)
+
+
 def test_decode_of_appended_values_near_the_largest():
     dev, q = None, randn(1, 2, 1, 64, seed=160)
     x = torch.randn(1, 1, 40, 64, generator=torch.Generator().manual_seed(161))
