@@ -41,7 +41,7 @@
 // 175 and 115 us (twice the products for the bytes).  One 128K sequence of 32
 // heads, 8-bit: 162 us, 6.6 TB/s.  About 10 us of each are fixed: the launch, the way to
 // the first tile (lengths, page number, page), the last blocks' tail and the
-// merge, which make up all of the 9.4 us of one sequence of 1000 rows.
+// merge, which make up all of the 9.0 us of one sequence of 1000 rows.
 //
 // Rounding: fp16 weights (half a step 2^-11) for 8-bit cells, and q as fp16
 // relative to the power of two of the row's largest element (exact but for
