@@ -43,10 +43,13 @@
 // the first tile (lengths, page number, page), the last blocks' tail and the
 // merge, which make up all of the 9.0 us of one sequence of 1000 rows.
 //
-// Rounding: fp16 weights (half a step 2^-11) for 8-bit cells, and q as fp16
-// relative to the power of two of the row's largest element (exact but for
-// elements 2^-14 below it); for bf16 cells q as it is and the weight as two bf16
-// terms (2^-16), since one would add as much error as the rounding of O.
+// Rounding: weights for 8-bit cells as two fp16 terms (2^-22); as one (2^-11) for more than 8
+// query rows with a bf16 output (2^-8), where the products bound the kernel.  Measured
+// (one term, two; us): 64 ragged sequences, 16 rows 116, 132, 8 rows 91.3, 92.4; 128K x
+// 32 heads 157.4, 158.6.  q for 8-bit cells as fp16 relative to the power
+// of two of the row's largest element (exact but for elements 2^-14 below it); for bf16
+// cells q as it is and the weight as two bf16 terms (2^-16), since one would add as much
+// error as the rounding of O.
 #include "dfa_serve.cuh"
 
 namespace dfa {
@@ -56,7 +59,17 @@ namespace paged {
 constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = kPagedTile;
-constexpr float kGrow = 8.f;               // rescale when the maximum grows by 2^8
+// M is set kHead below the running maximum, and set anew when a weight exceeds 2^kTop.
+// 8-bit cells have fp16 weights and use that type's range to its end (2^16): a weight
+// has all its bits down to 2^-25 of the largest one, and half a step of those below is
+// 2^-36 of it, so that the many small weights behind one large key add up to what they
+// should.  Measured (kHead 7, 11, 13; 64 ragged sequences, 16 query rows, us): 130.8,
+// 132.2, 133.6; with 8 rows no difference.
+template <bool F8>
+constexpr float kTop = F8 ? 15.f : 8.f;
+template <bool F8>
+constexpr float kHead = F8 ? 11.f : 0.f;
+constexpr float kGrow = 8.f;               // the sum's own reference grows by 2^8 at least
 constexpr float kNone = -1e30f;            // running maximum before the first key
 constexpr float kNear = 40.f;              // N = M while |log2 u_j| is at most this: the
                                            // terms are then 2^-80 or more of one another's
@@ -700,7 +713,7 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int 
         p.lse[at] = L == 0.f ? -INFINITY : (nx + log2f(L)) * kLn2;
 }
 
-template <int D, bool F8, int NB>
+template <int D, bool F8, int NB, bool TWO_TERMS>
 __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32_t ring,
                                         float* join, uint32_t q_rows, uint2* qs,
                                         const WaitCtx& wctx)
@@ -858,7 +871,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                                 make_float2(M[nb][0], M[nb][1]);
                     __syncwarp();
                 }
-                uint32_t pt[NB][2], pr[NB][2];  // P^T (and its bf16 remainder)
+                uint32_t pt[NB][2], pr[NB][2];  // P^T in two terms
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     // Exponents of the weights less the running maximum, rows 2t and
@@ -882,7 +895,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                                     x[k] = -INFINITY;
                     };
                     exponents(sc.y, M[nb][0], M[nb][1]);
-                    if (__any_sync(0xffffffffu, fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kGrow)) {
+                    if (__any_sync(0xffffffffu,
+                                   fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kTop<F8>)) {
                         exponents(sc.y, 0.f, 0.f);
                         float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, f[2];
 #pragma unroll
@@ -890,7 +904,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
-                            const float mn = fmaxf(M[nb][k], mx[k]);
+                            const float mn = fmaxf(M[nb][k], mx[k] - kHead<F8>);
                             f[k] = ex2(M[nb][k] - mn);
                             M[nb][k] = mn;
                             if (!F8 || !wide)
@@ -940,7 +954,14 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         if (F8) {
-                            pt[nb][k] = transpose8(pack_half2(w[2 * k], w[2 * k + 1]));
+                            const uint32_t hi = pack_half2(w[2 * k], w[2 * k + 1]);
+                            pt[nb][k] = transpose8(hi);
+                            if (TWO_TERMS) {
+                                const float2 y =
+                                    __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                pr[nb][k] =
+                                    transpose8(pack_half2(w[2 * k] - y.x, w[2 * k + 1] - y.y));
+                            }
                         } else {
                             const uint32_t hi = pack_bf16x2(w[2 * k], w[2 * k + 1]);
                             const uint32_t lo =
@@ -953,7 +974,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 // O^T += V^T P^T
                 auto weigh = [&](int nb, float(&d)[4], const uint32_t(&a)[4]) {
                     mma16816<F8>(d, a[0], a[1], a[2], a[3], pt[nb][0], pt[nb][1]);
-                    if (!F8)
+                    if (TWO_TERMS)
                         mma16816<F8>(d, a[0], a[1], a[2], a[3], pr[nb][0], pr[nb][1]);
                 };
                 if (!masked) {
@@ -1090,7 +1111,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         p.info[blockIdx.x] = info;
 }
 
-template <int D, bool F8, int NB>
+template <int D, bool F8, int NB, bool TWO_TERMS>
 __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ PagedParams p)
@@ -1133,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NB>::kResident)
             }
         }
     } else {
-        consume<D, F8, NB>(p, sh, ring, join, q_rows, qs, wctx);
+        consume<D, F8, NB, TWO_TERMS>(p, sh, ring, join, q_rows, qs, wctx);
     }
 }
 
@@ -1303,12 +1324,12 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     }
 }
 
-template <int D, bool F8, int NB>
+template <int D, bool F8, int NB, bool TWO_TERMS>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                    int num_sms, cudaStream_t stream)
 {
     using C = Cfg<D, F8, NB>;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F8, NB>,
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F8, NB, TWO_TERMS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess)
         return e;
@@ -1337,7 +1358,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = grid <= num_sms ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<D, F8, NB>, tk, tv, p);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<D, F8, NB, TWO_TERMS>, tk, tv, p);
     if (e != cudaSuccess || p.whole)
         return e;
     // The merge's blocks may start while the decode's end, and wait there.  With so few
@@ -1357,8 +1378,11 @@ template <int D, bool F8>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                         int num_sms, cudaStream_t stream)
 {
-    return p.G * p.T <= kPagedRows ? launch<D, F8, 1>(tk, tv, p, num_sms, stream)
-                                   : launch<D, F8, 2>(tk, tv, p, num_sms, stream);
+    if (p.G * p.T <= kPagedRows)
+        return launch<D, F8, 1, true>(tk, tv, p, num_sms, stream);
+    if (F8 && !p.o_fp32)  // (see "Rounding" above)
+        return launch<D, F8, 2, !F8>(tk, tv, p, num_sms, stream);
+    return launch<D, F8, 2, true>(tk, tv, p, num_sms, stream);
 }
 
 }  // namespace paged

@@ -1,0 +1,123 @@
+"""The ends of the serving operators' ranges, against plain fp64 forms: numbers far
+apart, very large or very small, and what the device reports."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as ref
+from long_context_flashattention_gb300 import dfa
+
+pytestmark = pytest.mark.gpu
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    dfa.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def randn(*shape, seed=0, dtype=BF16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit decode: the weights
+# ---------------------------------------------------------------------------
+def fine_tol(s, k, x, v, u, scale, terms=2):
+    """For one query row that sees keys k [n, d], values v with scales u [n], and has
+    the scores s (fp64): bounds on O's deviation relative to sum p |v|, and an
+    absolute one per feature.
+      dl   a score: d products summed in fp32, and its scaling; 2^x to two steps of
+           2^-23; a lane's sum takes two of every 64 keys one after the other, then
+           is joined over lanes, warps and blocks (64 additions);
+      acc  a tile is two products (the weights' two terms), each of which cuts the
+           sum off at 2^-23 once for its own terms and once for the total; as many
+           again as 16 tiles for the joins;
+      w    a weight as two fp16 terms, 2^-22, or as one, 2^-11; below fp16's normal
+           numbers half a step is 2^-25, where the largest weight is 2^11 or more."""
+    n, d = k.shape
+    tiles = -(-n // 64)
+    ds = (d + 4) * 2.0 ** -24 * scale * float((k.abs() @ x.abs()).max())
+    dl = ds + 2.0 ** -22 + (2 * tiles + 64) * 2.0 ** -24
+    acc = 4 * (tiles + 16) * 2.0 ** -23
+    p = torch.softmax(s, 0)
+    return (2 * dl + acc + 2.0 ** (-22 if terms == 2 else -11),
+            2.0 ** -36 * float((p * u).max()) * (v.abs() / u[:, None]).sum(0))
+
+
+@pytest.mark.parametrize("B,n", [(1, 131072), (600, 32768), (600, 2048)])
+@pytest.mark.parametrize("Hq", [4, 12])
+@pytest.mark.parametrize("p_sink,loud", [(0.9, 0), (0.99, 0), (0.996, 0), (0.99, 6), (0.996, -6)])
+def test_decode_tail_behind_a_sink(B, n, Hq, p_sink, loud):
+    """One key takes nearly all the probability and has a value of zero: the output
+    is the tail's, whose weights lie 2^9 to 2^25 below the largest.  A page in the
+    middle has louder or quieter values.  (All sequences read the same pages; with
+    600 of them most are not cut.)"""
+    d, page, scale = 64, 64, 0.125
+    g = torch.Generator().manual_seed(n + Hq)
+    pages = n // page
+    k = torch.randn(pages, 1, page, d, generator=g)
+    k[..., 0] = 0.0
+    v = 1.0 + torch.rand(pages, 1, page, d, generator=g)
+    k[0, 0, 0], v[0, 0, 0] = 0.0, 0.0
+    k[0, 0, 0, 0] = 1.0
+    vs = torch.ones(pages, 1)
+    vs[pages // 2] = 2.0 ** loud
+    k, v = k.to(E4M3), v.to(E4M3)
+    q = torch.randn(Hq, d, generator=g) * 0.5
+    # the tail's logits are normal with variance (63 / 64) / 4: E exp = exp(var / 2)
+    q[:, 0] = (math.log(n) + 0.123 + math.log(p_sink / (1 - p_sink))) / scale
+    q = q.to(BF16)
+    c = dfa.PagedCache(k.cuda(), v.cuda(),
+                       torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous(),
+                       torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                       k_scale=torch.ones(pages, 1, device="cuda"), v_scale=vs.cuda())
+    K, V = k.double().view(n, d), v.double().view(n, d) * vs.double().repeat_interleave(page, 0)
+    u = vs.double().repeat_interleave(page, 0)[:, 0]
+    qs = q.view(1, Hq, 1, d).expand(B, Hq, 1, d).contiguous().cuda()
+    for fp32 in (True, False):
+        o, lse = dfa.decode_paged(c, qs, scale=scale, out_fp32=fp32)
+        o, lse = o.cpu().double()[:, :, 0], lse.cpu().double()[:, :, 0]
+        for h in range(Hq):
+            x = q[h].double()
+            s = scale * (K @ x)
+            want = torch.softmax(s, 0) @ V
+            rel, floor = fine_tol(s, K, x, V, u, scale, 2 if fp32 or Hq <= 8 else 1)
+            tol = rel * want + floor
+            tol = tol + ref.HALF_STEP[torch.float32 if fp32 else BF16] * (want + tol)
+            err = (o[:, h] - want).abs()
+            assert (err <= tol).all(), (h, fp32, float((err / want).max()), float((tol / want).min()))
+            rel = fine_tol(s, K, x, V, u, scale)[0]
+            assert ((lse[:, h] - torch.logsumexp(s, 0)).abs() <= rel + 2.0 ** -23 * float(lse.max())).all()
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("d,page,lens", [(64, 16, [1, 200, 64]), (128, 64, [333, 17, 129]),
+                                         (128, 16, [90, 5, 700])])
+def test_decode_8_bit_in_fp32(d, page, lens, T):
+    """An fp32 output has fp32's accuracy: the weights are not rounded to fp16."""
+    c = ref.Cache(E4M3, 3, 2, d, page, -(-max(lens) // page), lens, seed=200 + d + page)
+    q, scale = randn(3, 8, T, d, seed=201), 1 / math.sqrt(d)
+    ql = [min(T, n) for n in lens]
+    O, LSE, _, _ = ref.attention(c, q, ql)
+    o, lse = dfa.decode_paged(c.cuda(), q.cuda(), out_fp32=True,
+                              q_lens=torch.tensor(ql, dtype=torch.int32, device="cuda"))
+    for b, L in enumerate(lens):
+        K, V = c.rows("k", b, L), c.rows("v", b, L)
+        pg = c.table[b, torch.arange(L) // page].long()
+        for h in range(8):
+            u = c.scales["v"][pg, h // 4].double()
+            for t in range(ql[b]):
+                n = L - ql[b] + t + 1
+                k, v, x = K[h // 4, :n], V[h // 4, :n], q[b, h, t].double()
+                s = scale * (k @ x)
+                rel, floor = fine_tol(s, k, x, v, u[:n], scale)
+                tol = rel * (torch.softmax(s, 0) @ v.abs()) + floor
+                ref.check(o[b, h, t], O[b, h, t], tol, torch.float32, (b, h, t))
+                assert abs(float(lse[b, h, t]) - float(LSE[b, h, t])) <= (
+                    rel + 2.0 ** -23 * abs(float(LSE[b, h, t])))
