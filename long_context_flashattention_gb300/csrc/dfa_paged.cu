@@ -9,11 +9,14 @@
 // The codes go into the matrix products as they are (e4m3 is exact in fp16); the
 // key's scale multiplies the score, the value's scale its weight.  Weights are
 // held as 2^(x_j + log2 u_j - M) with M the running maximum of the exponent, so
-// that they stay in fp16's range whatever the scales are.  The sum of
+// that they stay in fp16's range whatever the scales are.  The exponent is rounded to
+// fp32 like a score before M is taken off it, as M was when it was one of them: the
+// difference is then exact and at most zero however large both are.  The sum of
 // probabilities collects 2^(x_j - N) in fp32: N = M, and the weights over u_j are
 // its terms, as long as u_j is in [2^-40, 2^40]; from the first page on whose
 // scale is not (values near the type's ends, pages of zeros) N is the running
-// maximum of x_j itself.  O = 2^(M - N) (weighted sum) / (sum).
+// maximum of x_j itself, and M is held as N + D: D is small, and large scores drop out
+// of (x_j - N) + (log2 u_j - D).  O = 2^D (weighted sum) / (sum), D = 0 for M = N.
 //
 // What bounds it: HBM.  A cached row is read once and meets G*T query rows, a
 // few operations a byte: too few rows for a 128-row tcgen05 tile, so the products
@@ -123,10 +126,10 @@ struct Shared {
     uint64_t meet;                // of the consumer warps
     Piece run[2];                   // of the segments whose queries are there
     float4 scale[8][4];           // per stage and page: see page_scale
-    // maxima and sums of the warps at a segment's end; two sets, since a warp may
+    // N, D and sums of the warps at a segment's end; two sets, since a warp may
     // end the next segment while another still reads this one's
-    // (n: while it differs from m, a warp's entry is also where it is kept)
-    float m[2][kWarps][kPagedMaxRows], n[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
+    // (n: while D is not 0, a warp's entry is also where N is kept)
+    float n[2][kWarps][kPagedMaxRows], d[2][kWarps][kPagedMaxRows], l[2][kWarps][kPagedMaxRows];
     float qf[2][8];               // NB = 2: score factors of the query rows
     long long warp_sum[kThreads / 32];
     long long w0, w1, base;       // the block's range; first unit of sequence b
@@ -693,13 +696,13 @@ __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float s
     }
 }
 
-// Features f..f+3 of an output row, and its LSE: o is relative to 2^mx, L to 2^nx.
+// Features f..f+3 of an output row, and its LSE: o is relative to 2^(nx + dx), L to 2^nx.
 template <int D, bool F8>
-__device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int f, float mx,
-                                          float nx, float L, float4 o)
+__device__ __forceinline__ void write_row(const PagedParams& p, int64_t at, int f, float nx,
+                                          float dx, float L, float4 o)
 {
-    // 2^(mx - nx) in two halves: it may be below fp32's range where o makes up for it
-    const float half = F8 ? ex2(0.5f * (mx - nx)) : 1.f;
+    // 2^dx in two halves: it may be below fp32's range where o makes up for it
+    const float half = F8 ? ex2(0.5f * dx) : 1.f;
     const float inv = L == 0.f ? 0.f : half / L;  // (NaN stays NaN)
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
     if (F8)
@@ -781,7 +784,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         // keys up to all_see are visible to every row, keys from len on to none
         const int32_t all_see = p.causal ? len - n : len - 1;
         float O[NB][kMt][4], M[NB][2], l[NB][2];
-        bool wide = false;  // N has left M
+        bool wide = false;  // N has left M: M[][] is D, and N in shared memory
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -864,46 +867,60 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 float* own_n = sh.n[seg & 1][warp];
                 if (F8 && __builtin_expect(!wide && !(fabsf(sc.y) <= kNear), 0)) {
                     wide = true;
-                    if (g == 0)
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
+                    for (int nb = 0; nb < NB; ++nb) {
+                        if (g == 0)
                             *reinterpret_cast<float2*>(own_n + nb * 8 + 2 * t) =
                                 make_float2(M[nb][0], M[nb][1]);
+                        M[nb][0] = M[nb][1] = 0.f;
+                    }
                     __syncwarp();
                 }
                 uint32_t pt[NB][2], pr[NB][2];  // P^T in two terms
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    // Exponents of the weights less the running maximum, rows 2t and
-                    // 2t+1 of a pair, key g in x[0], x[1], key g + 8 in x[2], x[3].
+                    // Rows 2t and 2t+1 of a pair, key g in x[0], x[1], key g + 8 in x[2], x[3].
                     const uint64_t factor = F8 ? f2mul(rf[nb], f2pack(sc.x, sc.x)) : rf[nb];
                     uint64_t dot[2];
-                    float x[4];
+                    float x[4], w[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         dot[k] = f2add(f2pack(acc[nb][0][2 * k], acc[nb][0][2 * k + 1]),
                                        f2pack(acc[nb][1][2 * k], acc[nb][1][2 * k + 1]));
+                    // x = score + lu - (m0, m1), the former rounded first
                     auto exponents = [&](float lu, float m0, float m1) {
-                        const uint64_t off = f2pack((F8 ? lu : 0.f) - m0, (F8 ? lu : 0.f) - m1);
+                        const uint64_t off = f2pack(-m0, -m1);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            f2unpack(f2fma(dot[k], factor, off), x[2 * k], x[2 * k + 1]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint64_t sum = F8 ? f2fma(dot[k], factor, f2pack(lu, lu))
+                                                    : f2mul(dot[k], factor);
+                            f2unpack(f2add(sum, off), x[2 * k], x[2 * k + 1]);
+                        }
                         if (masked)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (base + g + 8 * (k >> 1) > lim[nb][k & 1])
                                     x[k] = -INFINITY;
                     };
-                    exponents(sc.y, M[nb][0], M[nb][1]);
-                    if (__any_sync(0xffffffffu,
-                                   fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kTop<F8>)) {
-                        exponents(sc.y, 0.f, 0.f);
-                        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, f[2];
+                    // does any x exceed a bound?
+                    auto exceeds = [&](float bound) {
+                        return __any_sync(0xffffffffu,
+                                          fmax3(x[0], x[1], fmaxf(x[2], x[3])) > bound);
+                    };
+                    // the rows' largest x
+                    auto largest = [&](float(&mx)[2]) {
+                        mx[0] = fmaxf(x[0], x[2]), mx[1] = fmaxf(x[1], x[3]);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+                    };
+                    // M (or D) up to what the largest x asks for, O (and the sum) with it
+                    auto raise = [&](const float(&mx)[2]) {
+                        float f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
                             const float mn = fmaxf(M[nb][k], mx[k] - kHead<F8>);
                             f[k] = ex2(M[nb][k] - mn);
                             M[nb][k] = mn;
@@ -915,41 +932,54 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 O[nb][m][k] *= f[k & 1];
-                        exponents(sc.y, M[nb][0], M[nb][1]);
-                    }
-                    float w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = ex2(x[k]);
+                    };
+                    float mx[2];
                     if (F8 && __builtin_expect(wide, 0)) {
                         float2* at = reinterpret_cast<float2*>(own_n + nb * 8 + 2 * t);
                         float2 N = *at;
                         exponents(0.f, N.x, N.y);
-                        if (__any_sync(0xffffffffu,
-                                       fmax3(x[0], x[1], fmaxf(x[2], x[3])) > kGrow)) {
+                        if (exceeds(kGrow)) {
                             exponents(0.f, 0.f, 0.f);
-                            float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) {
-                                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-                                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-                            }
+                            largest(mx);
                             mx[0] = fmaxf(N.x, mx[0]), mx[1] = fmaxf(N.y, mx[1]);
                             l[nb][0] *= ex2(N.x - mx[0]), l[nb][1] *= ex2(N.y - mx[1]);
+                            M[nb][0] += N.x - mx[0], M[nb][1] += N.y - mx[1];
                             N = make_float2(mx[0], mx[1]);
                             __syncwarp();
                             if (g == 0)
                                 *at = N;
                             exponents(0.f, N.x, N.y);
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            l[nb][k & 1] += ex2(x[k]);
                         __syncwarp();
-                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            l[nb][k & 1] += ex2(x[k]);
+                            x[k] += sc.y;
+                        }
+                        largest(mx);
+                        if (__any_sync(0xffffffffu, mx[0] - M[nb][0] > kTop<F8> ||
+                                                        mx[1] - M[nb][1] > kTop<F8>))
+                            raise(mx);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
+                            w[k] = ex2(x[k] - M[nb][k & 1]);
+                    } else {
+                        exponents(sc.y, M[nb][0], M[nb][1]);
+                        if (exceeds(kTop<F8>)) {
+                            exponents(sc.y, 0.f, 0.f);
+                            largest(mx);
+                            raise(mx);
+                            exponents(sc.y, M[nb][0], M[nb][1]);
+                            // kHead is rounded, too, where M is large (NaN stays NaN)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = x[k] > kTop<F8> ? kTop<F8> : x[k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            w[k] = ex2(x[k]);
                             l[nb][k & 1] = F8 ? fmaf(w[k], sc.z, l[nb][k & 1]) : l[nb][k & 1] + w[k];
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -1020,7 +1050,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 phase ^= 1;
             }
         }
-        // ---- join the warps: largest maximum, rescaled sums and O
+        // ---- join the warps: common references, rescaled sums and O
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1029,24 +1059,39 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
                 for (int o = 4; o < 32; o <<= 1)
                     l[nb][k] += __shfl_xor_sync(0xffffffffu, l[nb][k], o);
                 if (g == 0) {
-                    sh.m[seg & 1][warp][nb * 8 + 2 * t + k] = M[nb][k];
                     sh.l[seg & 1][warp][nb * 8 + 2 * t + k] = l[nb][k];
-                    if (F8 && !wide)
+                    if (!F8 || !wide)
                         sh.n[seg & 1][warp][nb * 8 + 2 * t + k] = M[nb][k];
+                    if (F8)
+                        sh.d[seg & 1][warp][nb * 8 + 2 * t + k] = wide ? M[nb][k] : 0.f;
                 }
             }
         if (!meet(sh, met, wctx))
             return;
+        // N and D of all warps together, and what a warp's O is multiplied by
+        const auto& ns = sh.n[seg & 1];
+        const auto& ds = sh.d[seg & 1];
+        auto common = [&](int r, float& nx, float& dx) {
+            nx = ns[0][r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w)
+                nx = fmaxf(nx, ns[w][r]);
+            dx = 0.f;
+            if (F8) {
+                dx = (ns[0][r] - nx) + ds[0][r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w)
+                    dx = fmaxf(dx, (ns[w][r] - nx) + ds[w][r]);
+            }
+        };
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int r = nb * 8 + 2 * t + k;
-                float mx = sh.m[seg & 1][0][r];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w)
-                    mx = fmaxf(mx, sh.m[seg & 1][w][r]);
-                const float f = ex2(M[nb][k] - mx);
+                float nx, dx;
+                common(r, nx, dx);
+                const float f = ex2((ns[warp][r] - nx) + ((F8 ? ds[warp][r] : 0.f) - dx));
                 if (r0 + r < R) {
                     float* dst = join + (warp * C::kRows + r) * C::kPitch;
 #pragma unroll
@@ -1072,13 +1117,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
         for (int r = threadIdx.x / kPerRow; r < C::kRows && r0 + r < R;
              r += 32 * kWarps / kPerRow) {
             const int f = threadIdx.x % kPerRow * 4;
-            const auto& ns = F8 ? sh.n[seg & 1] : sh.m[seg & 1];
-            float mx = sh.m[seg & 1][0][r], nx = ns[0][r], L = 0.f;
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                mx = fmaxf(mx, sh.m[seg & 1][w][r]);
-                nx = fmaxf(nx, ns[w][r]);
-            }
+            float nx, dx, L = 0.f;
+            common(r, nx, dx);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -1089,7 +1129,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             }
             if (!whole) {
                 if (f == 0)
-                    p.part_mnl[slot * C::kRows + r] = make_float4(mx, nx, L, 0.f);
+                    p.part_ndl[slot * C::kRows + r] = make_float4(nx, dx, L, 0.f);
                 *reinterpret_cast<float4*>(p.part_o + (slot * C::kRows + r) * D + f) = o;
                 continue;
             }
@@ -1098,7 +1138,7 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
             if (tq >= n)
                 continue;
             const int64_t at = ((int64_t)wk.b * p.Hq + h * p.G + gh) * p.T + tq;
-            write_row<D, F8>(p, at, f, mx, nx, L, o);
+            write_row<D, F8>(p, at, f, nx, dx, L, o);
         }
         if (!whole && wk.tile0 == 0) {
             // the group's blocks after this one that hold the rest: up to the last tile's
@@ -1199,28 +1239,40 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                         y[i / kGroups] = *reinterpret_cast<const float4*>(
                             p.part_o + (slot(c + i + grp) * ROWS + r) * D + f * 4);
             };
-            auto maxima = [&](int i) {
-                return i < k ? p.part_mnl[slot(i) * ROWS + r]
-                             : make_float4(kNone, kNone, 0.f, 0.f);
+            auto references = [&](int i) {
+                return i < k ? p.part_ndl[slot(i) * ROWS + r]
+                             : make_float4(kNone, 0.f, 0.f, 0.f);
+            };
+            auto warp_max = [](float x) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                return x;
             };
             fetch(0);
-            float4 mnl = maxima(lane);
-            float mx = mnl.x, nx = mnl.y;
+            float4 ndl = references(lane);
+            float nx = ndl.x, dx = 0.f;
+            bool apart = ndl.y != 0.f;
             for (int i = lane + 32; i < k; i += 32) {
-                const float4 more = maxima(i);
-                mx = fmaxf(mx, more.x), nx = fmaxf(nx, more.y);
+                const float4 more = references(i);
+                nx = fmaxf(nx, more.x);
+                apart |= more.y != 0.f;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
+            nx = warp_max(nx);
+            if (F8 && __any_sync(0xffffffffu, apart)) {
+                dx = (ndl.x - nx) + ndl.y;
+                for (int i = lane + 32; i < k; i += 32) {
+                    const float4 more = references(i);
+                    dx = fmaxf(dx, (more.x - nx) + more.y);
+                }
+                dx = warp_max(dx);
             }
             float L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = 0;;) {
-                const float w = ex2(mnl.x - mx);
+                const float w = ex2((ndl.x - nx) + (ndl.y - dx));
                 if (lane < 16)
-                    L += mnl.z * ex2(mnl.y - nx);
+                    L += ndl.z * ex2(ndl.x - nx);
 #pragma unroll
                 for (int i = 0; i < 16; i += kGroups) {
                     const float wi = __shfl_sync(0xffffffffu, w, i + grp);
@@ -1234,7 +1286,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 if (c >= k)
                     break;
                 fetch(c);
-                mnl = maxima(c + (lane & 15));
+                ndl = references(c + (lane & 15));
             }
 #pragma unroll
             for (int i = 8; i > 0; i >>= 1)
@@ -1247,11 +1299,11 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
             }
             if (grp == 0)
-                write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
+                write_row<D, F8>(p, at, f * 4, nx, dx, L, o);
         }
     } else {
         constexpr int kGroups = 256 / kPerRow, kAhead = 4;
-        __shared__ float wt[kPagedMaxCtas], red_m[8], red_n[8], red_l[8];
+        __shared__ float wt[kPagedMaxCtas], red_n[8], red_d[8], red_l[8];
         __shared__ float4 acc[256];
         const int grp = threadIdx.x / kPerRow, f = threadIdx.x % kPerRow;
         const int r = blockIdx.y;
@@ -1266,30 +1318,40 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         for (int i = 0; i < kAhead; ++i)
             if (grp + i * kGroups < k)
                 y[i] = partial(grp + i * kGroups);
-        float4 mnl[kPagedMaxCtas / 256];
-        float mx = kNone, nx = kNone;
+        auto block_max = [&](float x, float(&red)[8]) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0)
+                red[warp] = x;
+            __syncthreads();
+            for (int w = 0; w < 8; ++w)
+                x = fmaxf(x, red[w]);
+            return x;
+        };
+        float4 ndl[kPagedMaxCtas / 256];
+        float nx = kNone, dx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kPagedMaxCtas / 256; ++i) {
             const int at_i = threadIdx.x + i * 256;
-            mnl[i] = at_i < k ? p.part_mnl[slot(at_i) * ROWS + r]
-                              : make_float4(kNone, kNone, 0.f, 0.f);
-            mx = fmaxf(mx, mnl[i].x), nx = fmaxf(nx, mnl[i].y);
+            ndl[i] = at_i < k ? p.part_ndl[slot(at_i) * ROWS + r]
+                              : make_float4(kNone, 0.f, 0.f, 0.f);
+            nx = fmaxf(nx, ndl[i].x);
         }
+        nx = block_max(nx, red_n);
+        if (F8) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
+            for (int i = 0; i < kPagedMaxCtas / 256; ++i)
+                dx = fmaxf(dx, (ndl[i].x - nx) + ndl[i].y);
+            dx = block_max(dx, red_d);
+        } else {
+            dx = 0.f;
         }
-        if (lane == 0)
-            red_m[warp] = mx, red_n[warp] = nx;
-        __syncthreads();
-        for (int w = 0; w < 8; ++w)
-            mx = fmaxf(mx, red_m[w]), nx = fmaxf(nx, red_n[w]);
         float L = 0.f;
 #pragma unroll
         for (int i = 0; i < kPagedMaxCtas / 256; ++i) {
-            wt[threadIdx.x + i * 256] = ex2(mnl[i].x - mx);
-            L += mnl[i].z * ex2(mnl[i].y - nx);
+            wt[threadIdx.x + i * 256] = ex2((ndl[i].x - nx) + (ndl[i].y - dx));
+            L += ndl[i].z * ex2(ndl[i].x - nx);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -1319,7 +1381,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
                 const float4 x = acc[i * kPerRow + f];
                 o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             }
-            write_row<D, F8>(p, at, f * 4, mx, nx, L, o);
+            write_row<D, F8>(p, at, f * 4, nx, dx, L, o);
         }
     }
 }

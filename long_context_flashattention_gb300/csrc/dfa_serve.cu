@@ -262,14 +262,14 @@ int paged_rows(int64_t rows_per_head)
 }
 
 // Workspace of dfa_decode_paged: status word, one record per block, two partial
-// results (maxima and sum, O) per block.
+// results (references and sum, O) per block.
 struct PagedWs {
-    size_t info, mnl, o, bytes;
+    size_t info, ndl, o, bytes;
     PagedWs(int rows, int d)
     {
         info = kStatusBytes;
-        mnl = info + align256((size_t)kPagedMaxCtas * sizeof(int4));
-        o = mnl + align256((size_t)2 * kPagedMaxCtas * rows * sizeof(float4));
+        ndl = info + align256((size_t)kPagedMaxCtas * sizeof(int4));
+        o = ndl + align256((size_t)2 * kPagedMaxCtas * rows * sizeof(float4));
         bytes = o + align256((size_t)2 * kPagedMaxCtas * rows * d * 4);
     }
 };
@@ -491,7 +491,7 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     const PagedWs w(rows, p.c.d);
     p.row_groups = (G * T + rows - 1) / rows;
     p.info = (int4*)((char*)ws + w.info);
-    p.part_mnl = (float4*)((char*)ws + w.mnl);
+    p.part_ndl = (float4*)((char*)ws + w.ndl);
     p.part_o = (float*)((char*)ws + w.o);
     p.timeout_ns = kDefaultTimeoutNs;
     CUtensorMap tk, tv;

@@ -91,7 +91,8 @@ struct PagedParams {
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]
     int4* info;                   // [CTAs]: sequence, head and row group, CTAs that continue it
-    float4* part_mnl;             // [2 CTAs][rows]: what O and the sum are relative to (log2), sum
+    // [2 CTAs][rows]: what the sum is relative to (log2), what O is beyond that, sum
+    float4* part_ndl;
     float* part_o;                // [2 CTAs][rows][d]
     uint64_t timeout_ns;
 };

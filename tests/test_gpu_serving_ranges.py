@@ -121,3 +121,77 @@ def test_decode_8_bit_in_fp32(d, page, lens, T):
                 ref.check(o[b, h, t], O[b, h, t], tol, torch.float32, (b, h, t))
                 assert abs(float(lse[b, h, t]) - float(LSE[b, h, t])) <= (
                     rel + 2.0 ** -23 * abs(float(LSE[b, h, t])))
+
+
+# ---------------------------------------------------------------------------
+# decode: scores far from zero
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("Hq,T", [(2, 1), (12, 2)])
+@pytest.mark.parametrize("n,width", [(200, 13), (200, 40), (5000, 313)])
+@pytest.mark.parametrize("score", [-3e6, 7.3e8, -7.3e8, 1e25, -1e25])
+def test_decode_equal_scores_far_from_zero(dtype, Hq, T, n, width, score):
+    """Every score the same, very high or very low: the softmax is uniform over what
+    a token sees, in tables whose segments are cut and in short ones."""
+    uniform_over_equal_scores(dtype, Hq, T, n, width, score)
+
+
+def uniform_over_equal_scores(dtype, Hq, T, n, width, score):
+    d, page = 64, 16
+    c = ref.Cache(dtype, 1, 1, d, page, width, [n], seed=210)
+    k = torch.zeros(c.npages, 1, page, d)
+    k[..., 5] = -1.0 if dtype is E4M3 else -2.0 ** 60
+    c.cells["k"] = k.to(dtype)
+    if dtype is E4M3:
+        c.scales["k"][:] = 2.0 ** 60
+        c.scales["v"][:] = 0.25      # (equal: the kernel adds their logarithms to the scores)
+    q = torch.zeros(1, Hq, T, d)
+    q[..., 5] = -score / 2.0 ** 60
+    q = q.to(BF16)
+    x = -float(q[0, 0, 0, 5]) * 2.0 ** 60
+    o, lse = dfa.decode_paged(c.cuda(), q.cuda(), scale=1.0, out_fp32=True)
+    V = c.rows("v", 0, n)[0]
+    for t in range(T):
+        m = n - T + t + 1
+        want = V[:m].mean(0).expand(Hq, d)
+        # equal weights: an exact one, at most 2^8 below its reference, so that bf16's two
+        # terms and fp16's are exact too; m values summed in fp32 (as in fine_tol)
+        rel = 4 * (m / 64 + 17) * 2.0 ** -23 + (m + 64) * 2.0 ** -24
+        ref.check(o[0, :, t], want, rel * V[:m].abs().mean(0), torch.float32, t)
+        tol = 2.0 ** -21 * abs(x) + 2.0 ** -16   # log m to fp32's steps, and below
+        assert ((lse[0, :, t].cpu().double() - x - math.log(m)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("Hq,T", [(2, 1), (12, 2)])
+@pytest.mark.parametrize("loud", [13, 20, 24, 28, 40, 90])
+@pytest.mark.parametrize("exps", [[0], [0, -100, 3], [-100, 50], [-30, 30, -35]])
+def test_decode_one_key_far_above_the_others(dtype, Hq, T, loud, exps):
+    """Scores of up to 2^90 either way, and in 8 bits pages whose values are louder or
+    quieter by as much as 2^100: O is the value of the key with the highest score."""
+    if dtype is BF16 and len(exps) > 1:
+        pytest.skip("bf16 cells have no scales")
+    d, page, width, n = 64, 16, 40, 630
+    c = ref.Cache(dtype, 1, 1, d, page, width, [n], seed=214)
+    if dtype is E4M3:
+        e = torch.tensor([float(exps[i % len(exps)]) for i in range(width)])
+        c.scales["v"][c.table[0].long(), 0] = torch.exp2(e)
+    q = (randn(1, Hq, T, d, seed=215).float() * 2.0 ** loud).to(BF16)
+    K, V = c.rows("k", 0, n)[0], c.rows("v", 0, n)[0]
+    o, lse = dfa.decode_paged(c.cuda(), q.cuda(), scale=1.0, out_fp32=True)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    told = 0
+    for h in range(Hq):
+        for t in range(T):
+            m, x = n - T + t + 1, q[0, h, t].double()
+            s = K[:m] @ x
+            two = torch.topk(s, 2).values
+            ds = (d + 4) * 2.0 ** -24 * float((K[:m].abs() @ x.abs()).max())
+            if two[0] - two[1] <= 2 * ds + 100:   # 2^-100 / ln 2: times any other value nothing
+                continue
+            told += 1
+            want = V[int(s.argmax())]
+            # the weight is at most 2^15 and its own sum: O = (w c) 2^D / w, and two roundings
+            assert ((o[0, h, t] - want).abs() <= 2.0 ** -20 * want.abs() + 1e-20).all(), (h, t)
+            assert abs(float(lse[0, h, t]) - float(two[0])) <= ds + 2.0 ** -22 * abs(float(two[0]))
+    assert told >= 1
