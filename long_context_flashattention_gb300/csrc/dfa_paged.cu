@@ -53,6 +53,8 @@
 // of two of the row's largest element (exact but for elements 2^-14 below it); for bf16
 // cells q as it is and the weight as two bf16 terms (2^-16), since one would add as much
 // error as the rounding of O.
+#include <cfloat>
+
 #include "dfa_serve.cuh"
 
 namespace dfa {
@@ -73,7 +75,7 @@ constexpr float kTop = F8 ? 15.f : 8.f;
 template <bool F8>
 constexpr float kHead = F8 ? 11.f : 0.f;
 constexpr float kGrow = 8.f;               // the sum's own reference grows by 2^8 at least
-constexpr float kNone = -1e30f;            // running maximum before the first key
+constexpr float kNone = -FLT_MAX;          // running maximum before the first key
 constexpr float kNear = 40.f;              // N = M while |log2 u_j| is at most this: the
                                            // terms are then 2^-80 or more of one another's
                                            // weights, far from fp32's ends

@@ -163,6 +163,38 @@ def uniform_over_equal_scores(dtype, Hq, T, n, width, score):
 
 
 @pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("Hq,T", [(1, 1), (4, 3), (12, 2)])
+@pytest.mark.parametrize("n,width", [(3, 1), (1, 1), (200, 13), (200, 40), (5000, 313)])
+@pytest.mark.parametrize("score", [-3e30, -1.5e38, 1.5e38])
+def test_decode_lowest_scores_are_seen(dtype, Hq, T, n, width, score):
+    """Finite scores next to fp32's own lowest and highest count like any others (a row
+    without a visible key alone gives 0 and -inf)."""
+    if n < T:
+        pytest.skip("more tokens than rows")
+    uniform_over_equal_scores(dtype, Hq, T, n, width, score)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+def test_decode_lowest_scores_are_told_apart(dtype):
+    """One key a little less far down than the others takes all the weight."""
+    c = ref.Cache(dtype, 1, 1, 64, 16, 8, [120], seed=211)
+    k = torch.zeros(c.npages, 1, 16, 64)
+    k[..., 5] = -2.0
+    k[int(c.table[0, 4]), 0, 3, 5] = -1.75
+    if dtype is BF16:
+        k *= 2.0 ** 60
+    else:
+        c.scales["k"][:] = 2.0 ** 60
+    c.cells["k"] = k.to(dtype)
+    q = torch.zeros(1, 2, 1, 64, dtype=BF16)
+    q[..., 5] = 2.0 ** 45
+    o, lse = dfa.decode_paged(c.cuda(), q.cuda(), scale=1.0, out_fp32=True)
+    # the one weight is a power of two, its value has few bits: O is exact
+    assert torch.equal(o[0, 0, 0].cpu().double(), c.rows("v", 0, 120)[0, 67])
+    assert abs(float(lse[0, 0, 0]) / (-1.75 * 2.0 ** 105) - 1) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
 @pytest.mark.parametrize("Hq,T", [(2, 1), (12, 2)])
 @pytest.mark.parametrize("loud", [13, 20, 24, 28, 40, 90])
 @pytest.mark.parametrize("exps", [[0], [0, -100, 3], [-100, 50], [-30, 30, -35]])
