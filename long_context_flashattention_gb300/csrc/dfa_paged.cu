@@ -452,8 +452,8 @@ __device__ __forceinline__ void produce(const PagedParams& p, Shared& sh, uint32
                 id = -1;
             } else if (F8) {
                 const int64_t at = (int64_t)id * p.c.Hkv + h;
-                ks = __ldg(p.c.k_scale + at);
-                vs = __ldg(p.c.v_scale + at);
+                ks = __ldcg(p.c.k_scale + at);  // (an append may have just raised them)
+                vs = __ldcg(p.c.v_scale + at);
             }
         };
         check_window();

@@ -227,3 +227,44 @@ def test_decode_one_key_far_above_the_others(dtype, Hq, T, loud, exps):
             assert ((o[0, h, t] - want).abs() <= 2.0 ** -20 * want.abs() + 1e-20).all(), (h, t)
             assert abs(float(lse[0, h, t]) - float(two[0])) <= ds + 2.0 ** -22 * abs(float(two[0]))
     assert told >= 1
+
+
+# ---------------------------------------------------------------------------
+# an append and the decode that is launched while it runs
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_captured_behind_an_append_that_raises_scales(d, page):
+    """A step's append raises the scales of the page that the decode behind it reads,
+    moves on to new pages, and the lengths advance just before: 60 replays of one
+    graph, each against the same calls made one at a time."""
+    B, Hq, Hkv = 2, 4, 2
+    c = ref.Cache(E4M3, B, Hkv, d, page, 12, [3, page], seed=240)
+    a, b = c.cuda(), c.cuda()
+    ws = dfa.paged_workspace(a, Hq, 1)
+    ins = [torch.zeros(B, h, 1, d, dtype=BF16, device="cuda") for h in (Hq, Hkv, Hkv)]
+    spec = dfa.rope_spec(d, layout="half")
+    out, lse = torch.empty_like(ins[0]), torch.empty(B, Hq, 1, device="cuda")
+    qr = torch.empty_like(ins[0])
+    steps = 60
+
+    def step(cache, sync):
+        cache.seq_lens.add_(1)
+        dfa.cache_append(cache, ins[1], ins[2], rope=spec, q=ins[0], q_out=qr, ws=ws)
+        if sync:
+            torch.cuda.synchronize()
+        dfa.decode_paged(cache, qr, out=out, lse=lse, ws=ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(a, False)
+    for i in range(steps):
+        for j, t in enumerate(ins):
+            # louder and louder within a page, then quiet again
+            t.copy_(randn(*t.shape, seed=241 + 3 * i + j) * (2.0 ** (i % page) if j else 1.0))
+        g.replay()
+        got = out.clone(), lse.clone()
+        step(b, True)
+        assert torch.equal(out, got[0]) and torch.equal(lse, got[1]), i
+    dfa.stream_status(ws)
+    for n in ("k_scale", "v_scale"):
+        assert torch.equal(getattr(a, n), getattr(b, n))
