@@ -493,8 +493,9 @@ typedef struct dfa_paged_cache {
  * Rows from n on are not read.  With rope, K is rotated in fp32 and rounded
  * once to the cell's type (NULL: stored as it is); V is stored as it is.
  * E4M3: a NaN or an infinity is stored as NaN and does not count towards the
- * scale; rows of a touched page that were there before are requantised when its
- * scale rises; a page whose row 0 is among the new rows starts a new scale.
+ * scale; values above 240 * 2^120 are stored as that (256 * 2^120 would be an
+ * infinity); rows of a touched page that were there before are requantised when
+ * its scale rises; a page whose row 0 is among the new rows starts a new scale.
  * Storing the same rows again gives the same cells.
  *   k, v [B,Hkv,T,d] bf16 (strided); 1 <= T < 2^30.
  *   q, q_out [B,Hq,T,d] bf16 (strided): rows below new_lens[b] are rotated
@@ -512,9 +513,10 @@ dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* r
 /*
  * dfa_cache_gather -- cached rows [pos0, pos0 + L) of every sequence as
  * contiguous bf16, for calls that read plain tensors (a prompt's next chunk
- * attends to them with dfa_chunk_fwd).  code * scale is exact in bf16 (except
- * below its smallest normal number).  Rows behind a sequence's end are left as
- * they were.
+ * attends to them with dfa_chunk_fwd).  code * scale is exact in bf16 for the
+ * power-of-two scales that dfa_cache_append sets (except below bf16's smallest
+ * normal number), and rounded once for other scales.  Rows behind a sequence's
+ * end are left as they were.
  *   k_out, v_out [B,Hkv,L,d] bf16, 16-byte aligned; either may be NULL.
  *   ws: 256 bytes (the status word).
  */

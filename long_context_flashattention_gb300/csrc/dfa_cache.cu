@@ -58,14 +58,18 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
                       e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
+// The largest value that a cell may stand for: from scale 2^120 on, bf16's largest values
+// would be rounded up to 2^128, an infinity.
+constexpr float kLargest = 240.f * 0x1p120f;
+
 // Infinities become NaN (the conversion would store them as the largest finite
-// cell).
-__device__ __forceinline__ void no_infinities(float (&x)[8])
+// cell), and what is beyond the largest value that value.
+__device__ __forceinline__ void bound_values(float (&x)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (fabsf(x[i]) == INFINITY)
-            x[i] = NAN;
+        if (fabsf(x[i]) > kLargest)
+            x[i] = fabsf(x[i]) == INFINITY ? NAN : copysignf(kLargest, x[i]);
 }
 
 // Largest |x|, NaN left out (fmaxf does)
@@ -281,10 +285,10 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
         slot += step;
         step = -step;
         amax = group_max(amax, group, thread, threads, words, set);
-        if (amax == INFINITY) {  // (rare) once more, over finite values
+        if (amax > kLargest) {  // (rare) once more, over bounded values
             if (mine) {
-                no_infinities(a);
-                no_infinities(c);
+                bound_values(a);
+                bound_values(c);
             }
             amax = group_max(mine ? abs_max8(abs_max8(0.f, a), c) : 0.f, group, thread, threads,
                              words, set);

@@ -268,3 +268,52 @@ def test_captured_behind_an_append_that_raises_scales(d, page):
     dfa.stream_status(ws)
     for n in ("k_scale", "v_scale"):
         assert torch.equal(getattr(a, n), getattr(b, n))
+
+
+# ---------------------------------------------------------------------------
+# cells
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_largest_values_stay_finite(d, page):
+    """bf16's largest values, either sign, in an 8-bit page: the scale is 2^120 and
+    the largest finite multiple of it in a cell 240, since 256 * 2^120 is an
+    infinity.  Rows stored before are raised to the same scale; infinities and NaN
+    are still NaN."""
+    big = float(torch.finfo(BF16).max)
+    c = ref.Cache(E4M3, 2, 2, d, page, 2, [page + 4, 9], seed=220)
+    dev = c.cuda()
+    ws = dfa.paged_workspace(dev, 4, 1)
+    v = randn(2, 2, 6, d, seed=221)
+    edge = [big, -big, 1.9375 * 2.0 ** 127, -1.9375 * 2.0 ** 127, 1.9296875 * 2.0 ** 127,
+            1.875 * 2.0 ** 127, 448 * 2.0 ** 119, -2.0 ** 127]
+    want = [240.0, -240.0, 240.0, -240.0, 240.0, 240.0, 224.0, -128.0]
+    v[:, :, 3, :8] = torch.tensor(edge).to(BF16)
+    v[:, :, 4] = big
+    v[0, :, 5, 3], v[0, :, 5, 4] = float("nan"), float("inf")
+    dev.seq_lens -= 6
+    old = torch.full((2, 2, 2, d), 3e38, dtype=BF16)     # (scale 2^120) behind a page's beginning
+    dfa.cache_append(dev, old.cuda(), old.cuda(), ws=ws)
+    dev.seq_lens += 6
+    dfa.cache_append(dev, v.cuda(), v.cuda(), ws=ws)
+    dfa.stream_status(ws)
+    k_out, v_out = dfa.cache_gather(dev, page + 4, ws=ws)
+    for name, got in (("k", k_out), ("v", v_out)):
+        for b, L in enumerate([page + 4, 9]):
+            for j in (3, 4):
+                at = L - 6 + j
+                pg = int(c.table[b, at // page])
+                row = getattr(dev, name)[pg, :, at % page].float().cpu()
+                assert (getattr(dev, name + "_scale")[pg].cpu() == 2.0 ** 120).all()
+                assert (row == 240.0).all() if j == 4 else row[:, :8].tolist() == [want] * 2
+                assert torch.equal(got[b, :, at].double().cpu(), row.double() * 2.0 ** 120)
+            assert got[b, :, L - 6:L].isfinite().sum() == 2 * 6 * d - (4 if b == 0 else 0)
+    # a token that sees row 4 of the second sequence alone next to quiet ones
+    one = dfa.PagedCache(dev.k, dev.v, dev.block_table[1:].contiguous(),
+                         torch.tensor([8], dtype=torch.int32, device="cuda"),
+                         k_scale=torch.ones_like(dev.k_scale), v_scale=dev.v_scale)
+    q = torch.zeros(1, 2, 1, d, dtype=BF16, device="cuda")
+    o, lse = dfa.decode_paged(one, q, out_fp32=True)
+    V = v_out[1, :, :8].double().cpu()
+    assert o.isfinite().all()
+    ref.check(o[0, :, 0], V.mean(1), 2.0 ** -18 * V.abs().mean(1), torch.float32)
+    assert (lse.cpu().double() - math.log(8)).abs().max() <= 2.0 ** -20
