@@ -462,9 +462,9 @@ dfa_status dfa_rope(const dfa_rope_spec* spec, int32_t B, int32_t H, int64_t L, 
  * Lengths and page numbers are checked on the device: seq_lens[b] outside
  * [0, max_pages*page], a new or query length outside [0, T] or above the
  * sequence's, or a page outside [0, npages) is skipped (nothing is read or
- * written through it) and sets the workspace's status word, which
- * dfa_stream_status reports as DFA_ERR_BOUNDS; that sequence's outputs are
- * then invalid. */
+ * written through it) and sets the status word (the cache's status, or else the
+ * workspace's), which dfa_stream_status reports as DFA_ERR_BOUNDS; that
+ * sequence's outputs are then invalid. */
 enum { DFA_CACHE_BF16 = 0, DFA_CACHE_E4M3 = 1 };
 
 typedef struct dfa_paged_cache {
@@ -483,6 +483,9 @@ typedef struct dfa_paged_cache {
     int32_t max_pages;   /* width of block_table                            */
     const int32_t* block_table; /* [B][max_pages]                           */
     const int32_t* seq_lens;    /* [B]                                      */
+    void* status;        /* 256 zeroed bytes whose status word the calls on
+                            this cache set, whatever their workspaces (calls
+                            at once may share it); NULL: the workspace's    */
 } dfa_paged_cache;
 
 /*

@@ -199,6 +199,8 @@ dfa_status make_cache(CacheView* v, const dfa_paged_cache* c, void* ws, const ch
         return set_error(DFA_ERR_INVALID_ARG, "%s: a cache pointer is NULL", call);
     if (!aligned16(c->k) || !aligned16(c->v))
         return set_error(DFA_ERR_UNSUPPORTED, "%s: k and v must be 16-byte aligned", call);
+    if (((uintptr_t)c->status & 255u) != 0)
+        return set_error(DFA_ERR_INVALID_ARG, "%s: status must be 256-byte aligned", call);
     v->k = c->k;
     v->v = c->v;
     v->k_scale = e4m3 ? c->k_scale : nullptr;
@@ -214,7 +216,7 @@ dfa_status make_cache(CacheView* v, const dfa_paged_cache* c, void* ws, const ch
     v->page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
     v->max_pages = c->max_pages;
     v->e4m3 = e4m3;
-    v->status = (DevStatus*)ws;
+    v->status = (DevStatus*)(c->status ? c->status : ws);
     return DFA_OK;
 }
 

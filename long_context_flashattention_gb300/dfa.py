@@ -101,7 +101,8 @@ class PagedCacheDesc(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
-                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
@@ -646,7 +647,11 @@ class PagedCache:
     strided: k and v can be two halves of one tensor), with k_scale and v_scale
     [npages,Hkv] fp32 for 8 bits; block_table [B,max_pages] and seq_lens [B]
     int32.  Change their contents freely (cache.seq_lens += 1); a new table or
-    batch is a new PagedCache: the calls go by the tensors it was made with."""
+    batch is a new PagedCache: the calls go by the tensors it was made with.
+
+    The device checks lengths and pages.  A call that was given no workspace reports
+    them to cache.status, one with a workspace to that: stream_status(cache.status)
+    or stream_status(ws) raises what was found."""
 
     def __init__(self, k, v, block_table, seq_lens, k_scale=None, v_scale=None):
         dev = k.device
@@ -684,6 +689,11 @@ class PagedCache:
             _int32(block_table, "block_table", (B, max_pages), dev),
             _int32(seq_lens, "seq_lens", (B,), dev))
         self._ref = ctypes.byref(self.desc)
+        # for calls without a workspace, whose own nobody could read
+        self.status = torch.zeros(256, dtype=torch.uint8, device=dev)
+        self._own = PagedCacheDesc.from_buffer_copy(self.desc)
+        self._own.status = self.status.data_ptr()
+        self._own_ref = ctypes.byref(self._own)
 
     def __setattr__(self, name, value):
         if self.__dict__.get(name, value) is not value:
@@ -697,18 +707,21 @@ class PagedCache:
 
 def paged_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:
     """A workspace for the calls on this cache: Hq query heads, T tokens a
-    sequence at most.  It serves one call at a time."""
+    sequence at most.  It serves one call at a time, and the device's errors are then
+    reported to it."""
     # more rows than decode_paged takes: the other calls need the status word only
     n = _paged_desc(cache.B, Hq or cache.Hkv, cache.Hkv, T, cache.d, True, 1.0, False)[1]
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
 def _ws(ws, nbytes, cache, stream):
+    """A call's workspace, and the cache as the call sees it: errors go to the caller's
+    workspace, without one to the cache's status."""
     if ws is None:
-        return _new(stream, (nbytes,), torch.uint8, cache.device)
+        return _new(stream, (nbytes,), torch.uint8, cache.device), cache._own_ref
     if ws.dtype is not torch.uint8 or ws.device != cache.device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {cache.device}")
-    return ws
+    return ws, cache._ref
 
 
 def _plain(t, name, dtype, device, shape):
@@ -742,7 +755,7 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
     shape = (cache.B, cache.Hkv, T, cache.d)
     kp, ks = _rows(k, "k", torch.bfloat16, dev, shape)
     vp, vs = _rows(v, "v", torch.bfloat16, dev, shape)
-    ws = _ws(ws, 256, cache, stream)
+    ws, ref = _ws(ws, 256, cache, stream)
     Hq, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
         Hq = q.shape[1]
@@ -755,7 +768,7 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
             op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    code = lib().dfa_cache_append(cache._ref, None if rope is None else ctypes.byref(rope), T,
+    code = lib().dfa_cache_append(ref, None if rope is None else ctypes.byref(rope), T,
                                   _int32(new_lens, "new_lens", (cache.B,), dev), kp, ks, vp, vs,
                                   Hq, qp, qs, op, os_, ws.data_ptr(), ws.numel(), raw)
     if code:
@@ -774,8 +787,8 @@ def cache_gather(cache: PagedCache, L, pos0=0, k_out=None, v_out=None, ws=None, 
         k_out = _new(stream, shape, torch.bfloat16, dev)
     if v_out is None:
         v_out = _new(stream, shape, torch.bfloat16, dev)
-    ws = _ws(ws, 256, cache, stream)
-    code = lib().dfa_cache_gather(cache._ref, pos0, L,
+    ws, ref = _ws(ws, 256, cache, stream)
+    code = lib().dfa_cache_gather(ref, pos0, L,
                                   _plain(k_out, "k_out", torch.bfloat16, dev, shape),
                                   _plain(v_out, "v_out", torch.bfloat16, dev, shape),
                                   ws.data_ptr(), ws.numel(), raw)
@@ -805,8 +818,8 @@ def decode_paged(cache: PagedCache, q, q_lens=None, causal=True, scale=None, out
         lse = _new(stream, (B, Hq, T), torch.float32, dev)
     desc, need = _paged_desc(B, Hq, cache.Hkv, T, d, bool(causal),
                              1.0 / math.sqrt(d) if scale is None else scale, bool(out_fp32))
-    ws = _ws(ws, need, cache, stream)
-    code = lib().dfa_decode_paged(desc, cache._ref, T, _int32(q_lens, "q_lens", (B,), dev), qp, qs,
+    ws, ref = _ws(ws, need, cache, stream)
+    code = lib().dfa_decode_paged(desc, ref, T, _int32(q_lens, "q_lens", (B,), dev), qp, qs,
                                   _plain(out, "out", o_dtype, dev, shape),
                                   _plain(lse, "lse", torch.float32, dev, (B, Hq, T)),
                                   ws.data_ptr(), ws.numel(), raw)

@@ -317,3 +317,49 @@ def test_largest_values_stay_finite(d, page):
     assert o.isfinite().all()
     ref.check(o[0, :, 0], V.mean(1), 2.0 ** -18 * V.abs().mean(1), torch.float32)
     assert (lse.cpu().double() - math.log(8)).abs().max() <= 2.0 ** -20
+
+
+# ---------------------------------------------------------------------------
+# errors of the device
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+def test_errors_without_a_workspace_are_kept(dtype):
+    """Calls that were given no workspace report bad pages and lengths to the cache's
+    own status word; with a workspace, to that."""
+    c = ref.Cache(dtype, 2, 2, 64, 16, 3, [40, 40], seed=230)
+    dev = c.cuda()
+    k, q = randn(2, 2, 2, 64, seed=231).cuda(), randn(2, 4, 1, 64, seed=232).cuda()
+    calls = (lambda **kw: dfa.cache_append(dev, k, k, **kw),
+             lambda **kw: dfa.cache_gather(dev, 48, **kw),
+             lambda **kw: dfa.decode_paged(dev, q, **kw))
+    ws = dfa.paged_workspace(dev, 4, 1)
+    for bad in ("page", "length"):
+        for f in calls:
+            f()
+            dfa.stream_status(dev.status)
+        if bad == "page":
+            keep = int(dev.block_table[1, 2])
+            dev.block_table[1, 2] = c.npages
+        else:
+            dev.seq_lens[1] = 49
+        for f in calls:
+            f()
+            with pytest.raises(dfa.DfaError) as e:
+                dfa.stream_status(dev.status)
+            assert e.value.code == 6
+            dfa.stream_status(dev.status)  # read and cleared
+            f(ws=ws)
+            dfa.stream_status(dev.status)
+            with pytest.raises(dfa.DfaError):
+                dfa.stream_status(ws)
+        if bad == "page":
+            dev.block_table[1, 2] = keep
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls[2]()
+        g.replay()
+        if bad == "length":
+            with pytest.raises(dfa.DfaError):
+                dfa.stream_status(dev.status)
+            dev.seq_lens[1] = 40
+        dfa.stream_status(dev.status)
