@@ -46,13 +46,13 @@
 // the first tile (lengths, page number, page), the last blocks' tail and the
 // merge, which make up all of the 9.0 us of one sequence of 1000 rows.
 //
-// Rounding: weights for 8-bit cells as two fp16 terms (2^-22); as one (2^-11) for more than 8
-// query rows with a bf16 output (2^-8), where the products bound the kernel.  Measured
-// (one term, two; us): 64 ragged sequences, 16 rows 116, 132, 8 rows 91.3, 92.4; 128K x
-// 32 heads 157.4, 158.6.  q for 8-bit cells as fp16 relative to the power
-// of two of the row's largest element (exact but for elements 2^-14 below it); for bf16
-// cells q as it is and the weight as two bf16 terms (2^-16), since one would add as much
-// error as the rounding of O.
+// Rounding: weights for 8-bit cells as two fp16 terms (2^-22); as one (2^-11) for more
+// than 8 query rows with a bf16 output (2^-8), where the products bound the kernel.
+// Measured (one term, two; us): 64 ragged sequences, 16 rows 116, 132, 8 rows 91.3, 92.4;
+// 128K x 32 heads 157.4, 158.6.  q for 8-bit cells as fp16 relative to a power of two of
+// the row: exact but for elements below 2^-31 of its largest one, which are off by 2^-39 of
+// that at most.  For bf16 cells q as it is and the weight as two bf16 terms (2^-16), since
+// one would add as much error as the rounding of O.
 #include <cfloat>
 
 #include "dfa_serve.cuh"
@@ -653,8 +653,9 @@ struct Values<C, true> {
 
 // 8 query rows in shared memory as the products' operand (16 features a step, two
 // words a lane), rows that are not `there` (lane: row g) as zeros.  Returns the
-// factor of row g's scores.  e4m3: as fp16 relative to the power of two of the
-// row's largest element, in the order in which the lanes hold K's features.
+// factor of row g's scores.  e4m3: as fp16 relative to a power of two, at which the
+// row's largest element is next to fp16's end, in the order in which the lanes hold K's
+// features.
 template <int D, bool F8>
 __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float scale_log2,
                                               uint32_t (&q)[D / 16][2])
@@ -687,7 +688,8 @@ __device__ __forceinline__ float load_queries(uint32_t rows, bool there, float s
                 amax = fmaxf(amax, fmaxf(fabsf(bf16lo(q[s][k])), fabsf(bf16hi(q[s][k]))));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+        // the largest element to [2^14, 2^15): those down to 2^-31 of it stay exact
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126) - 14;
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)

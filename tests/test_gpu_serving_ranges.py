@@ -363,3 +363,34 @@ def test_errors_without_a_workspace_are_kept(dtype):
                 dfa.stream_status(dev.status)
             dev.seq_lens[1] = 40
         dfa.stream_status(dev.status)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit decode: the queries
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("loud", [12, 18, 26])
+def test_decode_queries_with_one_loud_element(loud, T):
+    """An element 2^26 times the others, where the keys are zero: the others count
+    in full."""
+    d, lens = 128, [70, 300]
+    c = ref.Cache(E4M3, 2, 1, d, 16, 19, lens, seed=212)
+    x = c.cells["k"].float()
+    x[..., 7] = torch.where(x[..., 7].isnan(), x[..., 7], torch.tensor(0.0))
+    c.cells["k"] = x.to(E4M3)
+    q = randn(2, 2, T, d, seed=213)
+    q[..., 7] = 1.5 * 2.0 ** loud
+    O, LSE, _, _ = ref.attention(c, q)
+    o, lse = dfa.decode_paged(c.cuda(), q.cuda(), out_fp32=True)
+    for b, L in enumerate(lens):
+        K, V = c.rows("k", b, L)[0], c.rows("v", b, L)[0]
+        u = c.scales["v"][c.table[b, torch.arange(L) // 16].long(), 0].double()
+        for h in range(2):
+            for t in range(T):
+                n, x = L - T + t + 1, q[b, h, t].double()
+                s = (K[:n] @ x) / math.sqrt(d)
+                rel, floor = fine_tol(s, K[:n], x, V[:n], u[:n], 1 / math.sqrt(d))
+                tol = rel * (torch.softmax(s, 0) @ V[:n].abs()) + floor
+                ref.check(o[b, h, t], O[b, h, t], tol, torch.float32, (b, h, t))
+                assert abs(float(lse[b, h, t]) - float(LSE[b, h, t])) <= (
+                    rel + 2.0 ** -23 * abs(float(LSE[b, h, t])))
