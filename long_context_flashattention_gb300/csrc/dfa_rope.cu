@@ -102,10 +102,11 @@ struct RopeRows {
 };
 
 // Few heads: the lanes that heads do not take go to other tokens.  Measured (bf16,
-// d 128, 2^20 rows of 1, 2, 4, 8 heads, us): 140, 100, 89, 86, where a warp a
-// token takes 515, 272, 146, 101.  Two rows a lane and 4 blocks an SM; 2 and 3: 129,
-// 101, 98, 95; 2 and 5 (spills): 168, 123, 113, 111; 4 and 2: 160, 129, 112, 106.
-// One head is bound by its own angles, 64 sincospif a row.
+// d 128, 2^20 rows of 1, 2, 4, 8 heads, us): 129, 99, 91, 89, where a warp a
+// token takes 515, 272, 146, 101.  Two rows a lane and 4 blocks an SM; with sincospif,
+// 141, 102, 92, 89, as against 2 and 3: 129, 101, 98, 95; 2 and 5 (spills): 168, 123,
+// 113, 111; 4 and 2: 160, 129, 112, 106.  One head is bound by its own 64 angles a row
+// (constant ones in their place: 89, 92, 92, 90).
 constexpr int kFewBatch = 2;
 
 template <typename E, int D, int G>

@@ -14,7 +14,8 @@ struct DevStatus;
 
 // A rotary embedding as the kernels use it.  turn[t] is pair t's frequency as a
 // 64-bit fraction of a full turn, so that (position * turn[t]) mod 2^64 is the
-// reduced angle: exact for every int32 position, in integer arithmetic.
+// reduced angle, in integer arithmetic: the reduction adds nothing to what the
+// frequency itself, made in fp64, is off by (about 2^-52 of it).
 struct RopeTable {
     uint64_t turn[64];
     float gain;

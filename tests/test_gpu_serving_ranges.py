@@ -394,3 +394,26 @@ def test_decode_queries_with_one_loud_element(loud, T):
                 ref.check(o[b, h, t], O[b, h, t], tol, torch.float32, (b, h, t))
                 assert abs(float(lse[b, h, t]) - float(LSE[b, h, t])) <= (
                     rel + 2.0 ** -23 * abs(float(LSE[b, h, t])))
+
+
+# ---------------------------------------------------------------------------
+# angles
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("d,H", [(128, 1), (64, 3), (128, 40)])
+def test_rope_cos_and_sin(layout, d, H):
+    """Rotated unit vectors are the cos and sin themselves.  Every quarter of the
+    turn, small and large positions.  The bound: what is left of the angle after
+    whole quarter turns is at most pi / 4 and has 24 bits, 2.4e-8; its cos and sin are
+    off by at most 7.5e-8 more; the frequency (fp64) by |position| f 2^-52."""
+    L = 4099
+    x = torch.zeros(1, H, L, d)
+    first = slice(0, d // 2) if layout == "half" else slice(0, d, 2)
+    x[..., first] = 1.0
+    pos = torch.randint(-20000, 20000, (1, L), generator=torch.Generator().manual_seed(d + H),
+                        dtype=torch.int32)
+    pos[0, :5] = torch.tensor([0, 1, -1, 2, 3])
+    got = dfa.rope(x.cuda(), dfa.rope_spec(d, layout=layout), positions=pos.cuda()).cpu().double()
+    want = ref.rope(x, pos[:, None], layout, d)
+    err = (got - want).abs().max()
+    assert err <= 1.0e-7 + 20000 * 2.0 ** -51, float(err)
