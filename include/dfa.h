@@ -521,7 +521,7 @@ dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* r
  * power-of-two scales that dfa_cache_append sets (except below bf16's smallest
  * normal number), and rounded once for other scales.  Rows behind a sequence's
  * end are left as they were.
- *   k_out, v_out [B,Hkv,L,d] bf16, 16-byte aligned; either may be NULL.
+ *   k_out, v_out [B,Hkv,L,d] bf16, 16-byte aligned, apart; either may be NULL.
  *   ws: 256 bytes (the status word).
  */
 dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t L, void* k_out,
@@ -538,7 +538,8 @@ dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t 
  * does not reach its result, NaN and infinities included.
  * desc supplies B, Hq, Hkv, d, causal, scale, o_fp32 (ndocs must be 0).
  *   q [B,Hq,T,d] bf16 (strided); o [B,Hq,T,d] bf16 or fp32 (o_fp32) and
- *   lse [B,Hq,T] fp32, contiguous.  (Hq/Hkv) * T <= 1024.
+ *   lse [B,Hq,T] fp32, contiguous, apart from each other and from q (o in q's
+ *   memory range is refused).  (Hq/Hkv) * T <= 1024.
  *   (From about 200 rows a head on, dfa_cache_gather and dfa_chunk_fwd are faster.)
  *   ws: dfa_decode_paged_workspace_size(desc, T) bytes (partials), whatever
  *   the lengths and the table.

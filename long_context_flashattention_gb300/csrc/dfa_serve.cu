@@ -91,6 +91,17 @@ dfa_status make_rows(Rows* r, const void* p, const int64_t* strides, int64_t B, 
     return DFA_OK;
 }
 
+// Bytes from a tensor's first row to the end of its last.
+size_t span_bytes(const Rows& r, int64_t B, int64_t H, int64_t L, int d, int elem_bytes)
+{
+    return (size_t)((B - 1) * r.sb + (H - 1) * r.sh + (L - 1) * r.sl + d) * elem_bytes;
+}
+
+bool spans_meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes)
+{
+    return (const char*)a < (const char*)b + b_bytes && (const char*)b < (const char*)a + a_bytes;
+}
+
 // Two tensors of one shape: the same one (in place), or apart.
 dfa_status check_apart(const Rows& x, const Rows& out, int64_t B, int64_t H, int64_t L, int d,
                        int elem_bytes, const char* names)
@@ -98,12 +109,8 @@ dfa_status check_apart(const Rows& x, const Rows& out, int64_t B, int64_t H, int
     if (x.p == out.p && (B <= 1 || x.sb == out.sb) && (H <= 1 || x.sh == out.sh) &&
         (L <= 1 || x.sl == out.sl))
         return DFA_OK;
-    auto bytes = [&](const Rows& r) {
-        return (size_t)((B - 1) * r.sb + (H - 1) * r.sh + (L - 1) * r.sl + d) * elem_bytes;
-    };
-    const char* a = (const char*)x.p;
-    const char* b = (const char*)out.p;
-    if (a < b + bytes(out) && b < a + bytes(x))
+    if (spans_meet(x.p, span_bytes(x, B, H, L, d, elem_bytes), out.p,
+                   span_bytes(out, B, H, L, d, elem_bytes)))
         return set_error(DFA_ERR_INVALID_ARG, "%s overlap without being the same tensor", names);
     return DFA_OK;
 }
@@ -421,6 +428,9 @@ dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t 
     const int64_t end = std::min(pos0 + L, rows);
     if (pos0 >= end || (!k_out && !v_out))
         return DFA_OK;  // no such rows
+    const size_t out_bytes = (size_t)p.c.B * p.c.Hkv * L * p.c.d * 2;
+    if (k_out && v_out && spans_meet(k_out, out_bytes, v_out, out_bytes))
+        return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_gather: k_out and v_out overlap");
     p.page0 = (int32_t)(pos0 / p.c.page);
     p.pages = (int32_t)((end - 1) / p.c.page) - p.page0 + 1;
     if ((int64_t)p.pages * p.c.Hkv * p.c.B > kMaxBlocks)
@@ -479,6 +489,10 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
     const size_t need = dfa_decode_paged_workspace_size(desc, T);
     if ((s = check_ws(ws, ws_bytes, need, "dfa_decode_paged")) != DFA_OK)
         return s;
+    // (blocks that read a sequence's queries run beside one that writes its result)
+    if (spans_meet(q, span_bytes(p.q, p.c.B, desc->Hq, T, p.c.d, 2), o,
+                   (size_t)p.c.B * desc->Hq * T * p.c.d * (desc->o_fp32 ? 4 : 2)))
+        return set_error(DFA_ERR_INVALID_ARG, "dfa_decode_paged: q and o overlap");
     p.q_lens = q_lens;
     p.Hq = desc->Hq;
     p.G = G;
