@@ -412,7 +412,7 @@ dfa_status dfa_permute_rope(const dfa_attn_desc* desc, int32_t inverse, const vo
  *                    (1 - u) f_t / factor + u f_t, u = (r - low) / (high - low).
  * f_t / (2 pi) is held as a 64-bit fraction of a turn, made in fp64, and
  * multiplied by the integer position modulo a turn.  cos and sin are off by at
- * most 1e-7 + |i| f_t 2^-52 (the last from f_t in fp64: 5e-7 at 2^31). */
+ * most 1e-7 + |i| f_t 2^-51 (the last from f_t in fp64: 1e-6 at 2^31). */
 enum { DFA_ROPE_INTERLEAVED = 0, /* pairs (2t, 2t + 1)              */
        DFA_ROPE_HALF = 1 };      /* pairs (t, t + rot_dim/2)        */
 enum { DFA_ROPE_PLAIN = 0, DFA_ROPE_LINEAR = 1, DFA_ROPE_BANDS = 2 };
@@ -535,7 +535,10 @@ dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t 
  * position, else every row of the sequence is.  A row that sees no key gives
  * O = 0, LSE = -inf; output rows from n on are left as they were.  What lies
  * in a page behind the sequence's end, or in rows that a token does not see,
- * does not reach its result, NaN and infinities included.
+ * does not reach its result, NaN and infinities included; in what it does see
+ * they make the result infinite or NaN.  Finite scores count to the ends of
+ * fp32's range.  Accuracy: as attention in fp32, weights rounded to 2^-16 (bf16
+ * cells) or 2^-22 (E4M3; to 2^-11 for (Hq/Hkv) * T > 8 with a bf16 output).
  * desc supplies B, Hq, Hkv, d, causal, scale, o_fp32 (ndocs must be 0).
  *   q [B,Hq,T,d] bf16 (strided); o [B,Hq,T,d] bf16 or fp32 (o_fp32) and
  *   lse [B,Hq,T] fp32, contiguous, apart from each other and from q (o in q's

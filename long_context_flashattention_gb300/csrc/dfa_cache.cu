@@ -16,10 +16,11 @@
 // 32K prompts below; three, four and six heads: 133, 137, 164 where two took 132).
 //
 // Measured: a 32K bf16 prompt of 3 x 32 heads of 128, 239 us, 6.7 TB/s; into 8 bits
-// with 8 key/value heads 129 us, 5.7 TB/s, with 32 253 us, 5.3 TB/s (a group waits for
+// with 8 key/value heads 128 us, 5.7 TB/s, with 32 248 us, 5.4 TB/s (a group waits for
 // its largest value between loads and stores); ragged chunks of 0..1000 tokens into
-// 16-row pages, 28 MB, 10.8 us (instruction issue 61 % while it runs, the launch and
-// the chain of loads the rest); one token of 64 sequences 3.9 us.
+// 16-row pages, 28 MB, 11.1 us (the launch and the chain of loads, and between them
+// instruction issue 60 % of the time, warps of a page at its barrier for the rest); one
+// token of 64 sequences 4.1 us.
 // Gather of two sequences of up to 64K rows of 8 heads, 604 MB: 81.5 us (part of what it
 // writes is still in L2 when it ends).
 //

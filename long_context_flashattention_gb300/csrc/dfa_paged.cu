@@ -18,10 +18,11 @@
 // maximum of x_j itself, and M is held as N + D: D is small, and large scores drop out
 // of (x_j - N) + (log2 u_j - D).  O = 2^D (weighted sum) / (sum), D = 0 for M = N.
 //
-// What bounds it: HBM.  A cached row is read once and meets G*T query rows, a
-// few operations a byte: too few rows for a 128-row tcgen05 tile, so the products
-// are the 16x8x16 warp products, with the cache in the 16-row operand and 8
-// query rows (NB = 1) or 16 (NB = 2) in the other: S^T = K Q^T, O^T = V^T P^T.
+// What bounds it: HBM, up to 8 query rows a head (16 in bf16): a cached row is read once
+// and meets G*T query rows, a few operations a byte.  The products are the 16x8x16 warp
+// products, with the cache in the 16-row operand and 8 query rows (NB = 1) or 16 (NB = 2)
+// in the other: S^T = K Q^T, O^T = V^T P^T.  With more rows the products and the
+// conversions bound it; tcgen05 with 128 keys in M would serve there, and is not built.
 //
 // Work.  (sequence, head) segments of 64-key tiles form one line, cut by cost over
 // a persistent grid whatever the lengths: a block's range covers whole segments,
@@ -30,9 +31,9 @@
 // graph follows them.  A head with more than 16 query rows has several groups of
 // them, and each group blocks of its own, cut alike: the groups' blocks read the same
 // tiles at about the same time, out of L2.  Measured (4 sequences of 32K rows, 8 heads,
-// bf16; 16, 32, 64, 128, 256 query rows, us): 92, 113, 195, 366, 709, where groups one
+// bf16; 16, 32, 64, 128, 256 query rows, us): 90, 113, 195, 366, 709, where groups one
 // behind the other on the line took 92, 162, 310, 604, 1182.  In 8 bits the products
-// bound it, 61, 102, 191, 369, 725 either way.
+// bound it, 58, 102, 191, 370, 725 either way.
 //
 // A block: warp 4 fetches pages by TMA into a ring of tiles (128- or 64-byte
 // swizzle; the page numbers and scales of 32 pages are looked up at a time);
@@ -40,11 +41,11 @@
 // of their own, joined at the segment's end.
 //
 // Measured (64 ragged sequences of up to 8192 rows, 8 heads of 128, 1.12 GB in
-// bf16): bf16 168 us, 6.7 TB/s, 8-bit 92 us, 6.1 TB/s; with 16 query rows a head
-// 175 and 115 us (twice the products for the bytes).  One 128K sequence of 32
+// bf16): bf16 167 us, 6.7 TB/s, 8-bit 93 us, 6.0 TB/s; with 16 query rows a head
+// 175 and 117 us (twice the products for the bytes).  One 128K sequence of 32
 // heads, 8-bit: 162 us, 6.6 TB/s.  About 10 us of each are fixed: the launch, the way to
 // the first tile (lengths, page number, page), the last blocks' tail and the
-// merge, which make up all of the 9.0 us of one sequence of 1000 rows.
+// merge, which make up all of the 9.5 us of one sequence of 1000 rows.
 //
 // Rounding: weights for 8-bit cells as two fp16 terms (2^-22); as one (2^-11) for more
 // than 8 query rows with a bf16 output (2^-8), where the products bound the kernel.

@@ -15,7 +15,7 @@ struct DevStatus;
 // A rotary embedding as the kernels use it.  turn[t] is pair t's frequency as a
 // 64-bit fraction of a full turn, so that (position * turn[t]) mod 2^64 is the
 // reduced angle, in integer arithmetic: the reduction adds nothing to what the
-// frequency itself, made in fp64, is off by (about 2^-52 of it).
+// frequency itself, made in fp64, is off by (2^-51 of it at most).
 struct RopeTable {
     uint64_t turn[64];
     float gain;
