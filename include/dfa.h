@@ -537,8 +537,10 @@ dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t 
  * in a page behind the sequence's end, or in rows that a token does not see,
  * does not reach its result, NaN and infinities included; in what it does see
  * they make the result infinite or NaN.  Finite scores count to the ends of
- * fp32's range.  Accuracy: as attention in fp32, weights rounded to 2^-16 (bf16
- * cells) or 2^-22 (E4M3; to 2^-11 for (Hq/Hkv) * T > 8 with a bf16 output).
+ * fp32's range (E4M3: where a query row's largest element times scale times a
+ * page's key scale is finite, too).  Accuracy: as attention in fp32, weights
+ * rounded to 2^-16 (bf16 cells) or 2^-22 (E4M3; to 2^-11 for (Hq/Hkv) * T > 8
+ * with a bf16 output).
  * desc supplies B, Hq, Hkv, d, causal, scale, o_fp32 (ndocs must be 0).
  *   q [B,Hq,T,d] bf16 (strided); o [B,Hq,T,d] bf16 or fp32 (o_fp32) and
  *   lse [B,Hq,T] fp32, contiguous, apart from each other and from q (o in q's

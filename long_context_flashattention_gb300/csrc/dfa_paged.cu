@@ -983,7 +983,8 @@ __device__ __forceinline__ void consume(const PagedParams& p, Shared& sh, uint32
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             w[k] = ex2(x[k]);
-                            l[nb][k & 1] = F8 ? fmaf(w[k], sc.z, l[nb][k & 1]) : l[nb][k & 1] + w[k];
+                            l[nb][k & 1] =
+                                F8 ? fmaf(w[k], sc.z, l[nb][k & 1]) : l[nb][k & 1] + w[k];
                         }
                     }
 #pragma unroll

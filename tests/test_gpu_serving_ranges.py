@@ -74,7 +74,7 @@ def test_decode_tail_behind_a_sink(B, n, Hq, p_sink, loud):
     q[:, 0] = (math.log(n) + 0.123 + math.log(p_sink / (1 - p_sink))) / scale
     q = q.to(BF16)
     c = dfa.PagedCache(k.cuda(), v.cuda(),
-                       torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous(),
+                       torch.arange(pages, dtype=torch.int32).repeat(B, 1).cuda(),
                        torch.full((B,), n, dtype=torch.int32, device="cuda"),
                        k_scale=torch.ones(pages, 1, device="cuda"), v_scale=vs.cuda())
     K, V = k.double().view(n, d), v.double().view(n, d) * vs.double().repeat_interleave(page, 0)
@@ -91,9 +91,10 @@ def test_decode_tail_behind_a_sink(B, n, Hq, p_sink, loud):
             tol = rel * want + floor
             tol = tol + ref.HALF_STEP[torch.float32 if fp32 else BF16] * (want + tol)
             err = (o[:, h] - want).abs()
-            assert (err <= tol).all(), (h, fp32, float((err / want).max()), float((tol / want).min()))
+            assert (err <= tol).all(), (h, fp32, float((err / want).max()))
             rel = fine_tol(s, K, x, V, u, scale)[0]
-            assert ((lse[:, h] - torch.logsumexp(s, 0)).abs() <= rel + 2.0 ** -23 * float(lse.max())).all()
+            off = (lse[:, h] - torch.logsumexp(s, 0)).abs()
+            assert (off <= rel + 2.0 ** -23 * float(lse.max())).all()
 
 
 @pytest.mark.parametrize("T", [1, 3])
