@@ -555,6 +555,158 @@ dfa_status dfa_decode_paged(const dfa_attn_desc* desc, const dfa_paged_cache* ca
                             void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * dfa_cache_append_at -- dfa_cache_append with rotary positions of their own: token t
+ * of sequence b is rotated at positions[b*T + t] (any int32) and stored in the row that
+ * dfa_cache_append gives it.  (Nodes of a tree of drafted tokens lie in the rows behind
+ * their sequence one after the other, and stand at the context's length plus their depth.)
+ *   positions [B][T] (device); rope is needed.
+ */
+dfa_status dfa_cache_append_at(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,
+                               const int32_t* new_lens, const int32_t* positions, const void* k,
+                               const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                               int32_t Hq, const void* q, const int64_t* q_strides, void* q_out,
+                               const int64_t* q_out_strides, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Branching sequences (serving): trees of drafted tokens checked in one pass, the rows
+ * of accepted ones moved together, and pools of pages that sequences share.  The pages
+ * describe no counterpart.
+ *
+ * A step with a drafted tree of n tokens a sequence: raise seq_lens by n,
+ * dfa_pages_reserve, dfa_tree_plan; in every layer dfa_cache_append_at and
+ * dfa_decode_tree; then, when a path has been accepted, dfa_cache_compact in every
+ * layer, lower seq_lens to what was kept, dfa_pages_trim.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * dfa_tree_plan -- who sees whom in each sequence's tree of drafted tokens, and the
+ * nodes' positions.  Sequence b's tree has n = q_lens[b] (NULL: T) nodes, in the last n
+ * of its seq_lens[b] rows; parents[b*T + t] is the node that node t continues, one
+ * before it (parents < t), or -1: node t continues the context.
+ *   mask[(b*T + t)*W + u/32], W = ceil(T/32): bit u%32 is set where u is t or one of
+ *   its ancestors; positions[b*T + t] = seq_lens[b] - n + (number of ancestors).
+ *   Rows from n on are left as they were.  1 <= T <= 1024.
+ * Another parent is reported (DFA_ERR_BOUNDS) and taken for -1.
+ *   ws: 256 bytes (the status word).
+ */
+dfa_status dfa_tree_plan(const dfa_paged_cache* cache, int32_t T, const int32_t* q_lens,
+                         const int32_t* parents, uint32_t* mask, int32_t* positions, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * dfa_decode_tree -- attention of a tree of drafted tokens over the paged cache.
+ * Sequence b has n = q_lens[b] (NULL: T) query tokens, nodes 0..n-1 of q, whose keys and
+ * values lie in its last n rows.  Node t sees every row before those, and of them row u
+ * where bit u of its mask is set (dfa_tree_plan makes masks of trees; any bits may be
+ * set, those from n on are not looked at).  A node that sees no key gives O = 0, LSE =
+ * -inf; output rows from n on are left as they were.  What lies in rows that a node does
+ * not see, or in a page behind the sequence's end, does not reach its result, NaN and
+ * infinities included; in what it does see they make the result infinite or NaN.
+ * desc supplies B, Hq, Hkv, d, scale, o_fp32 (ndocs must be 0; causal is not looked at).
+ *   q [B,Hq,T,d] bf16 (strided); mask [B][T][ceil(T/32)]; o [B,Hq,T,d] bf16 or fp32
+ *   (o_fp32) and lse [B,Hq,T] fp32, contiguous; o and lse apart from each other and
+ *   from q and mask.  (Hq/Hkv) * T <= 1024.
+ *   ws: dfa_decode_tree_workspace_size(desc, T) bytes, whatever the lengths and the table.
+ */
+size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T);
+dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
+                           const int32_t* q_lens, const uint32_t* mask, const void* q,
+                           const int64_t* q_strides, void* o, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * dfa_cache_compact -- of the last n = q_lens[b] (NULL: T) rows of every sequence, those
+ * in a list move together, in place: row seq_lens[b] - n + kept[b*A + i] goes to row
+ * seq_lens[b] - n + i, for i < kept_lens[b] (NULL: A).  The list increases strictly, within
+ * [0, n); another list is reported (DFA_ERR_BOUNDS) and its sequence left as it is.  The
+ * rows behind the last kept one are left without meaning; seq_lens is the caller's to
+ * lower (once, after the last layer).  With n = the sequence's length it throws out any
+ * tokens of a context.
+ * Pages that rows go to belong to one sequence (as for dfa_cache_append).  E4M3: such a
+ * page's scale becomes the largest of those that its rows came with; cells are shifted
+ * to it, and round where they become subnormal.
+ *   kept [B][A] and kept_lens [B] (device).  1 <= A <= T < 2^30.
+ *   ws: 256 bytes (the status word).
+ */
+dfa_status dfa_cache_compact(const dfa_paged_cache* cache, int32_t T, const int32_t* q_lens,
+                             int32_t A, const int32_t* kept, const int32_t* kept_lens, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* A pool of pages (plain data; every array is the caller's, on the device): the table
+ * and lengths of a cache (of the caches of all layers, which share them), and who holds
+ * what.  Sequence b holds the pages in entries 0..held[b]-1 of its row of the table;
+ * refs[i] counts the entries that hold page i, and a page without any is free.  A new
+ * pool has held = 0 and refs = 0.  Calls take the free pages of the lowest numbers first:
+ * what they give depends on the pool alone, not on the order in which blocks run.
+ * A pool serves one call at a time.  Numbers that cannot be (a length, a count, an entry
+ * of the table outside its range, a page released more often than held) are reported
+ * (DFA_ERR_BOUNDS) and their sequence or entry passed over. */
+typedef struct dfa_page_pool {
+    int32_t page;        /* rows per page: 16, 32, 64 or 128               */
+    int32_t B;           /* sequences                                       */
+    int32_t max_pages;   /* width of block_table                            */
+    int32_t reserved;    /* 0                                               */
+    int64_t npages;      /* pages                                           */
+    int32_t* block_table; /* [B][max_pages]                                 */
+    int32_t* held;       /* [B]                                             */
+    int32_t* refs;       /* [npages]                                        */
+    int32_t* seq_lens;   /* [B]                                             */
+    void* status;        /* as in dfa_paged_cache                           */
+} dfa_page_pool;
+
+/* Workspace of dfa_pages_fork and dfa_pages_reserve (status word first). */
+size_t dfa_pages_workspace_size(const dfa_page_pool* pool);
+
+/*
+ * dfa_pages_fork -- every sequence b becomes what sequence src[b] was before the call:
+ * its pages, which both then hold, and its length.  src[b] = b: stays; -1: becomes empty.
+ * (Beams that go on from others, a prompt's samples, sequences that end.)  Entries of the
+ * table behind a sequence's pages are left as they were.
+ *   src [B] (device); another number is reported and its sequence stays.
+ *   ws: dfa_pages_workspace_size(pool) bytes.
+ */
+dfa_status dfa_pages_fork(const dfa_page_pool* pool, const int32_t* src, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * dfa_pages_reserve -- pages for the last n = new_lens[b] (NULL: T) rows of every
+ * sequence, before they are stored (seq_lens counts them already).  Entries up to
+ * ceil(seq_lens[b]/page) that are missing get a free page.  A page that holds some of the
+ * new rows' places and has other holders too is replaced by a free one, and the pair
+ * (from, to) added to jobs for dfa_cache_copy; where its holders are all among the
+ * sequences that write it in this call, the last one keeps it.  Pages are taken in the
+ * order of sequences and entries; one that loses its last holder is free from the next
+ * call on.
+ *   info [4] (device, written): number of jobs; pages taken; 1 if there were too few
+ *   free pages or more than max_jobs jobs, else 0; 0.  In the former case nothing
+ *   else changes, the number of jobs is 0 and it is reported (DFA_ERR_BOUNDS).
+ *   jobs [max_jobs][2] (device), 8-byte aligned; entries from the number of jobs on are
+ *   left as they were.  0 <= T, max_jobs < 2^30.
+ *   ws: dfa_pages_workspace_size(pool) bytes.
+ */
+dfa_status dfa_pages_reserve(const dfa_page_pool* pool, int32_t T, const int32_t* new_lens,
+                             int32_t* jobs, int32_t max_jobs, int32_t* info, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * dfa_pages_trim -- every sequence gives back the pages that it holds behind its length:
+ * held[b] becomes min(held[b], ceil(seq_lens[b]/page)).  Length 0 gives back all.
+ *   ws: 256 bytes (the status word).
+ */
+dfa_status dfa_pages_trim(const dfa_page_pool* pool, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dfa_cache_copy -- copies pages of a cache, K, V and scales: jobs[2i] to jobs[2i + 1] for
+ * i < min(info[0], max_jobs) (both read on the device; dfa_pages_reserve writes them).
+ * No page that is copied to is in another job.  A pair with a number outside [0, npages)
+ * is reported and skipped.
+ *   jobs 8-byte aligned; 1 <= max_jobs < 2^30.  ws: 256 bytes (the status word).
+ */
+dfa_status dfa_cache_copy(const dfa_paged_cache* cache, const int32_t* jobs, int32_t max_jobs,
+                          const int32_t* info, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Ring schedule (host only, no device work) for the P workers of desc's
  * partition (Striped Attention Guide, "Workload Balance Theorem": at ring
  * step s worker p holds the keys of worker (p - s) mod P; "Intra-Block vs.

@@ -106,6 +106,7 @@ __device__ __forceinline__ void row_items(const AppendParams& p, const uint64_t*
         if (t >= n)
             continue;
         const int32_t pos = len - n + t;
+        const int32_t turn = p.positions ? p.positions[token] : pos;  // (token: b * T + t)
         const bool stores = !F8 && h1 > p.Hq;
         int32_t id = stores ? page_entry(p.c, b, pos >> p.c.page_log2) : 0;
         float cs[8], sn[8];
@@ -126,7 +127,7 @@ __device__ __forceinline__ void row_items(const AppendParams& p, const uint64_t*
             }
             if (h == h0) {  // while the first rows are on their way
                 if (p.t.half && h0 < p.Hq + Hk)  // (not for values alone)
-                    angles.at(pos, 1.f, cs, sn);
+                    angles.at(turn, 1.f, cs, sn);
                 if (stores && !is_page(p.c, b, id))
                     id = -1;
             }
@@ -266,10 +267,13 @@ __device__ __forceinline__ void page_job(const AppendParams& p, uint32_t job, in
                      ((int64_t)h0 << p.c.page_log2) * D;
     for (int32_t h = h0; h < h1; ++h, cells += p.c.page * D) {
         const float old = there > 0 && stores ? scales[h] : 0.f;
-        if (h == h0 && turned && mine)
+        if (h == h0 && turned && mine) {
+            const int32_t turn =
+                p.positions ? p.positions[(int64_t)b * p.T + row - first] : row;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                pair_angle(turns[unit_pair<8>(p.t, u, j)], p.t.gain, row, 1.f, cs[j], sn[j]);
+                pair_angle(turns[unit_pair<8>(p.t, u, j)], p.t.gain, turn, 1.f, cs[j], sn[j]);
+        }
         float a[8], c[8], amax = 0.f;
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         if (mine) {

@@ -57,6 +57,7 @@ struct AppendParams {
     CacheView c;
     RopeTable t;
     const int32_t* new_lens;      // [B] or NULL
+    const int32_t* positions;     // [B][T], of the rotation, or NULL: a row's place
     Rows k, v, q, q_out;
     int32_t T, Hq;
     int32_t pages;                // pages a sequence's new rows may touch

@@ -105,6 +105,14 @@ class PagedCacheDesc(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
+class PagePoolDesc(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_int32), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("npages", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2}
 
@@ -125,6 +133,7 @@ def lib():
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         D = ctypes.POINTER(AttnDesc)
         C = ctypes.POINTER(PagedCacheDesc)
+        P = ctypes.POINTER(PagePoolDesc)
         sigs = {
             "dfa_attn_fwd": (i32, [D, vp, vp, vp, vp, vp, vp, sz, vp]),
             "dfa_attn_bwd": (i32, [D, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -151,6 +160,17 @@ def lib():
             "dfa_cache_gather": (i32, [C, i64, i64, vp, vp, vp, sz, vp]),
             "dfa_decode_paged_workspace_size": (sz, [D, i32]),
             "dfa_decode_paged": (i32, [D, C, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "dfa_cache_append_at": (i32, [C, ctypes.POINTER(RopeSpec), i32, vp, vp, vp, vp, vp, vp,
+                                          i32, vp, vp, vp, vp, vp, sz, vp]),
+            "dfa_tree_plan": (i32, [C, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "dfa_decode_tree_workspace_size": (sz, [D, i32]),
+            "dfa_decode_tree": (i32, [D, C, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "dfa_cache_compact": (i32, [C, i32, vp, i32, vp, vp, vp, sz, vp]),
+            "dfa_cache_copy": (i32, [C, vp, i32, vp, vp, sz, vp]),
+            "dfa_pages_workspace_size": (sz, [P]),
+            "dfa_pages_fork": (i32, [P, vp, vp, sz, vp]),
+            "dfa_pages_reserve": (i32, [P, i32, vp, vp, i32, vp, vp, sz, vp]),
+            "dfa_pages_trim": (i32, [P, vp, sz, vp]),
             "dfa_make_schedule": (i32, [D, i32, i32, ctypes.POINTER(Schedule)]),
             "dfa_partition_map": (i32, [D, i32, ctypes.POINTER(PosMap)]),
             "dfa_workspace_size": (sz, [D, i32]),
@@ -740,13 +760,15 @@ def _paged_desc(B, Hq, Hkv, T, d, causal, scale, fp32):
 
 
 def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens=None, q=None,
-                 q_out=None, ws=None, stream=None):
+                 q_out=None, ws=None, stream=None, positions=None):
     """Store the new rows k, v [B,Hkv,T,d] bf16 (any strides with contiguous
     features) of every sequence at the end of its cached rows, keys rotated by
     rope on the way (dfa_cache_append).  cache.seq_lens counts them already;
     new_lens [B] int32: how many of the T are a sequence's (default: all).  With
     q [B,Hq,T,d] its rows are rotated too, into q_out (default: a new contiguous
-    tensor; rows from new_lens on are not written), which is returned."""
+    tensor; rows from new_lens on are not written), which is returned.  positions
+    [B,T] int32: where the rotation takes the rows to be, instead of where they are
+    stored (dfa_cache_append_at; tree_plan makes those of a tree)."""
     dev = cache.device
     raw = _raw_stream(dev, stream)
     if k.dim() != 4 or q is not None and q.dim() != 4:
@@ -768,9 +790,16 @@ def cache_append(cache: PagedCache, k, v, rope: RopeSpec | None = None, new_lens
             op, os_ = _rows(q_out, "q_out", torch.bfloat16, dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    code = lib().dfa_cache_append(ref, None if rope is None else ctypes.byref(rope), T,
-                                  _int32(new_lens, "new_lens", (cache.B,), dev), kp, ks, vp, vs,
-                                  Hq, qp, qs, op, os_, ws.data_ptr(), ws.numel(), raw)
+    spec = None if rope is None else ctypes.byref(rope)
+    new = _int32(new_lens, "new_lens", (cache.B,), dev)
+    if positions is None:
+        code = lib().dfa_cache_append(ref, spec, T, new, kp, ks, vp, vs, Hq, qp, qs, op, os_,
+                                      ws.data_ptr(), ws.numel(), raw)
+    else:
+        code = lib().dfa_cache_append_at(ref, spec, T, new,
+                                         _int32(positions, "positions", (cache.B, T), dev), kp,
+                                         ks, vp, vs, Hq, qp, qs, op, os_, ws.data_ptr(),
+                                         ws.numel(), raw)
     if code:
         _check(code)
     return q_out
@@ -826,6 +855,239 @@ def decode_paged(cache: PagedCache, q, q_lens=None, causal=True, scale=None, out
     if code:
         _check(code)
     return out, lse
+
+
+# ----------------------------------------------------------------------------
+# branching sequences: trees of drafted tokens, kept rows, shared pages
+# ----------------------------------------------------------------------------
+def _words(T):
+    return (T + 31) // 32
+
+
+def tree_plan(cache: PagedCache, parents, q_lens=None, mask=None, positions=None, ws=None,
+              stream=None):
+    """Plan of the trees of drafted tokens in the last q_lens [B] int32 (default: T) rows
+    of every sequence (dfa_tree_plan).  parents [B,T] int32: the node that a node
+    continues, one before it, or -1 for the context.  Returns (mask [B,T,ceil(T/32)]
+    int32: bit u of row t where node t sees node u, its ancestors and itself; positions
+    [B,T] int32: the context's length plus the node's depth).  Rows from q_lens on are not
+    written."""
+    dev = cache.device
+    raw = _raw_stream(dev, stream)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, T]")
+    B, T = cache.B, parents.shape[1]
+    par = _int32(parents, "parents", (B, T), dev)
+    if mask is None:
+        mask = _new(stream, (B, T, _words(T)), torch.int32, dev)
+    if positions is None:
+        positions = _new(stream, (B, T), torch.int32, dev)
+    ws, ref = _ws(ws, 256, cache, stream)
+    code = lib().dfa_tree_plan(ref, T, _int32(q_lens, "q_lens", (B,), dev), par,
+                               _int32(mask, "mask", (B, T, _words(T)), dev),
+                               _int32(positions, "positions", (B, T), dev), ws.data_ptr(),
+                               ws.numel(), raw)
+    if code:
+        _check(code)
+    return mask, positions
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_desc(B, Hq, Hkv, T, d, scale, fp32):
+    """dfa_decode_tree's descriptor (by reference) and workspace bytes (256 at least:
+    an invalid one is for the call to refuse)."""
+    ref = ctypes.byref(AttnDesc(B, Hq, Hkv, 1, d, True, scale, 1, 0, 1, fp32, 0, None))
+    return ref, max(256, int(lib().dfa_decode_tree_workspace_size(ref, T)))
+
+
+def tree_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:
+    """A workspace for decode_tree (and the other calls on this cache but decode_paged,
+    whose is paged_workspace): Hq query heads, T tokens a tree at most.  It serves one
+    call at a time, and the device's errors are then reported to it."""
+    Hq = Hq or cache.Hkv
+    n = max(_tree_desc(cache.B, Hq, cache.Hkv, t, cache.d, 1.0, False)[1] for t in (1, T))
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def decode_tree(cache: PagedCache, q, mask, q_lens=None, scale=None, out_fp32=False, ws=None,
+                out=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens over every sequence's cached rows
+    (dfa_decode_tree): q [B,Hq,T,d] bf16 (any strides with contiguous features), q_lens
+    [B] int32 of the T tokens per sequence (default: all), their keys and values in the
+    sequence's last rows.  mask [B,T,ceil(T/32)] int32: which of those each of them sees
+    (tree_plan); all see the rows before.  Returns (O [B,Hq,T,d], LSE [B,Hq,T]); rows from
+    q_lens on are not written."""
+    dev = cache.device
+    raw = _raw_stream(dev, stream)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B,Hq,T,d]")
+    B, Hq, T, d = shape
+    qp, qs = _rows(q, "q", torch.bfloat16, dev, (cache.B, Hq, T, cache.d))
+    if mask is None:
+        raise ValueError("decode_tree needs a mask (decode_paged takes chains without one)")
+    o_dtype = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out = _new(stream, shape, o_dtype, dev)
+    if lse is None:
+        lse = _new(stream, (B, Hq, T), torch.float32, dev)
+    desc, need = _tree_desc(B, Hq, cache.Hkv, T, d,
+                            1.0 / math.sqrt(d) if scale is None else scale, bool(out_fp32))
+    ws, ref = _ws(ws, need, cache, stream)
+    code = lib().dfa_decode_tree(desc, ref, T, _int32(q_lens, "q_lens", (B,), dev),
+                                 _int32(mask, "mask", (B, T, _words(T)), dev), qp, qs,
+                                 _plain(out, "out", o_dtype, dev, shape),
+                                 _plain(lse, "lse", torch.float32, dev, (B, Hq, T)),
+                                 ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
+    return out, lse
+
+
+def cache_compact(cache: PagedCache, kept, kept_lens=None, q_lens=None, T=None, ws=None,
+                  stream=None):
+    """Of the last q_lens [B] int32 (default: T) rows of every sequence, those whose
+    numbers stand in kept [B,A] int32 (the first kept_lens [B] of each row, default: all;
+    strictly increasing) move together, in place (dfa_cache_compact): row kept[i] of them
+    becomes row i.  T: the most rows that q_lens names (default: what a sequence can have).
+    seq_lens is the caller's to lower, after the last layer."""
+    dev = cache.device
+    raw = _raw_stream(dev, stream)
+    if kept.dim() != 2:
+        raise ValueError("kept must be [B, A]")
+    if T is None:
+        if q_lens is None:
+            raise ValueError("give T or q_lens")
+        T = max(cache.block_table.shape[1] * cache.page, kept.shape[1])
+    ws, ref = _ws(ws, 256, cache, stream)
+    code = lib().dfa_cache_compact(ref, T, _int32(q_lens, "q_lens", (cache.B,), dev),
+                                   kept.shape[1],
+                                   _int32(kept, "kept", (cache.B, kept.shape[1]), dev),
+                                   _int32(kept_lens, "kept_lens", (cache.B,), dev),
+                                   ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
+
+
+def cache_copy(cache: PagedCache, jobs, info, ws=None, stream=None):
+    """Copy pages of a cache, K, V and scales: the first info[0] (on the device) pairs
+    (from, to) of jobs [J,2] int32 (dfa_cache_copy; pages_reserve makes both)."""
+    dev = cache.device
+    raw = _raw_stream(dev, stream)
+    if jobs.dim() != 2:
+        raise ValueError("jobs must be [J, 2]")
+    J = jobs.shape[0]
+    ws, ref = _ws(ws, 256, cache, stream)
+    jobs = _int32(jobs, "jobs", (J, 2), dev)
+    info = _int32(info, "info", (4,), dev)
+    if J == 0:
+        return
+    code = lib().dfa_cache_copy(ref, jobs, J, info, ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
+
+
+class PagePool:
+    """The pages behind a cache, or behind the caches of all layers (dfa_page_pool), over
+    the caller's tensors, which it keeps alive: block_table [B,max_pages] and seq_lens [B]
+    int32, those of the caches; held [B] int32: the pages that each sequence holds, the
+    first entries of its row; refs [npages] int32: how many hold each page, 0 where it is
+    free.  Without held and refs a new pool of npages pages is made, which nobody holds yet.
+    Its calls run one at a time, and report numbers that cannot be to the workspace they
+    are given, or else to pool.status: stream_status(pool.status)."""
+
+    def __init__(self, block_table, seq_lens, page, held=None, refs=None, npages=None):
+        dev = block_table.device
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        B, max_pages = block_table.shape
+        if (held is None) != (refs is None) or (refs is None) == (npages is None):
+            raise ValueError("give held and refs, or npages")
+        if refs is None:
+            held = torch.zeros(B, dtype=torch.int32, device=dev)
+            refs = torch.zeros(npages, dtype=torch.int32, device=dev)
+        if refs.dim() != 1:
+            raise ValueError("refs must be [npages]")
+        self.device, self.B, self.page, self.npages = dev, B, page, refs.shape[0]
+        self.block_table, self.seq_lens, self.held, self.refs = block_table, seq_lens, held, refs
+        self.desc = PagePoolDesc(page, B, max_pages, 0, self.npages,
+                                 _int32(block_table, "block_table", (B, max_pages), dev),
+                                 _int32(held, "held", (B,), dev),
+                                 _int32(refs, "refs", (self.npages,), dev),
+                                 _int32(seq_lens, "seq_lens", (B,), dev))
+        self._ref = ctypes.byref(self.desc)
+        # for calls without a workspace, whose own nobody could read
+        self.status = torch.zeros(256, dtype=torch.uint8, device=dev)
+        self._own = PagePoolDesc.from_buffer_copy(self.desc)
+        self._own.status = self.status.data_ptr()
+        self._own_ref = ctypes.byref(self._own)
+        self._need = max(256, int(lib().dfa_pages_workspace_size(self._ref)))
+
+    def __setattr__(self, name, value):
+        if self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} of a PagePool stays: change its contents, or make a "
+                                 "new PagePool")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a PagePool stays: change its contents")
+
+
+def pages_workspace(pool: PagePool) -> torch.Tensor:
+    """A workspace for the calls on this pool.  The device's errors are then reported to
+    it."""
+    return torch.zeros(pool._need, dtype=torch.uint8, device=pool.device)
+
+
+def pages_fork(pool: PagePool, src, ws=None, stream=None):
+    """Every sequence b becomes what sequence src[b] (src [B] int32) was: its pages, which
+    both then hold, and its length; src[b] = b: stays, -1: becomes empty
+    (dfa_pages_fork)."""
+    raw = _raw_stream(pool.device, stream)
+    ws, ref = _ws(ws, pool._need, pool, stream)
+    if src is None:
+        raise ValueError("src must be [B]")
+    code = lib().dfa_pages_fork(ref, _int32(src, "src", (pool.B,), pool.device), ws.data_ptr(),
+                                ws.numel(), raw)
+    if code:
+        _check(code)
+
+
+def pages_reserve(pool: PagePool, T, new_lens=None, jobs=None, info=None, ws=None, stream=None):
+    """Pages for the last new_lens [B] int32 (default: T, which is also the most of them)
+    rows of every sequence, which seq_lens counts already: missing ones, and ones of their
+    own in place of those that others hold too (dfa_pages_reserve).  Returns (jobs [J,2],
+    info [4]) for cache_copy, to be called for every layer; info holds the number of jobs,
+    the pages taken, and whether the call was refused for want of pages or of room in
+    jobs, in which case it has changed nothing."""
+    dev = pool.device
+    raw = _raw_stream(dev, stream)
+    if jobs is None:
+        most = min(T // pool.page + 2, pool.block_table.shape[1])
+        jobs = _new(stream, (pool.B * most, 2), torch.int32, dev)
+    elif jobs.dim() != 2:
+        raise ValueError("jobs must be [J, 2]")
+    if info is None:
+        info = _new(stream, (4,), torch.int32, dev)
+    J = jobs.shape[0]
+    ws, ref = _ws(ws, pool._need, pool, stream)
+    code = lib().dfa_pages_reserve(ref, T, _int32(new_lens, "new_lens", (pool.B,), dev),
+                                   _int32(jobs, "jobs", (J, 2), dev), J,
+                                   _int32(info, "info", (4,), dev), ws.data_ptr(), ws.numel(),
+                                   raw)
+    if code:
+        _check(code)
+    return jobs, info
+
+
+def pages_trim(pool: PagePool, ws=None, stream=None):
+    """Every sequence gives back the pages that it holds behind its length
+    (dfa_pages_trim)."""
+    raw = _raw_stream(pool.device, stream)
+    ws, ref = _ws(ws, 256, pool, stream)
+    code = lib().dfa_pages_trim(ref, ws.data_ptr(), ws.numel(), raw)
+    if code:
+        _check(code)
 
 
 # ----------------------------------------------------------------------------
