@@ -56,6 +56,19 @@ struct PoolWs {
     }
 };
 
+// Workspace of dfa_decode_tree: status word, one record per block, two partial results
+// (references and sum, O) per block.
+struct TreeWs {
+    size_t info, ndl, o, bytes;
+    TreeWs(int rows, int d)
+    {
+        info = kStatusBytes;
+        ndl = info + align256((size_t)kTreeMaxCtas * sizeof(int4));
+        o = ndl + align256((size_t)2 * kTreeMaxCtas * rows * sizeof(float4));
+        bytes = o + align256((size_t)2 * kTreeMaxCtas * rows * d * 4);
+    }
+};
+
 dfa_status check_tree_tokens(int32_t T, const char* call)
 {
     if (T < 1)
@@ -105,7 +118,7 @@ size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T)
     if (!desc || T < 1 || desc->Hkv < 1 || desc->Hq < 1 || desc->Hq % desc->Hkv != 0 ||
         (desc->d != 64 && desc->d != 128) || (int64_t)(desc->Hq / desc->Hkv) * T > 1024)
         return 0;
-    return kStatusBytes;
+    return TreeWs(tree_rows(desc->Hq / desc->Hkv * T), desc->d).bytes;
 }
 
 dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
@@ -171,7 +184,17 @@ dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cac
     p.scale_log2 = scale_log2;
     p.o = o;
     p.lse = lse;
-    return launch_status(launch_decode_tree(p, num_sms(), (cudaStream_t)stream),
+    const TreeWs w(tree_rows(G * T), p.c.d);
+    p.info = (int4*)((char*)ws + w.info);
+    p.part_ndl = (float4*)((char*)ws + w.ndl);
+    p.part_o = (float*)((char*)ws + w.o);
+    p.timeout_ns = kDefaultTimeoutNs;
+    CUtensorMap tk, tv;
+    if ((s = make_page_map(&tk, p.c, p.c.k, kTreeTile, "dfa_decode_tree: k")) != DFA_OK)
+        return s;
+    if ((s = make_page_map(&tv, p.c, p.c.v, kTreeTile, "dfa_decode_tree: v")) != DFA_OK)
+        return s;
+    return launch_status(launch_decode_tree(tk, tv, p, num_sms(), (cudaStream_t)stream),
                          "dfa_decode_tree");
 }
 

@@ -9,7 +9,7 @@ namespace dfa {
 constexpr int kTreeMaxTokens = 1024;  // nodes of a tree
 constexpr int kTreeTile = 128;        // keys per tile
 constexpr int kTreeRows = 128;        // query rows of a tensor-core tile
-constexpr int kTreeMaxCtas = 256;
+constexpr int kTreeMaxCtas = 160;     // (152 SMs)
 
 struct TreePlanParams {
     CacheView c;
@@ -28,10 +28,23 @@ struct TreeParams {
     int32_t words;
     int32_t Hq, G, T, o_fp32;
     uint32_t inv_T;               // 2^21 / T, rounded up
+    int32_t row_groups;           // groups of query rows per key/value head
+    int32_t line_blocks;          // blocks of a group; block c of group rg: c * row_groups + rg
+    int32_t segment_cost;         // in tiles
+    int32_t whole;                // segments are not cut
     float scale_log2;
     void* o;                      // [B, Hq, T, d]
     float* lse;                   // [B, Hq, T]
+    int4* info;                   // [CTAs]: sequence, head and row group, CTAs that continue
+                                  // it, nodes
+    // [2 CTAs][rows]: what the sum is relative to (log2), what O is beyond that, sum
+    float4* part_ndl;
+    float* part_o;                // [2 CTAs][rows][d]
+    uint64_t timeout_ns;
 };
+
+// Query rows of a block.
+inline int tree_rows(int rows_per_head) { return rows_per_head <= kTreeRows ? kTreeRows : 2 * kTreeRows; }
 
 struct CompactParams {
     CacheView c;
@@ -80,7 +93,8 @@ struct ReserveParams {
 };
 
 cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream);
-cudaError_t launch_decode_tree(TreeParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_decode_tree(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p,
+                               int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_cache_copy(const CopyParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream);
