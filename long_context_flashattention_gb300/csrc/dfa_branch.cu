@@ -60,12 +60,12 @@ struct PoolWs {
 // (references and sum, O) per block.
 struct TreeWs {
     size_t info, ndl, o, bytes;
-    TreeWs(int rows, int d)
+    explicit TreeWs(int d)
     {
         info = kStatusBytes;
         ndl = info + align256((size_t)kTreeMaxCtas * sizeof(int4));
-        o = ndl + align256((size_t)2 * kTreeMaxCtas * rows * sizeof(float4));
-        bytes = o + align256((size_t)2 * kTreeMaxCtas * rows * d * 4);
+        o = ndl + align256((size_t)2 * kTreeMaxCtas * kTreeRows * sizeof(float4));
+        bytes = o + align256((size_t)2 * kTreeMaxCtas * kTreeRows * d * 4);
     }
 };
 
@@ -118,7 +118,7 @@ size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T)
     if (!desc || T < 1 || desc->Hkv < 1 || desc->Hq < 1 || desc->Hq % desc->Hkv != 0 ||
         (desc->d != 64 && desc->d != 128) || (int64_t)(desc->Hq / desc->Hkv) * T > 1024)
         return 0;
-    return TreeWs(tree_rows(desc->Hq / desc->Hkv * T), desc->d).bytes;
+    return TreeWs(desc->d).bytes;
 }
 
 dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
@@ -184,7 +184,7 @@ dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cac
     p.scale_log2 = scale_log2;
     p.o = o;
     p.lse = lse;
-    const TreeWs w(tree_rows(G * T), p.c.d);
+    const TreeWs w(p.c.d);
     p.info = (int4*)((char*)ws + w.info);
     p.part_ndl = (float4*)((char*)ws + w.ndl);
     p.part_o = (float*)((char*)ws + w.o);

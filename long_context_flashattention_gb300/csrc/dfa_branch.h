@@ -8,7 +8,7 @@ namespace dfa {
 
 constexpr int kTreeMaxTokens = 1024;  // nodes of a tree
 constexpr int kTreeTile = 128;        // keys per tile
-constexpr int kTreeRows = 128;        // query rows of a tensor-core tile
+constexpr int kTreeRows = 128;        // query rows of a block
 constexpr int kTreeMaxCtas = 160;     // (152 SMs)
 
 struct TreePlanParams {
@@ -42,9 +42,6 @@ struct TreeParams {
     float* part_o;                // [2 CTAs][rows][d]
     uint64_t timeout_ns;
 };
-
-// Query rows of a block.
-inline int tree_rows(int rows_per_head) { return rows_per_head <= kTreeRows ? kTreeRows : 2 * kTreeRows; }
 
 struct CompactParams {
     CacheView c;

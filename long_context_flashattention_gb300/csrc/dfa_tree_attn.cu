@@ -7,9 +7,9 @@
 //   O = 2^D (sum_j 2^(x_j - N + log2 u_j - D) w_j) / (sum_j 2^(x_j - N)),
 //   LSE = ln 2 (N + log2 sum),
 // with N the running maximum of the scores, and D that of the weights' exponents beyond it
-// (0 for bf16 cells), so that weights fit their type whatever the scales are.  A score is
-// rounded to fp32 before N is taken off it, as N was when it was one of them: the
-// difference is exact however large both are.  Weights are the sum's terms times
+// (0 for bf16 cells), so that weights fit their type whatever the scales are.  Scores far
+// from zero are rounded to fp32 before N is taken off them, as N was when it was one of
+// them: the difference is exact however large both are.  Weights are the sum's terms times
 // 2^(log2 u_j - D), where every u_j of a tile is in [2^-40, 2^40], and else powers of their
 // own.
 //
@@ -17,16 +17,17 @@
 // its mask has.  Only tiles that reach into the tree or over the sequence's end look at
 // masks; a row of the tile is 128 bits.
 //
-// A block (one an SM) keeps 128 query rows (TILES = 1), or 256 (TILES = 2), and walks over
-// 128-key tiles of the cache:
+// A block (one an SM) keeps 128 query rows and walks over 128-key tiles of the cache:
 //   warp 9       pages by TMA into a ring of K and V tiles, 128-byte swizzle;
 //   warps 12-15  (8-bit cells) those to fp16, in the same layout;
-//   warps 10-11  a segment's queries (8-bit cells: fp16 relative to a power of two of the
-//                row: exact but for elements below 2^-31 of its largest one);
+//   warps 10-11  the next segment's queries (8-bit cells: fp16 relative to a power of two
+//                of the row: exact but for elements below 2^-31 of its largest one);
 //   warp 8       S = Q K^T into TMEM, O += P V with P from TMEM (over S's columns);
-//   warps 0-7    softmax, a thread a row, O rescaled in TMEM when M has to rise.  TILES =
-//                1: the two groups of four warps take the tiles in turn, each with an O, M
-//                and sum of its own, joined at the segment's end; TILES = 2: 128 rows each.
+//   warps 0-3    softmax of the tile's first 64 keys, warps 4-7 of the others, a thread a
+//                row, each with an N, D, sum and O of its own, joined at the segment's end.
+//                O is rescaled in TMEM when D (or N) has to rise.
+// S has two buffers, and the scores of tile i + 2 are issued behind the products of tile i:
+// the next tile's are there when a tile's softmax ends.
 //
 // Work: (sequence, head, row group) segments form one line, cut by cost over a grid of
 // one block an SM: a block's range covers whole segments, whose result it writes, and up
@@ -51,19 +52,26 @@ namespace tree {
 
 constexpr int kTile = kTreeTile;
 constexpr int kRing = 8;                  // tiles whose scales are kept
-constexpr int kRuns = 4;                  // segments that are announced ahead
-constexpr float kGrow = 8.f;              // N rises when a term exceeds 2^8
+constexpr int kRuns = 2;                  // segments that are announced ahead
+// N rises when a term exceeds 2^kGrow.  (bf16 weights have fp32's range: no sum comes near
+// its end, and a rise costs a pass over O.)
+template <bool F8>
+constexpr float kGrow = F8 ? 8.f : 60.f;
 // D is set kHead below the largest exponent, and set anew when a weight exceeds 2^kTop
 // (fp16 weights use that type's range to its end, so that those far below the largest
 // keep their bits).
 constexpr float kTop = 15.f, kHead = 11.f;
 constexpr float kNone = -FLT_MAX;         // running maximum before the first key
+constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
+                                          // taken off them (else both in one operation: N,
+                                          // rounded, is then off by 2^-4 at most)
 constexpr float kNear = 40.f;             // terms times 2^(log2 u_j - D) are weights while
                                           // |log2 u_j| is at most this
 constexpr float kLn2 = 0.69314718055994531f;
 // Where no sequence can be longer than so many tiles, segments are not cut and there is
 // nothing to merge.
 constexpr int kWhole = 2;
+constexpr int kSiteShared = 109;         // of DFA_ERR_BOUNDS in DevStatus::where
 constexpr uint32_t kWideTile = 256;       // flag of a tile, beside the missing pages' bits
 
 // A run of tiles [tile0, tile0 + nt) of one segment: key/value head h, row group rg of
@@ -74,58 +82,57 @@ struct Piece {
     long long w;  // the segment's first unit on the line
 };
 
-template <int D, bool F8, int TILES>
+// How weights are held: in one term; in two, side by side in the operand's columns; in two
+// in its rows, where at most 64 of the 128 rows have queries: rows r and r + 64 are the
+// same query's, and the second row's weights are what the first's leave.
+enum Terms { kOne, kColumns, kLanes };
+
+template <int D, bool F8>
 struct Cfg {
     static constexpr int kThreads = F8 ? 512 : 384;
-    static constexpr int kRows = TILES * kTreeRows;
     static constexpr int kTileBytes = kTile * D * 2;      // a K, V or Q tile of 16-bit elements
     static constexpr int kRawBytes = kTile * D;
-    static constexpr int kSlots = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
-    static constexpr int kRaw = !F8 ? 0 : D == 128 ? (TILES == 1 ? 5 : 3) : 6;
-    static constexpr int kQ0 = 0;
-    static constexpr int kSlot0 = TILES * kTileBytes;
-    static constexpr int kRaw0 = kSlot0 + kSlots * kTileBytes;
+    // slots of K and V tiles: K's are free when its scores are there, V's two tiles later
+    static constexpr int kK = F8 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
+    static constexpr int kV = F8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 5);
+    static constexpr int kRaw = !F8 ? 0 : D == 128 ? 3 : 6;
+    static constexpr int kK0 = 2 * kTileBytes;            // behind two segments' queries
+    static constexpr int kV0 = kK0 + kK * kTileBytes;
+    static constexpr int kRaw0 = kV0 + kV * kTileBytes;
     static constexpr int kShared0 = kRaw0 + kRaw * kRawBytes;
-    static constexpr int kCopies = F8 ? kRaw : kSlots;    // slots that TMA fills
-    // Registers: the threads' total at launch is shared out anew.
-    static constexpr int kRegsMath = 192;
-    static constexpr int kRegsCtl = F8 ? 56 : 120;
-    static constexpr int kRegsConv = 72;
-    static_assert(F8 ? 2 * kRegsMath + kRegsCtl + kRegsConv == 4 * 128
-                     : 2 * kRegsMath + kRegsCtl == 3 * 168, "register budget");
     static constexpr int kReaders = 8 + 1 + 2 + (F8 ? 4 : 0);  // warps that read a run
 };
 
+template <bool F8>
 struct TileInfo {
-    float2 scale[8];   // per page: K's scale, log2 of V's
-    uint32_t flags;    // pages that are not there; kWideTile
-    uint32_t pad;
+    float2 scale[F8 ? 8 : 1];  // per page: K's scale, log2 of V's
+    uint32_t flags;            // pages that are not there; kWideTile
 };
 
-template <int D, bool F8, int TILES>
+template <int D, bool F8>
 struct Shared {
-    using C = Cfg<D, F8, TILES>;
-    uint64_t full[C::kSlots], empty[C::kSlots];           // tiles for the products
+    using C = Cfg<D, F8>;
+    uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
     uint64_t raw_full[F8 ? C::kRaw : 1], raw_empty[F8 ? C::kRaw : 1];
-    uint64_t s_full[2], p_full[2], o_full, o_empty, q_full, q_empty;
-    uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet;
+    uint64_t s_full[2], p_full[2][2], pv_done, o_empty, q_full[2], q_empty[2];
+    uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, seconds;
     Piece run[kRuns];
-    TileInfo info[kRing];
-    long long warp_sum[16];
+    TileInfo<F8> info[kRing];
     long long w0, w1, base, each, rest;
     int32_t b, block;
     uint32_t tmem, abort;
-    uint32_t bad[3][32];       // nodes whose values are not finite
+    union {
+        long long warp_sum[16];  // while the range is found
+        uint32_t bad[3][32];     // nodes whose values are not finite
+    };
     uint32_t any_bad[3];
-    float qf[F8 ? C::kRows : 1];                          // score factors of the rows
-    // of the two groups, where they share the rows: N, D, sum; two sets, since a group
-    // may end the next segment while the other still reads this one's
-    static constexpr int kBoth = TILES == 1 ? kTreeRows : 1;
-    float n[2][2][kBoth], l[2][2][kBoth], d[2][2][F8 ? kBoth : 1];
+    float qf[F8 ? 2 : 1][F8 ? kTreeRows : 1];             // score factors of the rows
+    // of the two groups: N, sum, D
+    float n[2][kTreeRows], l[2][kTreeRows], d[F8 ? 2 : 1][F8 ? kTreeRows : 1];
 };
 
-template <int D, bool F8, int TILES>
-constexpr int kSmem = Cfg<D, F8, TILES>::kShared0 + (int)sizeof(Shared<D, F8, TILES>) + 1024;
+template <int D, bool F8>
+constexpr int kSmem = Cfg<D, F8>::kShared0 + (int)sizeof(Shared<D, F8>);
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2, int c3)
@@ -336,24 +343,37 @@ __device__ __forceinline__ bool next_run(SH& sh, uint32_t seg, Piece& run, const
     return run.nt > 0;
 }
 
+// A place in a ring of SLOTS, and the phase that its barriers are in.
+template <int SLOTS>
+struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == SLOTS) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // producer: the tiles' pages, and what there is to know of them
 // ---------------------------------------------------------------------------
-template <int D, bool F8, int TILES>
-__device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8, TILES>& sh,
-                                        uint32_t slots, const CUtensorMap& tk,
+template <int D, bool F8>
+__device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
+                                        uint32_t smem, const CUtensorMap& tk,
                                         const CUtensorMap& tv, const WaitCtx& wctx)
 {
-    using C = Cfg<D, F8, TILES>;
+    using C = Cfg<D, F8>;
     constexpr int kPlanes = F8 ? 1 : D / 64;            // boxes side by side
     constexpr int kBoxRow = F8 ? D : 128;               // bytes of a box's row
     constexpr int kBytes = F8 ? C::kRawBytes : C::kTileBytes;
     const int lane = threadIdx.x & 31;
     const int32_t page = p.c.page;
     const int32_t per_tile = kTile / page;
-    uint64_t* full = F8 ? sh.raw_full : sh.full;
-    uint64_t* empty = F8 ? sh.raw_empty : sh.empty;
-    uint32_t st = 0, phase = 0, seg = 0, gt = 0;
+    Ring<F8 ? C::kRaw : C::kK> kr;  // 8-bit cells: of K and V in turn
+    Ring<C::kV> vr;
+    uint32_t seg = 0, gt = 0;
     Walk wk;
     wk.start(p, sh, blockIdx.x - sh.block * p.row_groups);
     bool more = wk.next(p);
@@ -409,31 +429,36 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8, TILES
             const uint32_t boxes = __ballot_sync(0xffffffffu, load);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
+                uint64_t* full = F8 ? &sh.raw_full[kr.at] : kv ? &sh.v_full[vr.at] : &sh.k_full[kr.at];
+                uint64_t* empty =
+                    F8 ? &sh.raw_empty[kr.at] : kv ? &sh.v_empty[vr.at] : &sh.k_empty[kr.at];
+                const uint32_t slot = smem + (F8 ? C::kRaw0 + kr.at * kBytes
+                                              : kv ? C::kV0 + vr.at * kBytes
+                                                   : C::kK0 + kr.at * kBytes);
                 // (passes at once in the first round: the phase before the barrier's first)
-                const bool ok = mbar_wait(&empty[st], phase ^ 1, wctx, 50);
+                const bool ok = mbar_wait(empty, (F8 || !kv ? kr.phase : vr.phase) ^ 1, wctx, 50);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 if (lane == 0)
-                    mbar_expect(&full[st], __popc(boxes) * (page * D * (F8 ? 1 : 2)));
+                    mbar_expect(full, __popc(boxes) * (page * D * (F8 ? 1 : 2)));
                 __syncwarp();
                 if (load) {
-                    const uint32_t dst = slots + st * kBytes + lane * page * kBoxRow;
+                    const uint32_t dst = slot + lane * page * kBoxRow;
 #pragma unroll
                     for (int pl = 0; pl < kPlanes; ++pl)
-                        tma_load_4d(dst + pl * kTile * 128, kv ? &tv : &tk, &full[st], pl * 64, 0,
-                                    h, my);
+                        tma_load_4d(dst + pl * kTile * 128, kv ? &tv : &tk, full, pl * 64, 0, h, my);
                 }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&full[st]);
-                if (++st == C::kCopies) {
-                    st = 0;
-                    phase ^= 1;
-                }
+                    mbar_arrive(full);
+                if (F8 || !kv)
+                    kr.next();
+                else
+                    vr.next();
             }
             // What the softmax has to know.  (A tile's entry is written anew kRing tiles
             // later, when the ring's slots say that its softmax is long done.)
-            TileInfo& info = sh.info[gt % kRing];
+            TileInfo<F8>& info = sh.info[gt % kRing];
             const float my_ks = __shfl_sync(0xffffffffu, ks, src & 31);
             const float my_vs = __shfl_sync(0xffffffffu, vs, src & 31);
             float lu = 0.f;
@@ -445,8 +470,8 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8, TILES
                                             log2f(__uint_as_float((bits & 0x7fffffu) | (127u << 23)));
             }
             const bool wide = F8 && __any_sync(0xffffffffu, !(fabsf(lu) <= kNear));
-            if (lane < per_tile)
-                info.scale[lane] = make_float2(load ? my_ks : 0.f, lu);
+            if (F8 && lane < per_tile)
+                info.scale[lane] = make_float2(load ? my_ks : 1.f, lu);
             const uint32_t missing = ~boxes & ((1u << per_tile) - 1);
             if (lane == 0)
                 info.flags = missing | (wide ? kWideTile : 0u);
@@ -467,38 +492,43 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8, TILES
 // ---------------------------------------------------------------------------
 // queries of the segments
 // ---------------------------------------------------------------------------
-template <int D, bool F8, int TILES>
-__device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8, TILES>& sh,
-                                             uint32_t qs, const WaitCtx& wctx)
+// (Rows without a query stay as they are: nobody looks at what comes of them.)
+template <int D, bool F8, Terms TERMS>
+__device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>& sh, uint32_t qs,
+                                             const WaitCtx& wctx)
 {
-    using C = Cfg<D, F8, TILES>;
+    using C = Cfg<D, F8>;
     constexpr int kPerRow = D / 8;                 // lanes of a row, 8 elements each
     constexpr int kRowsAt = 64 / kPerRow;          // rows of the two warps at a time
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     const int t = threadIdx.x & 63, c = t % kPerRow;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 53); ++seg) {
-        const bool ok = mbar_wait(&sh.q_empty, (seg & 1) ^ 1, wctx, 54);
+        const bool ok = mbar_wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
         if (!__all_sync(0xffffffffu, ok))
             return;
-        for (int32_t r0 = t / kPerRow; r0 < C::kRows; r0 += kBatch * kRowsAt) {
+        const uint32_t to = qs + (seg & 1) * C::kTileBytes;
+        const int32_t rows = min(kTreeRows, p.G * p.T - run.rg * kTreeRows);
+        for (int32_t r0 = 0; r0 < rows; r0 += kBatch * kRowsAt) {
             uint4 x[kBatch];
+            bool there[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int32_t r = run.rg * C::kRows + r0 + k * kRowsAt;
+                const int32_t row = r0 + t / kPerRow + k * kRowsAt;
                 int32_t gh, tq;
-                split_row(p, r, gh, tq);
+                split_row(p, run.rg * kTreeRows + row, gh, tq);
+                there[k] = row < rows && tq < run.n;
                 x[k] = make_uint4(0, 0, 0, 0);
-                if (r < p.G * p.T && tq < run.n)
+                if (there[k])
                     x[k] = *reinterpret_cast<const uint4*>(
                         (const __nv_bfloat16*)p.q.p + run.b * p.q.sb +
                         (int64_t)(run.h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl + c * 8);
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int32_t row = r0 + k * kRowsAt;
+                const int32_t row = r0 + t / kPerRow + k * kRowsAt;
+                uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                 if (F8) {
-                    uint32_t* w = &x[k].x;
                     float amax = 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -512,18 +542,24 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8, 
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         w[i] = pack_half2(bf16lo(w[i]) * inv, bf16hi(w[i]) * inv);
-                    if (c == 0)
-                        sh.qf[row] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (there[k] && c == 0)
+#pragma unroll
+                        for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i)
+                            sh.qf[seg & 1][row + 64 * i] =
+                                p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
                 }
-                st_shared_v4(qs + (row / kTreeRows) * C::kTileBytes + (c >> 3) * (kTreeRows * 128) +
-                                 sw128_offset(row % kTreeRows, c & 7),
-                             x[k].x, x[k].y, x[k].z, x[k].w);
+                if (there[k])
+#pragma unroll
+                    for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i)
+                        st_shared_v4(to + (c >> 3) * (kTreeRows * 128) +
+                                         sw128_offset(row + 64 * i, c & 7),
+                                     w[0], w[1], w[2], w[3]);
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if ((t & 31) == 0)
-            mbar_arrive(&sh.q_full);
+            mbar_arrive(&sh.q_full[seg & 1]);
     }
 }
 
@@ -533,22 +569,27 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8, 
 // A warp takes 32 rows.  Eight lanes at a time read 16 bytes each and write twice that,
 // which the swizzles keep free of bank conflicts where the two rows they are of differ in
 // bits 0 and 2 (128-byte rows), or in bit 0 (64-byte rows, two to a line).
-template <int D, int TILES>
-__device__ __forceinline__ void convert(const TreeParams& p, Shared<D, true, TILES>& sh,
-                                        uint32_t slots, uint32_t raw, const WaitCtx& wctx)
+template <int D>
+__device__ __forceinline__ void convert(Shared<D, true>& sh, uint32_t smem, const WaitCtx& wctx)
 {
-    using C = Cfg<D, true, TILES>;
+    using C = Cfg<D, true>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int sub = lane & 7, g = lane >> 3;
-    uint32_t rs = 0, rphase = 0, st = 0, phase = 0;
+    Ring<C::kRaw> rr;
+    Ring<C::kK> kr;
+    Ring<C::kV> vr;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 55); ++seg) {
         for (int32_t i = 0; i < 2 * run.nt; ++i) {
-            bool ok = mbar_wait(&sh.raw_full[rs], rphase, wctx, 56);
-            ok = ok && mbar_wait(&sh.empty[st], phase ^ 1, wctx, 57);
+            const bool is_v = i & 1;
+            bool ok = mbar_wait(&sh.raw_full[rr.at], rr.phase, wctx, 56);
+            ok = ok && (is_v ? mbar_wait(&sh.v_empty[vr.at], vr.phase ^ 1, wctx, 57)
+                             : mbar_wait(&sh.k_empty[kr.at], kr.phase ^ 1, wctx, 58));
             if (!__all_sync(0xffffffffu, ok))
                 return;
-            const uint32_t from = raw + rs * C::kRawBytes, to = slots + st * C::kTileBytes;
+            const uint32_t from = smem + C::kRaw0 + rr.at * C::kRawBytes;
+            const uint32_t to = smem + (is_v ? C::kV0 + vr.at * C::kTileBytes
+                                             : C::kK0 + kr.at * C::kTileBytes);
 #pragma unroll
             for (int it = 0; it < D / 16; ++it) {
                 uint32_t row, ch, src;
@@ -575,17 +616,14 @@ __device__ __forceinline__ void convert(const TreeParams& p, Shared<D, true, TIL
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.full[st]);
-                mbar_arrive(&sh.raw_empty[rs]);
+                mbar_arrive(is_v ? &sh.v_full[vr.at] : &sh.k_full[kr.at]);
+                mbar_arrive(&sh.raw_empty[rr.at]);
             }
-            if (++rs == C::kRaw) {
-                rs = 0;
-                rphase ^= 1;
-            }
-            if (++st == C::kSlots) {
-                st = 0;
-                phase ^= 1;
-            }
+            rr.next();
+            if (is_v)
+                vr.next();
+            else
+                kr.next();
         }
     }
 }
@@ -593,136 +631,109 @@ __device__ __forceinline__ void convert(const TreeParams& p, Shared<D, true, TIL
 // ---------------------------------------------------------------------------
 // products, issued by one thread
 // ---------------------------------------------------------------------------
-template <int D, bool F8, int TILES, bool TWO>
-__device__ __forceinline__ void multiply(Shared<D, F8, TILES>& sh, uint32_t qs, uint32_t slots,
-                                         uint32_t tmem, const WaitCtx& wctx)
+template <int D, bool F8, Terms TERMS>
+__device__ __forceinline__ void multiply(Shared<D, F8>& sh, uint32_t smem, uint32_t tmem,
+                                         const WaitCtx& wctx)
 {
-    using C = Cfg<D, F8, TILES>;
+    using C = Cfg<D, F8>;
     const int lane = threadIdx.x & 31;
-    const uint64_t dQ = sdesc_sw128(qs, 16, 1024);
-    const uint64_t dK = sdesc_sw128(slots, 16, 1024);
-    const uint64_t dV = sdesc_sw128(slots, 16384, 1024);
-    uint32_t gt = 0;
-    // slot and phase of the next K tile, and of the V tile whose product is next
-    uint32_t ks = 0, kphase = 0, vs = 1, vphase = 0;
-    auto two_on = [](uint32_t& s, uint32_t& ph) {
-        s += 2;
-        if (s >= (uint32_t)C::kSlots) {
-            s -= C::kSlots;
-            ph ^= 1;
-        }
-    };
-    auto scores = [&](int t, int w) {  // S_w = Q_t K^T
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_ss(tmem + w * 128, sdesc_add(dQ, t * C::kTileBytes + off),
-                   sdesc_add(dK, ks * C::kTileBytes + off), idesc<F8>(128, false), kk > 0);
-        }
-        tc_commit(&sh.s_full[w]);
-    };
-    auto outputs = [&](int w, bool add) {  // O_w += P_w V
-#pragma unroll
-        for (int kk = 0; kk < (TWO ? 16 : 8); ++kk)
-            mma_ts(tmem + 256 + w * D, tmem + w * 128 + kk * 8,
-                   sdesc_add(dV, vs * C::kTileBytes + (kk & 7) * 2048), idesc<F8>(D, true),
-                   (add || kk > 0) ? 1u : 0u);
-    };
-    uint32_t pc[2] = {0, 0};
+    const uint64_t dQ = sdesc_sw128(smem, 16, 1024);
+    const uint64_t dK = sdesc_sw128(smem + C::kK0, 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem + C::kV0, 16384, 1024);
+    Ring<C::kK> kr;
+    Ring<C::kV> vr;
+    // The scores go ahead of the products by two tiles, into the next segment if need be.
     Piece run;
-    for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 20); ++seg) {
+    uint32_t s_tile = 0, s_seg = 0;   // tile whose scores are next, and its segment
+    int32_t s_left = 0, s_nt = 0;     // tiles of that segment still to come
+    int32_t nts[2] = {0, 0};          // tiles of the segments, by their parity
+    bool more = true;
+    auto next_scores = [&]() -> bool {  // S = Q K^T; false: the block is giving up
+        if (s_left == 0) {
+            if (!more)
+                return true;
+            const bool there = next_run(sh, s_seg, run, wctx, 20);
+            if (!there) {
+                more = false;
+                nts[s_seg & 1] = 0;
+                return *wctx.abort_flag == 0;
+            }
+            s_left = s_nt = run.nt;
+            nts[s_seg & 1] = run.nt;
+            ++s_seg;
+        }
+        const uint32_t seg = s_seg - 1;
         bool ok = true;
         if (lane == 0) {
-            const int32_t nt = run.nt;
-            ok = mbar_wait(&sh.q_full, seg & 1, wctx, 21);
-            auto next_scores = [&](bool last) {
-                ok = ok && mbar_wait(&sh.full[ks], kphase, wctx, 22);
-                if (!ok)
-                    return;
+            ok = (s_left < s_nt || mbar_wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21)) &&
+                 mbar_wait(&sh.k_full[kr.at], kr.phase, wctx, 22);
+            if (ok) {
                 tc_fence_after();
-                scores(0, gt & 1);
-                tc_commit(&sh.empty[ks]);
-                if (last)
-                    tc_commit(&sh.q_empty);
-                two_on(ks, kphase);
-            };
-            if (TILES == 1) {
-                // gt counts the tiles whose scores are next
-                if (ok)
-                    next_scores(nt == 1);
-                ++gt;
-                for (int32_t i = 0; ok && i < nt; ++i) {
-                    if (i + 1 < nt) {
-                        next_scores(i + 2 == nt);
-                        ++gt;
-                    }
-                    const uint32_t w = (gt - (i + 1 < nt ? 2 : 1)) & 1;
-                    ok = ok && (i > 0 || mbar_wait(&sh.o_empty, (seg & 1) ^ 1, wctx, 23)) &&
-                         mbar_wait(&sh.full[vs], vphase, wctx, 24) &&
-                         mbar_wait(&sh.p_full[w], pc[w] & 1, wctx, 25);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    mma_ss(tmem + (s_tile & 1) * 128,
+                           sdesc_add(dQ, (seg & 1) * C::kTileBytes + off),
+                           sdesc_add(dK, kr.at * C::kTileBytes + off), idesc<F8>(128, false), kk > 0);
+                }
+                tc_commit(&sh.s_full[s_tile & 1]);
+                tc_commit(&sh.k_empty[kr.at]);
+                if (s_left == 1)
+                    tc_commit(&sh.q_empty[seg & 1]);
+            }
+        }
+        --s_left;
+        ++s_tile;
+        kr.next();
+        return __shfl_sync(0xffffffffu, (int)ok, 0);
+    };
+    if (!next_scores() || !next_scores())
+        return;
+    uint32_t gt = 0;
+    for (uint32_t seg = 0;; ++seg) {
+        const int32_t nt = seg < s_seg ? nts[seg & 1] : 0;
+        if (nt == 0)
+            break;
+        for (int32_t i = 0; i < nt; ++i, ++gt) {
+            bool ok = true;
+            if (lane == 0) {
+                ok = (i > 0 || mbar_wait(&sh.o_empty, (seg & 1) ^ 1, wctx, 23)) &&
+                     mbar_wait(&sh.v_full[vr.at], vr.phase, wctx, 24);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {  // O_w += P_w V, 64 keys
+                    ok = ok && mbar_wait(&sh.p_full[w][gt & 1], (gt >> 1) & 1, wctx, 25 + w);
                     if (!ok)
                         break;
-                    ++pc[w];
                     tc_fence_after();
-                    outputs(w, i >= 2);
-                    tc_commit(&sh.empty[vs]);
-                    two_on(vs, vphase);
-                }
-            } else {
-                for (int32_t i = -1; ok && i < nt; ++i) {
-                    if (i >= 0)
-                        ok = ok && (i > 0 || mbar_wait(&sh.o_empty, (seg & 1) ^ 1, wctx, 23)) &&
-                             mbar_wait(&sh.full[vs], vphase, wctx, 24);
-                    if (i + 1 < nt)
-                        ok = ok && (i >= 0 || mbar_wait(&sh.full[ks], kphase, wctx, 22));
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (i >= 0) {
-                            ok = ok && mbar_wait(&sh.p_full[w], pc[w] & 1, wctx, 25 + w);
-                            ++pc[w];
-                            tc_fence_after();
-                            if (ok)
-                                outputs(w, i > 0);
-                            if (w == 1 && ok)
-                                tc_commit(&sh.empty[vs]);
-                            if (w == 0 && i + 1 < nt)
-                                ok = ok && mbar_wait(&sh.full[ks], kphase, wctx, 22);
-                        }
-                        if (i + 1 < nt && ok) {
-                            tc_fence_after();
-                            scores(w, w);
-                            if (w == 1) {
-                                tc_commit(&sh.empty[ks]);
-                                if (i + 2 == nt)
-                                    tc_commit(&sh.q_empty);
-                            }
-                        }
-                    }
-                    if (i >= 0)
-                        two_on(vs, vphase);
-                    if (i + 1 < nt)
-                        two_on(ks, kphase);
+                    for (int kk = 0; kk < (TERMS == kColumns ? 8 : 4); ++kk)
+                        mma_ts(tmem + 256 + w * D, tmem + (gt & 1) * 128 + w * 64 + kk * 8,
+                               sdesc_add(dV, vr.at * C::kTileBytes + (w * 4 + (kk & 3)) * 2048),
+                               idesc<F8>(D, true), (i > 0 || kk > 0) ? 1u : 0u);
+                }
+                if (ok) {
+                    tc_commit(&sh.v_empty[vr.at]);
+                    tc_commit(&sh.pv_done);
                 }
             }
-            if (ok)
-                tc_commit(&sh.o_full);
+            vr.next();
+            if (!__shfl_sync(0xffffffffu, (int)ok, 0) || !next_scores())
+                return;
         }
-        if (!__shfl_sync(0xffffffffu, (int)ok, 0))
-            return;
     }
 }
 
 // ---------------------------------------------------------------------------
 // softmax
 // ---------------------------------------------------------------------------
-// Which of the 128 keys from key `base` on a node sees: of the rows before the tree all,
-// of the tree's those of its mask (NULL: none), of missing pages none.
+// Which of the 64 keys from key `base` on a node sees: of the rows before the tree all,
+// of the tree's those of its mask (NULL: none), of missing pages (from `base` on) none.
 __device__ __forceinline__ void visible(const TreeParams& p, const Piece& run, int32_t base,
-                                        const uint32_t* mask, uint32_t missing, uint32_t (&vis)[4])
+                                        const uint32_t* mask, uint32_t missing, uint32_t (&vis)[2])
 {
     const int32_t tree0 = run.len - run.n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int32_t k0 = base + 32 * i, off = k0 - tree0;  // node of the word's first key
         uint32_t bits = off <= -32 ? ~0u : off < 0 ? (1u << -off) - 1 : 0u;
         if (mask && off > -32 && off < run.n) {
@@ -740,8 +751,9 @@ __device__ __forceinline__ void visible(const TreeParams& p, const Piece& run, i
         vis[i] = bits;
     }
     if (missing) {
-        for (int k = 0; k < kTile / 16; ++k)
-            if (missing >> (16 * k >> p.c.page_log2) & 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (missing >> k & 1)
                 vis[k >> 1] &= ~(0xffffu << (16 * (k & 1)));
     }
 }
@@ -771,9 +783,9 @@ __device__ __noinline__ void add_apart(const TreeParams& p, const Piece& run, co
         float dot = 0.f, lu = 0.f;
         for (int f = 0; f < D; ++f)
             dot = fmaf(__bfloat162float(q[f]), cell(p.c.k, f), dot);
-        float x = dot * p.scale_log2;
+        float x = __fmul_rn(dot, p.scale_log2);
         if (F8) {
-            x *= p.c.k_scale[(int64_t)id * p.c.Hkv + run.h];
+            x = __fmul_rn(x, p.c.k_scale[(int64_t)id * p.c.Hkv + run.h]);
             lu = log2f(p.c.v_scale[(int64_t)id * p.c.Hkv + run.h]);
         }
         const float w = ex2((x - N) + (lu - Dd));
@@ -796,15 +808,14 @@ __device__ __forceinline__ float row_lse(float nx, float L)
     return L == 0.f ? -INFINITY : (nx + log2f(L)) * kLn2;
 }
 
-// Zeros rows of a V tile that are not the sequence's or whose page is missing, and rows
-// of the tree with values that are not finite, which it notes.  A thread a row.
+// Zeros a row of a V tile if it is not the sequence's or its page is missing, and if it is
+// the tree's and has values that are not finite, which it notes.
 template <int D, bool F8, typename SH>
-__device__ __forceinline__ void mend_values(const TreeParams& p, SH& sh, const Piece& run,
-                                            uint32_t vt, int32_t base, int32_t row,
-                                            uint32_t missing, uint32_t seg)
+__device__ __forceinline__ void mend_values(SH& sh, const Piece& run, uint32_t vt, int32_t base,
+                                            int32_t row, bool missing, uint32_t seg)
 {
     const int32_t j = base + row, node = j - (run.len - run.n);
-    const bool gone = j >= run.len || (missing >> (row >> p.c.page_log2) & 1);
+    const bool gone = j >= run.len || missing;
     if (!gone && node < 0)
         return;
     bool bad = false;
@@ -831,95 +842,162 @@ __device__ __forceinline__ void mend_values(const TreeParams& p, SH& sh, const P
     }
 }
 
-template <int D, bool F8, int TILES, bool TWO>
-__device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES>& sh,
-                                        uint32_t slots, uint32_t tmem, const WaitCtx& wctx)
+// Weights of a row's 64 keys from their scores r, as the products' operand at tP (TMEM):
+// 32 columns, and 32 of second terms (kLanes: `second` rows have those alone).  Returns
+// the sum of the terms.  FAR: scores are rounded before N is taken off, and weights are
+// powers of their own.
+template <bool F8, Terms TERMS, bool FAR, typename INFO>
+__device__ __forceinline__ float weights(const uint32_t (&r)[64], uint32_t tP, const INFO& ti,
+                                         int k0, int page_log2, float factor, float N, float Dd,
+                                         bool second)
 {
-    using C = Cfg<D, F8, TILES>;
+    const uint64_t off = f2pack(-N, -N);
+    uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // 32 keys at a time
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {  // 16 of a page
+            float2 sc = make_float2(1.f, 0.f);
+            if (F8)
+                sc = ti.scale[(k0 + 32 * k + 16 * g) >> page_log2];
+            const float fk = F8 ? factor * sc.x : factor, lu = F8 ? sc.y - Dd : 0.f;
+            const float up = F8 && !FAR ? ex2(lu) : 1.f;
+            const uint64_t f2 = f2pack(fk, fk), up2 = f2pack(up, up);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = 8 * g + i, at = 32 * k + 2 * j;
+                const float s0 = __uint_as_float(r[at]), s1 = __uint_as_float(r[at + 1]);
+                float a, b;
+                if (FAR) {  // (a packed product and sum would be joined to one operation)
+                    a = __fadd_rn(__fmul_rn(s0, fk), -N);
+                    b = __fadd_rn(__fmul_rn(s1, fk), -N);
+                } else {
+                    f2unpack(f2fma(f2pack(s0, s1), f2, off), a, b);
+                }
+                const float ea = a, eb = b;
+                a = ex2(a);
+                b = ex2(b);
+                sum[j & 1] = f2add(sum[j & 1], f2pack(a, b));
+                if (F8) {
+                    if (FAR) {
+                        a = ex2(ea + lu);
+                        b = ex2(eb + lu);
+                    } else {
+                        f2unpack(f2mul(f2pack(a, b), up2), a, b);
+                    }
+                    hi[j] = pack_half2(a, b);
+                    if (TERMS == kColumns || (TERMS == kLanes && second)) {
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+                        lo[j] = pack_half2(a - y.x, b - y.y);
+                    }
+                } else {
+                    // the first term cut off, not rounded: its bits are the upper half's
+                    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                    hi[j] = __byte_perm(ua, ub, 0x7632);
+                    if (TERMS == kColumns || second) {
+                        float c, d;
+                        f2unpack(f2add(f2pack(a, b),
+                                       f2pack(__uint_as_float((ua & 0xffff0000u) ^ 0x80000000u),
+                                              __uint_as_float((ub & 0xffff0000u) ^ 0x80000000u))),
+                                 c, d);
+                        lo[j] = pack_bf16x2(c, d);
+                    }
+                }
+                if (TERMS == kLanes && second)
+                    hi[j] = lo[j];
+            }
+        }
+        tmem_st16(tP + 16 * k, hi);
+        if (TERMS == kColumns)
+            tmem_st16(tP + 32 + 16 * k, lo);
+    }
+    float s0, s1, s2, s3;
+    f2unpack(sum[0], s0, s1);
+    f2unpack(sum[1], s2, s3);
+    return (s0 + s1) + (s2 + s3);
+}
+
+template <int D, bool F8, Terms TERMS>
+__device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, uint32_t smem,
+                                        uint32_t tmem, const WaitCtx& wctx)
+{
+    using C = Cfg<D, F8>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = warp >> 2, rit = (warp & 3) * 32 + lane;  // group, row of the tile
+    const int w = warp >> 2, rit = (warp & 3) * 32 + lane;  // group, row
+    const bool second = TERMS == kLanes && (warp & 2);
+    const int row = TERMS == kLanes ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256;
+    const uint32_t tS = tmem + lanes + w * 64, tO = tmem + lanes + 256;
     const int32_t R = p.G * p.T;
-    uint32_t gt = 0, sc = 0, met = 0;
+    uint32_t gt = 0, met = 0;
     int4 info = make_int4(0, 0, 0, 0);
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 30); ++seg) {
-        const int32_t r0 = run.rg * C::kRows + (TILES == 2 ? w * kTreeRows : 0);
         int32_t gh, tq;
-        split_row(p, r0 + rit, gh, tq);
-        const bool valid = r0 + rit < R && tq < run.n;
+        split_row(p, run.rg * kTreeRows + row, gh, tq);
+        const bool valid = run.rg * kTreeRows + row < R && tq < run.n;
         const uint32_t* mask =
             valid ? p.mask + ((int64_t)run.b * p.T + tq) * p.words : nullptr;
         float factor = p.scale_log2;
         if (F8) {
-            const bool ok = mbar_wait(&sh.q_full, seg & 1, wctx, 31);
+            const bool ok = mbar_wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 31);
             if (!__all_sync(0xffffffffu, ok))
                 return;
-            factor = sh.qf[(TILES == 2 ? w * kTreeRows : 0) + rit];
+            factor = sh.qf[seg & 1][rit];
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.q_empty);
+            if (TERMS != kLanes && lane == 0)
+                mbar_arrive(&sh.q_empty[seg & 1]);
         }
         float N = kNone, Dd = 0.f, l = 0.f;
-        bool first = true;
         for (int32_t i = 0; i < run.nt; ++i, ++gt) {
-            if (TILES == 1 && (gt & 1) != (uint32_t)w)
-                continue;
-            const int32_t base = (run.tile0 + i) * kTile;
+            const int32_t base = (run.tile0 + i) * kTile + w * 64;  // the group's 64 keys
             bool ok = mbar_wait(&sh.info_full[gt % kRing], (gt / kRing) & 1, wctx, 32);
             if (!__all_sync(0xffffffffu, ok))
                 return;
-            const TileInfo& ti = sh.info[gt % kRing];
-            const uint32_t flags = ti.flags, missing = flags & 0xffu;
-            const bool masked = base + kTile > run.len - run.n || missing;
-            uint32_t vis[4];
+            const TileInfo<F8>& ti = sh.info[gt % kRing];
+            const uint32_t flags = ti.flags;
+            // 16 keys a bit
+            uint32_t missing = 0;
+            if (flags & 0xffu)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    missing |= (flags >> ((w * 64 + 16 * k) >> p.c.page_log2) & 1u) << k;
+            const bool masked = base + 64 > run.len - run.n || missing;
+            uint32_t vis[2];
             if (masked)
                 visible(p, run, base, mask, missing, vis);
-            ok = mbar_wait(&sh.s_full[w], sc & 1, wctx, 33);
+            const uint32_t buf = (gt & 1) * 128;
+            ok = mbar_wait(&sh.s_full[gt & 1], (gt >> 1) & 1, wctx, 33);
             if (!__all_sync(0xffffffffu, ok))
                 return;
-            ++sc;
             tc_fence_after();
-            uint32_t r[128];
-            tmem_ld32(tS + 0, r);
-            tmem_ld32(tS + 32, r + 32);
-            tmem_ld32(tS + 64, r + 64);
-            tmem_ld32(tS + 96, r + 96);
+            uint32_t r[64];
+            tmem_ld32(tS + buf, r);
+            tmem_ld32(tS + buf + 32, r + 32);
             tmem_ld_wait();
             tmem_reg_fence32(r);
             tmem_reg_fence32(r + 32);
-            tmem_reg_fence32(r + 64);
-            tmem_reg_fence32(r + 96);
-            float x[128];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float fk = F8 ? factor * ti.scale[16 * k >> p.c.page_log2].x : factor;
-                const uint64_t f2 = f2pack(fk, fk);
-#pragma unroll
-                for (int j = 16 * k; j < 16 * k + 16; j += 2)
-                    f2unpack(f2mul(f2pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2),
-                             x[j], x[j + 1]);
-            }
             if (masked) {
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    x[j] = vis[j / 32] >> (j % 32) & 1 ? x[j] : -INFINITY;
+                for (int j = 0; j < 64; ++j)
+                    r[j] = vis[j / 32] >> (j % 32) & 1 ? r[j] : 0xff800000u;  // -inf
             }
-            float top[8];  // of 16 keys each
+            float top[4];  // of 16 keys each
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float m = fmaxf(x[16 * k], x[16 * k + 1]);
+            for (int k = 0; k < 4; ++k) {
+                float m = fmaxf(__uint_as_float(r[16 * k]), __uint_as_float(r[16 * k + 1]));
 #pragma unroll
                 for (int j = 16 * k + 2; j < 16 * k + 16; j += 2)
-                    m = fmax3(m, x[j], x[j + 1]);
-                top[k] = m;
+                    m = fmax3(m, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                // (rounded: N may become one of them, and is taken off them)
+                top[k] = __fmul_rn(
+                    m, F8 ? factor * ti.scale[(w * 64 + 16 * k) >> p.c.page_log2].x : factor);
             }
-            const float mx = fmaxf(fmax3(fmax3(top[0], top[1], top[2]), top[3], top[4]),
-                                   fmax3(top[5], top[6], top[7]));
+            const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
             // N up to the largest score, D up to the largest exponent, O with them
             float f = 1.f;
-            bool rise = mx - N > kGrow;
+            bool rise = valid && mx - N > kGrow<F8>;
             if (rise) {
                 f = ex2(N - mx);
                 l *= f;
@@ -929,18 +1007,29 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
             if (F8) {
                 float me = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    me = fmaxf(me, (top[k] - N) + ti.scale[16 * k >> p.c.page_log2].y);
-                rise = me - Dd > kTop;
+                for (int k = 0; k < 4; ++k)
+                    me = fmaxf(me, (top[k] - N) + ti.scale[(w * 64 + 16 * k) >> p.c.page_log2].y);
+                rise = valid && me - Dd > kTop;
                 f = 1.f;
                 if (rise) {
                     f = ex2(Dd - (me - kHead));
                     Dd = me - kHead;
                 }
             }
-            // O is as the product of this group's tile before this one left it: it was
-            // issued before these scores
-            if (!first && __any_sync(0xffffffffu, rise)) {
+            const bool far = valid && fabsf(N) >= kFar && N != kNone;
+            if (__any_sync(0xffffffffu, far) || (F8 && (flags & kWideTile)))
+                l += weights<F8, TERMS, true>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
+                                              second);
+            else
+                l += weights<F8, TERMS, false>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
+                                               second);
+            if (i > 0 && __any_sync(0xffffffffu, rise)) {
+                // (late, since it has to wait for the product before this one; the one before
+                // that was done when these scores were)
+                ok = mbar_wait(&sh.pv_done, (gt - 1) & 1, wctx, 37);
+                if (!__all_sync(0xffffffffu, ok))
+                    return;
+                tc_fence_after();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {
                     uint32_t o[16];
@@ -953,80 +1042,34 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
                     tmem_st16(tO + w * D + c0, o);
                 }
             }
-            first = false;
-            const uint64_t off = f2pack(-N, -N);
-            const bool wide = F8 && (flags & kWideTile);
-            uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // 32 keys at a time
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int at = 32 * k + 2 * j;
-                    const float lu = F8 ? ti.scale[(at & ~15) >> p.c.page_log2].y - Dd : 0.f;
-                    const uint64_t e = f2add(f2pack(x[at], x[at + 1]), off);
-                    float a, b;
-                    f2unpack(e, a, b);
-                    a = ex2(a);
-                    b = ex2(b);
-                    sum[j & 1] = f2add(sum[j & 1], f2pack(a, b));
-                    if (F8) {
-                        if (__builtin_expect(wide, 0)) {
-                            f2unpack(f2add(e, f2pack(lu, lu)), a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                        } else {
-                            const float g = ex2(lu);
-                            f2unpack(f2mul(f2pack(a, b), f2pack(g, g)), a, b);
-                        }
-                        hi[j] = pack_half2(a, b);
-                        if (TWO) {
-                            const float2 y =
-                                __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-                            lo[j] = pack_half2(a - y.x, b - y.y);
-                        }
-                    } else {
-                        hi[j] = pack_bf16x2(a, b);
-                        if (TWO)
-                            lo[j] = pack_bf16x2(a - bf16lo(hi[j]), b - bf16hi(hi[j]));
-                    }
-                }
-                tmem_st16(tS + 16 * k, hi);
-                if (TWO)
-                    tmem_st16(tS + 64 + 16 * k, lo);
-            }
-            float s0, s1, s2, s3;
-            f2unpack(sum[0], s0, s1);
-            f2unpack(sum[1], s2, s3);
-            l += (s0 + s1) + (s2 + s3);
             tmem_st_wait();
-            // V's rows that not everyone sees (TILES = 2: the first group's weights are
-            // waited for before either product with this tile)
-            if (masked && (TILES == 1 || w == 0)) {
-                const uint32_t at = 2 * gt + 1, vs = at % C::kSlots;
-                ok = mbar_wait(&sh.full[vs], (at / C::kSlots) & 1, wctx, 34);
+            if (masked) {  // V's rows that not everyone sees
+                const uint32_t vs = gt % C::kV;
+                ok = mbar_wait(&sh.v_full[vs], (gt / C::kV) & 1, wctx, 34);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
-                mend_values<D, F8>(p, sh, run, slots + vs * C::kTileBytes, base, rit, missing, seg);
+                if (rit < 64)
+                    mend_values<D, F8>(sh, run, smem + C::kV0 + vs * C::kTileBytes, base - w * 64,
+                                       w * 64 + rit, missing >> (rit >> 4) & 1, seg);
             }
             tc_fence_before();
-            mbar_arrive(&sh.p_full[w]);
+            mbar_arrive(&sh.p_full[w][gt & 1]);
         }
-        // ---- the segment's rows
-        float n0 = N, d0 = F8 ? Dd : 0.f;
-        const bool had[2] = {TILES == 2 || run.nt > 1 || ((gt - 1) & 1) == 0,
-                             TILES == 2 || run.nt > 1 || ((gt - 1) & 1) == 1};
-        if (TILES == 1) {
-            sh.n[seg & 1][w][rit] = n0;
-            sh.l[seg & 1][w][rit] = l;
-            if (F8)
-                sh.d[seg & 1][w][rit] = d0;
-        }
-        bool ok = mbar_wait(&sh.o_full, seg & 1, wctx, 35);
+        // ---- the segment's rows.  (The product before the last one first: a barrier tells
+        // a phase from the next only.  When these are done, nobody reads the groups' sums
+        // of the segment before any more.)
+        bool ok = mbar_wait(&sh.pv_done, (gt - 2) & 1, wctx, 38) &&
+                  mbar_wait(&sh.pv_done, (gt - 1) & 1, wctx, 35);
+        if (!__all_sync(0xffffffffu, ok))
+            return;
+        sh.n[w][rit] = N;
+        sh.l[w][rit] = l;
+        if (F8)
+            sh.d[w][rit] = Dd;
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.meet);
-        ok = ok && mbar_wait(&sh.meet, met, wctx, 36);
+        ok = mbar_wait(&sh.meet, met, wctx, 36);
         met ^= 1;
         if (!__all_sync(0xffffffffu, ok))
             return;
@@ -1036,48 +1079,68 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
             if (lane == 0)
                 sh.any_bad[(seg + 2) % 3] = 0;
         }
-        float fw[2] = {1.f, 1.f};
-        if (TILES == 1) {
-            const float na = sh.n[seg & 1][0][rit], nb = sh.n[seg & 1][1][rit];
-            const float nx = fmaxf(na, nb);
-            float da = na - nx, db = nb - nx, dx = 0.f;
-            l = sh.l[seg & 1][0][rit] * ex2(da) + sh.l[seg & 1][1][rit] * ex2(db);
-            if (F8) {
-                da += sh.d[seg & 1][0][rit];
-                db += sh.d[seg & 1][1][rit];
-                dx = fmaxf(da, db);
-            }
-            fw[0] = ex2(da - dx);
-            fw[1] = ex2(db - dx);
-            n0 = nx;
-            d0 = dx;
+        const float na = sh.n[0][rit], nb = sh.n[1][rit];
+        const float nx = fmaxf(na, nb);
+        float da = na - nx, db = nb - nx, dx = 0.f;
+        l = sh.l[0][rit] * ex2(da) + sh.l[1][rit] * ex2(db);
+        if (F8) {
+            da += sh.d[0][rit];
+            db += sh.d[1][rit];
+            dx = fmaxf(da, db);
         }
+        const float fa = ex2(da - dx), fb = ex2(db - dx);
         const bool whole = run.nt == run.tiles;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (run.tile0 == 0 ? 1 : 0);
-        const int64_t prow = slot * C::kRows + (TILES == 2 ? w * kTreeRows : 0) + rit;
+        const int64_t prow = slot * kTreeRows + row;
         const int64_t orow = ((int64_t)run.b * p.Hq + run.h * p.G + gh) * p.T + tq;
-        const float2 inv = row_factors<D, F8>(d0, l);
-        // TILES = 1: the groups take half of the features each
-        constexpr int kCols = TILES == 1 ? D / 2 : D;
-#pragma unroll 1
-        for (int c0 = TILES == 1 ? w * kCols : 0, end = c0 + kCols; c0 < end; c0 += 32) {
-            float o[32];
-            uint32_t t[32];
+        const float2 inv = row_factors<D, F8>(dx, l);
+        // The groups take half of the features each.  kLanes: second terms come by way of
+        // the segment's queries, which are done with.
+        const uint32_t pass = smem + (seg & 1) * C::kTileBytes + w * (64 * D * 2) + row * 128;
+        auto combined = [&](int c0, float (&o)[32]) {
+            uint32_t ta[32], tb[32];
+            tmem_ld32(tO + c0, ta);
+            tmem_ld32(tO + D + c0, tb);
+            tmem_ld_wait();
+            tmem_reg_fence32(ta);
+            tmem_reg_fence32(tb);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-                o[k] = 0.f;
+                o[k] = fmaf(fa, __uint_as_float(ta[k]), fb * __uint_as_float(tb[k]));
+        };
+        if (TERMS == kLanes) {
+            if (second) {
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    float o[32];
+                    combined(w * (D / 2) + 32 * c, o);
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                if (TILES == 2 ? a != w : !had[a])
-                    continue;
-                tmem_ld32(tO + a * D + c0, t);
-                tmem_ld_wait();
-                tmem_reg_fence32(t);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    o[k] = TILES == 1 ? fmaf(fw[a], __uint_as_float(t[k]), o[k])
-                                      : __uint_as_float(t[k]);
+                    for (int k = 0; k < 8; ++k)
+                        st_shared_v4(pass + c * (64 * 128) + ((k ^ (row & 7)) << 4),
+                                     __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                     __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.seconds);
+            } else {
+                ok = mbar_wait(&sh.seconds, met ^ 1, wctx, 39);
+                if (!__all_sync(0xffffffffu, ok))
+                    return;
             }
+        }
+#pragma unroll 1
+        for (int c = 0; c < (second ? 0 : D / 64); ++c) {
+            const int c0 = w * (D / 2) + 32 * c;
+            float o[32];
+            combined(c0, o);
+            if (TERMS == kLanes)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 x = lds128(pass + c * (64 * 128) + ((k ^ (row & 7)) << 4));
+                    o[4 * k] += __uint_as_float(x.x), o[4 * k + 1] += __uint_as_float(x.y);
+                    o[4 * k + 2] += __uint_as_float(x.z), o[4 * k + 3] += __uint_as_float(x.w);
+                }
             if (!valid)
                 continue;
             if (__builtin_expect(sh.any_bad[seg % 3], 0)) {
@@ -1085,7 +1148,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     y[k] = o[k];
-                add_apart<D, F8>(p, run, sh.bad[seg % 3], mask, gh, tq, n0, d0, c0, y);
+                add_apart<D, F8>(p, run, sh.bad[seg % 3], mask, gh, tq, nx, dx, c0, y);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     o[k] = y[k];
@@ -1117,11 +1180,16 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
         }
         tc_fence_before();
         mbar_arrive(&sh.o_empty);
-        if (valid && (TILES == 2 || w == 0)) {
+        if (TERMS == kLanes) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.q_empty[seg & 1]);
+        }
+        if (valid && w == 0 && !second) {
             if (whole)
-                p.lse[orow] = row_lse(n0, l);
+                p.lse[orow] = row_lse(nx, l);
             else
-                p.part_ndl[prow] = make_float4(n0, d0, l, 0.f);
+                p.part_ndl[prow] = make_float4(nx, dx, l, 0.f);
         }
         if (!whole && run.tile0 == 0) {
             // the group's blocks after this one that hold the rest: up to the last tile's
@@ -1134,23 +1202,32 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8, TILES
         p.info[blockIdx.x] = info;
 }
 
-template <int D, bool F8, int TILES, bool TWO>
-__global__ void __launch_bounds__(Cfg<D, F8, TILES>::kThreads, 1)
+template <int D, bool F8, Terms TERMS>
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeParams p)
 {
-    using C = Cfg<D, F8, TILES>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Shared<D, F8, TILES>& sh = *reinterpret_cast<Shared<D, F8, TILES>*>(smem + C::kShared0);
-    const uint32_t qs = smem_u32(smem) + C::kQ0, slots = smem_u32(smem) + C::kSlot0;
-    const uint32_t raw = smem_u32(smem) + C::kRaw0;
+    using C = Cfg<D, F8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {  // (the swizzle patterns begin there)
+        if (threadIdx.x == 0) {
+            p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+            cache_fault(p.c.status, kSiteShared, blockIdx.x);
+        }
+        return;
+    }
+    Shared<D, F8>& sh = *reinterpret_cast<Shared<D, F8>*>(smem + C::kShared0);
+    const uint32_t base = smem_u32(smem);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         sh.abort = 0;
-        for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(&sh.full[s], F8 ? 4 : 1);
-            mbar_init(&sh.empty[s], 1);
+        for (int s = 0; s < C::kK; ++s) {
+            mbar_init(&sh.k_full[s], F8 ? 4 : 1);
+            mbar_init(&sh.k_empty[s], 1);
+        }
+        for (int s = 0; s < C::kV; ++s) {
+            mbar_init(&sh.v_full[s], F8 ? 4 : 1);
+            mbar_init(&sh.v_empty[s], 1);
         }
         for (int s = 0; s < C::kRaw; ++s) {
             mbar_init(&sh.raw_full[s], 1);
@@ -1158,12 +1235,13 @@ __global__ void __launch_bounds__(Cfg<D, F8, TILES>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.p_full[s], 128);
+            mbar_init(&sh.p_full[0][s], 128);
+            mbar_init(&sh.p_full[1][s], 128);
+            mbar_init(&sh.q_full[s], 2);
+            mbar_init(&sh.q_empty[s], F8 || TERMS == kLanes ? 9 : 1);
         }
-        mbar_init(&sh.o_full, 1);
+        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.o_empty, 256);
-        mbar_init(&sh.q_full, 2);
-        mbar_init(&sh.q_empty, F8 ? 9 : 1);
         for (int s = 0; s < kRuns; ++s) {
             mbar_init(&sh.run_full[s], 1);
             mbar_init(&sh.run_empty[s], C::kReaders);
@@ -1171,45 +1249,42 @@ __global__ void __launch_bounds__(Cfg<D, F8, TILES>::kThreads, 1)
         for (int s = 0; s < kRing; ++s)
             mbar_init(&sh.info_full[s], 1);
         mbar_init(&sh.meet, 8);
+        mbar_init(&sh.seconds, 4);
         fence_barrier_init();
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
         p.info[blockIdx.x] = make_int4(0, 0, 0, 0);  // for a block that gives up
     }
-    if (threadIdx.x < 96)
-        sh.bad[threadIdx.x / 32][threadIdx.x % 32] = 0;
-    if (threadIdx.x < 3)
-        sh.any_bad[threadIdx.x] = 0;
     if (warp == 8) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
+    find_range<C::kThreads>(p, sh);
+    if (threadIdx.x < 96)
+        sh.bad[threadIdx.x / 32][threadIdx.x % 32] = 0;
+    if (threadIdx.x < 3)
+        sh.any_bad[threadIdx.x] = 0;
     tc_fence_before();
-    find_range<C::kThreads>(p, sh);  // also orders the initialisation
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
     if (warp < 8) {
-        reg_alloc<C::kRegsMath>();
-        softmax<D, F8, TILES, TWO>(p, sh, slots, tmem, wctx);
-    } else if (warp < 12) {
-        reg_dealloc<C::kRegsCtl>();
-        if (warp == 8) {
-            multiply<D, F8, TILES, TWO>(sh, qs, slots, tmem, wctx);
-        } else if (warp == 9) {
-            produce<D, F8, TILES>(p, sh, F8 ? raw : slots, tk, tv, wctx);
-            if (*wctx.abort_flag) {
-                // let copies in flight land before the block's shared memory goes
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 2000000ull) {
-                }
+        softmax<D, F8, TERMS>(p, sh, base, tmem, wctx);
+    } else if (warp == 8) {
+        multiply<D, F8, TERMS>(sh, base, tmem, wctx);
+    } else if (warp == 9) {
+        produce<D, F8>(p, sh, base, tk, tv, wctx);
+        if (*wctx.abort_flag) {
+            // let copies in flight land before the block's shared memory goes
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000ull) {
             }
-        } else {
-            load_queries<D, F8, TILES>(p, sh, qs, wctx);
         }
+    } else if (warp < 12) {
+        load_queries<D, F8, TERMS>(p, sh, base, wctx);
     } else if constexpr (F8) {
-        reg_dealloc<C::kRegsConv>();
-        convert<D, TILES>(p, sh, slots, raw, wctx);
+        convert<D>(sh, base, wctx);
     }
     __syncwarp();
     tc_fence_before();
@@ -1222,32 +1297,32 @@ __global__ void __launch_bounds__(Cfg<D, F8, TILES>::kThreads, 1)
 
 // Rows of the segments that several blocks share: block c holds such a segment's
 // beginning, the info[c].z blocks of its group after it the rest.  One warp a row.
-template <int D, bool F8, int ROWS>
+template <int D, bool F8>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TreeParams p)
 {
     const int4 info = p.info[blockIdx.x];
     const int k = info.z + 1;
     if (info.z <= 0)
         return;
-    const int32_t h = info.y / p.row_groups, r0 = (info.y - h * p.row_groups) * ROWS;
+    const int32_t h = info.y / p.row_groups, r0 = (info.y - h * p.row_groups) * kTreeRows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int own = 2 * blockIdx.x, step = 2 * p.row_groups;
     auto slot = [&](int i) -> int64_t { return i == 0 ? own + 1 : own + i * step; };
     constexpr int V = D / 32;  // features of a lane
-    for (int r = blockIdx.y * 8 + warp; r < ROWS && r0 + r < p.G * p.T; r += gridDim.y * 8) {
+    for (int r = blockIdx.y * 8 + warp; r < kTreeRows && r0 + r < p.G * p.T; r += gridDim.y * 8) {
         int32_t gh, tq;
         split_row(p, r0 + r, gh, tq);
         if (tq >= info.w)
             continue;
         float nx = kNone, dx = F8 ? -INFINITY : 0.f;
         for (int i = lane; i < k; i += 32)
-            nx = fmaxf(nx, p.part_ndl[slot(i) * ROWS + r].x);
+            nx = fmaxf(nx, p.part_ndl[slot(i) * kTreeRows + r].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
         if (F8) {
             for (int i = lane; i < k; i += 32) {
-                const float4 y = p.part_ndl[slot(i) * ROWS + r];
+                const float4 y = p.part_ndl[slot(i) * kTreeRows + r];
                 dx = fmaxf(dx, (y.x - nx) + y.y);
             }
 #pragma unroll
@@ -1258,14 +1333,14 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tree
         for (int c = 0; c < k; c += 32) {
             float4 y = make_float4(kNone, 0.f, 0.f, 0.f);
             if (c + lane < k)
-                y = p.part_ndl[slot(c + lane) * ROWS + r];
+                y = p.part_ndl[slot(c + lane) * kTreeRows + r];
             const float wt = ex2((y.x - nx) + (y.y - dx));
             L += y.z * ex2(y.x - nx);
             const int end = min(32, k - c);
 #pragma unroll 4
             for (int i = 0; i < end; ++i) {
                 const float wi = __shfl_sync(0xffffffffu, wt, i);
-                const float* from = p.part_o + (slot(c + i) * ROWS + r) * D + lane * V;
+                const float* from = p.part_o + (slot(c + i) * kTreeRows + r) * D + lane * V;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     acc[v] = fmaf(wi, from[v], acc[v]);
@@ -1292,15 +1367,15 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tree
     }
 }
 
-template <int D, bool F8, int TILES, bool TWO>
+template <int D, bool F8, Terms TERMS>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, int num_sms,
                    cudaStream_t stream)
 {
-    using C = Cfg<D, F8, TILES>;
-    static_assert(kSmem<D, F8, TILES> <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<D, F8, TILES, TWO>,
+    using C = Cfg<D, F8>;
+    static_assert(kSmem<D, F8> <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<D, F8, TERMS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem<D, F8, TILES>);
+                                         kSmem<D, F8>);
     if (e != cudaSuccess)
         return e;
     // a block an SM, no more than there can be pieces
@@ -1308,31 +1383,29 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, 
     const int32_t longest = max(1, ceil_div(p.c.max_pages * p.c.page, kTile));
     p.whole = longest <= kWhole;
     const int64_t pieces = min(segments, (int64_t)kTreeMaxCtas) * (p.whole ? 1 : longest);
-    p.row_groups = ceil_div(p.G * p.T, C::kRows);
+    p.row_groups = ceil_div(p.G * p.T, kTreeRows);
     const int most = min(kTreeMaxCtas, num_sms);
     p.line_blocks = (int)min((int64_t)max(1, most / p.row_groups), pieces);
     const int grid = p.line_blocks * p.row_groups;
     p.segment_cost = 2;
-    decode_tree_kernel<D, F8, TILES, TWO>
-        <<<grid, C::kThreads, kSmem<D, F8, TILES>, stream>>>(tk, tv, p);
+    decode_tree_kernel<D, F8, TERMS><<<grid, C::kThreads, kSmem<D, F8>, stream>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.whole)
         return e;
-    const int rows = min(C::kRows, p.G * p.T);
-    merge_kernel<D, F8, C::kRows><<<dim3(grid, (rows + 7) / 8), 256, 0, stream>>>(p);
+    const int rows = min(kTreeRows, p.G * p.T);
+    merge_kernel<D, F8><<<dim3(grid, (rows + 7) / 8), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int D, bool F8>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, int num_sms,
-                        cudaStream_t stream)
+cudaError_t launch_terms(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, int num_sms,
+                         cudaStream_t stream)
 {
-    const bool one = p.G * p.T <= kTreeRows;
-    if (F8 && !p.o_fp32)  // (see "Rounding" above)
-        return one ? launch<D, F8, 1, !F8>(tk, tv, p, num_sms, stream)
-                   : launch<D, F8, 2, !F8>(tk, tv, p, num_sms, stream);
-    return one ? launch<D, F8, 1, true>(tk, tv, p, num_sms, stream)
-               : launch<D, F8, 2, true>(tk, tv, p, num_sms, stream);
+    if constexpr (F8)
+        if (!p.o_fp32)  // (see "Rounding" above)
+            return launch<D, F8, kOne>(tk, tv, p, num_sms, stream);
+    return p.G * p.T <= 64 ? launch<D, F8, kLanes>(tk, tv, p, num_sms, stream)
+                           : launch<D, F8, kColumns>(tk, tv, p, num_sms, stream);
 }
 
 }  // namespace tree
@@ -1341,10 +1414,10 @@ cudaError_t launch_decode_tree(const CUtensorMap& tk, const CUtensorMap& tv, Tre
                                int num_sms, cudaStream_t stream)
 {
     if (p.c.e4m3)
-        return p.c.d == 128 ? tree::launch_rows<128, true>(tk, tv, p, num_sms, stream)
-                            : tree::launch_rows<64, true>(tk, tv, p, num_sms, stream);
-    return p.c.d == 128 ? tree::launch_rows<128, false>(tk, tv, p, num_sms, stream)
-                        : tree::launch_rows<64, false>(tk, tv, p, num_sms, stream);
+        return p.c.d == 128 ? tree::launch_terms<128, true>(tk, tv, p, num_sms, stream)
+                            : tree::launch_terms<64, true>(tk, tv, p, num_sms, stream);
+    return p.c.d == 128 ? tree::launch_terms<128, false>(tk, tv, p, num_sms, stream)
+                        : tree::launch_terms<64, false>(tk, tv, p, num_sms, stream);
 }
 
 }  // namespace dfa
