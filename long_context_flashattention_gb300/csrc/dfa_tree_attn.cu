@@ -20,9 +20,9 @@
 // A block (one an SM) keeps 128 query rows and walks over 128-key tiles of the cache:
 //   warp 9       pages by TMA into a ring of K and V tiles, 128-byte swizzle;
 //   warps 12-15  (8-bit cells) those to fp16, in the same layout;
-//   warps 10-11  the next segment's queries (8-bit cells: fp16 relative to a power of two
+//   warp 11      the next segment's queries (8-bit cells: fp16 relative to a power of two
 //                of the row: exact but for elements below 2^-31 of its largest one);
-//   warp 8       S = Q K^T into TMEM, O += P V with P from TMEM (over S's columns);
+//   warps 8, 10  S = Q K^T into TMEM, O += P V with P from TMEM (over S's columns);
 //   warps 0-3    softmax of the tile's first 64 keys, warps 4-7 of the others, a thread a
 //                row, each with an N, D, sum and O of its own, joined at the segment's end.
 //                O is rescaled in TMEM when D (or N) has to rise.
@@ -114,7 +114,7 @@ struct Shared {
     using C = Cfg<D, F8>;
     uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
     uint64_t raw_full[F8 ? C::kRaw : 1], raw_empty[F8 ? C::kRaw : 1];
-    uint64_t s_full[2], p_full[2][2], pv_done, o_empty, q_full[2], q_empty[2];
+    uint64_t s_full[2], s_free[2], p_full[2][2], o_empty, q_full[2], q_empty[2];
     uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, seconds;
     Piece run[kRuns];
     TileInfo<F8> info[kRing];
@@ -133,6 +133,27 @@ struct Shared {
 
 template <int D, bool F8>
 constexpr int kSmem = Cfg<D, F8>::kShared0 + (int)sizeof(Shared<D, F8>);
+
+// mbar_wait with its loop out of the way: the roles' inner loops are to fit the first
+// instruction caches, which they share.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where)
+{
+    return mbar_wait(bar, parity, w, where);
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where)
+{
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, w, where);
+}
+
+// columns of a row's 8 words
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2, int c3)
@@ -333,7 +354,7 @@ template <typename SH>
 __device__ __forceinline__ bool next_run(SH& sh, uint32_t seg, Piece& run, const WaitCtx& wctx,
                                          int where)
 {
-    const bool ok = mbar_wait(&sh.run_full[seg % kRuns], (seg / kRuns) & 1, wctx, where);
+    const bool ok = wait(&sh.run_full[seg % kRuns], (seg / kRuns) & 1, wctx, where);
     if (!__all_sync(0xffffffffu, ok))
         return false;
     run = sh.run[seg % kRuns];
@@ -383,7 +404,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
         return win + lane < end ? page_entry(p.c, x.b, win + lane) : -1;
     };
     auto announce = [&](bool end) {
-        const bool ok = mbar_wait(&sh.run_empty[seg % kRuns], (seg / kRuns + 1) & 1, wctx, 51);
+        const bool ok = wait(&sh.run_empty[seg % kRuns], (seg / kRuns + 1) & 1, wctx, 51);
         if (!__all_sync(0xffffffffu, ok))
             return false;
         if (lane == 0) {
@@ -436,7 +457,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
                                               : kv ? C::kV0 + vr.at * kBytes
                                                    : C::kK0 + kr.at * kBytes);
                 // (passes at once in the first round: the phase before the barrier's first)
-                const bool ok = mbar_wait(empty, (F8 || !kv ? kr.phase : vr.phase) ^ 1, wctx, 50);
+                const bool ok = wait(empty, (F8 || !kv ? kr.phase : vr.phase) ^ 1, wctx, 50);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 if (lane == 0)
@@ -499,12 +520,12 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>&
 {
     using C = Cfg<D, F8>;
     constexpr int kPerRow = D / 8;                 // lanes of a row, 8 elements each
-    constexpr int kRowsAt = 64 / kPerRow;          // rows of the two warps at a time
+    constexpr int kRowsAt = 32 / kPerRow;          // rows of the warp at a time
     constexpr int kBatch = 8;
-    const int t = threadIdx.x & 63, c = t % kPerRow;
+    const int t = threadIdx.x & 31, c = t % kPerRow;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 53); ++seg) {
-        const bool ok = mbar_wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
+        const bool ok = wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
         if (!__all_sync(0xffffffffu, ok))
             return;
         const uint32_t to = qs + (seg & 1) * C::kTileBytes;
@@ -558,7 +579,7 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>&
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if ((t & 31) == 0)
+        if (t == 0)
             mbar_arrive(&sh.q_full[seg & 1]);
     }
 }
@@ -575,6 +596,19 @@ __device__ __forceinline__ void convert(Shared<D, true>& sh, uint32_t smem, cons
     using C = Cfg<D, true>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int sub = lane & 7, g = lane >> 3;
+    // offsets of the thread's first 16 codes (128-byte rows: of either half of a row), and
+    // of the 16-byte chunks that they become; then every 8 rows
+    uint32_t src[D / 64], dst[D / 64][2];
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half) {
+        const uint32_t row = warp * 32 + (D == 128 ? ((sub >> 2) ? g ^ 5 : g) : g * 2 + (sub >> 2));
+        const uint32_t ch = (sub & 3) + 4 * half;
+        src[half] = D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4)
+                             : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            dst[half][e] = half * (kTile * 128) + sw128_offset(row, 2 * (sub & 3) + e);
+    }
     Ring<C::kRaw> rr;
     Ring<C::kK> kr;
     Ring<C::kV> vr;
@@ -582,35 +616,29 @@ __device__ __forceinline__ void convert(Shared<D, true>& sh, uint32_t smem, cons
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 55); ++seg) {
         for (int32_t i = 0; i < 2 * run.nt; ++i) {
             const bool is_v = i & 1;
-            bool ok = mbar_wait(&sh.raw_full[rr.at], rr.phase, wctx, 56);
-            ok = ok && (is_v ? mbar_wait(&sh.v_empty[vr.at], vr.phase ^ 1, wctx, 57)
-                             : mbar_wait(&sh.k_empty[kr.at], kr.phase ^ 1, wctx, 58));
+            bool ok = wait(&sh.raw_full[rr.at], rr.phase, wctx, 56);
+            ok = ok && (is_v ? wait(&sh.v_empty[vr.at], vr.phase ^ 1, wctx, 57)
+                             : wait(&sh.k_empty[kr.at], kr.phase ^ 1, wctx, 58));
             if (!__all_sync(0xffffffffu, ok))
                 return;
             const uint32_t from = smem + C::kRaw0 + rr.at * C::kRawBytes;
             const uint32_t to = smem + (is_v ? C::kV0 + vr.at * C::kTileBytes
                                              : C::kK0 + kr.at * C::kTileBytes);
 #pragma unroll
-            for (int it = 0; it < D / 16; ++it) {
-                uint32_t row, ch, src;
-                if (D == 128) {
-                    row = warp * 32 + (it >> 1) * 8 + ((sub >> 2) ? g ^ 5 : g);
-                    ch = (sub & 3) + 4 * (it & 1);
-                    src = row * 128 + ((ch ^ (row & 7)) << 4);
-                } else {
-                    row = warp * 32 + it * 8 + g * 2 + (sub >> 2);
-                    ch = sub & 3;
-                    src = row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-                }
-                const uint4 x = lds128(from + src);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int half = 0; half < D / 64; ++half) {
+                uint4 x[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t c16 = 2 * ch + e;
-                    st_shared_v4(to + (c16 >> 3) * (kTile * 128) + sw128_offset(row, c16 & 7),
-                                 e4m3x2_half2(w[2 * e] & 0xffffu), e4m3x2_half2(w[2 * e] >> 16),
-                                 e4m3x2_half2(w[2 * e + 1] & 0xffffu),
-                                 e4m3x2_half2(w[2 * e + 1] >> 16));
+                for (int k = 0; k < 4; ++k)
+                    x[k] = lds128(from + src[half] + k * 8 * D);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        st_shared_v4(to + dst[half][e] + k * 1024, e4m3x2_half2(w[2 * e] & 0xffffu),
+                                     e4m3x2_half2(w[2 * e] >> 16),
+                                     e4m3x2_half2(w[2 * e + 1] & 0xffffu),
+                                     e4m3x2_half2(w[2 * e + 1] >> 16));
                 }
             }
             fence_proxy_async_smem();
@@ -629,96 +657,117 @@ __device__ __forceinline__ void convert(Shared<D, true>& sh, uint32_t smem, cons
 }
 
 // ---------------------------------------------------------------------------
-// products, issued by one thread
+// products, issued by a thread of one warp each, so that neither waits for the other's
+// barriers
 // ---------------------------------------------------------------------------
-template <int D, bool F8, Terms TERMS>
-__device__ __forceinline__ void multiply(Shared<D, F8>& sh, uint32_t smem, uint32_t tmem,
-                                         const WaitCtx& wctx)
+// The warps go through their loops whole, and one lane is elected at each instruction:
+// descriptors and addresses are then the warp's, and stay in its uniform registers.
+// Measured (clk to issue a product with both operands in shared memory, and with one in
+// TMEM): 43 and 39, by one lane's loop 73 and 111.
+__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void commit_one(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, const WaitCtx& w,
+                                         int where)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, w, where));
+}
+
+// S = Q K^T, up to two tiles ahead of the products
+template <int D, bool F8>
+__device__ __forceinline__ void multiply_scores(Shared<D, F8>& sh, uint32_t smem,
+                                                const WaitCtx& wctx)
 {
     using C = Cfg<D, F8>;
-    const int lane = threadIdx.x & 31;
     const uint64_t dQ = sdesc_sw128(smem, 16, 1024);
     const uint64_t dK = sdesc_sw128(smem + C::kK0, 16, 1024);
-    const uint64_t dV = sdesc_sw128(smem + C::kV0, 16384, 1024);
     Ring<C::kK> kr;
-    Ring<C::kV> vr;
-    // The scores go ahead of the products by two tiles, into the next segment if need be.
-    Piece run;
-    uint32_t s_tile = 0, s_seg = 0;   // tile whose scores are next, and its segment
-    int32_t s_left = 0, s_nt = 0;     // tiles of that segment still to come
-    int32_t nts[2] = {0, 0};          // tiles of the segments, by their parity
-    bool more = true;
-    auto next_scores = [&]() -> bool {  // S = Q K^T; false: the block is giving up
-        if (s_left == 0) {
-            if (!more)
-                return true;
-            const bool there = next_run(sh, s_seg, run, wctx, 20);
-            if (!there) {
-                more = false;
-                nts[s_seg & 1] = 0;
-                return *wctx.abort_flag == 0;
-            }
-            s_left = s_nt = run.nt;
-            nts[s_seg & 1] = run.nt;
-            ++s_seg;
-        }
-        const uint32_t seg = s_seg - 1;
-        bool ok = true;
-        if (lane == 0) {
-            ok = (s_left < s_nt || mbar_wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21)) &&
-                 mbar_wait(&sh.k_full[kr.at], kr.phase, wctx, 22);
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                    mma_ss(tmem + (s_tile & 1) * 128,
-                           sdesc_add(dQ, (seg & 1) * C::kTileBytes + off),
-                           sdesc_add(dK, kr.at * C::kTileBytes + off), idesc<F8>(128, false), kk > 0);
-                }
-                tc_commit(&sh.s_full[s_tile & 1]);
-                tc_commit(&sh.k_empty[kr.at]);
-                if (s_left == 1)
-                    tc_commit(&sh.q_empty[seg & 1]);
-            }
-        }
-        --s_left;
-        ++s_tile;
-        kr.next();
-        return __shfl_sync(0xffffffffu, (int)ok, 0);
-    };
-    if (!next_scores() || !next_scores())
-        return;
     uint32_t gt = 0;
-    for (uint32_t seg = 0;; ++seg) {
-        const int32_t nt = seg < s_seg ? nts[seg & 1] : 0;
-        if (nt == 0)
-            break;
-        for (int32_t i = 0; i < nt; ++i, ++gt) {
-            bool ok = true;
-            if (lane == 0) {
-                ok = (i > 0 || mbar_wait(&sh.o_empty, (seg & 1) ^ 1, wctx, 23)) &&
-                     mbar_wait(&sh.v_full[vr.at], vr.phase, wctx, 24);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {  // O_w += P_w V, 64 keys
-                    ok = ok && mbar_wait(&sh.p_full[w][gt & 1], (gt >> 1) & 1, wctx, 25 + w);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < (TERMS == kColumns ? 8 : 4); ++kk)
-                        mma_ts(tmem + 256 + w * D, tmem + (gt & 1) * 128 + w * 64 + kk * 8,
-                               sdesc_add(dV, vr.at * C::kTileBytes + (w * 4 + (kk & 3)) * 2048),
-                               idesc<F8>(D, true), (i > 0 || kk > 0) ? 1u : 0u);
-                }
-                if (ok) {
-                    tc_commit(&sh.v_empty[vr.at]);
-                    tc_commit(&sh.pv_done);
-                }
-            }
-            vr.next();
-            if (!__shfl_sync(0xffffffffu, (int)ok, 0) || !next_scores())
+    Piece run;
+    for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 20); ++seg) {
+        const uint64_t q = sdesc_add(dQ, (seg & 1) * C::kTileBytes);
+        if (!wait_all(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21))
+            return;
+        const int32_t nt = __shfl_sync(0xffffffffu, run.nt, 0);
+        for (int32_t i = 0; i < nt; ++i, ++gt, kr.next()) {
+            if (!wait_all(&sh.s_free[gt & 1], ((gt >> 1) & 1) ^ 1, wctx, 27) ||
+                !wait_all(&sh.k_full[kr.at], kr.phase, wctx, 22))
                 return;
+            tc_fence_after();
+            const uint64_t k = sdesc_add(dK, kr.at * C::kTileBytes);
+            const uint32_t to = (gt & 1) * 128;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                mma_ss_one(to, sdesc_add(q, off), sdesc_add(k, off), idesc<F8>(128, false), kk > 0);
+            }
+            commit_one(&sh.s_full[gt & 1]);
+            commit_one(&sh.k_empty[kr.at]);
+            if (i + 1 == nt)
+                commit_one(&sh.q_empty[seg & 1]);
+        }
+    }
+}
+
+// O_w += P_w V, of 64 keys each
+template <int D, bool F8, Terms TERMS>
+__device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem,
+                                                const WaitCtx& wctx)
+{
+    using C = Cfg<D, F8>;
+    const uint64_t dV = sdesc_sw128(smem + C::kV0, 16384, 1024);
+    Ring<C::kV> vr;
+    uint32_t gt = 0;
+    Piece run;
+    for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 28); ++seg) {
+        if (!wait_all(&sh.o_empty, (seg & 1) ^ 1, wctx, 23))
+            return;
+        const int32_t nt = __shfl_sync(0xffffffffu, run.nt, 0);
+        for (int32_t i = 0; i < nt; ++i, ++gt, vr.next()) {
+            if (!wait_all(&sh.v_full[vr.at], vr.phase, wctx, 24))
+                return;
+            const uint64_t v = sdesc_add(dV, vr.at * C::kTileBytes);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!wait_all(&sh.p_full[w][gt & 1], (gt >> 1) & 1, wctx, 25 + w))
+                    return;
+                tc_fence_after();
+                const uint32_t from = (gt & 1) * 128 + w * 64;
+#pragma unroll
+                for (int kk = 0; kk < (TERMS == kColumns ? 8 : 4); ++kk)
+                    mma_ts_one(256 + w * D,
+                               from + (TERMS == kColumns ? (kk & 3) * 16 + (kk >> 2) * 8 : kk * 8),
+                               sdesc_add(v, (w * 4 + (kk & 3)) * 2048), idesc<F8>(D, true),
+                               (i > 0 || kk > 0) ? 1u : 0u);
+            }
+            commit_one(&sh.s_free[gt & 1]);
+            commit_one(&sh.v_empty[vr.at]);
         }
     }
 }
@@ -728,9 +777,10 @@ __device__ __forceinline__ void multiply(Shared<D, F8>& sh, uint32_t smem, uint3
 // ---------------------------------------------------------------------------
 // Which of the 64 keys from key `base` on a node sees: of the rows before the tree all,
 // of the tree's those of its mask (NULL: none), of missing pages (from `base` on) none.
-__device__ __forceinline__ void visible(const TreeParams& p, const Piece& run, int32_t base,
-                                        const uint32_t* mask, uint32_t missing, uint32_t (&vis)[2])
+__device__ __noinline__ uint2 visible(const TreeParams& p, const Piece& run, int32_t base,
+                                        const uint32_t* mask, uint32_t missing)
 {
+    uint32_t vis[2];
     const int32_t tree0 = run.len - run.n;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -750,12 +800,11 @@ __device__ __forceinline__ void visible(const TreeParams& p, const Piece& run, i
         }
         vis[i] = bits;
     }
-    if (missing) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (missing >> k & 1)
-                vis[k >> 1] &= ~(0xffffu << (16 * (k & 1)));
-    }
+    for (int k = 0; k < 4; ++k)
+        if (missing >> k & 1)
+            vis[k >> 1] &= ~(0xffffu << (16 * (k & 1)));
+    return make_uint2(vis[0], vis[1]);
 }
 
 // Adds the values of the nodes in `bad`, which the products left out, to features
@@ -811,7 +860,7 @@ __device__ __forceinline__ float row_lse(float nx, float L)
 // Zeros a row of a V tile if it is not the sequence's or its page is missing, and if it is
 // the tree's and has values that are not finite, which it notes.
 template <int D, bool F8, typename SH>
-__device__ __forceinline__ void mend_values(SH& sh, const Piece& run, uint32_t vt, int32_t base,
+__device__ __noinline__ void mend_values(SH& sh, const Piece& run, uint32_t vt, int32_t base,
                                             int32_t row, bool missing, uint32_t seg)
 {
     const int32_t j = base + row, node = j - (run.len - run.n);
@@ -842,75 +891,79 @@ __device__ __forceinline__ void mend_values(SH& sh, const Piece& run, uint32_t v
     }
 }
 
-// Weights of a row's 64 keys from their scores r, as the products' operand at tP (TMEM):
-// 32 columns, and 32 of second terms (kLanes: `second` rows have those alone).  Returns
-// the sum of the terms.  FAR: scores are rounded before N is taken off, and weights are
-// powers of their own.
-template <bool F8, Terms TERMS, bool FAR, typename INFO>
-__device__ __forceinline__ float weights(const uint32_t (&r)[64], uint32_t tP, const INFO& ti,
+__device__ __forceinline__ void hide16(uint32_t (&r)[16], uint32_t seen)
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        r[j] = seen >> j & 1 ? r[j] : 0xff800000u;  // -inf
+}
+
+// The weights y of 16 keys as the products' operand, in place of their scores (TMEM): 8
+// columns for 16 keys, one behind the other (kColumns: 8, and 8 of second terms, where
+// the keys' scores were).  kLanes: `second` rows have second terms alone.
+template <bool F8, Terms TERMS>
+__device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&y)[16], bool second)
+{
+    uint32_t hi[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = y[2 * j], b = y[2 * j + 1];
+        // bf16: the first term cut off, not rounded: its bits are the upper half's
+        hi[j] = F8 ? pack_half2(a, b)
+                   : __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    }
+    if (TERMS == kColumns || (TERMS == kLanes && second)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = y[2 * j], b = y[2 * j + 1];
+            float c, d;
+            if (F8) {
+                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+                c = a - z.x, d = b - z.y;
+            } else {
+                const uint32_t ua = __float_as_uint(a) & 0xffff0000u;
+                const uint32_t ub = __float_as_uint(b) & 0xffff0000u;
+                f2unpack(f2add(f2pack(a, b), f2pack(__uint_as_float(ua ^ 0x80000000u),
+                                                    __uint_as_float(ub ^ 0x80000000u))),
+                         c, d);
+            }
+            hi[TERMS == kLanes ? j : 8 + j] = F8 ? pack_half2(c, d) : pack_bf16x2(c, d);
+        }
+    }
+    if (TERMS == kColumns)
+        tmem_st16(tS + 16 * k, hi);
+    else
+        tmem_st8(tS + 8 * k, hi);
+}
+
+// Weights of a row's 64 keys from their scores r.  Returns the sum of the terms.
+template <bool F8, Terms TERMS, typename INFO>
+__device__ __forceinline__ float weights(const uint32_t (&r)[4][16], uint32_t tS, const INFO& ti,
                                          int k0, int page_log2, float factor, float N, float Dd,
                                          bool second)
 {
     const uint64_t off = f2pack(-N, -N);
     uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {  // 32 keys at a time
-        uint32_t hi[16], lo[16];
+    for (int k = 0; k < 4; ++k) {
+        float2 sc = make_float2(1.f, 0.f);
+        if (F8)
+            sc = ti.scale[(k0 + 16 * k) >> page_log2];
+        const float fk = F8 ? factor * sc.x : factor, up = F8 ? ex2(sc.y - Dd) : 1.f;
+        const uint64_t f2 = f2pack(fk, fk), up2 = f2pack(up, up);
+        float y[16];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {  // 16 of a page
-            float2 sc = make_float2(1.f, 0.f);
+        for (int j = 0; j < 16; j += 2) {
+            float a, b;
+            f2unpack(f2fma(f2pack(__uint_as_float(r[k][j]), __uint_as_float(r[k][j + 1])), f2, off),
+                     a, b);
+            uint64_t e = f2pack(ex2(a), ex2(b));
+            sum[j >> 1 & 1] = f2add(sum[j >> 1 & 1], e);
             if (F8)
-                sc = ti.scale[(k0 + 32 * k + 16 * g) >> page_log2];
-            const float fk = F8 ? factor * sc.x : factor, lu = F8 ? sc.y - Dd : 0.f;
-            const float up = F8 && !FAR ? ex2(lu) : 1.f;
-            const uint64_t f2 = f2pack(fk, fk), up2 = f2pack(up, up);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = 8 * g + i, at = 32 * k + 2 * j;
-                const float s0 = __uint_as_float(r[at]), s1 = __uint_as_float(r[at + 1]);
-                float a, b;
-                if (FAR) {  // (a packed product and sum would be joined to one operation)
-                    a = __fadd_rn(__fmul_rn(s0, fk), -N);
-                    b = __fadd_rn(__fmul_rn(s1, fk), -N);
-                } else {
-                    f2unpack(f2fma(f2pack(s0, s1), f2, off), a, b);
-                }
-                const float ea = a, eb = b;
-                a = ex2(a);
-                b = ex2(b);
-                sum[j & 1] = f2add(sum[j & 1], f2pack(a, b));
-                if (F8) {
-                    if (FAR) {
-                        a = ex2(ea + lu);
-                        b = ex2(eb + lu);
-                    } else {
-                        f2unpack(f2mul(f2pack(a, b), up2), a, b);
-                    }
-                    hi[j] = pack_half2(a, b);
-                    if (TERMS == kColumns || (TERMS == kLanes && second)) {
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-                        lo[j] = pack_half2(a - y.x, b - y.y);
-                    }
-                } else {
-                    // the first term cut off, not rounded: its bits are the upper half's
-                    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                    hi[j] = __byte_perm(ua, ub, 0x7632);
-                    if (TERMS == kColumns || second) {
-                        float c, d;
-                        f2unpack(f2add(f2pack(a, b),
-                                       f2pack(__uint_as_float((ua & 0xffff0000u) ^ 0x80000000u),
-                                              __uint_as_float((ub & 0xffff0000u) ^ 0x80000000u))),
-                                 c, d);
-                        lo[j] = pack_bf16x2(c, d);
-                    }
-                }
-                if (TERMS == kLanes && second)
-                    hi[j] = lo[j];
-            }
+                e = f2mul(e, up2);
+            f2unpack(e, y[j], y[j + 1]);
         }
-        tmem_st16(tP + 16 * k, hi);
-        if (TERMS == kColumns)
-            tmem_st16(tP + 32 + 16 * k, lo);
+        store_weights<F8, TERMS>(tS, k, y, second);
     }
     float s0, s1, s2, s3;
     f2unpack(sum[0], s0, s1);
@@ -918,9 +971,44 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[64], uint32_t tP, c
     return (s0 + s1) + (s2 + s3);
 }
 
+// The same where scores are far from zero, or the tile's value scales from one another:
+// scores are rounded before N is taken off, and weights are powers of their own.
+template <bool F8, Terms TERMS, typename INFO>
+__device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, int page_log2,
+                                          uint32_t vis0, uint32_t vis1, float factor, float N,
+                                          float Dd, bool second)
+{
+    // (all of them first: second terms take the place of scores)
+    float x[4][16], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t r[16];
+        tmem_ld16(tS + 16 * k, r);
+        tmem_ld_wait();
+        tmem_reg_fence16(r);
+        hide16(r, (k < 2 ? vis0 : vis1) >> (16 * (k & 1)));
+        const float fk = F8 ? factor * ti.scale[(k0 + 16 * k) >> page_log2].x : factor;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            // (a packed product and sum would be joined to one operation)
+            x[k][j] = __fadd_rn(__fmul_rn(__uint_as_float(r[j]), fk), -N);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float lu = F8 ? ti.scale[(k0 + 16 * k) >> page_log2].y - Dd : 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            sum += ex2(x[k][j]);
+            x[k][j] = ex2(x[k][j] + lu);
+        }
+        store_weights<F8, TERMS>(tS, k, x[k], second);
+    }
+    return sum;
+}
+
 template <int D, bool F8, Terms TERMS>
 __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, uint32_t smem,
-                                        uint32_t tmem, const WaitCtx& wctx)
+                                        const WaitCtx& wctx)
 {
     using C = Cfg<D, F8>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -928,7 +1016,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
     const bool second = TERMS == kLanes && (warp & 2);
     const int row = TERMS == kLanes ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + w * 64, tO = tmem + lanes + 256;
+    const uint32_t tS = lanes + w * 64, tO = lanes + 256;  // (all of TMEM is the block's)
     const int32_t R = p.G * p.T;
     uint32_t gt = 0, met = 0;
     int4 info = make_int4(0, 0, 0, 0);
@@ -941,7 +1029,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             valid ? p.mask + ((int64_t)run.b * p.T + tq) * p.words : nullptr;
         float factor = p.scale_log2;
         if (F8) {
-            const bool ok = mbar_wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 31);
+            const bool ok = wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 31);
             if (!__all_sync(0xffffffffu, ok))
                 return;
             factor = sh.qf[seg & 1][rit];
@@ -952,7 +1040,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         float N = kNone, Dd = 0.f, l = 0.f;
         for (int32_t i = 0; i < run.nt; ++i, ++gt) {
             const int32_t base = (run.tile0 + i) * kTile + w * 64;  // the group's 64 keys
-            bool ok = mbar_wait(&sh.info_full[gt % kRing], (gt / kRing) & 1, wctx, 32);
+            bool ok = wait(&sh.info_full[gt % kRing], (gt / kRing) & 1, wctx, 32);
             if (!__all_sync(0xffffffffu, ok))
                 return;
             const TileInfo<F8>& ti = sh.info[gt % kRing];
@@ -964,32 +1052,36 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 for (int k = 0; k < 4; ++k)
                     missing |= (flags >> ((w * 64 + 16 * k) >> p.c.page_log2) & 1u) << k;
             const bool masked = base + 64 > run.len - run.n || missing;
-            uint32_t vis[2];
-            if (masked)
-                visible(p, run, base, mask, missing, vis);
+            uint32_t vis[2] = {~0u, ~0u};
+            if (masked) {
+                const uint2 v = visible(p, run, base, mask, missing);
+                vis[0] = v.x, vis[1] = v.y;
+            }
             const uint32_t buf = (gt & 1) * 128;
-            ok = mbar_wait(&sh.s_full[gt & 1], (gt >> 1) & 1, wctx, 33);
+            ok = wait(&sh.s_full[gt & 1], (gt >> 1) & 1, wctx, 33);
             if (!__all_sync(0xffffffffu, ok))
                 return;
             tc_fence_after();
-            uint32_t r[64];
-            tmem_ld32(tS + buf, r);
-            tmem_ld32(tS + buf + 32, r + 32);
-            tmem_ld_wait();
-            tmem_reg_fence32(r);
-            tmem_reg_fence32(r + 32);
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    r[j] = vis[j / 32] >> (j % 32) & 1 ? r[j] : 0xff800000u;  // -inf
-            }
             float top[4];  // of 16 keys each
+            uint32_t r[4][16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tmem_ld16(tS + buf + 16 * k, r[k]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tmem_reg_fence16(r[k]);
+            if (__builtin_expect(masked, 0)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    hide16(r[k], vis[k >> 1] >> (16 * (k & 1)));
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float m = fmaxf(__uint_as_float(r[16 * k]), __uint_as_float(r[16 * k + 1]));
+                float m = fmaxf(__uint_as_float(r[k][0]), __uint_as_float(r[k][1]));
 #pragma unroll
-                for (int j = 16 * k + 2; j < 16 * k + 16; j += 2)
-                    m = fmax3(m, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                for (int j = 2; j < 16; j += 2)
+                    m = fmax3(m, __uint_as_float(r[k][j]), __uint_as_float(r[k][j + 1]));
                 // (rounded: N may become one of them, and is taken off them)
                 top[k] = __fmul_rn(
                     m, F8 ? factor * ti.scale[(w * 64 + 16 * k) >> p.c.page_log2].x : factor);
@@ -1016,17 +1108,17 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                     Dd = me - kHead;
                 }
             }
-            const bool far = valid && fabsf(N) >= kFar && N != kNone;
-            if (__any_sync(0xffffffffu, far) || (F8 && (flags & kWideTile)))
-                l += weights<F8, TERMS, true>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
-                                              second);
+            const bool far = __any_sync(0xffffffffu, valid && fabsf(N) >= kFar && N != kNone) ||
+                             (F8 && (flags & kWideTile));
+            if (__builtin_expect(far, 0))
+                l += weights_far<F8, TERMS>(tS + buf, ti, w * 64, p.c.page_log2, vis[0], vis[1],
+                                            factor, N, Dd, second);
             else
-                l += weights<F8, TERMS, false>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
-                                               second);
+                l += weights<F8, TERMS>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
+                                        second);
             if (i > 0 && __any_sync(0xffffffffu, rise)) {
-                // (late, since it has to wait for the product before this one; the one before
-                // that was done when these scores were)
-                ok = mbar_wait(&sh.pv_done, (gt - 1) & 1, wctx, 37);
+                // (late, since it has to wait for the product before this one)
+                ok = wait(&sh.s_free[(gt - 1) & 1], ((gt - 1) >> 1) & 1, wctx, 37);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 tc_fence_after();
@@ -1045,7 +1137,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             tmem_st_wait();
             if (masked) {  // V's rows that not everyone sees
                 const uint32_t vs = gt % C::kV;
-                ok = mbar_wait(&sh.v_full[vs], (gt / C::kV) & 1, wctx, 34);
+                ok = wait(&sh.v_full[vs], (gt / C::kV) & 1, wctx, 34);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 if (rit < 64)
@@ -1055,11 +1147,9 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             tc_fence_before();
             mbar_arrive(&sh.p_full[w][gt & 1]);
         }
-        // ---- the segment's rows.  (The product before the last one first: a barrier tells
-        // a phase from the next only.  When these are done, nobody reads the groups' sums
-        // of the segment before any more.)
-        bool ok = mbar_wait(&sh.pv_done, (gt - 2) & 1, wctx, 38) &&
-                  mbar_wait(&sh.pv_done, (gt - 1) & 1, wctx, 35);
+        // ---- the segment's rows.  (When its last product is done, nobody reads the groups'
+        // sums of the segment before any more.)
+        bool ok = wait(&sh.s_free[(gt - 1) & 1], ((gt - 1) >> 1) & 1, wctx, 35);
         if (!__all_sync(0xffffffffu, ok))
             return;
         sh.n[w][rit] = N;
@@ -1069,7 +1159,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.meet);
-        ok = mbar_wait(&sh.meet, met, wctx, 36);
+        ok = wait(&sh.meet, met, wctx, 36);
         met ^= 1;
         if (!__all_sync(0xffffffffu, ok))
             return;
@@ -1124,7 +1214,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 if (lane == 0)
                     mbar_arrive(&sh.seconds);
             } else {
-                ok = mbar_wait(&sh.seconds, met ^ 1, wctx, 39);
+                ok = wait(&sh.seconds, met ^ 1, wctx, 39);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
             }
@@ -1235,12 +1325,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.s_free[s], 1);
             mbar_init(&sh.p_full[0][s], 128);
             mbar_init(&sh.p_full[1][s], 128);
-            mbar_init(&sh.q_full[s], 2);
+            mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.q_empty[s], F8 || TERMS == kLanes ? 9 : 1);
         }
-        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.o_empty, 256);
         for (int s = 0; s < kRuns; ++s) {
             mbar_init(&sh.run_full[s], 1);
@@ -1267,12 +1357,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
     const WaitCtx wctx{&sh.abort, p.c.status, p.timeout_ns};
-    if (warp < 8) {
-        softmax<D, F8, TERMS>(p, sh, base, tmem, wctx);
+    if (sh.tmem != 0) {  // (all 512 columns: they begin at 0)
+        if (threadIdx.x == 0)
+            cache_fault(p.c.status, kSiteShared, blockIdx.x);
+    } else if (warp < 8) {
+        softmax<D, F8, TERMS>(p, sh, base, wctx);
     } else if (warp == 8) {
-        multiply<D, F8, TERMS>(sh, base, tmem, wctx);
+        multiply_scores<D, F8>(sh, base, wctx);
+    } else if (warp == 10) {
+        multiply_values<D, F8, TERMS>(sh, base, wctx);
     } else if (warp == 9) {
         produce<D, F8>(p, sh, base, tk, tv, wctx);
         if (*wctx.abort_flag) {
@@ -1291,7 +1385,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(sh.tmem, 512);
     }
 }
 
