@@ -26,8 +26,8 @@
 //   warps 0-3    softmax of the tile's first 64 keys, warps 4-7 of the others, a thread a
 //                row, each with an N, D, sum and O of its own, joined at the segment's end.
 //                O is rescaled in TMEM when D (or N) has to rise.
-// S has two buffers, and the scores of tile i + 2 are issued behind the products of tile i:
-// the next tile's are there when a tile's softmax ends.
+// S has two buffers (three for d = 64): the next tile's scores are there when a tile's
+// softmax ends.
 //
 // Work: (sequence, head, row group) segments form one line, cut by cost over a grid of
 // one block an SM: a block's range covers whole segments, whose result it writes, and up
@@ -53,14 +53,14 @@ namespace tree {
 constexpr int kTile = kTreeTile;
 constexpr int kRing = 8;                  // tiles whose scales are kept
 constexpr int kRuns = 2;                  // segments that are announced ahead
-// N rises when a term exceeds 2^kGrow.  (bf16 weights have fp32's range: no sum comes near
-// its end, and a rise costs a pass over O.)
-template <bool F8>
-constexpr float kGrow = F8 ? 8.f : 60.f;
-// D is set kHead below the largest exponent, and set anew when a weight exceeds 2^kTop
-// (fp16 weights use that type's range to its end, so that those far below the largest
-// keep their bits).
-constexpr float kTop = 15.f, kHead = 11.f;
+// N rises when a term exceeds 2^kGrow: no sum comes near fp32's end, and for bf16 weights,
+// which have that range, a rise costs a pass over O.
+constexpr float kGrow = 60.f;
+// fp16 weights: D is set kHead below the largest exponent, and set anew, with a pass over
+// O, when a weight exceeds 2^kTop.  Between the two is room for larger weights to come;
+// kHead is what small ones behind a large one have left: half a step of fp16's subnormals
+// is 2^-33 of the largest weight, 2^-16 for 128K of them together.
+constexpr float kTop = 15.f, kHead = 8.f;
 constexpr float kNone = -FLT_MAX;         // running maximum before the first key
 constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
                                           // taken off them (else both in one operation: N,
@@ -92,6 +92,9 @@ struct Cfg {
     static constexpr int kThreads = F8 ? 512 : 384;
     static constexpr int kTileBytes = kTile * D * 2;      // a K, V or Q tile of 16-bit elements
     static constexpr int kRawBytes = kTile * D;
+    // buffers of S: as many as TMEM has room for beside two O
+    static constexpr int kS = D == 128 ? 2 : 3;
+    static constexpr int kO0 = kS * 128;                  // column of O
     // slots of K and V tiles: K's are free when its scores are there, V's two tiles later
     static constexpr int kK = F8 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
     static constexpr int kV = F8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 5);
@@ -114,7 +117,7 @@ struct Shared {
     using C = Cfg<D, F8>;
     uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
     uint64_t raw_full[F8 ? C::kRaw : 1], raw_empty[F8 ? C::kRaw : 1];
-    uint64_t s_full[2], s_free[2], p_full[2][2], o_empty, q_full[2], q_empty[2];
+    uint64_t s_full[C::kS], s_free[C::kS], p_full[2][C::kS], o_empty, q_full[2], q_empty[2];
     uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, seconds;
     Piece run[kRuns];
     TileInfo<F8> info[kRing];
@@ -513,7 +516,8 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
 // ---------------------------------------------------------------------------
 // queries of the segments
 // ---------------------------------------------------------------------------
-// (Rows without a query stay as they are: nobody looks at what comes of them.)
+// All of a segment's on their way at once, then, for 8-bit cells, each lane turns what it
+// copied.  (Rows without a query stay as they are: nobody looks at what comes of them.)
 template <int D, bool F8, Terms TERMS>
 __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>& sh, uint32_t qs,
                                              const WaitCtx& wctx)
@@ -521,65 +525,75 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>&
     using C = Cfg<D, F8>;
     constexpr int kPerRow = D / 8;                 // lanes of a row, 8 elements each
     constexpr int kRowsAt = 32 / kPerRow;          // rows of the warp at a time
-    constexpr int kBatch = 8;
-    const int t = threadIdx.x & 31, c = t % kPerRow;
+    const int lane = threadIdx.x & 31, c = lane % kPerRow;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 53); ++seg) {
         const bool ok = wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
         if (!__all_sync(0xffffffffu, ok))
             return;
-        const uint32_t to = qs + (seg & 1) * C::kTileBytes;
+        const uint32_t to = qs + (seg & 1) * C::kTileBytes + (c >> 3) * (kTreeRows * 128);
         const int32_t rows = min(kTreeRows, p.G * p.T - run.rg * kTreeRows);
-        for (int32_t r0 = 0; r0 < rows; r0 += kBatch * kRowsAt) {
-            uint4 x[kBatch];
-            bool there[kBatch];
+        const __nv_bfloat16* q =
+            (const __nv_bfloat16*)p.q.p + run.b * p.q.sb + (int64_t)run.h * p.G * p.q.sh + c * 8;
+        for (int32_t row = lane / kPerRow; row < rows; row += kRowsAt) {
+            int32_t gh, tq;
+            split_row(p, run.rg * kTreeRows + row, gh, tq);
+            if (tq >= run.n)
+                continue;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int32_t row = r0 + t / kPerRow + k * kRowsAt;
-                int32_t gh, tq;
-                split_row(p, run.rg * kTreeRows + row, gh, tq);
-                there[k] = row < rows && tq < run.n;
-                x[k] = make_uint4(0, 0, 0, 0);
-                if (there[k])
-                    x[k] = *reinterpret_cast<const uint4*>(
-                        (const __nv_bfloat16*)p.q.p + run.b * p.q.sb +
-                        (int64_t)(run.h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl + c * 8);
-            }
+            for (int i = 0; i < (TERMS == kLanes && !F8 ? 2 : 1); ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 to + sw128_offset(row + 64 * i, c & 7)),
+                             "l"(q + gh * p.q.sh + tq * p.q.sl)
+                             : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (F8) {
+            constexpr int kBatch = 8;  // rows a lane at a time
+            for (int32_t r0 = lane / kPerRow; r0 < kTreeRows; r0 += kBatch * kRowsAt) {
+                if (r0 - lane / kPerRow >= rows)
+                    break;
+                uint4 x[kBatch];
+                float amax[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int32_t row = r0 + t / kPerRow + k * kRowsAt;
-                uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                if (F8) {
-                    float amax = 0.f;
+                for (int k = 0; k < kBatch; ++k) {
+                    x[k] = lds128(to + sw128_offset(r0 + k * kRowsAt, c & 7));
+                    amax[k] = fmaxf(fmaxf(fmaxf(fabsf(bf16lo(x[k].x)), fabsf(bf16hi(x[k].x))),
+                                          fmaxf(fabsf(bf16lo(x[k].y)), fabsf(bf16hi(x[k].y)))),
+                                    fmaxf(fmaxf(fabsf(bf16lo(x[k].z)), fabsf(bf16hi(x[k].z))),
+                                          fmaxf(fabsf(bf16lo(x[k].w)), fabsf(bf16hi(x[k].w)))));
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+                for (int o = 1; o < kPerRow; o <<= 1)
 #pragma unroll
-                    for (int o = 1; o < kPerRow; o <<= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    for (int k = 0; k < kBatch; ++k)
+                        amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int32_t row = r0 + k * kRowsAt;
                     // the largest element to [2^14, 2^15): those down to 2^-31 of it stay exact
-                    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126) - 14;
+                    const int e =
+                        min(max((int)(__float_as_uint(amax[k]) >> 23) - 127, -100), 126) - 14;
                     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         w[i] = pack_half2(bf16lo(w[i]) * inv, bf16hi(w[i]) * inv);
-                    if (there[k] && c == 0)
+                    if (row < rows)
 #pragma unroll
-                        for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i)
-                            sh.qf[seg & 1][row + 64 * i] =
-                                p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                        for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i) {
+                            st_shared_v4(to + sw128_offset(row + 64 * i, c & 7), w[0], w[1], w[2],
+                                         w[3]);
+                            if (c == 0)
+                                sh.qf[seg & 1][row + 64 * i] =
+                                    p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                        }
                 }
-                if (there[k])
-#pragma unroll
-                    for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i)
-                        st_shared_v4(to + (c >> 3) * (kTreeRows * 128) +
-                                         sw128_offset(row + 64 * i, c & 7),
-                                     w[0], w[1], w[2], w[3]);
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (t == 0)
+        if (lane == 0)
             mbar_arrive(&sh.q_full[seg & 1]);
     }
 }
@@ -699,7 +713,7 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, const W
     return __all_sync(0xffffffffu, wait(bar, parity, w, where));
 }
 
-// S = Q K^T, up to two tiles ahead of the products
+// S = Q K^T, as many tiles ahead of the products as there are buffers
 template <int D, bool F8>
 __device__ __forceinline__ void multiply_scores(Shared<D, F8>& sh, uint32_t smem,
                                                 const WaitCtx& wctx)
@@ -708,26 +722,26 @@ __device__ __forceinline__ void multiply_scores(Shared<D, F8>& sh, uint32_t smem
     const uint64_t dQ = sdesc_sw128(smem, 16, 1024);
     const uint64_t dK = sdesc_sw128(smem + C::kK0, 16, 1024);
     Ring<C::kK> kr;
-    uint32_t gt = 0;
+    Ring<C::kS> sr;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 20); ++seg) {
         const uint64_t q = sdesc_add(dQ, (seg & 1) * C::kTileBytes);
         if (!wait_all(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21))
             return;
         const int32_t nt = __shfl_sync(0xffffffffu, run.nt, 0);
-        for (int32_t i = 0; i < nt; ++i, ++gt, kr.next()) {
-            if (!wait_all(&sh.s_free[gt & 1], ((gt >> 1) & 1) ^ 1, wctx, 27) ||
+        for (int32_t i = 0; i < nt; ++i, sr.next(), kr.next()) {
+            if (!wait_all(&sh.s_free[sr.at], sr.phase ^ 1, wctx, 27) ||
                 !wait_all(&sh.k_full[kr.at], kr.phase, wctx, 22))
                 return;
             tc_fence_after();
             const uint64_t k = sdesc_add(dK, kr.at * C::kTileBytes);
-            const uint32_t to = (gt & 1) * 128;
+            const uint32_t to = sr.at * 128;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                 mma_ss_one(to, sdesc_add(q, off), sdesc_add(k, off), idesc<F8>(128, false), kk > 0);
             }
-            commit_one(&sh.s_full[gt & 1]);
+            commit_one(&sh.s_full[sr.at]);
             commit_one(&sh.k_empty[kr.at]);
             if (i + 1 == nt)
                 commit_one(&sh.q_empty[seg & 1]);
@@ -743,30 +757,30 @@ __device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem
     using C = Cfg<D, F8>;
     const uint64_t dV = sdesc_sw128(smem + C::kV0, 16384, 1024);
     Ring<C::kV> vr;
-    uint32_t gt = 0;
+    Ring<C::kS> sr;
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 28); ++seg) {
         if (!wait_all(&sh.o_empty, (seg & 1) ^ 1, wctx, 23))
             return;
         const int32_t nt = __shfl_sync(0xffffffffu, run.nt, 0);
-        for (int32_t i = 0; i < nt; ++i, ++gt, vr.next()) {
+        for (int32_t i = 0; i < nt; ++i, sr.next(), vr.next()) {
             if (!wait_all(&sh.v_full[vr.at], vr.phase, wctx, 24))
                 return;
             const uint64_t v = sdesc_add(dV, vr.at * C::kTileBytes);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                if (!wait_all(&sh.p_full[w][gt & 1], (gt >> 1) & 1, wctx, 25 + w))
+                if (!wait_all(&sh.p_full[w][sr.at], sr.phase, wctx, 25 + w))
                     return;
                 tc_fence_after();
-                const uint32_t from = (gt & 1) * 128 + w * 64;
+                const uint32_t from = sr.at * 128 + w * 64;
 #pragma unroll
                 for (int kk = 0; kk < (TERMS == kColumns ? 8 : 4); ++kk)
-                    mma_ts_one(256 + w * D,
+                    mma_ts_one(C::kO0 + w * D,
                                from + (TERMS == kColumns ? (kk & 3) * 16 + (kk >> 2) * 8 : kk * 8),
                                sdesc_add(v, (w * 4 + (kk & 3)) * 2048), idesc<F8>(D, true),
                                (i > 0 || kk > 0) ? 1u : 0u);
             }
-            commit_one(&sh.s_free[gt & 1]);
+            commit_one(&sh.s_free[sr.at]);
             commit_one(&sh.v_empty[vr.at]);
         }
     }
@@ -1016,9 +1030,10 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
     const bool second = TERMS == kLanes && (warp & 2);
     const int row = TERMS == kLanes ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = lanes + w * 64, tO = lanes + 256;  // (all of TMEM is the block's)
+    const uint32_t tS = lanes + w * 64, tO = lanes + C::kO0;  // (all of TMEM is the block's)
     const int32_t R = p.G * p.T;
     uint32_t gt = 0, met = 0;
+    Ring<C::kS> sr, last;  // the tile's S, and the one before's
     int4 info = make_int4(0, 0, 0, 0);
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 30); ++seg) {
@@ -1057,8 +1072,8 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 const uint2 v = visible(p, run, base, mask, missing);
                 vis[0] = v.x, vis[1] = v.y;
             }
-            const uint32_t buf = (gt & 1) * 128;
-            ok = wait(&sh.s_full[gt & 1], (gt >> 1) & 1, wctx, 33);
+            const uint32_t buf = sr.at * 128;
+            ok = wait(&sh.s_full[sr.at], sr.phase, wctx, 33);
             if (!__all_sync(0xffffffffu, ok))
                 return;
             tc_fence_after();
@@ -1089,7 +1104,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
             // N up to the largest score, D up to the largest exponent, O with them
             float f = 1.f;
-            bool rise = valid && mx - N > kGrow<F8>;
+            bool rise = valid && mx - N > kGrow;
             if (rise) {
                 f = ex2(N - mx);
                 l *= f;
@@ -1118,20 +1133,24 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                                         second);
             if (i > 0 && __any_sync(0xffffffffu, rise)) {
                 // (late, since it has to wait for the product before this one)
-                ok = wait(&sh.s_free[(gt - 1) & 1], ((gt - 1) >> 1) & 1, wctx, 37);
+                ok = wait(&sh.s_free[last.at], last.phase, wctx, 37);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + w * D + c0, o);
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t o[2][32];
+                    tmem_ld32(tO + w * D + c0, o[0]);
+                    tmem_ld32(tO + w * D + c0 + 32, o[1]);
                     tmem_ld_wait();
-                    tmem_reg_fence16(o);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st16(tO + w * D + c0, o);
+                    for (int a = 0; a < 2; ++a) {
+                        tmem_reg_fence32(o[a]);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[a][k] = __float_as_uint(__uint_as_float(o[a][k]) * f);
+                        tmem_st32(tO + w * D + c0 + 32 * a, o[a]);
+                    }
                 }
             }
             tmem_st_wait();
@@ -1145,11 +1164,13 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                                        w * 64 + rit, missing >> (rit >> 4) & 1, seg);
             }
             tc_fence_before();
-            mbar_arrive(&sh.p_full[w][gt & 1]);
+            mbar_arrive(&sh.p_full[w][sr.at]);
+            last = sr;
+            sr.next();
         }
         // ---- the segment's rows.  (When its last product is done, nobody reads the groups'
         // sums of the segment before any more.)
-        bool ok = wait(&sh.s_free[(gt - 1) & 1], ((gt - 1) >> 1) & 1, wctx, 35);
+        bool ok = wait(&sh.s_free[last.at], last.phase, wctx, 35);
         if (!__all_sync(0xffffffffu, ok))
             return;
         sh.n[w][rit] = N;
@@ -1323,11 +1344,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_init(&sh.raw_full[s], 1);
             mbar_init(&sh.raw_empty[s], 4);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < C::kS; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.s_free[s], 1);
             mbar_init(&sh.p_full[0][s], 128);
             mbar_init(&sh.p_full[1][s], 128);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.q_empty[s], F8 || TERMS == kLanes ? 9 : 1);
         }
