@@ -103,6 +103,10 @@ struct Cfg {
     static constexpr int kV0 = kK0 + kK * kTileBytes;
     static constexpr int kRaw0 = kV0 + kV * kTileBytes;
     static constexpr int kShared0 = kRaw0 + kRaw * kRawBytes;
+    // What a segment costs a block beside its tiles, in tiles.  Measured (1, 2, 4, 6): bf16,
+    // 64 ragged sequences of 16 nodes 190.6, 188.5, 194.4, 200.5 us; 8 bits, 8 sequences
+    // of 60 nodes 126.7, 119.5, 116.5, 112.3, 4 of 128 86.5, 86.0, 83.8, 82.1.
+    static constexpr int kSegmentCost = F8 ? 5 : 2;
     static constexpr int kReaders = 8 + 1 + 2 + (F8 ? 4 : 0);  // warps that read a run
 };
 
@@ -117,7 +121,7 @@ struct Shared {
     using C = Cfg<D, F8>;
     uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
     uint64_t raw_full[F8 ? C::kRaw : 1], raw_empty[F8 ? C::kRaw : 1];
-    uint64_t s_full[C::kS], s_free[C::kS], p_full[2][C::kS], o_empty, q_full[2], q_empty[2];
+    uint64_t s_full[C::kS], s_free[C::kS], p_full[2][C::kS], o_empty, q_full[2], q_empty[2], q_first;
     uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, seconds;
     Piece run[kRuns];
     TileInfo<F8> info[kRing];
@@ -215,6 +219,15 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len, int32_t n)
     return n > 0 ? max(1, ceil_div(len, kTile)) : 0;
 }
 
+// Out of line, as what follows that is not in an inner loop: the code that a block goes
+// through once or once a segment comes from far away, 128 bytes at a time.
+__device__ __forceinline__ int2 rows_of(const TreeParams& p, int32_t b)
+{
+    int32_t len, n;
+    seq_rows(p.c, p.q_lens, p.T, b, len, n);
+    return make_int2(len, n);
+}
+
 // a / b for a >= 0, b > 0, the short way where a has 32 bits
 __device__ __forceinline__ long long divide(long long a, int32_t b)
 {
@@ -241,7 +254,8 @@ struct Walk : Piece {
         fresh = true;
         if (w >= w1)
             return;
-        seq_rows(p.c, p.q_lens, p.T, b, len, n);
+        const int2 r = rows_of(p, b);
+        len = r.x, n = r.y;
         tiles = tiles_of(len, n);
         const long long at = w - sh.base, unit = tiles + p.segment_cost;
         h = (int32_t)min(divide(at, (int32_t)unit), (long long)p.c.Hkv - 1);
@@ -263,7 +277,8 @@ struct Walk : Piece {
                 do {
                     if (++b >= p.c.B)
                         return false;
-                    seq_rows(p.c, p.q_lens, p.T, b, len, n);
+                    const int2 r = rows_of(p, b);
+                    len = r.x, n = r.y;
                     tiles = tiles_of(len, n);
                 } while (tiles == 0);
             }
@@ -291,9 +306,8 @@ __device__ __forceinline__ void find_range(const TreeParams& p, SH& sh)
     const int32_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, p.c.B);
     long long sum = 0;
     for (int32_t b = b0; b < b1; ++b) {
-        int32_t len, n;
-        seq_rows(p.c, p.q_lens, p.T, b, len, n);
-        const int32_t tiles = tiles_of(len, n);
+        const int2 r = rows_of(p, b);
+        const int32_t tiles = tiles_of(r.x, r.y);
         sum += tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
     }
     long long incl = sum;
@@ -327,9 +341,8 @@ __device__ __forceinline__ void find_range(const TreeParams& p, SH& sh)
     if (w0 < w1 && incl - sum <= w0 && w0 < incl) {
         long long base = incl - sum;
         for (int32_t b = b0; b < b1; ++b) {
-            int32_t len, n;
-            seq_rows(p.c, p.q_lens, p.T, b, len, n);
-            const int32_t tiles = tiles_of(len, n);
+            const int2 r = rows_of(p, b);
+            const int32_t tiles = tiles_of(r.x, r.y);
             const long long t = tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
             if (w0 < base + t) {
                 sh.b = b;
@@ -516,84 +529,91 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
 // ---------------------------------------------------------------------------
 // queries of the segments
 // ---------------------------------------------------------------------------
-// All of a segment's on their way at once, then, for 8-bit cells, each lane turns what it
-// copied.  (Rows without a query stay as they are: nobody looks at what comes of them.)
-template <int D, bool F8, Terms TERMS>
-__device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>& sh, uint32_t qs,
-                                             const WaitCtx& wctx)
+// Queries of a segment into its buffer, by WARPS warps: all on their way at once, then,
+// for 8-bit cells, each lane turns what it copied.  (Rows without a query stay as they
+// are: nobody looks at what comes of them.)
+template <int D, bool F8, Terms TERMS, int WARPS>
+__device__ __forceinline__ void copy_queries(const TreeParams& p, Shared<D, F8>& sh, uint32_t qs,
+                                             const Piece& run, uint32_t seg, int warp)
 {
     using C = Cfg<D, F8>;
     constexpr int kPerRow = D / 8;                 // lanes of a row, 8 elements each
-    constexpr int kRowsAt = 32 / kPerRow;          // rows of the warp at a time
+    constexpr int kRowsAt = 32 / kPerRow * WARPS;  // rows at a time
     const int lane = threadIdx.x & 31, c = lane % kPerRow;
-    Piece run;
-    for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 53); ++seg) {
-        const bool ok = wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
-        if (!__all_sync(0xffffffffu, ok))
-            return;
-        const uint32_t to = qs + (seg & 1) * C::kTileBytes + (c >> 3) * (kTreeRows * 128);
-        const int32_t rows = min(kTreeRows, p.G * p.T - run.rg * kTreeRows);
-        const __nv_bfloat16* q =
-            (const __nv_bfloat16*)p.q.p + run.b * p.q.sb + (int64_t)run.h * p.G * p.q.sh + c * 8;
-        for (int32_t row = lane / kPerRow; row < rows; row += kRowsAt) {
-            int32_t gh, tq;
-            split_row(p, run.rg * kTreeRows + row, gh, tq);
-            if (tq >= run.n)
-                continue;
+    const int32_t first = warp * (32 / kPerRow) + lane / kPerRow;
+    const uint32_t to = qs + (seg & 1) * C::kTileBytes + (c >> 3) * (kTreeRows * 128);
+    const int32_t rows = min(kTreeRows, p.G * p.T - run.rg * kTreeRows);
+    const __nv_bfloat16* q =
+        (const __nv_bfloat16*)p.q.p + run.b * p.q.sb + (int64_t)run.h * p.G * p.q.sh + c * 8;
+#pragma unroll 4
+    for (int32_t row = first; row < rows; row += kRowsAt) {
+        int32_t gh, tq;
+        split_row(p, run.rg * kTreeRows + row, gh, tq);
+        if (tq < run.n)
 #pragma unroll
             for (int i = 0; i < (TERMS == kLanes && !F8 ? 2 : 1); ++i)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                  to + sw128_offset(row + 64 * i, c & 7)),
                              "l"(q + gh * p.q.sh + tq * p.q.sl)
                              : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (F8) {
-            constexpr int kBatch = 8;  // rows a lane at a time
-            for (int32_t r0 = lane / kPerRow; r0 < kTreeRows; r0 += kBatch * kRowsAt) {
-                if (r0 - lane / kPerRow >= rows)
-                    break;
-                uint4 x[kBatch];
-                float amax[kBatch];
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (F8) {
+        constexpr int kBatch = 8 / (WARPS == 1 ? 1 : D == 128 ? 1 : 2);  // rows a lane at a time
+        for (int32_t r0 = first; r0 - first < rows; r0 += kBatch * kRowsAt) {
+            uint4 x[kBatch];
+            float amax[kBatch];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    x[k] = lds128(to + sw128_offset(r0 + k * kRowsAt, c & 7));
-                    amax[k] = fmaxf(fmaxf(fmaxf(fabsf(bf16lo(x[k].x)), fabsf(bf16hi(x[k].x))),
-                                          fmaxf(fabsf(bf16lo(x[k].y)), fabsf(bf16hi(x[k].y)))),
-                                    fmaxf(fmaxf(fabsf(bf16lo(x[k].z)), fabsf(bf16hi(x[k].z))),
-                                          fmaxf(fabsf(bf16lo(x[k].w)), fabsf(bf16hi(x[k].w)))));
-                }
+            for (int k = 0; k < kBatch; ++k) {
+                x[k] = lds128(to + sw128_offset(r0 + k * kRowsAt, c & 7));
+                amax[k] = fmaxf(fmaxf(fmaxf(fabsf(bf16lo(x[k].x)), fabsf(bf16hi(x[k].x))),
+                                      fmaxf(fabsf(bf16lo(x[k].y)), fabsf(bf16hi(x[k].y)))),
+                                fmaxf(fmaxf(fabsf(bf16lo(x[k].z)), fabsf(bf16hi(x[k].z))),
+                                      fmaxf(fabsf(bf16lo(x[k].w)), fabsf(bf16hi(x[k].w)))));
+            }
 #pragma unroll
-                for (int o = 1; o < kPerRow; o <<= 1)
+            for (int o = 1; o < kPerRow; o <<= 1)
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+                for (int k = 0; k < kBatch; ++k)
+                    amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int32_t row = r0 + k * kRowsAt;
-                    // the largest element to [2^14, 2^15): those down to 2^-31 of it stay exact
-                    const int e =
-                        min(max((int)(__float_as_uint(amax[k]) >> 23) - 127, -100), 126) - 14;
-                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            for (int k = 0; k < kBatch; ++k) {
+                const int32_t row = r0 + k * kRowsAt;
+                // the largest element to [2^14, 2^15): those down to 2^-31 of it stay exact
+                const int e = min(max((int)(__float_as_uint(amax[k]) >> 23) - 127, -100), 126) - 14;
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = pack_half2(bf16lo(w[i]) * inv, bf16hi(w[i]) * inv);
-                    if (row < rows)
+                for (int i = 0; i < 4; ++i)
+                    w[i] = pack_half2(bf16lo(w[i]) * inv, bf16hi(w[i]) * inv);
+                if (row < rows)
 #pragma unroll
-                        for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i) {
-                            st_shared_v4(to + sw128_offset(row + 64 * i, c & 7), w[0], w[1], w[2],
-                                         w[3]);
-                            if (c == 0)
-                                sh.qf[seg & 1][row + 64 * i] =
-                                    p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-                        }
-                }
+                    for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i) {
+                        st_shared_v4(to + sw128_offset(row + 64 * i, c & 7), w[0], w[1], w[2], w[3]);
+                        if (c == 0)
+                            sh.qf[seg & 1][row + 64 * i] =
+                                p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+                    }
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// (The first segment's are copied by the softmax warps, who would wait for them.)
+template <int D, bool F8, Terms TERMS>
+__device__ __forceinline__ void load_queries(const TreeParams& p, Shared<D, F8>& sh, uint32_t qs,
+                                             const WaitCtx& wctx)
+{
+    Piece run;
+    for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 53); ++seg) {
+        const bool ok = wait(&sh.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, wctx, 54);
+        if (!__all_sync(0xffffffffu, ok))
+            return;
+        if (seg > 0)
+            copy_queries<D, F8, TERMS, 1>(p, sh, qs, run, seg, 0);
+        if ((threadIdx.x & 31) == 0)
             mbar_arrive(&sh.q_full[seg & 1]);
     }
 }
@@ -726,7 +746,8 @@ __device__ __forceinline__ void multiply_scores(Shared<D, F8>& sh, uint32_t smem
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 20); ++seg) {
         const uint64_t q = sdesc_add(dQ, (seg & 1) * C::kTileBytes);
-        if (!wait_all(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21))
+        if (!wait_all(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 21) ||
+            (seg == 0 && !wait_all(&sh.q_first, 0, wctx, 21)))
             return;
         const int32_t nt = __shfl_sync(0xffffffffu, run.nt, 0);
         for (int32_t i = 0; i < nt; ++i, sr.next(), kr.next()) {
@@ -791,25 +812,25 @@ __device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem
 // ---------------------------------------------------------------------------
 // Which of the 64 keys from key `base` on a node sees: of the rows before the tree all,
 // of the tree's those of its mask (NULL: none), of missing pages (from `base` on) none.
-__device__ __noinline__ uint2 visible(const TreeParams& p, const Piece& run, int32_t base,
-                                        const uint32_t* mask, uint32_t missing)
+__device__ __noinline__ uint2 visible(int32_t tree0, int32_t n, int32_t words, int32_t base,
+                                      const uint32_t* mask, uint32_t missing)
 {
     uint32_t vis[2];
-    const int32_t tree0 = run.len - run.n;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int32_t k0 = base + 32 * i, off = k0 - tree0;  // node of the word's first key
         uint32_t bits = off <= -32 ? ~0u : off < 0 ? (1u << -off) - 1 : 0u;
-        if (mask && off > -32 && off < run.n) {
+        if (mask && off > -32 && off < n) {
             uint32_t m;
             if (off < 0) {
                 m = mask[0] << -off;
             } else {
                 const int32_t w = off >> 5;
-                const uint32_t lo = mask[w], hi = w + 1 < p.words ? mask[w + 1] : 0u;
+                const uint32_t lo = mask[w];
+                const uint32_t hi = w + 1 < words ? mask[w + 1] : 0u;
                 m = __funnelshift_r(lo, hi, off & 31);
             }
-            const int32_t left = run.n - off;  // nodes from here on
+            const int32_t left = n - off;  // nodes from here on
             bits |= left >= 32 ? m : m & ((1u << left) - 1);
         }
         vis[i] = bits;
@@ -822,37 +843,40 @@ __device__ __noinline__ uint2 visible(const TreeParams& p, const Piece& run, int
 }
 
 // Adds the values of the nodes in `bad`, which the products left out, to features
-// [f0, f0 + 32) of a row's O (relative to 2^(N + D)).
+// [f0, f0 + 16) of a row's O (relative to 2^(N + D)).
 template <int D, bool F8>
-__device__ __noinline__ void add_apart(const TreeParams& p, const Piece& run, const uint32_t* bad,
-                                       const uint32_t* mask, int32_t gh, int32_t tq, float N,
-                                       float Dd, int f0, float* o)
+__device__ __noinline__ void add_apart(const TreeParams& p, int32_t b, int32_t h, int32_t len,
+                                       int32_t n, const uint32_t* bad, const uint32_t* mask,
+                                       int32_t gh, int32_t tq, float N, float Dd, int f0, float* o)
 {
-    const __nv_bfloat16* q = (const __nv_bfloat16*)p.q.p + run.b * p.q.sb +
-                             (int64_t)(run.h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl;
-    for (int32_t u = 0; u < run.n; ++u) {
+    const __nv_bfloat16* q = (const __nv_bfloat16*)p.q.p + b * p.q.sb +
+                             (int64_t)(h * p.G + gh) * p.q.sh + (int64_t)tq * p.q.sl;
+#pragma unroll 1
+    for (int32_t u = 0; u < n; ++u) {
         if (!(bad[u >> 5] & mask[u >> 5] & (1u << (u & 31))))
             continue;
-        const int32_t j = run.len - run.n + u;
-        const int32_t id = page_of(p.c, run.b, j >> p.c.page_log2);
+        const int32_t j = len - n + u;
+        const int32_t id = page_of(p.c, b, j >> p.c.page_log2);
         if (id < 0)
             continue;
         const int64_t at = (int64_t)id * p.c.page_stride +
-                           (((int64_t)run.h << p.c.page_log2) + (j & (p.c.page - 1))) * D;
+                           (((int64_t)h << p.c.page_log2) + (j & (p.c.page - 1))) * D;
         auto cell = [&](const void* cells, int f) {
             return F8 ? e4m3x2_float2(((const uint8_t*)cells)[at + f]).x
                       : __bfloat162float(((const __nv_bfloat16*)cells)[at + f]);
         };
         float dot = 0.f, lu = 0.f;
+#pragma unroll 1
         for (int f = 0; f < D; ++f)
             dot = fmaf(__bfloat162float(q[f]), cell(p.c.k, f), dot);
         float x = __fmul_rn(dot, p.scale_log2);
         if (F8) {
-            x = __fmul_rn(x, p.c.k_scale[(int64_t)id * p.c.Hkv + run.h]);
-            lu = log2f(p.c.v_scale[(int64_t)id * p.c.Hkv + run.h]);
+            x = __fmul_rn(x, p.c.k_scale[(int64_t)id * p.c.Hkv + h]);
+            lu = log2f(p.c.v_scale[(int64_t)id * p.c.Hkv + h]);
         }
         const float w = ex2((x - N) + (lu - Dd));
-        for (int f = 0; f < 32; ++f)
+#pragma unroll 1
+        for (int f = 0; f < 16; ++f)
             o[f] = fmaf(w, cell(p.c.v, f0 + f), o[f]);
     }
 }
@@ -873,18 +897,16 @@ __device__ __forceinline__ float row_lse(float nx, float L)
 
 // Zeros a row of a V tile if it is not the sequence's or its page is missing, and if it is
 // the tree's and has values that are not finite, which it notes.
-template <int D, bool F8, typename SH>
-__device__ __noinline__ void mend_values(SH& sh, const Piece& run, uint32_t vt, int32_t base,
-                                            int32_t row, bool missing, uint32_t seg)
+template <int D, bool F8>
+__device__ __noinline__ void mend_values(uint32_t vt, int32_t row, int32_t node, bool gone,
+                                         uint32_t* bad_nodes, uint32_t* any_bad)
 {
-    const int32_t j = base + row, node = j - (run.len - run.n);
-    const bool gone = j >= run.len || missing;
     if (!gone && node < 0)
         return;
     bool bad = false;
     if (!gone) {
         constexpr uint32_t kHi = F8 ? 0x7c000000u : 0x7f800000u, kLo = F8 ? 0x7c00u : 0x7f80u;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
             const uint4 x = lds128(vt + (c >> 3) * (kTile * 128) + sw128_offset(row, c & 7));
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -893,12 +915,12 @@ __device__ __noinline__ void mend_values(SH& sh, const Piece& run, uint32_t vt, 
                 bad |= (w[i] & kHi) == kHi || (w[i] & kLo) == kLo;
         }
         if (bad) {
-            atomicOr(&sh.bad[seg % 3][node >> 5], 1u << (node & 31));
-            sh.any_bad[seg % 3] = 1;
+            atomicOr(bad_nodes + (node >> 5), 1u << (node & 31));
+            *any_bad = 1;
         }
     }
     if (gone || bad) {
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c)
             st_shared_v4(vt + (c >> 3) * (kTile * 128) + sw128_offset(row, c & 7), 0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -992,30 +1014,37 @@ __device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, i
                                           uint32_t vis0, uint32_t vis1, float factor, float N,
                                           float Dd, bool second)
 {
-    // (all of them first: second terms take the place of scores)
-    float x[4][16], sum = 0.f;
-#pragma unroll
+    // (differences in place of all scores first: second terms take the place of some)
+    float sum = 0.f;
+    uint32_t r[16];
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
-        uint32_t r[16];
         tmem_ld16(tS + 16 * k, r);
         tmem_ld_wait();
         tmem_reg_fence16(r);
         hide16(r, (k < 2 ? vis0 : vis1) >> (16 * (k & 1)));
         const float fk = F8 ? factor * ti.scale[(k0 + 16 * k) >> page_log2].x : factor;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            // (a packed product and sum would be joined to one operation)
-            x[k][j] = __fadd_rn(__fmul_rn(__uint_as_float(r[j]), fk), -N);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float lu = F8 ? ti.scale[(k0 + 16 * k) >> page_log2].y - Dd : 0.f;
-#pragma unroll
         for (int j = 0; j < 16; ++j) {
-            sum += ex2(x[k][j]);
-            x[k][j] = ex2(x[k][j] + lu);
+            // (a packed product and sum would be joined to one operation)
+            const float x = __fadd_rn(__fmul_rn(__uint_as_float(r[j]), fk), -N);
+            sum += ex2(x);
+            r[j] = __float_as_uint(x);
         }
-        store_weights<F8, TERMS>(tS, k, x[k], second);
+        tmem_st16(tS + 16 * k, r);
+    }
+    tmem_st_wait();
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        tmem_ld16(tS + 16 * k, r);
+        tmem_ld_wait();
+        tmem_reg_fence16(r);
+        const float lu = F8 ? ti.scale[(k0 + 16 * k) >> page_log2].y - Dd : 0.f;
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            y[j] = ex2(__uint_as_float(r[j]) + lu);
+        store_weights<F8, TERMS>(tS, k, y, second);
     }
     return sum;
 }
@@ -1037,6 +1066,11 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
     int4 info = make_int4(0, 0, 0, 0);
     Piece run;
     for (uint32_t seg = 0; next_run(sh, seg, run, wctx, 30); ++seg) {
+        if (seg == 0) {
+            copy_queries<D, F8, TERMS, 8>(p, sh, smem, run, 0, warp);
+            if (lane == 0)
+                mbar_arrive(&sh.q_first);
+        }
         int32_t gh, tq;
         split_row(p, run.rg * kTreeRows + row, gh, tq);
         const bool valid = run.rg * kTreeRows + row < R && tq < run.n;
@@ -1044,7 +1078,8 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             valid ? p.mask + ((int64_t)run.b * p.T + tq) * p.words : nullptr;
         float factor = p.scale_log2;
         if (F8) {
-            const bool ok = wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 31);
+            const bool ok = wait(&sh.q_full[seg & 1], (seg >> 1) & 1, wctx, 31) &&
+                            (seg > 0 || wait(&sh.q_first, 0, wctx, 31));
             if (!__all_sync(0xffffffffu, ok))
                 return;
             factor = sh.qf[seg & 1][rit];
@@ -1069,7 +1104,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             const bool masked = base + 64 > run.len - run.n || missing;
             uint32_t vis[2] = {~0u, ~0u};
             if (masked) {
-                const uint2 v = visible(p, run, base, mask, missing);
+                const uint2 v = visible(run.len - run.n, run.n, p.words, base, mask, missing);
                 vis[0] = v.x, vis[1] = v.y;
             }
             const uint32_t buf = sr.at * 128;
@@ -1138,19 +1173,15 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                     return;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t o[2][32];
-                    tmem_ld32(tO + w * D + c0, o[0]);
-                    tmem_ld32(tO + w * D + c0 + 32, o[1]);
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + w * D + c0, o);
                     tmem_ld_wait();
+                    tmem_reg_fence32(o);
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        tmem_reg_fence32(o[a]);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[a][k] = __float_as_uint(__uint_as_float(o[a][k]) * f);
-                        tmem_st32(tO + w * D + c0 + 32 * a, o[a]);
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st32(tO + w * D + c0, o);
                 }
             }
             tmem_st_wait();
@@ -1159,9 +1190,13 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 ok = wait(&sh.v_full[vs], (gt / C::kV) & 1, wctx, 34);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
-                if (rit < 64)
-                    mend_values<D, F8>(sh, run, smem + C::kV0 + vs * C::kTileBytes, base - w * 64,
-                                       w * 64 + rit, missing >> (rit >> 4) & 1, seg);
+                if (rit < 64) {
+                    const int32_t j = base + rit;
+                    mend_values<D, F8>(smem + C::kV0 + vs * C::kTileBytes, w * 64 + rit,
+                                       j - (run.len - run.n),
+                                       j >= run.len || (missing >> (rit >> 4) & 1),
+                                       sh.bad[seg % 3], &sh.any_bad[seg % 3]);
+                }
             }
             tc_fence_before();
             mbar_arrive(&sh.p_full[w][sr.at]);
@@ -1205,89 +1240,83 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         const int64_t prow = slot * kTreeRows + row;
         const int64_t orow = ((int64_t)run.b * p.Hq + run.h * p.G + gh) * p.T + tq;
         const float2 inv = row_factors<D, F8>(dx, l);
-        // The groups take half of the features each.  kLanes: second terms come by way of
-        // the segment's queries, which are done with.
-        const uint32_t pass = smem + (seg & 1) * C::kTileBytes + w * (64 * D * 2) + row * 128;
-        auto combined = [&](int c0, float (&o)[32]) {
-            uint32_t ta[32], tb[32];
-            tmem_ld32(tO + c0, ta);
-            tmem_ld32(tO + D + c0, tb);
-            tmem_ld_wait();
-            tmem_reg_fence32(ta);
-            tmem_reg_fence32(tb);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                o[k] = fmaf(fa, __uint_as_float(ta[k]), fb * __uint_as_float(tb[k]));
+        // The groups take half of the features each, 16 at a time.  kLanes: second terms come
+        // by way of the segment's queries, which are done with.
+        const uint32_t pass = smem + (seg & 1) * C::kTileBytes + w * (64 * D * 2) + row * (D * 2);
+        auto chunk = [&](int c, int k) {  // 16 bytes k of 16 features c
+            return pass + (((4 * c + k) ^ (row & 7)) << 4);
         };
-        if (TERMS == kLanes) {
-            if (second) {
-#pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    float o[32];
-                    combined(w * (D / 2) + 32 * c, o);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        st_shared_v4(pass + c * (64 * 128) + ((k ^ (row & 7)) << 4),
-                                     __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
-                                     __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.seconds);
-            } else {
-                ok = wait(&sh.seconds, met ^ 1, wctx, 39);
-                if (!__all_sync(0xffffffffu, ok))
-                    return;
-            }
+        if (TERMS == kLanes && !second) {
+            ok = wait(&sh.seconds, met ^ 1, wctx, 39);
+            if (!__all_sync(0xffffffffu, ok))
+                return;
         }
 #pragma unroll 1
-        for (int c = 0; c < (second ? 0 : D / 64); ++c) {
-            const int c0 = w * (D / 2) + 32 * c;
-            float o[32];
-            combined(c0, o);
-            if (TERMS == kLanes)
+        for (int c = 0; c < D / 32; ++c) {
+            const int c0 = w * (D / 2) + 16 * c;
+            float o[16];
+            uint32_t ta[16], tb[16];
+            tmem_ld16(tO + c0, ta);
+            tmem_ld16(tO + D + c0, tb);
+            tmem_ld_wait();
+            tmem_reg_fence16(ta);
+            tmem_reg_fence16(tb);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 x = lds128(pass + c * (64 * 128) + ((k ^ (row & 7)) << 4));
+            for (int k = 0; k < 16; ++k)
+                o[k] = fmaf(fa, __uint_as_float(ta[k]), fb * __uint_as_float(tb[k]));
+            if (TERMS == kLanes) {
+                if (second) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        st_shared_v4(chunk(c, k), __float_as_uint(o[4 * k]),
+                                     __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                                     __float_as_uint(o[4 * k + 3]));
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 x = lds128(chunk(c, k));
                     o[4 * k] += __uint_as_float(x.x), o[4 * k + 1] += __uint_as_float(x.y);
                     o[4 * k + 2] += __uint_as_float(x.z), o[4 * k + 3] += __uint_as_float(x.w);
                 }
+            }
             if (!valid)
                 continue;
             if (__builtin_expect(sh.any_bad[seg % 3], 0)) {
-                float y[32];
+                float y[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int k = 0; k < 16; ++k)
                     y[k] = o[k];
-                add_apart<D, F8>(p, run, sh.bad[seg % 3], mask, gh, tq, nx, dx, c0, y);
+                add_apart<D, F8>(p, run.b, run.h, run.len, run.n, sh.bad[seg % 3], mask, gh, tq, nx,
+                                 dx, c0, y);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int k = 0; k < 16; ++k)
                     o[k] = y[k];
             }
-            if (!whole) {
-                float4* to = reinterpret_cast<float4*>(p.part_o + prow * D + c0);
+            if (whole)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                continue;
-            }
+                for (int k = 0; k < 16; ++k)
+                    o[k] = F8 ? o[k] * inv.x * inv.y : o[k] * inv.x;
+            if (!whole || p.o_fp32) {
+                float4* to = reinterpret_cast<float4*>(
+                    (whole ? (float*)p.o + orow * D : p.part_o + prow * D) + c0);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                o[k] = F8 ? o[k] * inv.x * inv.y : o[k] * inv.x;
-            if (p.o_fp32) {
-                float4* to = reinterpret_cast<float4*>((float*)p.o + orow * D + c0);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 4; ++k)
                     to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             } else {
                 uint4* to = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + orow * D + c0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 2; ++k)
                     to[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]),
                                        pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
                                        pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
                                        pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
             }
+        }
+        if (second) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.seconds);
         }
         tc_fence_before();
         mbar_arrive(&sh.o_empty);
@@ -1355,6 +1384,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_init(&sh.q_empty[s], F8 || TERMS == kLanes ? 9 : 1);
         }
         mbar_init(&sh.o_empty, 256);
+        mbar_init(&sh.q_first, 8);
         for (int s = 0; s < kRuns; ++s) {
             mbar_init(&sh.run_full[s], 1);
             mbar_init(&sh.run_empty[s], C::kReaders);
@@ -1504,7 +1534,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, 
     const int most = min(kTreeMaxCtas, num_sms);
     p.line_blocks = (int)min((int64_t)max(1, most / p.row_groups), pieces);
     const int grid = p.line_blocks * p.row_groups;
-    p.segment_cost = 2;
+    p.segment_cost = C::kSegmentCost;
     decode_tree_kernel<D, F8, TERMS><<<grid, C::kThreads, kSmem<D, F8>, stream>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.whole)
