@@ -212,8 +212,8 @@ dfa_status dfa_cache_compact(const dfa_paged_cache* cache, int32_t T, const int3
                          "dfa_cache_compact: need 1 <= A <= T and T < 2^30");
     if (!kept)
         return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_compact: kept is NULL");
-    if ((int64_t)2 * p.c.Hkv * p.c.B > kMaxBlocks)
-        return set_error(DFA_ERR_UNSUPPORTED, "dfa_cache_compact: B * Hkv above 2^30");
+    if ((int64_t)2 * kCompactMaxParts * p.c.Hkv * p.c.B > kMaxBlocks)
+        return set_error(DFA_ERR_UNSUPPORTED, "dfa_cache_compact: B * Hkv must be below 2^28");
     if ((s = check_ws(ws, ws_bytes, kStatusBytes, "dfa_cache_compact")) != DFA_OK)
         return s;
     p.q_lens = q_lens;

@@ -43,6 +43,8 @@ struct TreeParams {
     uint64_t timeout_ns;
 };
 
+constexpr int kCompactMaxParts = 4;  // blocks of a sequence's head and K or V
+
 struct CompactParams {
     CacheView c;
     const int32_t* q_lens;        // [B] or NULL
@@ -81,6 +83,8 @@ struct ReserveParams {
     PoolView p;
     const int32_t* new_lens;      // [B] or NULL
     int32_t T, max_jobs;
+    int32_t here;                 // the deciding block takes the pages, too
+    int32_t lanes_log2;           // threads that look at a sequence's pages
     int2* jobs;
     int32_t* info;                // [4]
     int2* offset;                 // [B]: pages and jobs of the sequences before
@@ -95,7 +99,7 @@ cudaError_t launch_decode_tree(const CUtensorMap& tk, const CUtensorMap& tv, Tre
 cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_cache_copy(const CopyParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream);
-cudaError_t launch_pages_reserve(const ReserveParams& p, cudaStream_t stream);
+cudaError_t launch_pages_reserve(ReserveParams& p, cudaStream_t stream);
 cudaError_t launch_pages_trim(const PoolView& p, cudaStream_t stream);
 
 }  // namespace dfa

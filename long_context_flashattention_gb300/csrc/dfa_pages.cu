@@ -112,10 +112,9 @@ struct Wanted {
     int32_t held, first, mid, need;
 };
 
-__device__ __forceinline__ Wanted wanted(const ReserveParams& p, int32_t b, bool report)
+__device__ __forceinline__ Wanted wanted(const ReserveParams& p, int32_t b, bool report,
+                                         int32_t len, int32_t n, int32_t held)
 {
-    const int32_t len = p.p.seq_lens[b], n = p.new_lens ? p.new_lens[b] : p.T;
-    const int32_t held = p.p.held[b];
     const int32_t page = 1 << p.p.page_log2;
     if (len < 0 || len > (int64_t)p.p.max_pages * page || n < 0 || n > p.T || n > len ||
         held < 0 || held > p.p.max_pages) {
@@ -129,6 +128,109 @@ __device__ __forceinline__ Wanted wanted(const ReserveParams& p, int32_t b, bool
     const int32_t need = (len + page - 1) >> p.p.page_log2;
     const int32_t first = n > 0 ? (len - n) >> p.p.page_log2 : need;
     return {held, first, max(first, min(held, need)), max(held, need)};
+}
+
+__device__ __forceinline__ int32_t new_rows(const ReserveParams& p, int32_t b)
+{
+    return p.new_lens ? p.new_lens[b] : p.T;
+}
+
+__device__ __forceinline__ Wanted wanted(const ReserveParams& p, int32_t b, bool report)
+{
+    return wanted(p, b, report, p.p.seq_lens[b], new_rows(p, b), p.p.held[b]);
+}
+
+// Calls f(sequence, page, its holders) for the pages that will be written to, a sequence by
+// `lanes` threads: four sequences at once, so that their loads (lengths, then entries, then
+// holders) are on their way together.  Pages that are none are reported or passed over.
+template <class F>
+__device__ __forceinline__ void each_written(const ReserveParams& p, int lanes_log2, bool report,
+                                             F f)
+{
+    constexpr int kAtOnce = 4;
+    const int32_t lanes = 1 << lanes_log2, mine = threadIdx.x & (lanes - 1);
+    const int32_t step = kReserveThreads >> lanes_log2;
+    for (int32_t b0 = threadIdx.x >> lanes_log2; b0 < p.p.B; b0 += kAtOnce * step) {
+        int32_t len[kAtOnce], n[kAtOnce], held[kAtOnce], id[kAtOnce], refs[kAtOnce];
+        Wanted w[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int32_t b = b0 + k * step;
+            len[k] = b < p.p.B ? p.p.seq_lens[b] : 0;
+            n[k] = b < p.p.B ? new_rows(p, b) : 0;
+            held[k] = b < p.p.B ? p.p.held[b] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            w[k] = wanted(p, b0 + k * step, report && mine == 0, len[k], n[k], held[k]);
+            w[k].first += mine;
+        }
+        for (bool more = true; more;) {
+            more = false;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                id[k] = w[k].first < w[k].mid
+                            ? p.p.table[(int64_t)(b0 + k * step) * p.p.max_pages + w[k].first]
+                            : -1;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                refs[k] = id[k] >= 0 && id[k] < p.p.npages ? p.p.refs[id[k]] : -1;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (w[k].first < w[k].mid) {
+                    if (id[k] >= 0 && id[k] < p.p.npages)
+                        f(b0 + k * step, id[k], refs[k]);
+                    else if (report)
+                        cache_fault(p.p.status, kSitePage, b0 + k * step);
+                }
+                w[k].first += lanes;
+                more |= w[k].first < w[k].mid;
+            }
+        }
+    }
+}
+
+// (Pages with one holder have no entries in `writers` and `last`.  A page that is copied has
+// two holders or more until its last copy is taken: the copying sequence and one that keeps.)
+__device__ __forceinline__ bool is_copied(const ReserveParams& p, int32_t b, int32_t id)
+{
+    return id >= 0 && id < p.p.npages && p.p.refs[id] > 1 && p.writers[id] > 0 && p.last[id] != b;
+}
+
+// Sequence b takes its share of the `total` free pages, by a warp.  (The tests of indexes
+// are for lengths that change while the kernel runs.)
+__device__ __forceinline__ void take_pages(const ReserveParams& p, int32_t b, int32_t total)
+{
+    const int lane = threadIdx.x & 31;
+    const Wanted w = wanted(p, b, false);
+    const int2 at = p.offset[b];
+    int32_t* row = p.p.table + (int64_t)b * p.p.max_pages;
+    int32_t taken = 0;
+    auto take = [&](int32_t i) -> int32_t {
+        if (at.x + i >= total)
+            return -1;
+        const int32_t id = p.free[at.x + i];
+        p.p.refs[id] = 1;
+        return id;
+    };
+    for (int32_t e0 = w.first; e0 < w.mid; e0 += 32) {
+        const int32_t e = e0 + lane, id = e < w.mid ? row[e] : -1;
+        const bool mine = is_copied(p, b, id);
+        const uint32_t all = __ballot_sync(0xffffffffu, mine);
+        const int32_t i = taken + __popc(all & ((1u << lane) - 1));
+        if (mine && at.y + i < p.max_jobs) {
+            const int32_t to = take(i);
+            row[e] = to;
+            p.jobs[at.y + i] = make_int2(id, to);
+            atomicSub(p.p.refs + id, 1);
+        }
+        taken += __popc(all);
+    }
+    for (int32_t e = w.held + lane; e < w.need; e += 32)
+        row[e] = take(taken + e - w.held);
+    __syncwarp();
+    if (lane == 0 && w.need > w.held)
+        p.p.held[b] = w.need;
 }
 
 // Exclusive sums of two numbers over the block's threads, and their totals.
@@ -164,56 +266,57 @@ __global__ void __launch_bounds__(kReserveThreads)
     __shared__ int32_t counts[kScan * kReserveWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t B = p.p.B;
-    auto entry = [&](int32_t b, int32_t e) { return p.p.table[(int64_t)b * p.p.max_pages + e]; };
+    // The first round's pages, on their way while it is found out how many are needed.
+    int32_t holders[kScan];
+    auto look = [&](int64_t base) {
+#pragma unroll
+        for (int k = 0; k < kScan; ++k) {
+            const int64_t id = base + k * kReserveThreads + threadIdx.x;
+            holders[k] = id < p.p.npages ? p.p.refs[id] : 1;
+        }
+    };
+    look(0);
     // Pages that will be written to and have other holders: how many of their holders
     // write, and the last of them, which keeps the page if all do.
-    for (int32_t b = threadIdx.x; b < B; b += kReserveThreads) {
-        const Wanted w = wanted(p, b, true);
-        for (int32_t e = w.first; e < w.mid; ++e) {
-            const int32_t id = entry(b, e);
-            if (pool_page(p.p, b, id)) {
-                p.last[id] = -1;
-                p.writers[id] = 0;
-            }
+    bool shared = false;
+    each_written(p, p.lanes_log2, true, [&](int32_t, int32_t id, int32_t refs) {
+        if (refs > 1) {
+            p.last[id] = -1;
+            p.writers[id] = 0;
+            shared = true;
         }
-    }
-    __syncthreads();
-    for (int32_t b = threadIdx.x; b < B; b += kReserveThreads) {
-        const Wanted w = wanted(p, b, false);
-        for (int32_t e = w.first; e < w.mid; ++e) {
-            const int32_t id = entry(b, e);
-            if (id >= 0 && id < p.p.npages && p.p.refs[id] > 1) {
+    });
+    shared = __syncthreads_or(shared);
+    if (shared) {
+        each_written(p, p.lanes_log2, false, [&](int32_t b, int32_t id, int32_t refs) {
+            if (refs > 1) {
                 atomicMax(p.last + id, b);
                 atomicAdd(p.writers + id, 1);
             }
-        }
-    }
-    __syncthreads();
-    // (decided once, by the last writer: refs change further down)
-    for (int32_t b = threadIdx.x; b < B; b += kReserveThreads) {
-        const Wanted w = wanted(p, b, false);
-        for (int32_t e = w.first; e < w.mid; ++e) {
-            const int32_t id = entry(b, e);
-            if (id >= 0 && id < p.p.npages && p.last[id] == b && p.writers[id] != p.p.refs[id])
+        });
+        __syncthreads();
+        // (decided once, by the last writer: refs change further down)
+        each_written(p, p.lanes_log2, false, [&](int32_t b, int32_t id, int32_t refs) {
+            if (refs > 1 && p.last[id] == b && p.writers[id] != refs)
                 p.last[id] = INT32_MAX;  // nobody keeps it
-        }
+        });
+        __syncthreads();
     }
-    __syncthreads();
-    auto copied = [&](int32_t b, int32_t id) {
-        return id >= 0 && id < p.p.npages && p.writers[id] > 0 && p.last[id] != b;
-    };
     int2 sum = make_int2(0, 0), total;
-    for (int32_t b0 = 0; b0 < B; b0 += kReserveThreads) {
-        const int32_t b = b0 + threadIdx.x;
+    const int lanes_log2 = shared ? p.lanes_log2 : 0;  // (else no entry is looked at)
+    const int32_t lanes = 1 << lanes_log2, part = threadIdx.x & (lanes - 1);
+    for (int32_t b0 = 0; b0 < B; b0 += kReserveThreads >> lanes_log2) {
+        const int32_t b = b0 + (threadIdx.x >> lanes_log2);
         int2 mine = make_int2(0, 0);
         if (b < B) {
             const Wanted w = wanted(p, b, false);
-            for (int32_t e = w.first; e < w.mid; ++e)
-                mine.y += copied(b, entry(b, e));
-            mine.x = mine.y + w.need - w.held;
+            if (shared)
+                for (int32_t e = w.first + part; e < w.mid; e += lanes)
+                    mine.y += is_copied(p, b, p.p.table[(int64_t)b * p.p.max_pages + e]);
+            mine.x = mine.y + (part == 0 ? w.need - w.held : 0);
         }
         const int2 at = block_scan(mine, total, warp_sums);
-        if (b < B)
+        if (b < B && part == 0)
             p.offset[b] = make_int2(sum.x + at.x, sum.y + at.y);
         sum.x += total.x;
         sum.y += total.y;
@@ -223,14 +326,11 @@ __global__ void __launch_bounds__(kReserveThreads)
     for (int64_t base = 0; base < p.p.npages && found < sum.x && sum.y <= p.max_jobs;
          base += kScan * kReserveThreads) {
         uint32_t here[kScan];
+        if (base > 0)
+            look(base);
 #pragma unroll
         for (int k = 0; k < kScan; ++k) {
-            const int64_t id = base + k * kReserveThreads + threadIdx.x;
-            here[k] = id < p.p.npages ? (uint32_t)p.p.refs[id] : 1u;
-        }
-#pragma unroll
-        for (int k = 0; k < kScan; ++k) {
-            here[k] = __ballot_sync(0xffffffffu, here[k] == 0);
+            here[k] = __ballot_sync(0xffffffffu, holders[k] == 0);
             if (lane == 0)
                 counts[k * kReserveWarps + warp] = __popc(here[k]);
         }
@@ -259,41 +359,19 @@ __global__ void __launch_bounds__(kReserveThreads)
         if (refused)
             cache_fault(p.p.status, kSitePool, sum.x);
     }
-    if (refused)
+    if (refused || !p.here)
         return;
     __syncthreads();  // the list of free pages
-    for (int32_t b = warp; b < B; b += kReserveWarps) {
-        const Wanted w = wanted(p, b, false);
-        const int2 at = p.offset[b];
-        int32_t* row = p.p.table + (int64_t)b * p.p.max_pages;
-        int32_t taken = 0;
-        // (the tests of indexes are for lengths that change while the kernel runs)
-        auto take = [&](int32_t i) -> int32_t {
-            if (at.x + i >= sum.x)
-                return -1;
-            const int32_t id = p.free[at.x + i];
-            p.p.refs[id] = 1;
-            return id;
-        };
-        for (int32_t e0 = w.first; e0 < w.mid; e0 += 32) {
-            const int32_t e = e0 + lane, id = e < w.mid ? row[e] : -1;
-            const bool mine = copied(b, id);
-            const uint32_t all = __ballot_sync(0xffffffffu, mine);
-            const int32_t i = taken + __popc(all & ((1u << lane) - 1));
-            if (mine && at.y + i < p.max_jobs) {
-                const int32_t to = take(i);
-                row[e] = to;
-                p.jobs[at.y + i] = make_int2(id, to);
-                atomicSub(p.p.refs + id, 1);
-            }
-            taken += __popc(all);
-        }
-        for (int32_t e = w.held + lane; e < w.need; e += 32)
-            row[e] = take(taken + e - w.held);
-        __syncwarp();
-        if (lane == 0 && w.need > w.held)
-            p.p.held[b] = w.need;
-    }
+    for (int32_t b = warp; b < B; b += kReserveWarps)
+        take_pages(p, b, sum.x);
+}
+
+// Pages of many sequences, where one block would go through them in many rounds.
+__global__ void __launch_bounds__(128) take_kernel(const __grid_constant__ ReserveParams p)
+{
+    const int32_t b = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (b < p.p.B && !p.info[2])
+        take_pages(p, b, p.info[1]);
 }
 
 // One warp per sequence.
@@ -374,19 +452,38 @@ __device__ __forceinline__ uint4 rescaled16(const uint4& w, float f)
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// A block per sequence, head and K or V, page after page of where the rows go to: row
-// i goes to place i and comes from place kept[i] >= i, so that no row of a later page
-// is overwritten before it is read.
+// A block per sequence, head, K or V (and for bf16 cells, which have no scale in common, 64
+// bytes of the rows), batch after batch of rows whose places end with a page: row i goes to
+// place i and comes from place kept[i] >= i, so that no row of a later batch is overwritten
+// before it is read, and no page of one is another's.  Where a batch's rows come from is
+// looked up while the batch before is on its way.
+//
+// Bound by HBM for many rows: half of 16 contexts of up to 8191 rows of 8 heads (269 MB
+// moved) 70 us, 3.8 TB/s, where single rows of 128 bytes are read here and there; page after
+// page, without looking ahead, 152 us.  A path of a few rows takes the chain of loads, 4 us.
+constexpr int kCompactThreads = 256, kCompactWords = 16;  // 16-byte words a thread at a time
+
 template <bool F8, int D>
-__global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ CompactParams p)
+constexpr int kCompactParts = F8 ? 1 : D / 32;
+static_assert(kCompactParts<false, 128> == kCompactMaxParts);
+
+template <bool F8, int D>
+__global__ void __launch_bounds__(kCompactThreads)
+    compact_kernel(const __grid_constant__ CompactParams p)
 {
-    constexpr int kPerRow = D * (F8 ? 1 : 2) / 16;       // 16-byte words of a row
-    constexpr int kMost = (128 * kPerRow + 255) / 256;   // of a page, a thread
+    constexpr int kParts = kCompactParts<F8, D>;
+    constexpr int kPerRow = D * (F8 ? 1 : 2) / 16 / kParts;  // 16-byte words of a row
+    constexpr int kRows = kCompactThreads * kCompactWords / kPerRow;  // of a batch
+    constexpr int kRowWarp = kCompactThreads / kPerRow;  // rows of one word a thread
+    __shared__ const uint4* from[2][kRows];              // NULL: no such page
+    __shared__ float scale_of[F8 ? 2 : 1][F8 ? kRows : 1];
+    __shared__ uint32_t top[F8 ? 2 : 1][F8 ? kRows / 16 + 1 : 1];  // of a batch's pages
     __shared__ int32_t moved_from;
-    __shared__ uint32_t top;
-    const int32_t b = blockIdx.x / (2 * p.c.Hkv);
-    const int32_t h = (blockIdx.x - b * 2 * p.c.Hkv) >> 1;
-    const bool is_v = blockIdx.x & 1;
+    const uint32_t item = blockIdx.x / kParts;
+    const int32_t part = blockIdx.x % kParts;
+    const int32_t b = item / (2 * p.c.Hkv);
+    const int32_t h = (item - b * 2 * p.c.Hkv) >> 1;
+    const bool is_v = item & 1;
     int32_t len, n;
     seq_rows(p.c, p.q_lens, p.T, b, len, n);
     const int32_t a = p.kept_lens ? p.kept_lens[b] : p.A;
@@ -397,9 +494,10 @@ __global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ Co
     bool bad = a < 0 || a > p.A || a > n;
     int32_t stays = INT32_MAX;
     if (!bad)
-        for (int32_t i = threadIdx.x; i < a; i += 256) {
-            const int32_t x = kept[i];
-            bad |= x < 0 || x >= n || (i > 0 && kept[i - 1] >= x);
+#pragma unroll 4
+        for (int32_t i = threadIdx.x; i < a; i += kCompactThreads) {
+            const int32_t x = kept[i], before = i > 0 ? kept[i - 1] : -1;
+            bad |= x <= before || x >= n;
             if (x != i)
                 stays = min(stays, i);
         }
@@ -419,64 +517,89 @@ __global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ Co
     float* scales = is_v ? p.c.v_scale : p.c.k_scale;
     auto row_at = [&](int32_t id, int32_t r) {
         return cells + ((int64_t)id * p.c.page_stride + (((int64_t)h << p.c.page_log2) + r) * D) *
-                           (F8 ? 1 : 2);
+                           (F8 ? 1 : 2) + part * kPerRow * 16;
     };
-    for (int32_t pg = (first + i0) >> p.c.page_log2; pg << p.c.page_log2 < end; ++pg) {
-        const int32_t start = pg << p.c.page_log2;
-        const int32_t lo = max(first + i0, start), hi = min(end, start + page);
-        const int32_t to = page_of(p.c, b, pg);
-        uint4 x[kMost];
-        float s[kMost];
-        bool there[kMost];
-        float mine = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int32_t w = k * 256 + threadIdx.x, r = lo + w / kPerRow;
-            there[k] = false;
-            if (r >= hi)
-                continue;
-            const int32_t from = first + kept[r - first];
-            const int32_t id = page_of(p.c, b, from >> p.c.page_log2);
-            there[k] = id >= 0 && to >= 0;
-            if (!there[k])
-                continue;
-            x[k] = reinterpret_cast<const uint4*>(row_at(id, from & (page - 1)))[w % kPerRow];
+    auto batch_end = [&](int32_t lo) { return min(end, (lo & ~(page - 1)) + kRows); };
+    // Where the rows of [lo, batch_end(lo)) come from, and the largest of their scales for
+    // each page that they go to.
+    auto look_up = [&](int32_t lo, int set) {
+        const int32_t hi = batch_end(lo), start = lo & ~(page - 1);
+        for (int32_t r = lo + (int32_t)threadIdx.x; r < hi; r += kCompactThreads) {
+            const int32_t j = first + kept[r - first];
+            const int32_t id = page_of(p.c, b, j >> p.c.page_log2);
+            from[set][r - start] =
+                id >= 0 ? reinterpret_cast<const uint4*>(row_at(id, j & (page - 1))) : nullptr;
             if (F8) {
-                s[k] = scales[(int64_t)id * p.c.Hkv + h];
-                mine = fmaxf(mine, s[k]);
+                const float s = id >= 0 ? scales[(int64_t)id * p.c.Hkv + h] : 0.f;
+                scale_of[set][r - start] = s;
+                atomicMax(&top[set][(r - start) >> p.c.page_log2], __float_as_uint(s));
             }
         }
-        float scale = 1.f;
+    };
+    auto clear = [&](int set) {
+        if (F8)
+            for (int i = threadIdx.x; i <= kRows / 16; i += kCompactThreads)
+                top[set][i] = 0;
+    };
+    clear(0);
+    __syncthreads();
+    look_up(first + i0, 0);
+    int set = 0;
+    for (int32_t lo = first + i0; lo < end; set ^= 1) {
+        const int32_t hi = batch_end(lo), start = lo & ~(page - 1);
+        __syncthreads();  // the rows are looked up; the other set has been used
         if (F8) {
-            const float old = to >= 0 ? scales[(int64_t)to * p.c.Hkv + h] : 1.f;
-            if (threadIdx.x == 0)
-                top = 0;
+            clear(set ^ 1);
             __syncthreads();
-            atomicMax(&top, __float_as_uint(lo > start ? fmaxf(mine, old) : mine));
-            __syncthreads();
-            scale = __uint_as_float(top);
-            if (to >= 0 && lo > start && scale != old) {
-                // the rows that stay, to the new scale
-                const float f = old / scale;
-                for (int32_t w = threadIdx.x; w < (lo - start) * kPerRow; w += 256) {
-                    uint4* cell = reinterpret_cast<uint4*>(row_at(to, w / kPerRow)) + w % kPerRow;
+        }
+        const int32_t at = threadIdx.x / kPerRow, word = threadIdx.x % kPerRow;
+        uint4 x[kCompactWords];
+#pragma unroll
+        for (int k = 0; k < kCompactWords; ++k) {
+            const int32_t r = start + at + k * kRowWarp;
+            if (r >= lo && r < hi && from[set][r - start])
+                x[k] = from[set][r - start][word];
+        }
+        if (hi < end)
+            look_up(hi, set ^ 1);
+        // The rows of the first page that stay: to the page's new scale.
+        const int32_t to0 = page_of(p.c, b, lo >> p.c.page_log2);
+        float old = 0.f;
+        if (F8 && lo > start && to0 >= 0)
+            old = scales[(int64_t)to0 * p.c.Hkv + h];
+        __syncthreads();  // all rows of the batch have been read, and the old scale
+        if (F8 && lo > start && to0 >= 0) {
+            const float s = fmaxf(old, __uint_as_float(top[set][0]));
+            if (s != old) {
+                const float f = old / s;
+                for (int32_t w = threadIdx.x; w < (lo - start) * kPerRow; w += kCompactThreads) {
+                    uint4* cell = reinterpret_cast<uint4*>(row_at(to0, w / kPerRow)) + w % kPerRow;
                     *cell = rescaled16(*cell, f);
                 }
             }
-            if (threadIdx.x == 0 && to >= 0 && scale > 0.f)
-                scales[(int64_t)to * p.c.Hkv + h] = scale;
         }
-        __syncthreads();  // all rows of the page have been read, and the old scale
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int32_t w = k * 256 + threadIdx.x, r = lo + w / kPerRow;
-            if (!there[k])
+        for (int k = 0; k < kCompactWords; ++k) {
+            const int32_t r = start + at + k * kRowWarp;
+            if (r < lo || r >= hi || !from[set][r - start])
                 continue;
-            if (F8 && s[k] != scale)
-                x[k] = rescaled16(x[k], s[k] / scale);
-            reinterpret_cast<uint4*>(row_at(to, r - start))[w % kPerRow] = x[k];
+            const int32_t pg = r >> p.c.page_log2, id = page_of(p.c, b, pg);
+            if (id < 0)
+                continue;
+            if (F8) {
+                float s = __uint_as_float(top[set][(r - start) >> p.c.page_log2]);
+                if (pg << p.c.page_log2 == start)
+                    s = fmaxf(s, old);
+                const float mine = scale_of[set][r - start];
+                if (mine != s)
+                    x[k] = rescaled16(x[k], mine / s);
+                // (the page's first row here, or its first one at all)
+                if (word == 0 && (r == lo || (r & (page - 1)) == 0))
+                    scales[(int64_t)id * p.c.Hkv + h] = s;
+            }
+            reinterpret_cast<uint4*>(row_at(id, r & (page - 1)))[word] = x[k];
         }
-        __syncthreads();
+        lo = hi;
     }
 }
 
@@ -493,9 +616,20 @@ cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t launch_pages_reserve(const ReserveParams& p, cudaStream_t stream)
+cudaError_t launch_pages_reserve(ReserveParams& p, cudaStream_t stream)
 {
+    // One warp a sequence, in two rounds at most; where there are more, in blocks of their
+    // own behind this one.
+    p.here = p.p.B <= 2 * kReserveWarps;
+    // A thread for each page that T rows can reach, a warp at most.
+    const int32_t pages = p.T > 0 ? ((p.T - 1) >> p.p.page_log2) + 2 : 1;
+    for (p.lanes_log2 = 0; p.lanes_log2 < 5 && 1 << p.lanes_log2 < pages;)
+        ++p.lanes_log2;
     reserve_kernel<<<1, kReserveThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.here)
+        return e;
+    take_kernel<<<(p.p.B + 3) / 4, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -515,13 +649,16 @@ cudaError_t launch_cache_copy(const CopyParams& p, int num_sms, cudaStream_t str
 
 cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream)
 {
-    const unsigned grid = 2u * p.c.Hkv * p.c.B;
+    const unsigned heads = 2u * p.c.Hkv * p.c.B;
     if (p.c.e4m3)
-        p.c.d == 128 ? compact_kernel<true, 128><<<grid, 256, 0, stream>>>(p)
-                     : compact_kernel<true, 64><<<grid, 256, 0, stream>>>(p);
+        p.c.d == 128 ? compact_kernel<true, 128><<<heads, kCompactThreads, 0, stream>>>(p)
+                     : compact_kernel<true, 64><<<heads, kCompactThreads, 0, stream>>>(p);
+    else if (p.c.d == 128)
+        compact_kernel<false, 128>
+            <<<heads * kCompactParts<false, 128>, kCompactThreads, 0, stream>>>(p);
     else
-        p.c.d == 128 ? compact_kernel<false, 128><<<grid, 256, 0, stream>>>(p)
-                     : compact_kernel<false, 64><<<grid, 256, 0, stream>>>(p);
+        compact_kernel<false, 64>
+            <<<heads * kCompactParts<false, 64>, kCompactThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -8,57 +8,83 @@ namespace {
 
 constexpr int kSiteParent = 103;  // of DFA_ERR_BOUNDS in DevStatus::where
 
-// One block per sequence.  sees[t] begins as node t itself and up[t] as its parent;
-// a step adds what the node up[t] sees and moves up[t] to where that one points, so
-// that after k steps the 2^k - 1 nearest ancestors are in.  (A word may be read
-// while another thread adds to it: whatever it has more by then are ancestors too.)
-__global__ void __launch_bounds__(1024) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
+// One block per sequence, nodes in groups of 32.  First, every group by a warp of its own:
+// which of a node's ancestors are in its group, and the nearest one before the group, by
+// doubling how far up the lanes know.  Then group after group: a node sees what that one
+// sees, and in its own group's word the former.  A warp takes four nodes, a lane a word;
+// of node t only words up to t / 32 are kept.
+//
+// Bound by the output for many deep trees (256 of 1024 nodes, 34 MB: 15 us; one doubling
+// of whole rows per step took 107), by the chain of loads for small ones (64 of up to 60
+// nodes: 2.5 us).
+__global__ void __launch_bounds__(256) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
 {
-    extern __shared__ uint32_t smem[];
+    extern __shared__ uint32_t sees[];            // group g: 32 nodes of g + 1 words
+    // of a node: the nearest ancestor before its group, as the place of its words and its
+    // group (<< 16), or -1; the ancestors in the group; how many there are in all
+    __shared__ __align__(16) int32_t from[kTreeMaxTokens];
+    __shared__ __align__(16) uint32_t own[kTreeMaxTokens];
+    __shared__ int16_t ancestor[kTreeMaxTokens], depth[kTreeMaxTokens];
     const int32_t T = p.T, W = p.words, b = blockIdx.x;
-    volatile uint32_t* sees = smem;                    // [T][W]
-    volatile int32_t* up = (int32_t*)(smem + T * W);   // [T]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t len, n;
     seq_rows(p.c, p.q_lens, T, b, len, n);
-    for (int32_t t = threadIdx.x; t < n; t += blockDim.x) {
-        int32_t parent = p.parents[(int64_t)b * T + t];
+    const int32_t groups = (n + 31) / 32;
+    for (int32_t g = warp; g < groups; g += 8) {
+        const int32_t t = 32 * g + lane;
+        int32_t parent = t < n ? p.parents[(int64_t)b * T + t] : -1;
         if (parent < -1 || parent >= t) {
             cache_fault(p.c.status, kSiteParent, b);
             parent = -1;
         }
-        up[t] = parent;
-    }
-    for (int32_t i = threadIdx.x; i < n * W; i += blockDim.x) {
-        const int32_t t = i / W, w = i - t * W;
-        sees[i] = t >> 5 == w ? 1u << (t & 31) : 0u;
+        const bool inside = parent >= 32 * g;
+        int32_t up = inside ? parent - 32 * g : lane;  // (a node without one here: itself)
+        uint32_t bits = 1u << lane;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            bits |= __shfl_sync(0xffffffffu, bits, up);
+            up = __shfl_sync(0xffffffffu, up, up);
+        }
+        // (up: the ancestor here whose parent is not)
+        const int32_t f = __shfl_sync(0xffffffffu, parent, up), fg = f >> 5;
+        ancestor[t] = (int16_t)f;
+        from[t] = f < 0 ? -1 : (fg + 1) * (16 * fg + (f & 31)) | fg << 16;
+        own[t] = bits;
     }
     __syncthreads();
-    for (bool more = true; more;) {
-        for (int32_t i = threadIdx.x; i < n * W; i += blockDim.x) {
-            const int32_t t = i / W, w = i - t * W;
-            const int32_t at = up[t];
-            if (at >= 0 && w <= at >> 5)
-                sees[i] = sees[i] | sees[at * W + w];
+    const int32_t t4 = warp * 4;  // the warp's nodes of a group
+    uint32_t* out = p.mask + ((int64_t)b * T + t4) * W + lane;
+    for (int32_t g = 0; g < groups; ++g, out += 32 * W) {
+        const int4 f4 = *reinterpret_cast<const int4*>(from + 32 * g + t4);
+        const uint4 o4 = *reinterpret_cast<const uint4*>(own + 32 * g + t4);
+        const int32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+        const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+        uint32_t word[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            word[k] = lane == g ? o[k] : 0u;
+            if (f[k] >= 0 && lane <= f[k] >> 16)
+                word[k] = sees[(f[k] & 0xffff) + lane];
+        }
+        if (lane <= g) {
+            uint32_t* to = sees + (g + 1) * (16 * g + t4) + lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k, to += g + 1)
+                *to = word[k];
+        }
+        if (lane < W)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (32 * g + t4 + k < n)
+                    out[k * W] = word[k];
+        if (warp == 0) {
+            const int32_t t = 32 * g + lane, a = ancestor[t];
+            const int32_t d = (a < 0 ? -1 : depth[a]) + __popc(own[t]);
+            depth[t] = (int16_t)d;
+            if (t < n)
+                p.positions[(int64_t)b * T + t] = len - n + d;
         }
         __syncthreads();
-        // (T <= blockDim.x)
-        int32_t next = -1;
-        if ((int32_t)threadIdx.x < n) {
-            const int32_t at = up[threadIdx.x];
-            next = at >= 0 ? up[at] : -1;
-        }
-        __syncthreads();
-        if ((int32_t)threadIdx.x < n)
-            up[threadIdx.x] = next;
-        more = __syncthreads_or(next >= 0);
-    }
-    for (int32_t i = threadIdx.x; i < n * W; i += blockDim.x)
-        p.mask[(int64_t)b * T * W + i] = sees[i];
-    for (int32_t t = threadIdx.x; t < n; t += blockDim.x) {
-        int32_t seen = 0;
-        for (int32_t w = 0; w <= t >> 5; ++w)
-            seen += __popc(sees[t * W + w]);
-        p.positions[(int64_t)b * T + t] = len - n + seen - 1;
     }
 }
 
@@ -66,14 +92,13 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const __grid_constant__
 
 cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream)
 {
-    const int smem = p.T * (p.words + 1) * 4;
+    const int groups = p.words;
+    const int most = 16 * 32 * 33 * 4, smem = groups > 1 ? 16 * groups * (groups + 1) * 4 : 128;
     const cudaError_t e = cudaFuncSetAttribute(
-        tree_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kTreeMaxTokens * (kTreeMaxTokens / 32 + 1) * 4);
+        tree_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess)
         return e;
-    const int threads = min(1024, max(32, (p.T * min(p.words, 4) + 31) / 32 * 32));
-    tree_plan_kernel<<<p.c.B, threads, smem, stream>>>(p);
+    tree_plan_kernel<<<p.c.B, 256, smem, stream>>>(p);
     return cudaGetLastError();
 }
 

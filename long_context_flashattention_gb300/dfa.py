@@ -994,7 +994,8 @@ class PagePool:
     first entries of its row; refs [npages] int32: how many hold each page, 0 where it is
     free.  Without held and refs a new pool of npages pages is made, which nobody holds yet.
     Its calls run one at a time, and report numbers that cannot be to the workspace they
-    are given, or else to pool.status: stream_status(pool.status)."""
+    are given, or else to pool.status: stream_status(pool.status).  Graphs of its calls need
+    it alive."""
 
     def __init__(self, block_table, seq_lens, page, held=None, refs=None, npages=None):
         dev = block_table.device
@@ -1022,6 +1023,8 @@ class PagePool:
         self._own.status = self.status.data_ptr()
         self._own_ref = ctypes.byref(self._own)
         self._need = max(256, int(lib().dfa_pages_workspace_size(self._ref)))
+        self._scratch = torch.empty(self._need, dtype=torch.uint8, device=dev)
+        self._raw = (torch.cuda.current_stream(dev).cuda_stream if dev.type == "cuda" else None)
 
     def __setattr__(self, name, value):
         if self.__dict__.get(name, value) is not value:
@@ -1031,6 +1034,17 @@ class PagePool:
 
     def __delattr__(self, name):
         raise AttributeError(f"{name} of a PagePool stays: change its contents")
+
+
+def _pool_ws(ws, nbytes, pool, stream, raw):
+    """A call's workspace, and the pool as the call sees it: errors go to the caller's
+    workspace, without one to the pool's status.  (The pool's calls run one at a time: what
+    they need beside their arguments is the pool's.)"""
+    if ws is None:
+        if stream is not None or raw != pool._raw:
+            pool._scratch.record_stream(stream or torch.cuda.current_stream(pool.device))
+        return pool._scratch, pool._own_ref
+    return _ws(ws, nbytes, pool, stream)
 
 
 def pages_workspace(pool: PagePool) -> torch.Tensor:
@@ -1044,7 +1058,7 @@ def pages_fork(pool: PagePool, src, ws=None, stream=None):
     both then hold, and its length; src[b] = b: stays, -1: becomes empty
     (dfa_pages_fork)."""
     raw = _raw_stream(pool.device, stream)
-    ws, ref = _ws(ws, pool._need, pool, stream)
+    ws, ref = _pool_ws(ws, pool._need, pool, stream, raw)
     if src is None:
         raise ValueError("src must be [B]")
     code = lib().dfa_pages_fork(ref, _int32(src, "src", (pool.B,), pool.device), ws.data_ptr(),
@@ -1070,7 +1084,7 @@ def pages_reserve(pool: PagePool, T, new_lens=None, jobs=None, info=None, ws=Non
     if info is None:
         info = _new(stream, (4,), torch.int32, dev)
     J = jobs.shape[0]
-    ws, ref = _ws(ws, pool._need, pool, stream)
+    ws, ref = _pool_ws(ws, pool._need, pool, stream, raw)
     code = lib().dfa_pages_reserve(ref, T, _int32(new_lens, "new_lens", (pool.B,), dev),
                                    _int32(jobs, "jobs", (J, 2), dev), J,
                                    _int32(info, "info", (4,), dev), ws.data_ptr(), ws.numel(),
@@ -1084,7 +1098,7 @@ def pages_trim(pool: PagePool, ws=None, stream=None):
     """Every sequence gives back the pages that it holds behind its length
     (dfa_pages_trim)."""
     raw = _raw_stream(pool.device, stream)
-    ws, ref = _ws(ws, 256, pool, stream)
+    ws, ref = _pool_ws(ws, 256, pool, stream, raw)
     code = lib().dfa_pages_trim(ref, ws.data_ptr(), ws.numel(), raw)
     if code:
         _check(code)
