@@ -459,9 +459,11 @@ __device__ __forceinline__ uint4 rescaled16(const uint4& w, float f)
 // looked up while the batch before is on its way.
 //
 // Bound by HBM for many rows: half of 16 contexts of up to 8191 rows of 8 heads (269 MB
-// moved) 70 us, 3.8 TB/s, where single rows of 128 bytes are read here and there; page after
-// page, without looking ahead, 152 us.  A path of a few rows takes the chain of loads, 4 us.
-constexpr int kCompactThreads = 256, kCompactWords = 16;  // 16-byte words a thread at a time
+// moved) 54 us, 4.9 TB/s: single rows are read, every other one.  Batches of twice as many
+// rows, half as many blocks on an SM: 69 us; page after page, without looking ahead, 152 us;
+// whole rows of bf16, fewer blocks, 81 us, and 32 bytes of them 91 us (before the smaller
+// batches).  A path of a few rows takes the chain of loads, 4 us.
+constexpr int kCompactThreads = 256, kCompactWords = 8;  // 16-byte words a thread at a time
 
 template <bool F8, int D>
 constexpr int kCompactParts = F8 ? 1 : D / 32;

@@ -34,7 +34,7 @@
 // to two cut ones, whose partials merge_kernel joins.  The lengths are read on the
 // device, so a captured graph follows them.
 //
-// Rounding: weights as two bf16 terms (2^-16) for bf16 cells; for 8-bit cells as one fp16
+// Rounding: weights as two bf16 terms (2^-17) for bf16 cells; for 8-bit cells as one fp16
 // term (2^-11) with a bf16 output, as two (2^-22) with an fp32 one.  Sums, maxima and O in
 // fp32.
 //
@@ -944,9 +944,7 @@ __device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float a = y[2 * j], b = y[2 * j + 1];
-        // bf16: the first term cut off, not rounded: its bits are the upper half's
-        hi[j] = F8 ? pack_half2(a, b)
-                   : __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+        hi[j] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
     }
     if (TERMS == kColumns || (TERMS == kLanes && second)) {
 #pragma unroll
@@ -957,10 +955,10 @@ __device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&
                 const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
                 c = a - z.x, d = b - z.y;
             } else {
-                const uint32_t ua = __float_as_uint(a) & 0xffff0000u;
-                const uint32_t ub = __float_as_uint(b) & 0xffff0000u;
-                f2unpack(f2add(f2pack(a, b), f2pack(__uint_as_float(ua ^ 0x80000000u),
-                                                    __uint_as_float(ub ^ 0x80000000u))),
+                // (the negative of the first term)
+                const uint32_t na = (hi[j] << 16) ^ 0x80000000u;
+                const uint32_t nb = (hi[j] & 0xffff0000u) ^ 0x80000000u;
+                f2unpack(f2add(f2pack(a, b), f2pack(__uint_as_float(na), __uint_as_float(nb))),
                          c, d);
             }
             hi[TERMS == kLanes ? j : 8 + j] = F8 ? pack_half2(c, d) : pack_bf16x2(c, d);
