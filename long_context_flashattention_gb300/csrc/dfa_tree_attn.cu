@@ -126,7 +126,7 @@ struct Shared {
     Piece run[kRuns];
     TileInfo<F8> info[kRing];
     long long w0, w1, base, each, rest;
-    int32_t b, block;
+    int32_t b, block, rows, nodes;
     uint32_t tmem, abort;
     union {
         long long warp_sum[16];  // while the range is found
@@ -254,8 +254,7 @@ struct Walk : Piece {
         fresh = true;
         if (w >= w1)
             return;
-        const int2 r = rows_of(p, b);
-        len = r.x, n = r.y;
+        len = sh.rows, n = sh.nodes;
         tiles = tiles_of(len, n);
         const long long at = w - sh.base, unit = tiles + p.segment_cost;
         h = (int32_t)min(divide(at, (int32_t)unit), (long long)p.c.Hkv - 1);
@@ -300,13 +299,16 @@ __device__ __forceinline__ void find_range(const TreeParams& p, SH& sh)
     const int32_t block = blockIdx.x / p.row_groups;
     if (threadIdx.x == 0) {
         sh.b = 0;
+        sh.rows = 0;
+        sh.nodes = 0;
         sh.block = block;
         sh.base = 0;
     }
     const int32_t b0 = threadIdx.x * chunk, b1 = min(b0 + chunk, p.c.B);
     long long sum = 0;
+    int2 r = make_int2(0, 0);  // of the thread's last sequence
     for (int32_t b = b0; b < b1; ++b) {
-        const int2 r = rows_of(p, b);
+        r = rows_of(p, b);
         const int32_t tiles = tiles_of(r.x, r.y);
         sum += tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
     }
@@ -341,12 +343,15 @@ __device__ __forceinline__ void find_range(const TreeParams& p, SH& sh)
     if (w0 < w1 && incl - sum <= w0 && w0 < incl) {
         long long base = incl - sum;
         for (int32_t b = b0; b < b1; ++b) {
-            const int2 r = rows_of(p, b);
+            if (chunk > 1)
+                r = rows_of(p, b);
             const int32_t tiles = tiles_of(r.x, r.y);
             const long long t = tiles ? (long long)(tiles + p.segment_cost) * per_seq : 0;
             if (w0 < base + t) {
                 sh.b = b;
                 sh.base = base;
+                sh.rows = r.x;
+                sh.nodes = r.y;
                 break;
             }
             base += t;
@@ -1454,21 +1459,29 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tree
     const int own = 2 * blockIdx.x, step = 2 * p.row_groups;
     auto slot = [&](int i) -> int64_t { return i == 0 ? own + 1 : own + i * step; };
     constexpr int V = D / 32;  // features of a lane
+    constexpr int kAtOnce = 4;  // partial rows on their way (8: 1 to 2 us more for 3 of them)
     for (int r = blockIdx.y * 8 + warp; r < kTreeRows && r0 + r < p.G * p.T; r += gridDim.y * 8) {
         int32_t gh, tq;
         split_row(p, r0 + r, gh, tq);
         if (tq >= info.w)
             continue;
-        float nx = kNone, dx = F8 ? -INFINITY : 0.f;
-        for (int i = lane; i < k; i += 32)
-            nx = fmaxf(nx, p.part_ndl[slot(i) * kTreeRows + r].x);
+        // (one round of 32 partials, kept in registers, where there are no more)
+        auto ndl = [&](int i) {
+            return i < k ? p.part_ndl[slot(i) * kTreeRows + r] : make_float4(kNone, 0.f, 0.f, 0.f);
+        };
+        float4 y = ndl(lane);
+        float nx = y.x, dx = F8 ? -INFINITY : 0.f;
+        for (int i = lane + 32; i < k; i += 32)
+            nx = fmaxf(nx, ndl(i).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
         if (F8) {
-            for (int i = lane; i < k; i += 32) {
-                const float4 y = p.part_ndl[slot(i) * kTreeRows + r];
-                dx = fmaxf(dx, (y.x - nx) + y.y);
+            if (lane < k)
+                dx = (y.x - nx) + y.y;
+            for (int i = lane + 32; i < k; i += 32) {
+                const float4 z = ndl(i);
+                dx = fmaxf(dx, (z.x - nx) + z.y);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -1476,19 +1489,34 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tree
         }
         float L = 0.f, acc[V] = {};
         for (int c = 0; c < k; c += 32) {
-            float4 y = make_float4(kNone, 0.f, 0.f, 0.f);
-            if (c + lane < k)
-                y = p.part_ndl[slot(c + lane) * kTreeRows + r];
+            if (c > 0)
+                y = ndl(c + lane);
             const float wt = ex2((y.x - nx) + (y.y - dx));
             L += y.z * ex2(y.x - nx);
             const int end = min(32, k - c);
-#pragma unroll 4
-            for (int i = 0; i < end; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, wt, i);
-                const float* from = p.part_o + (slot(c + i) * kTreeRows + r) * D + lane * V;
+#pragma unroll 1
+            for (int i0 = 0; i0 < end; i0 += kAtOnce) {
+                float x[kAtOnce][V];
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    acc[v] = fmaf(wi, from[v], acc[v]);
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const float* from =
+                        p.part_o + (slot(c + min(i0 + j, end - 1)) * kTreeRows + r) * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 z = *reinterpret_cast<const float4*>(from);
+                        x[j][0] = z.x, x[j][1] = z.y, x[j][2] = z.z, x[j][3] = z.w;
+                    } else {
+                        const float2 z = *reinterpret_cast<const float2*>(from);
+                        x[j][0] = z.x, x[j][1] = z.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const float wi = __shfl_sync(0xffffffffu, wt, i0 + j);
+                    if (i0 + j < end)
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            acc[v] = fmaf(wi, x[j][v], acc[v]);
+                }
             }
         }
 #pragma unroll
