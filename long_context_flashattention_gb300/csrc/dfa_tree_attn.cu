@@ -103,10 +103,11 @@ struct Cfg {
     static constexpr int kV0 = kK0 + kK * kTileBytes;
     static constexpr int kRaw0 = kV0 + kV * kTileBytes;
     static constexpr int kShared0 = kRaw0 + kRaw * kRawBytes;
-    // What a segment costs a block beside its tiles, in tiles.  Measured (1, 2, 4, 6): bf16,
-    // 64 ragged sequences of 16 nodes 190.6, 188.5, 194.4, 200.5 us; 8 bits, 8 sequences
-    // of 60 nodes 126.7, 119.5, 116.5, 112.3, 4 of 128 86.5, 86.0, 83.8, 82.1.
-    static constexpr int kSegmentCost = F8 ? 5 : 2;
+    // What a segment costs a block beside its tiles, in tiles.  Measured: bf16 (1, 2, 3, 4),
+    // 64 ragged sequences of 16 nodes 194.4, 187.0, 188.7, 191.9 us; 8 bits (3, 5, 8), 8
+    // sequences of 240 rows 103.7, 102.5, 103.2, 4 of 128 rows 74.7, 73.5, 73.8, but 4 of
+    // 16 rows 66.0, 66.8, 67.7.
+    static constexpr int segment_cost(int rows) { return !F8 ? 2 : rows > 64 ? 5 : 3; }
     static constexpr int kReaders = 8 + 1 + 2 + (F8 ? 4 : 0);  // warps that read a run
 };
 
@@ -424,12 +425,13 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
         const int32_t end = ceil_div(min(x.len, (x.tile0 + x.nt) * kTile), page);
         return win + lane < end ? page_entry(p.c, x.b, win + lane) : -1;
     };
-    auto announce = [&](bool end) {
+    // Segment `seg` to all readers, or that there is none.
+    auto announce = [&](uint32_t seg, const Piece& run, bool end) {
         const bool ok = wait(&sh.run_empty[seg % kRuns], (seg / kRuns + 1) & 1, wctx, 51);
         if (!__all_sync(0xffffffffu, ok))
             return false;
         if (lane == 0) {
-            sh.run[seg % kRuns] = wk;
+            sh.run[seg % kRuns] = run;
             if (end)
                 sh.run[seg % kRuns].nt = 0;
             mbar_arrive(&sh.run_full[seg % kRuns]);
@@ -437,9 +439,9 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
         return true;
     };
     int32_t next_id = more ? entry(wk, (wk.tile0 * kTile) >> p.c.page_log2) : -1;
+    if (!announce(0, wk, !more))
+        return;
     for (; more; ++seg) {
-        if (!announce(false))
-            return;
         const int32_t h = wk.h;
         const int32_t pages_end = ceil_div(min(wk.len, (wk.tile0 + wk.nt) * kTile), page);
         int32_t win = (wk.tile0 * kTile) >> p.c.page_log2, id = next_id;
@@ -523,12 +525,15 @@ __device__ __forceinline__ void produce(const TreeParams& p, Shared<D, F8>& sh,
             if (i == look) {
                 more_next = nx.next(p);
                 next_id = more_next ? entry(nx, (nx.tile0 * kTile) >> p.c.page_log2) : -1;
+                // (at once: its queries take one warp several tiles' time.  All readers have
+                // the segment before this one, or what they need to come to it.)
+                if (!announce(seg + 1, nx, !more_next))
+                    return;
             }
         }
         wk = nx;
         more = more_next;
     }
-    announce(true);
 }
 
 // ---------------------------------------------------------------------------
@@ -1241,7 +1246,10 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         const bool whole = run.nt == run.tiles;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (run.tile0 == 0 ? 1 : 0);
         const int64_t prow = slot * kTreeRows + row;
-        const int64_t orow = ((int64_t)run.b * p.Hq + run.h * p.G + gh) * p.T + tq;
+        // (a partial's O: four features of all rows, then the next four)
+        float4* const pout = reinterpret_cast<float4*>(p.part_o) + slot * (kTreeRows * D / 4) + row;
+        const int64_t orow =  // (of the segment one behind the other)
+            ((int64_t)run.b * p.Hq + run.h * p.G) * p.T + run.rg * kTreeRows + row;
         const float2 inv = row_factors<D, F8>(dx, l);
         // The groups take half of the features each, 16 at a time.  kLanes: second terms come
         // by way of the segment's queries, which are done with.
@@ -1301,11 +1309,12 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 for (int k = 0; k < 16; ++k)
                     o[k] = F8 ? o[k] * inv.x * inv.y : o[k] * inv.x;
             if (!whole || p.o_fp32) {
-                float4* to = reinterpret_cast<float4*>(
-                    (whole ? (float*)p.o + orow * D : p.part_o + prow * D) + c0);
+                float4* to = whole ? reinterpret_cast<float4*>((float*)p.o + orow * D + c0)
+                                   : pout + (c0 / 4) * kTreeRows;
+                const int step = whole ? 1 : kTreeRows;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    to[k * step] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             } else {
                 uint4* to = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + orow * D + c0);
 #pragma unroll
@@ -1446,98 +1455,89 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 }
 
 // Rows of the segments that several blocks share: block c holds such a segment's
-// beginning, the info[c].z blocks of its group after it the rest.  One warp a row.
+// beginning, the info[c].z blocks of its group after it the rest.  A block takes 32 rows'
+// 32 features, a thread four of a row: a warp reads four features of all rows, as they lie
+// together, and the rows are put together again in shared memory.
 template <int D, bool F8>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TreeParams p)
 {
+    constexpr int kAtOnce = 4;  // partials on their way
+    __shared__ float4 out[32][9];
     const int4 info = p.info[blockIdx.x];
     const int k = info.z + 1;
-    if (info.z <= 0)
-        return;
     const int32_t h = info.y / p.row_groups, r0 = (info.y - h * p.row_groups) * kTreeRows;
+    const int32_t first = blockIdx.y / (D / 32) * 32;  // row of the block's first
+    if (info.z <= 0 || r0 + first >= p.G * p.T)
+        return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.y % (D / 32) * 8;           // the block's features, by four
     const int own = 2 * blockIdx.x, step = 2 * p.row_groups;
-    auto slot = [&](int i) -> int64_t { return i == 0 ? own + 1 : own + i * step; };
-    constexpr int V = D / 32;  // features of a lane
-    constexpr int kAtOnce = 4;  // partial rows on their way (8: 1 to 2 us more for 3 of them)
-    for (int r = blockIdx.y * 8 + warp; r < kTreeRows && r0 + r < p.G * p.T; r += gridDim.y * 8) {
-        int32_t gh, tq;
-        split_row(p, r0 + r, gh, tq);
-        if (tq >= info.w)
-            continue;
-        // (one round of 32 partials, kept in registers, where there are no more)
-        auto ndl = [&](int i) {
-            return i < k ? p.part_ndl[slot(i) * kTreeRows + r] : make_float4(kNone, 0.f, 0.f, 0.f);
-        };
-        float4 y = ndl(lane);
-        float nx = y.x, dx = F8 ? -INFINITY : 0.f;
-        for (int i = lane + 32; i < k; i += 32)
-            nx = fmaxf(nx, ndl(i).x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float nx = kNone, dx = F8 ? -INFINITY : 0.f, L = 0.f;
+    const float4* parts = reinterpret_cast<const float4*>(p.part_o) + first + lane;
+    for (int i0 = 0; i0 < k; i0 += kAtOnce) {
+        float4 y[kAtOnce], o[kAtOnce];  // reference, exponent and sum; O
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, o));
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t slot = i0 + j == 0 ? own + 1 : own + (i0 + j) * step;
+            y[j] = make_float4(kNone, F8 ? -INFINITY : 0.f, 0.f, 0.f);
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + j < k) {
+                y[j] = p.part_ndl[slot * kTreeRows + first + lane];
+                o[j] = parts[(slot * (D / 4) + c + warp) * kTreeRows];
+            }
+        }
+        float n2 = nx;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            n2 = fmaxf(n2, y[j].x);
+        float d2 = dx;
         if (F8) {
-            if (lane < k)
-                dx = (y.x - nx) + y.y;
-            for (int i = lane + 32; i < k; i += 32) {
-                const float4 z = ndl(i);
-                dx = fmaxf(dx, (z.x - nx) + z.y);
-            }
+            d2 += nx - n2;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                dx = fmaxf(dx, __shfl_xor_sync(0xffffffffu, dx, o));
+            for (int j = 0; j < kAtOnce; ++j)
+                d2 = fmaxf(d2, (y[j].x - n2) + y[j].y);
         }
-        float L = 0.f, acc[V] = {};
-        for (int c = 0; c < k; c += 32) {
-            if (c > 0)
-                y = ndl(c + lane);
-            const float wt = ex2((y.x - nx) + (y.y - dx));
-            L += y.z * ex2(y.x - nx);
-            const int end = min(32, k - c);
-#pragma unroll 1
-            for (int i0 = 0; i0 < end; i0 += kAtOnce) {
-                float x[kAtOnce][V];
+        const float down = i0 == 0 ? 0.f : ex2((nx - n2) + (F8 ? dx - d2 : 0.f));
+        acc.x *= down, acc.y *= down, acc.z *= down, acc.w *= down;
+        L *= ex2(nx - n2);
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const float* from =
-                        p.part_o + (slot(c + min(i0 + j, end - 1)) * kTreeRows + r) * D + lane * V;
-                    if constexpr (V == 4) {
-                        const float4 z = *reinterpret_cast<const float4*>(from);
-                        x[j][0] = z.x, x[j][1] = z.y, x[j][2] = z.z, x[j][3] = z.w;
-                    } else {
-                        const float2 z = *reinterpret_cast<const float2*>(from);
-                        x[j][0] = z.x, x[j][1] = z.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const float wi = __shfl_sync(0xffffffffu, wt, i0 + j);
-                    if (i0 + j < end)
-#pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            acc[v] = fmaf(wi, x[j][v], acc[v]);
-                }
-            }
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (i0 + j >= k)
+                break;
+            const float w = ex2((y[j].x - n2) + (F8 ? y[j].y - d2 : 0.f));
+            L = fmaf(y[j].z, ex2(y[j].x - n2), L);
+            acc.x = fmaf(w, o[j].x, acc.x), acc.y = fmaf(w, o[j].y, acc.y);
+            acc.z = fmaf(w, o[j].z, acc.z), acc.w = fmaf(w, o[j].w, acc.w);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            L += __shfl_xor_sync(0xffffffffu, L, o);
-        const float2 inv = row_factors<D, F8>(dx, L);
-        const int64_t at = ((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            acc[v] = F8 ? acc[v] * inv.x * inv.y : acc[v] * inv.x;
-            if (p.o_fp32)
-                ((float*)p.o)[at * D + lane * V + v] = acc[v];
-        }
-        if (!p.o_fp32)
-#pragma unroll
-            for (int v = 0; v < V; v += 2)
-                reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.o + at * D + lane * V)[v / 2] =
-                    pack_bf16x2(acc[v], acc[v + 1]);
-        if (lane == 0)
-            p.lse[at] = row_lse(nx, L);
+        nx = n2;
+        dx = d2;
     }
+    const float2 inv = row_factors<D, F8>(dx, L);
+    if (F8)
+        acc.x *= inv.x, acc.y *= inv.x, acc.z *= inv.x, acc.w *= inv.x;
+    const float last = F8 ? inv.y : inv.x;
+    out[lane][warp] = make_float4(acc.x * last, acc.y * last, acc.z * last, acc.w * last);
+    __syncthreads();
+    int32_t gh, tq;
+    if (c == 0 && warp == 0 && r0 + first + lane < p.G * p.T) {
+        split_row(p, r0 + first + lane, gh, tq);
+        if (tq < info.w)
+            p.lse[((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq] = row_lse(nx, L);
+    }
+    const int r = threadIdx.x >> 3, f = threadIdx.x & 7;
+    if (r0 + first + r >= p.G * p.T)
+        return;
+    split_row(p, r0 + first + r, gh, tq);
+    if (tq >= info.w)
+        return;
+    const float4 x = out[r][f];
+    const int64_t at = (((int64_t)info.x * p.Hq + h * p.G + gh) * p.T + tq) * D + (c + f) * 4;
+    if (p.o_fp32)
+        *reinterpret_cast<float4*>((float*)p.o + at) = x;
+    else
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + at) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
 template <int D, bool F8, Terms TERMS>
@@ -1560,13 +1560,13 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, 
     const int most = min(kTreeMaxCtas, num_sms);
     p.line_blocks = (int)min((int64_t)max(1, most / p.row_groups), pieces);
     const int grid = p.line_blocks * p.row_groups;
-    p.segment_cost = C::kSegmentCost;
+    p.segment_cost = C::segment_cost(p.G * p.T);
     decode_tree_kernel<D, F8, TERMS><<<grid, C::kThreads, kSmem<D, F8>, stream>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.whole)
         return e;
     const int rows = min(kTreeRows, p.G * p.T);
-    merge_kernel<D, F8><<<dim3(grid, (rows + 7) / 8), 256, 0, stream>>>(p);
+    merge_kernel<D, F8><<<dim3(grid, ceil_div(rows, 32) * (D / 32)), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
