@@ -302,3 +302,39 @@ def test_pool_captured_and_replayed():
         assert jobs[:len(want)].tolist() == want
         same(pool, model)
     dfa.stream_status(pool.status)
+
+
+def test_pool_on_other_streams():
+    """The calls go to their stream or the current one; a pool may go while they run."""
+    first = torch.cuda.current_stream()
+    for named in (True, False):
+        s = torch.cuda.Stream()
+        pool, model = new_pool(9, 6, 80, 16)
+        pool.seq_lens.copy_(i32([20] * 9))
+        model.lens = [20] * 9
+        src, tensors = i32([0] * 9), (pool.held, pool.refs, pool.block_table, pool.seq_lens)
+        s.wait_stream(first)
+        kw = {"stream": s} if named else {}
+        with torch.cuda.stream(first if named else s):
+            jobs, info = dfa.pages_reserve(pool, 20, **kw)
+            dfa.pages_fork(pool, src, **kw)
+            with torch.cuda.stream(s):
+                pool.seq_lens.add_(1)
+            jobs, info = dfa.pages_reserve(pool, 1, **kw)
+            dfa.pages_trim(pool, **kw)
+        want, taken, _ = model.reserve([20] * 9, 100)
+        model.fork([0] * 9)
+        model.lens = [21] * 9
+        want, taken, refused = model.reserve([1] * 9, 100)
+        model.trim()
+        desc = pool.desc
+        del pool
+        junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert info.tolist() == [len(want), taken, refused, 0]
+        assert jobs[:len(want)].tolist() == want
+        held, refs, table, lens = (t.tolist() for t in tensors)
+        assert held == [len(p) for p in model.pages] and refs == model.refs()
+        assert lens == model.lens and desc.B == 9 and len(junk) == 8
+        for b, p in enumerate(model.pages):
+            assert table[b][:len(p)] == p

@@ -399,6 +399,45 @@ def test_tree_captured_and_replayed_as_sequences_grow():
         assert torch.equal(pos.cpu().long(), i32(lens, "cpu")[:, None] - T + sees.sum(-1) - 1)
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("G,T,d", [(2, 3, 64), (5, 16, 128)])
+def test_tree_sequences_of_no_rows_to_several_tiles(dtype, G, T, d):
+    """More sequences than blocks, so that blocks go from one short segment to the next;
+    sequences without a node between them."""
+    B, page, width = 240, 32, 16
+    g = torch.Generator().manual_seed(d)
+    lens = [int(x) for x in torch.randint(0, 400, (B,), generator=g)]
+    lens[40:80] = [int(x) for x in torch.randint(1, 40, (40,), generator=g)]
+    n = [min(L, int(x)) for L, x in zip(lens, torch.randint(0, T + 1, (B,), generator=g))]
+    n[100:120] = [0] * 20
+    c = ref.Cache(dtype, 1, 1, d, page, width, [512], seed=d)
+    c.B, c.table, c.lens = B, c.table.repeat(B, 1), i32(lens, "cpu")   # (the same pages)
+    q = randn(B, G, T, d, seed=60)
+    sees = bref.sees_of(bref.random_parents(B, T, seed=61))
+    check_tree(c, c.cuda(), q, sees, n, fp32=(G == 5,))
+
+
+def test_tree_graphs_that_share_a_workspace():
+    """One workspace, made for the larger of two calls, in two graphs replayed in turn."""
+    calls, graphs = [], []
+    for dtype, G, T, L in ((E4M3, 4, 30, 4000), (BF16, 1, 3, 900)):
+        c = ref.Cache(dtype, 2, 2, 128, 64, 64, [L, L // 3], seed=L)
+        sees = bref.sees_of(bref.random_parents(2, T, seed=T))
+        calls.append((c.cuda(), randn(2, 2 * G, T, 128, seed=62).cuda(), bref.pack(sees).cuda()))
+    want = [dfa.decode_tree(*a) for a in calls]
+    ws = dfa.tree_workspace(calls[0][0], 8, 30)
+    for a in calls:
+        graphs.append((torch.cuda.CUDAGraph(), []))
+        with torch.cuda.graph(graphs[-1][0]):
+            graphs[-1][1].extend(dfa.decode_tree(*a, ws=ws))
+    for _ in range(3):
+        for (g, got), (o, lse) in zip(graphs, want):
+            got[0].zero_()
+            g.replay()
+            assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    dfa.stream_status(ws)
+
+
 def test_tree_on_two_streams_at_once():
     c = ref.Cache(BF16, 4, 4, 128, 32, 100, [3000, 2000, 1000, 17], seed=34)
     dev = c.cuda()
@@ -499,6 +538,23 @@ def test_compact(dtype, page, d):
     kept = torch.zeros(8, 300, dtype=torch.int32)
     for b in range(8):
         kept[b, :a[b]] = some(n[b], a[b], b)
+    check_compact(c, kept, a, n)
+
+
+@pytest.mark.parametrize("dtype,page,d", [(E4M3, 16, 128), (E4M3, 128, 64), (BF16, 64, 128),
+                                          (BF16, 32, 64)])
+def test_compact_long(dtype, page, d):
+    """Several batches of rows, the first of which stay; scales that go up and down."""
+    lens, n, a = [2900, 1500], [2877, 1500], [2000, 1499]
+    c = ref.Cache(dtype, 2, 1, d, page, -(-2900 // page), lens, seed=63)
+    if dtype is E4M3:
+        g = torch.Generator().manual_seed(64)
+        for name in "kv":
+            c.scales[name] *= 2.0 ** torch.randint(-4, 5, c.scales[name].shape, generator=g)
+    kept = torch.zeros(2, 2000, dtype=torch.int32)
+    kept[0, :40] = torch.arange(40)
+    kept[0, 40:2000] = 40 + some(n[0] - 40, 1960, 65)
+    kept[1, :1499] = some(1500, 1499, 66)
     check_compact(c, kept, a, n)
 
 
