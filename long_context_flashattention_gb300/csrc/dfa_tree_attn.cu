@@ -34,9 +34,10 @@
 // to two cut ones, whose partials merge_kernel joins.  The lengths are read on the
 // device, so a captured graph follows them.
 //
-// Rounding: weights as two bf16 terms (2^-17) for bf16 cells; for 8-bit cells as one fp16
-// term (2^-11) with a bf16 output, as two (2^-22) with an fp32 one.  Sums, maxima and O in
-// fp32.
+// Rounding: weights as two bf16 terms (2^-17) for bf16 cells, with an fp32 output and at
+// most 64 query rows a head as three (2^-25; with more there is no room in TMEM beside
+// them); for 8-bit cells as one fp16 term (2^-11) with a bf16 output, as two (2^-22) with an
+// fp32 one.  Sums, maxima and O in fp32; see kChain.
 //
 // Values that are not finite, in a row that some nodes see and others do not, would reach
 // the others as 0 * inf.  Such rows (looked for in tiles that reach into the tree) are
@@ -61,6 +62,12 @@ constexpr float kGrow = 60.f;
 // kHead is what small ones behind a large one have left: half a step of fp16's subnormals
 // is 2^-33 of the largest weight, 2^-16 for 128K of them together.
 constexpr float kTop = 15.f, kHead = 8.f;
+// A product adds to O by cutting off what fp32 does not hold, which makes O smaller each
+// time, in the end by 2^-24 of it for every other product.  For fp32 outputs a sum of so many
+// tiles is set apart (in the workspace; the next begins at 0) and added at the segment's end:
+// off by 2.7e-6 in place of 3.5e-6 after 128K rows, 54 tiles a block, for 71 us in place of
+// 67; every 16 tiles 2.5e-6 and 73 us.
+constexpr int kChain = 32;
 constexpr float kNone = -FLT_MAX;         // running maximum before the first key
 constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
                                           // taken off them (else both in one operation: N,
@@ -84,8 +91,11 @@ struct Piece {
 
 // How weights are held: in one term; in two, side by side in the operand's columns; in two
 // in its rows, where at most 64 of the 128 rows have queries: rows r and r + 64 are the
-// same query's, and the second row's weights are what the first's leave.
-enum Terms { kOne, kColumns, kLanes };
+// same query's, and the second row's weights are what the first's leave; in three: two in
+// the rows, the third in the first's columns.
+enum Terms { kOne, kColumns, kLanes, kThree };
+constexpr bool by_rows(Terms t) { return t == kLanes || t == kThree; }
+constexpr bool by_columns(Terms t) { return t == kColumns || t == kThree; }
 
 template <int D, bool F8>
 struct Cfg {
@@ -135,7 +145,7 @@ struct Shared {
     };
     uint32_t any_bad[3];
     float qf[F8 ? 2 : 1][F8 ? kTreeRows : 1];             // score factors of the rows
-    // of the two groups: N, sum, D
+    // of the two groups: N (before, what is set apart of O is to be multiplied by), sum, D
     float n[2][kTreeRows], l[2][kTreeRows], d[F8 ? 2 : 1][F8 ? kTreeRows : 1];
 };
 
@@ -386,6 +396,22 @@ __device__ __forceinline__ bool next_run(SH& sh, uint32_t seg, Piece& run, const
     return run.nt > 0;
 }
 
+// Is the output fp32?  (What launch_terms leaves open is known to the compiler.)
+template <bool F8, Terms TERMS>
+__device__ __forceinline__ bool is_fp32(const TreeParams& p)
+{
+    if (TERMS == kOne || (TERMS == kLanes && !F8))
+        return false;
+    return F8 || TERMS == kThree || p.o_fp32;
+}
+
+// The tile i of a segment begins a chain where i & this is 0.
+template <bool F8, Terms TERMS>
+__device__ __forceinline__ int32_t chain_mask(const TreeParams& p)
+{
+    return is_fp32<F8, TERMS>(p) ? kChain - 1 : INT32_MAX;
+}
+
 // A place in a ring of SLOTS, and the phase that its barriers are in.
 template <int SLOTS>
 struct Ring {
@@ -561,7 +587,7 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, Shared<D, F8>&
         split_row(p, run.rg * kTreeRows + row, gh, tq);
         if (tq < run.n)
 #pragma unroll
-            for (int i = 0; i < (TERMS == kLanes && !F8 ? 2 : 1); ++i)
+            for (int i = 0; i < (by_rows(TERMS) && !F8 ? 2 : 1); ++i)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                  to + sw128_offset(row + 64 * i, c & 7)),
                              "l"(q + gh * p.q.sh + tq * p.q.sl)
@@ -598,7 +624,7 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, Shared<D, F8>&
                     w[i] = pack_half2(bf16lo(w[i]) * inv, bf16hi(w[i]) * inv);
                 if (row < rows)
 #pragma unroll
-                    for (int i = 0; i < (TERMS == kLanes ? 2 : 1); ++i) {
+                    for (int i = 0; i < (by_rows(TERMS) ? 2 : 1); ++i) {
                         st_shared_v4(to + sw128_offset(row + 64 * i, c & 7), w[0], w[1], w[2], w[3]);
                         if (c == 0)
                             sh.qf[seg & 1][row + 64 * i] =
@@ -782,7 +808,7 @@ __device__ __forceinline__ void multiply_scores(Shared<D, F8>& sh, uint32_t smem
 
 // O_w += P_w V, of 64 keys each
 template <int D, bool F8, Terms TERMS>
-__device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem,
+__device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem, int32_t chain,
                                                 const WaitCtx& wctx)
 {
     using C = Cfg<D, F8>;
@@ -805,11 +831,11 @@ __device__ __forceinline__ void multiply_values(Shared<D, F8>& sh, uint32_t smem
                 tc_fence_after();
                 const uint32_t from = sr.at * 128 + w * 64;
 #pragma unroll
-                for (int kk = 0; kk < (TERMS == kColumns ? 8 : 4); ++kk)
+                for (int kk = 0; kk < (by_columns(TERMS) ? 8 : 4); ++kk)
                     mma_ts_one(C::kO0 + w * D,
-                               from + (TERMS == kColumns ? (kk & 3) * 16 + (kk >> 2) * 8 : kk * 8),
+                               from + (by_columns(TERMS) ? (kk & 3) * 16 + (kk >> 2) * 8 : kk * 8),
                                sdesc_add(v, (w * 4 + (kk & 3)) * 2048), idesc<F8>(D, true),
-                               (i > 0 || kk > 0) ? 1u : 0u);
+                               ((i & chain) || kk > 0) ? 1u : 0u);
             }
             commit_one(&sh.s_free[sr.at]);
             commit_one(&sh.v_empty[vr.at]);
@@ -946,7 +972,8 @@ __device__ __forceinline__ void hide16(uint32_t (&r)[16], uint32_t seen)
 
 // The weights y of 16 keys as the products' operand, in place of their scores (TMEM): 8
 // columns for 16 keys, one behind the other (kColumns: 8, and 8 of second terms, where
-// the keys' scores were).  kLanes: `second` rows have second terms alone.
+// the keys' scores were).  kLanes: `second` rows have second terms alone; kThree: they and
+// zeros, the others third terms beside the first.
 template <bool F8, Terms TERMS>
 __device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&y)[16], bool second)
 {
@@ -956,25 +983,35 @@ __device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&
         const float a = y[2 * j], b = y[2 * j + 1];
         hi[j] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
     }
-    if (TERMS == kColumns || (TERMS == kLanes && second)) {
+    // what a term of bf16 (fp16) leaves
+    auto rest = [](float& a, float& b, uint32_t term) {
+        if (F8) {
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&term));
+            a -= z.x, b -= z.y;
+        } else {
+            const uint32_t na = (term << 16) ^ 0x80000000u;
+            const uint32_t nb = (term & 0xffff0000u) ^ 0x80000000u;
+            f2unpack(f2add(f2pack(a, b), f2pack(__uint_as_float(na), __uint_as_float(nb))), a, b);
+        }
+    };
+    if (by_columns(TERMS) || (TERMS == kLanes && second)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float a = y[2 * j], b = y[2 * j + 1];
-            float c, d;
-            if (F8) {
-                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-                c = a - z.x, d = b - z.y;
+            float a = y[2 * j], b = y[2 * j + 1];
+            rest(a, b, hi[j]);
+            const uint32_t next = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
+            if (TERMS != kThree) {
+                hi[TERMS == kLanes ? j : 8 + j] = next;
+            } else if (second) {
+                hi[j] = next;
+                hi[8 + j] = 0;
             } else {
-                // (the negative of the first term)
-                const uint32_t na = (hi[j] << 16) ^ 0x80000000u;
-                const uint32_t nb = (hi[j] & 0xffff0000u) ^ 0x80000000u;
-                f2unpack(f2add(f2pack(a, b), f2pack(__uint_as_float(na), __uint_as_float(nb))),
-                         c, d);
+                rest(a, b, next);
+                hi[8 + j] = pack_bf16x2(a, b);
             }
-            hi[TERMS == kLanes ? j : 8 + j] = F8 ? pack_half2(c, d) : pack_bf16x2(c, d);
         }
     }
-    if (TERMS == kColumns)
+    if (by_columns(TERMS))
         tmem_st16(tS + 16 * k, hi);
     else
         tmem_st8(tS + 8 * k, hi);
@@ -1057,6 +1094,55 @@ __device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, i
     return sum;
 }
 
+// A row of a group's O (TMEM) added to what is set apart of it, f times that; f = 0: none.
+template <int D>
+__device__ __noinline__ void set_apart(uint32_t tO, float4* apart, float f)
+{
+    tmem_st_wait();
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c0, o);
+        tmem_ld_wait();
+        tmem_reg_fence32(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float4* at = apart + (c0 / 4 + k) * kTreeRows;
+            float4 x = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            if (f != 0.f) {
+                const float4 y = *at;
+                x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z),
+                                fmaf(f, y.w, x.w));
+            }
+            *at = x;
+        }
+    }
+}
+
+// And f times what is set apart added to O.
+template <int D>
+__device__ __noinline__ void take_back(uint32_t tO, const float4* apart, float f)
+{
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c0, o);
+        tmem_ld_wait();
+        tmem_reg_fence32(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 y = apart[(c0 / 4 + k) * kTreeRows];
+            o[4 * k] = __float_as_uint(fmaf(f, y.x, __uint_as_float(o[4 * k])));
+            o[4 * k + 1] = __float_as_uint(fmaf(f, y.y, __uint_as_float(o[4 * k + 1])));
+            o[4 * k + 2] = __float_as_uint(fmaf(f, y.z, __uint_as_float(o[4 * k + 2])));
+            o[4 * k + 3] = __float_as_uint(fmaf(f, y.w, __uint_as_float(o[4 * k + 3])));
+        }
+        tmem_st32(tO + c0, o);
+    }
+    tmem_st_wait();
+}
+
 template <int D, bool F8, Terms TERMS>
 __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, uint32_t smem,
                                         const WaitCtx& wctx)
@@ -1064,11 +1150,13 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
     using C = Cfg<D, F8>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp >> 2, rit = (warp & 3) * 32 + lane;  // group, row
-    const bool second = TERMS == kLanes && (warp & 2);
-    const int row = TERMS == kLanes ? rit & 63 : rit;       // ..., of the segment
+    const bool second = by_rows(TERMS) && (warp & 2);
+    const int row = by_rows(TERMS) ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = lanes + w * 64, tO = lanes + C::kO0;  // (all of TMEM is the block's)
-    const int32_t R = p.G * p.T;
+    const int32_t R = p.G * p.T, chain = chain_mask<F8, TERMS>(p);
+    float4* const apart = reinterpret_cast<float4*>(p.apart) +
+                          (2 * (int64_t)blockIdx.x + w) * (kTreeRows * D / 4) + rit;
     uint32_t gt = 0, met = 0;
     Ring<C::kS> sr, last;  // the tile's S, and the one before's
     int4 info = make_int4(0, 0, 0, 0);
@@ -1092,7 +1180,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 return;
             factor = sh.qf[seg & 1][rit];
             __syncwarp();
-            if (TERMS != kLanes && lane == 0)
+            if (!by_rows(TERMS) && lane == 0)
                 mbar_arrive(&sh.q_empty[seg & 1]);
         }
         float N = kNone, Dd = 0.f, l = 0.f;
@@ -1174,14 +1262,16 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             else
                 l += weights<F8, TERMS>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
                                         second);
-            if (i > 0 && __any_sync(0xffffffffu, rise)) {
+            const bool end_chain = i > 0 && (i & chain) == 0;
+            const bool rises = __any_sync(0xffffffffu, rise);
+            if (i > 0 && (rises || end_chain)) {
                 // (late, since it has to wait for the product before this one)
                 ok = wait(&sh.s_free[last.at], last.phase, wctx, 37);
                 if (!__all_sync(0xffffffffu, ok))
                     return;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < (rises ? D : 0); c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(tO + w * D + c0, o);
                     tmem_ld_wait();
@@ -1190,6 +1280,12 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                     for (int k = 0; k < 32; ++k)
                         o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                     tmem_st32(tO + w * D + c0, o);
+                }
+                if (i > chain)
+                    sh.n[w][rit] *= f;
+                if (end_chain) {
+                    set_apart<D>(tO + w * D, apart, i > kChain ? sh.n[w][rit] : 0.f);
+                    sh.n[w][rit] = 1.f;
                 }
             }
             tmem_st_wait();
@@ -1216,6 +1312,11 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         bool ok = wait(&sh.s_free[last.at], last.phase, wctx, 35);
         if (!__all_sync(0xffffffffu, ok))
             return;
+        if (run.nt - 1 > chain) {
+            tc_fence_after();
+            take_back<D>(tO + w * D, apart, sh.n[w][rit]);
+            tc_fence_before();
+        }
         sh.n[w][rit] = N;
         sh.l[w][rit] = l;
         if (F8)
@@ -1251,13 +1352,13 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         const int64_t orow =  // (of the segment one behind the other)
             ((int64_t)run.b * p.Hq + run.h * p.G) * p.T + run.rg * kTreeRows + row;
         const float2 inv = row_factors<D, F8>(dx, l);
-        // The groups take half of the features each, 16 at a time.  kLanes: second terms come
+        // The groups take half of the features each, 16 at a time.  By rows: second terms come
         // by way of the segment's queries, which are done with.
         const uint32_t pass = smem + (seg & 1) * C::kTileBytes + w * (64 * D * 2) + row * (D * 2);
         auto chunk = [&](int c, int k) {  // 16 bytes k of 16 features c
             return pass + (((4 * c + k) ^ (row & 7)) << 4);
         };
-        if (TERMS == kLanes && !second) {
+        if (by_rows(TERMS) && !second) {
             ok = wait(&sh.seconds, met ^ 1, wctx, 39);
             if (!__all_sync(0xffffffffu, ok))
                 return;
@@ -1275,7 +1376,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 o[k] = fmaf(fa, __uint_as_float(ta[k]), fb * __uint_as_float(tb[k]));
-            if (TERMS == kLanes) {
+            if (by_rows(TERMS)) {
                 if (second) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -1308,7 +1409,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     o[k] = F8 ? o[k] * inv.x * inv.y : o[k] * inv.x;
-            if (!whole || p.o_fp32) {
+            if (!whole || is_fp32<F8, TERMS>(p)) {
                 float4* to = whole ? reinterpret_cast<float4*>((float*)p.o + orow * D + c0)
                                    : pout + (c0 / 4) * kTreeRows;
                 const int step = whole ? 1 : kTreeRows;
@@ -1332,7 +1433,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         }
         tc_fence_before();
         mbar_arrive(&sh.o_empty);
-        if (TERMS == kLanes) {
+        if (by_rows(TERMS)) {
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.q_empty[seg & 1]);
@@ -1393,7 +1494,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.q_full[s], 1);
-            mbar_init(&sh.q_empty[s], F8 || TERMS == kLanes ? 9 : 1);
+            mbar_init(&sh.q_empty[s], F8 || by_rows(TERMS) ? 9 : 1);
         }
         mbar_init(&sh.o_empty, 256);
         mbar_init(&sh.q_first, 8);
@@ -1431,7 +1532,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     } else if (warp == 8) {
         multiply_scores<D, F8>(sh, base, wctx);
     } else if (warp == 10) {
-        multiply_values<D, F8, TERMS>(sh, base, wctx);
+        multiply_values<D, F8, TERMS>(sh, base, chain_mask<F8, TERMS>(p), wctx);
     } else if (warp == 9) {
         produce<D, F8>(p, sh, base, tk, tv, wctx);
         if (*wctx.abort_flag) {
@@ -1574,11 +1675,16 @@ template <int D, bool F8>
 cudaError_t launch_terms(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, int num_sms,
                          cudaStream_t stream)
 {
+    // (see "Rounding" above, and is_fp32)
     if constexpr (F8)
-        if (!p.o_fp32)  // (see "Rounding" above)
+        if (!p.o_fp32)
             return launch<D, F8, kOne>(tk, tv, p, num_sms, stream);
-    return p.G * p.T <= 64 ? launch<D, F8, kLanes>(tk, tv, p, num_sms, stream)
-                           : launch<D, F8, kColumns>(tk, tv, p, num_sms, stream);
+    if (p.G * p.T > 64)
+        return launch<D, F8, kColumns>(tk, tv, p, num_sms, stream);
+    if constexpr (!F8)
+        if (p.o_fp32)
+            return launch<D, F8, kThree>(tk, tv, p, num_sms, stream);
+    return launch<D, F8, kLanes>(tk, tv, p, num_sms, stream);
 }
 
 }  // namespace tree

@@ -905,7 +905,7 @@ def tree_workspace(cache: PagedCache, Hq=None, T=1) -> torch.Tensor:
     whose is paged_workspace): Hq query heads, T tokens a tree at most.  It serves one
     call at a time, and the device's errors are then reported to it."""
     Hq = Hq or cache.Hkv
-    n = max(_tree_desc(cache.B, Hq, cache.Hkv, t, cache.d, 1.0, False)[1] for t in (1, T))
+    n = max(_tree_desc(cache.B, Hq, cache.Hkv, t, cache.d, 1.0, True)[1] for t in (1, T))
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 

@@ -173,6 +173,31 @@ def test_tree_long_and_many(dtype, B, Hkv, G, T, L, page, d):
     check_tree(c, c.cuda(), q[check], sees, fp32=(False,))
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("G,T", [(1, 2), (8, 16)])
+@pytest.mark.parametrize("louder", [False, True])
+def test_tree_fp32_over_many_tiles(dtype, G, T, louder):
+    """More than 40 tiles to a block, whose sums are set apart on the way; scores (or, in 8
+    bits, values) that rise before and after that, by steps which what came before them
+    outlives and does not."""
+    B, Hkv, d, page = 20, 8, 64, 64
+    lens = [5900 - 31 * b for b in range(B)]
+    c = ref.Cache(dtype, 1, Hkv, d, page, -(-5900 // page), [5900], seed=T)
+    if louder:
+        for p in range(c.table.shape[1]):
+            at = int(c.table[0, p])
+            if dtype is E4M3:
+                c.scales["v"][at] *= 2.0 ** (p // 4)
+                c.scales["k"][at] *= 2.0 ** (3 * (p >= 25) + 2 * (p >= 75))
+            else:
+                x = c.cells["k"][at].float() * 2.0 ** (4 * (p >= 25) + 2 * (p >= 75))
+                c.cells["k"][at] = x.to(dtype)
+    c.B, c.table, c.lens = B, c.table.repeat(B, 1), i32(lens, "cpu")   # (the same pages)
+    q = randn(B, Hkv * G, T, d, seed=67)
+    sees = bref.sees_of(bref.random_parents(B, T, seed=68))
+    check_tree(c, c.cuda(), q, sees, fp32=(True,))
+
+
 def test_tree_equals_a_chain():
     """A chain is what decode_paged computes."""
     c = ref.Cache(E4M3, 3, 2, 128, 64, 20, [1200, 77, 640], seed=11)
