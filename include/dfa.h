@@ -2,7 +2,8 @@
  * dfa.h -- C ABI of libdfa: exact causal blockwise attention (forward and
  * recomputation backward), chunk-pair partials, log-sum-exp merge, sequence
  * permutes and ring schedules, rotary positions and decoding over a paged
- * 8-bit key/value cache, for NVIDIA GB300 (sm_103a).
+ * 8-bit key/value cache, with trees of drafted tokens and pages that sequences
+ * share, for NVIDIA GB300 (sm_103a).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -629,7 +630,7 @@ dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cac
  * tokens of a context.
  * Pages that rows go to belong to one sequence (as for dfa_cache_append).  E4M3: such a
  * page's scale becomes the largest of those that its rows came with; cells are shifted
- * to it, and round where they become subnormal.
+ * to it, and round where they become subnormal (scales that are no powers of two: once).
  *   kept [B][A] and kept_lens [B] (device).  1 <= A <= T < 2^30.
  *   ws: 256 bytes (the status word).
  */
