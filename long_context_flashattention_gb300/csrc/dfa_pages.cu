@@ -43,9 +43,10 @@ __device__ __forceinline__ void release(const PoolView& p, int32_t b, int32_t id
 // ---------------------------------------------------------------------------
 // fork: what the sequences will hold, gathered before anything changes; then taken over
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) fork_gather_kernel(const __grid_constant__ ForkParams p)
+// What sequence b will hold: entries i, i + step, ..
+__device__ __forceinline__ void fork_gather(const ForkParams& p, int32_t b, int32_t i, int32_t step)
 {
-    const int32_t b = blockIdx.x, src = p.src[b];
+    const int32_t src = p.src[b];
     if (src == b)
         return;
     int32_t held = 0, len = 0;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(256) fork_gather_kernel(const __grid_constant_
         ok = pages_held(p.p, src, held);
         len = p.p.seq_lens[src];
     }
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
+    if (i == 0) {
         p.held[b] = ok ? held : -1;  // -1: stays as it is
         p.lens[b] = len;
     }
@@ -64,24 +65,25 @@ __global__ void __launch_bounds__(256) fork_gather_kernel(const __grid_constant_
         return;
     const int32_t* from = p.p.table + (int64_t)src * p.p.max_pages;
     int32_t* to = p.rows + (int64_t)b * p.p.max_pages;
-    for (int32_t e = blockIdx.y * blockDim.x + threadIdx.x; e < held; e += gridDim.y * blockDim.x)
+    for (int32_t e = i; e < held; e += step)
         to[e] = from[e];
 }
 
-// (Entries that stay, the shared beginning of beams for one, cost no atomics.)
-__global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__ ForkParams p)
+// (Entries that stay, the shared beginning of beams for one, cost no atomics.)  Returns
+// whether `held` and `len` are b's from now on, which is to be written when all have read
+// what it held.
+__device__ __forceinline__ bool fork_apply(const ForkParams& p, int32_t b, int32_t i, int32_t step)
 {
-    const int32_t b = blockIdx.x;
     if (p.src[b] == b)
-        return;
+        return false;
     const int32_t held = p.held[b];
     int32_t old_held;
     if (held < 0 || !pages_held(p.p, b, old_held))
-        return;
+        return false;
     int32_t* row = p.p.table + (int64_t)b * p.p.max_pages;
     const int32_t* from = p.rows + (int64_t)b * p.p.max_pages;
     const int32_t end = max(held, old_held);
-    for (int32_t e = threadIdx.x; e < end; e += blockDim.x) {
+    for (int32_t e = i; e < end; e += step) {
         const int32_t was = e < old_held ? row[e] : -1, now = e < held ? from[e] : -1;
         if (was == now && e < old_held && e < held)
             continue;
@@ -93,11 +95,41 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__
         if (e < old_held)
             release(p.p, b, was);
     }
-    __syncthreads();  // everyone has read what it held
-    if (threadIdx.x == 0) {
-        p.p.held[b] = held;
-        p.p.seq_lens[b] = p.lens[b];
-    }
+    return true;
+}
+
+__device__ __forceinline__ void fork_end(const ForkParams& p, int32_t b)
+{
+    p.p.held[b] = p.held[b];
+    p.p.seq_lens[b] = p.lens[b];
+}
+
+__global__ void __launch_bounds__(256) fork_gather_kernel(const __grid_constant__ ForkParams p)
+{
+    fork_gather(p, blockIdx.x, blockIdx.y * blockDim.x + threadIdx.x, gridDim.y * blockDim.x);
+}
+
+__global__ void __launch_bounds__(256) fork_apply_kernel(const __grid_constant__ ForkParams p)
+{
+    const bool taken = fork_apply(p, blockIdx.x, threadIdx.x, blockDim.x);
+    __syncthreads();
+    if (taken && threadIdx.x == 0)
+        fork_end(p, blockIdx.x);
+}
+
+// Both for a few sequences, a warp each, in one launch (8 beams: 4.4 -> 3.5 us).
+constexpr int kForkHere = 32;
+
+__global__ void __launch_bounds__(32 * kForkHere) fork_kernel(const __grid_constant__ ForkParams p)
+{
+    const int32_t b = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (b < p.p.B)
+        fork_gather(p, b, lane, 32);
+    __syncthreads();
+    const bool taken = b < p.p.B && fork_apply(p, b, lane, 32);
+    __syncwarp();
+    if (taken && lane == 0)
+        fork_end(p, b);
 }
 
 // ---------------------------------------------------------------------------
@@ -609,6 +641,10 @@ __global__ void __launch_bounds__(kCompactThreads)
 
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream)
 {
+    if (p.p.B <= kForkHere && p.p.max_pages <= 1024) {  // (32 rounds of a warp)
+        fork_kernel<<<1, 32 * kForkHere, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     const unsigned parts = max(1, min(8, p.p.max_pages / 2048));
     fork_gather_kernel<<<dim3(p.p.B, parts), 256, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();

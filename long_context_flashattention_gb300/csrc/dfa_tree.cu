@@ -21,10 +21,9 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(const __grid_constant__ 
 {
     extern __shared__ uint32_t sees[];            // group g: 32 nodes of g + 1 words
     // of a node: the nearest ancestor before its group, as the place of its words and its
-    // group (<< 16), or -1; the ancestors in the group; how many there are in all
+    // group (<< 16), or -1; the ancestors in the group
     __shared__ __align__(16) int32_t from[kTreeMaxTokens];
     __shared__ __align__(16) uint32_t own[kTreeMaxTokens];
-    __shared__ int16_t ancestor[kTreeMaxTokens], depth[kTreeMaxTokens];
     const int32_t T = p.T, W = p.words, b = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t len, n;
@@ -47,16 +46,15 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(const __grid_constant__ 
         }
         // (up: the ancestor here whose parent is not)
         const int32_t f = __shfl_sync(0xffffffffu, parent, up), fg = f >> 5;
-        ancestor[t] = (int16_t)f;
         from[t] = f < 0 ? -1 : (fg + 1) * (16 * fg + (f & 31)) | fg << 16;
         own[t] = bits;
     }
     __syncthreads();
     const int32_t t4 = warp * 4;  // the warp's nodes of a group
     uint32_t* out = p.mask + ((int64_t)b * T + t4) * W + lane;
+    int4 f4 = *reinterpret_cast<const int4*>(from + t4);
+    uint4 o4 = *reinterpret_cast<const uint4*>(own + t4);
     for (int32_t g = 0; g < groups; ++g, out += 32 * W) {
-        const int4 f4 = *reinterpret_cast<const int4*>(from + 32 * g + t4);
-        const uint4 o4 = *reinterpret_cast<const uint4*>(own + 32 * g + t4);
         const int32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
         const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
         uint32_t word[4];
@@ -72,19 +70,22 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(const __grid_constant__ 
             for (int k = 0; k < 4; ++k, to += g + 1)
                 *to = word[k];
         }
-        if (lane < W)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (32 * g + t4 + k < n)
-                    out[k * W] = word[k];
-        if (warp == 0) {
-            const int32_t t = 32 * g + lane, a = ancestor[t];
-            const int32_t d = (a < 0 ? -1 : depth[a]) + __popc(own[t]);
-            depth[t] = (int16_t)d;
-            if (t < n)
-                p.positions[(int64_t)b * T + t] = len - n + d;
+        const int32_t t = 32 * g + t4;
+        if (g + 1 < groups) {
+            f4 = *reinterpret_cast<const int4*>(from + t + 32);
+            o4 = *reinterpret_cast<const uint4*>(own + t + 32);
         }
-        __syncthreads();
+        __syncthreads();  // (then the next group; what is left of this one beside it)
+        int32_t depth = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (lane < W && t + k < n)
+                out[k * W] = word[k];
+            const int32_t bits = __reduce_add_sync(0xffffffffu, __popc(word[k]));
+            depth = lane == k ? bits : depth;
+        }
+        if (lane < 4 && t + lane < n)
+            p.positions[(int64_t)b * T + t + lane] = len - n + depth - 1;
     }
 }
 
