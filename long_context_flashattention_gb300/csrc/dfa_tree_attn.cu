@@ -57,11 +57,14 @@ constexpr int kRuns = 2;                  // segments that are announced ahead
 // N rises when a term exceeds 2^kGrow: no sum comes near fp32's end, and for bf16 weights,
 // which have that range, a rise costs a pass over O.
 constexpr float kGrow = 60.f;
-// fp16 weights: D is set kHead below the largest exponent, and set anew, with a pass over
+// fp16 weights: D is set `head` below the largest exponent, and set anew, with a pass over
 // O, when a weight exceeds 2^kTop.  Between the two is room for larger weights to come;
-// kHead is what small ones behind a large one have left: half a step of fp16's subnormals
-// is 2^-33 of the largest weight, 2^-16 for 128K of them together.
-constexpr float kTop = 15.f, kHead = 8.f;
+// `head` is what small ones behind a large one have left: half a step of fp16's subnormals
+// is 2^-33 of the largest weight, 2^-16 for 128K of them together, with 8 (fp32
+// outputs), 2^-29 and 2^-12 at worst with 4 (bf16 outputs, which are rounded to 2^-9; trees
+// of 60 over 16K 100 us in place of 103, 15 of 40 tiles having made a pass over O before):
+// head() below.
+constexpr float kTop = 15.f;
 // A product adds to O by cutting off what fp32 does not hold, which makes O smaller each
 // time, in the end by 2^-24 of it for every other product.  For fp32 outputs a sum of so many
 // tiles is set apart (in the workspace; the next begins at 0) and added at the segment's end:
@@ -92,9 +95,12 @@ struct Piece {
 // How weights are held: in one term; in two, side by side in the operand's columns; in two
 // in its rows, where at most 64 of the 128 rows have queries: rows r and r + 64 are the
 // same query's, and the second row's weights are what the first's leave; in three: two in
-// the rows, the third in the first's columns.
-enum Terms { kOne, kColumns, kLanes, kThree };
-constexpr bool by_rows(Terms t) { return t == kLanes || t == kThree; }
+// the rows, the third in the first's columns.  kSplit: one term, but rows r and r + 64 are
+// the same query's, each with half of the keys (and zeros, N, D and O of its own).
+enum Terms { kOne, kColumns, kLanes, kThree, kSplit };
+constexpr bool by_rows(Terms t) { return t == kLanes || t == kThree || t == kSplit; }
+constexpr float head(Terms t) { return t == kOne || t == kSplit ? 4.f : 8.f; }
+constexpr int chunks(Terms t) { return t == kSplit ? 2 : 4; }  // of 16 keys, a row's of a tile
 constexpr bool by_columns(Terms t) { return t == kColumns || t == kThree; }
 
 template <int D, bool F8>
@@ -400,7 +406,7 @@ __device__ __forceinline__ bool next_run(SH& sh, uint32_t seg, Piece& run, const
 template <bool F8, Terms TERMS>
 __device__ __forceinline__ bool is_fp32(const TreeParams& p)
 {
-    if (TERMS == kOne || (TERMS == kLanes && !F8))
+    if (TERMS == kOne || TERMS == kSplit || (TERMS == kLanes && !F8))
         return false;
     return F8 || TERMS == kThree || p.o_fp32;
 }
@@ -975,7 +981,7 @@ __device__ __forceinline__ void hide16(uint32_t (&r)[16], uint32_t seen)
 // the keys' scores were).  kLanes: `second` rows have second terms alone; kThree: they and
 // zeros, the others third terms beside the first.
 template <bool F8, Terms TERMS>
-__device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&y)[16], bool second)
+__device__ __forceinline__ void store_weights(uint32_t tP, int k, const float (&y)[16], bool second)
 {
     uint32_t hi[16];
 #pragma unroll
@@ -1012,21 +1018,21 @@ __device__ __forceinline__ void store_weights(uint32_t tS, int k, const float (&
         }
     }
     if (by_columns(TERMS))
-        tmem_st16(tS + 16 * k, hi);
+        tmem_st16(tP + 16 * k, hi);
     else
-        tmem_st8(tS + 8 * k, hi);
+        tmem_st8(tP + 8 * k, hi);
 }
 
 // Weights of a row's 64 keys from their scores r.  Returns the sum of the terms.
 template <bool F8, Terms TERMS, typename INFO>
-__device__ __forceinline__ float weights(const uint32_t (&r)[4][16], uint32_t tS, const INFO& ti,
-                                         int k0, int page_log2, float factor, float N, float Dd,
-                                         bool second)
+__device__ __forceinline__ float weights(const uint32_t (&r)[chunks(TERMS)][16], uint32_t tP,
+                                         const INFO& ti, int k0, int page_log2, float factor,
+                                         float N, float Dd, bool second)
 {
     const uint64_t off = f2pack(-N, -N);
     uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < chunks(TERMS); ++k) {
         float2 sc = make_float2(1.f, 0.f);
         if (F8)
             sc = ti.scale[(k0 + 16 * k) >> page_log2];
@@ -1044,7 +1050,7 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[4][16], uint32_t tS
                 e = f2mul(e, up2);
             f2unpack(e, y[j], y[j + 1]);
         }
-        store_weights<F8, TERMS>(tS, k, y, second);
+        store_weights<F8, TERMS>(tP, k, y, second);
     }
     float s0, s1, s2, s3;
     f2unpack(sum[0], s0, s1);
@@ -1055,15 +1061,15 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[4][16], uint32_t tS
 // The same where scores are far from zero, or the tile's value scales from one another:
 // scores are rounded before N is taken off, and weights are powers of their own.
 template <bool F8, Terms TERMS, typename INFO>
-__device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, int page_log2,
-                                          uint32_t vis0, uint32_t vis1, float factor, float N,
-                                          float Dd, bool second)
+__device__ __noinline__ float weights_far(uint32_t tS, uint32_t tP, const INFO& ti, int k0,
+                                          int page_log2, uint32_t vis0, uint32_t vis1,
+                                          float factor, float N, float Dd, bool second)
 {
     // (differences in place of all scores first: second terms take the place of some)
     float sum = 0.f;
     uint32_t r[16];
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < chunks(TERMS); ++k) {
         tmem_ld16(tS + 16 * k, r);
         tmem_ld_wait();
         tmem_reg_fence16(r);
@@ -1080,7 +1086,7 @@ __device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, i
     }
     tmem_st_wait();
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < chunks(TERMS); ++k) {
         tmem_ld16(tS + 16 * k, r);
         tmem_ld_wait();
         tmem_reg_fence16(r);
@@ -1089,7 +1095,7 @@ __device__ __noinline__ float weights_far(uint32_t tS, const INFO& ti, int k0, i
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             y[j] = ex2(__uint_as_float(r[j]) + lu);
-        store_weights<F8, TERMS>(tS, k, y, second);
+        store_weights<F8, TERMS>(tP, k, y, second);
     }
     return sum;
 }
@@ -1149,8 +1155,11 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
 {
     using C = Cfg<D, F8>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kChunks = chunks(TERMS);
     const int w = warp >> 2, rit = (warp & 3) * 32 + lane;  // group, row
     const bool second = by_rows(TERMS) && (warp & 2);
+    const int half = TERMS == kSplit && second;             // the second of its group's keys
+    const int k0 = w * 64 + half * 32;                      // its first key of a tile
     const int row = by_rows(TERMS) ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = lanes + w * 64, tO = lanes + C::kO0;  // (all of TMEM is the block's)
@@ -1208,31 +1217,36 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             if (!__all_sync(0xffffffffu, ok))
                 return;
             tc_fence_after();
-            float top[4];  // of 16 keys each
-            uint32_t r[4][16];
+            float top[kChunks];  // of 16 keys each
+            uint32_t r[kChunks][16];
+            const uint32_t tR = tS + buf + half * 32, tP = tS + buf + half * 16;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tmem_ld16(tS + buf + 16 * k, r[k]);
+            for (int k = 0; k < kChunks; ++k)
+                tmem_ld16(tR + 16 * k, r[k]);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kChunks; ++k)
                 tmem_reg_fence16(r[k]);
             if (__builtin_expect(masked, 0)) {
+                if (half)
+                    vis[0] = vis[1];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < kChunks; ++k)
                     hide16(r[k], vis[k >> 1] >> (16 * (k & 1)));
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kChunks; ++k) {
                 float m = fmaxf(__uint_as_float(r[k][0]), __uint_as_float(r[k][1]));
 #pragma unroll
                 for (int j = 2; j < 16; j += 2)
                     m = fmax3(m, __uint_as_float(r[k][j]), __uint_as_float(r[k][j + 1]));
                 // (rounded: N may become one of them, and is taken off them)
-                top[k] = __fmul_rn(
-                    m, F8 ? factor * ti.scale[(w * 64 + 16 * k) >> p.c.page_log2].x : factor);
+                top[k] = __fmul_rn(m, F8 ? factor * ti.scale[(k0 + 16 * k) >> p.c.page_log2].x
+                                         : factor);
             }
-            const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+            const float mx = kChunks == 2 ? fmaxf(top[0], top[1])
+                                          : fmaxf(fmax3(top[0], top[1], top[kChunks - 2]),
+                                                  top[kChunks - 1]);
             // N up to the largest score, D up to the largest exponent, O with them
             float f = 1.f;
             bool rise = valid && mx - N > kGrow;
@@ -1245,23 +1259,26 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             if (F8) {
                 float me = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    me = fmaxf(me, (top[k] - N) + ti.scale[(w * 64 + 16 * k) >> p.c.page_log2].y);
+                for (int k = 0; k < kChunks; ++k)
+                    me = fmaxf(me, (top[k] - N) + ti.scale[(k0 + 16 * k) >> p.c.page_log2].y);
                 rise = valid && me - Dd > kTop;
                 f = 1.f;
                 if (rise) {
-                    f = ex2(Dd - (me - kHead));
-                    Dd = me - kHead;
+                    f = ex2(Dd - (me - head(TERMS)));
+                    Dd = me - head(TERMS);
                 }
             }
             const bool far = __any_sync(0xffffffffu, valid && fabsf(N) >= kFar && N != kNone) ||
                              (F8 && (flags & kWideTile));
             if (__builtin_expect(far, 0))
-                l += weights_far<F8, TERMS>(tS + buf, ti, w * 64, p.c.page_log2, vis[0], vis[1],
-                                            factor, N, Dd, second);
+                l += weights_far<F8, TERMS>(tR, tP, ti, k0, p.c.page_log2, vis[0], vis[1], factor,
+                                            N, Dd, second);
             else
-                l += weights<F8, TERMS>(r, tS + buf, ti, w * 64, p.c.page_log2, factor, N, Dd,
-                                        second);
+                l += weights<F8, TERMS>(r, tP, ti, k0, p.c.page_log2, factor, N, Dd, second);
+            if (TERMS == kSplit) {  // the other half's keys (whose scores nobody reads any more)
+                const uint32_t zero[16] = {};
+                tmem_st16(tS + buf + (1 - half) * 16, zero);
+            }
             const bool end_chain = i > 0 && (i & chain) == 0;
             const bool rises = __any_sync(0xffffffffu, rise);
             if (i > 0 && (rises || end_chain)) {
@@ -1335,13 +1352,19 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 sh.any_bad[(seg + 2) % 3] = 0;
         }
         const float na = sh.n[0][rit], nb = sh.n[1][rit];
-        const float nx = fmaxf(na, nb);
+        const float nc = TERMS == kSplit ? sh.n[0][rit ^ 64] : na;
+        const float nd = TERMS == kSplit ? sh.n[1][rit ^ 64] : nb;
+        const float nx = TERMS == kSplit ? fmaxf(fmaxf(na, nb), fmaxf(nc, nd)) : fmaxf(na, nb);
         float da = na - nx, db = nb - nx, dx = 0.f;
         l = sh.l[0][rit] * ex2(da) + sh.l[1][rit] * ex2(db);
+        if (TERMS == kSplit)
+            l += sh.l[0][rit ^ 64] * ex2(nc - nx) + sh.l[1][rit ^ 64] * ex2(nd - nx);
         if (F8) {
             da += sh.d[0][rit];
             db += sh.d[1][rit];
             dx = fmaxf(da, db);
+            if (TERMS == kSplit)
+                dx = fmaxf(dx, fmaxf((nc - nx) + sh.d[0][rit ^ 64], (nd - nx) + sh.d[1][rit ^ 64]));
         }
         const float fa = ex2(da - dx), fb = ex2(db - dx);
         const bool whole = run.nt == run.tiles;
@@ -1678,7 +1701,8 @@ cudaError_t launch_terms(const CUtensorMap& tk, const CUtensorMap& tv, TreeParam
     // (see "Rounding" above, and is_fp32)
     if constexpr (F8)
         if (!p.o_fp32)
-            return launch<D, F8, kOne>(tk, tv, p, num_sms, stream);
+            return p.G * p.T > 64 ? launch<D, F8, kOne>(tk, tv, p, num_sms, stream)
+                                  : launch<D, F8, kSplit>(tk, tv, p, num_sms, stream);
     if (p.G * p.T > 64)
         return launch<D, F8, kColumns>(tk, tv, p, num_sms, stream);
     if constexpr (!F8)
