@@ -139,7 +139,7 @@ struct Shared {
     uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
     uint64_t raw_full[F8 ? C::kRaw : 1], raw_empty[F8 ? C::kRaw : 1];
     uint64_t s_full[C::kS], s_free[C::kS], p_full[2][C::kS], o_empty, q_full[2], q_empty[2], q_first;
-    uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, seconds;
+    uint64_t run_full[kRuns], run_empty[kRuns], info_full[kRing], meet, handed;
     Piece run[kRuns];
     TileInfo<F8> info[kRing];
     long long w0, w1, base, each, rest;
@@ -1375,19 +1375,17 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         const int64_t orow =  // (of the segment one behind the other)
             ((int64_t)run.b * p.Hq + run.h * p.G) * p.T + run.rg * kTreeRows + row;
         const float2 inv = row_factors<D, F8>(dx, l);
-        // The groups take half of the features each, 16 at a time.  By rows: second terms come
-        // by way of the segment's queries, which are done with.
+        // The groups take half of the features each, 16 at a time.  By rows: the two rows of a
+        // query hand each other half of those, by way of the segment's queries, which are done
+        // with (one row handing over all: 256 short sequences 146 us in place of 139, in 8 bits
+        // 195 in place of 182).
         const uint32_t pass = smem + (seg & 1) * C::kTileBytes + w * (64 * D * 2) + row * (D * 2);
         auto chunk = [&](int c, int k) {  // 16 bytes k of 16 features c
             return pass + (((4 * c + k) ^ (row & 7)) << 4);
         };
-        if (by_rows(TERMS) && !second) {
-            ok = wait(&sh.seconds, met ^ 1, wctx, 39);
-            if (!__all_sync(0xffffffffu, ok))
-                return;
-        }
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int s = 0; s < D / 32; ++s) {
+            const int c = by_rows(TERMS) && !second ? s ^ (D / 64) : s;
             const int c0 = w * (D / 2) + 16 * c;
             float o[16];
             uint32_t ta[16], tb[16];
@@ -1400,13 +1398,21 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
             for (int k = 0; k < 16; ++k)
                 o[k] = fmaf(fa, __uint_as_float(ta[k]), fb * __uint_as_float(tb[k]));
             if (by_rows(TERMS)) {
-                if (second) {
+                if (s < D / 64) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         st_shared_v4(chunk(c, k), __float_as_uint(o[4 * k]),
                                      __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
                                      __float_as_uint(o[4 * k + 3]));
                     continue;
+                }
+                if (s == D / 64) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.handed);
+                    ok = wait(&sh.handed, met ^ 1, wctx, 39);
+                    if (!__all_sync(0xffffffffu, ok))
+                        return;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -1448,11 +1454,6 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                                        pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
                                        pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
             }
-        }
-        if (second) {
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.seconds);
         }
         tc_fence_before();
         mbar_arrive(&sh.o_empty);
@@ -1528,7 +1529,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         for (int s = 0; s < kRing; ++s)
             mbar_init(&sh.info_full[s], 1);
         mbar_init(&sh.meet, 8);
-        mbar_init(&sh.seconds, 4);
+        mbar_init(&sh.handed, 8);
         fence_barrier_init();
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
