@@ -85,6 +85,10 @@ def test_plan_reports_a_parent_that_cannot_be():
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
+def rows_max(c):
+    return max(float(bref.rows(c, "v", b, int(c.lens[b])).abs().max()) for b in range(c.B))
+
+
 def check_tree(c, dev, q, sees, q_lens=None, scale=None, fp32=(False, True), ws=None, **kw):
     B, Hq, T, d = q.shape
     if ws is None:
@@ -271,6 +275,60 @@ def test_tree_non_finite_nodes_stay_where_they_are_seen(dtype, G, bad):
 
 
 @pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("G", [1, 4, 16])
+def test_tree_nan_nodes_with_bf16_outputs(dtype, G):
+    T, d, L = 12, 128, 300
+    sees = bref.sees_of(bref.random_parents(2, T, seed=70, roots=0.3))
+    c = ref.Cache(dtype, 2, 1, d, 32, -(-L // 32), [L, T], seed=71)
+    q = randn(2, G, T, d, seed=72)
+    w = 2.0 ** -11 if dtype is E4M3 else 2.0 ** -16
+    O, LSE, tO, tL = bref.attention(c, q, sees, weight=w)
+    node = 3
+    for b, n in ((0, L), (1, T)):
+        j = n - T + node
+        x = c.cells["v"].float()
+        x[int(c.table[b, j // 32]), 0, j % 32, 100] = float("nan")
+        c.cells["v"] = x.to(dtype)
+    o, lse = dfa.decode_tree(c.cuda(), q.cuda(), bref.pack(sees).cuda())
+    ref.check(lse, LSE, tL, torch.float32)
+    for b in range(2):
+        for t in range(T):
+            hit = bool(sees[b, t, node])
+            f = torch.ones(d, dtype=torch.bool)
+            f[100] = not hit
+            # (the node's own weight is then fp32's, the others' as before: no more than w)
+            ref.check(o[b, :, t][:, f], O[b, :, t][:, f], tO[b, :, t][:, f], BF16, (b, t))
+            assert not hit or o[b, :, t, 100].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("G", [2, 30])
+@pytest.mark.parametrize("off", [2.0 ** 13, -2.0 ** 20])
+def test_tree_far_scores_with_bf16_outputs(dtype, G, off):
+    """As below, at offsets on either side of where scores are rounded first."""
+    T, d = 3, 64
+    c = ref.Cache(dtype, 1, 1, d, 64, 4, [200], seed=73)
+    x = c.cells["k"].float()
+    x[..., 1:] = torch.where(x[..., 1:] > 0, 0.25, -0.25) * (x[..., 1:] == x[..., 1:])
+    x[..., 0] = 1.0
+    c.cells["k"] = x.to(dtype)
+    if c.scales:
+        c.scales["k"][:] = 1.0
+    q = torch.zeros(1, G, T, d)
+    q[..., 1:9] = 0.5
+    sees = bref.sees_of(bref.random_parents(1, T, seed=74))
+    base = bref.attention(c, q.to(BF16), sees, scale=1.0)
+    q[..., 0] = off
+    o, lse = dfa.decode_tree(c.cuda(), q.to(BF16).cuda(), bref.pack(sees).cuda(), scale=1.0)
+    step = 3 * 2.0 ** -23 * abs(off)
+    vmax = float(rows_max(c))
+    # two steps of the offset's size as below; fp16 weights, the output's rounding
+    tol = vmax * (math.expm1(2 * step) + 2.0 ** -10 + 2.0 ** -8)
+    assert (o.cpu().double() - base[0]).abs().max() <= tol
+    assert (lse.cpu().double() - (base[1] + off)).abs().max() <= 2 * step + 2.0 ** -18
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
 @pytest.mark.parametrize("far", [1e4, -1e4, 3e7, -3e7])
 def test_tree_scores_far_from_zero(dtype, far):
     """A common offset of all scores, exact in fp32, changes nothing but the LSE: it is
@@ -303,10 +361,6 @@ def test_tree_scores_far_from_zero(dtype, far):
     assert (o.cpu().double() - base[0]).abs().max() <= vmax * spread + 2.0 ** -15 * vmax
     assert (lse.cpu().double() - (base[1] + math.copysign(off, far))).abs().max() <= (
         2 * step + 2.0 ** -18)
-
-
-def rows_max(c):
-    return max(float(bref.rows(c, "v", b, int(c.lens[b])).abs().max()) for b in range(c.B))
 
 
 @pytest.mark.parametrize("dtype", [E4M3, BF16])
@@ -351,6 +405,36 @@ def test_tree_extreme_value_scales(loud, T):
     q = randn(2, 8, T, d, seed=23)
     sees = bref.sees_of(bref.random_parents(2, T, seed=24))
     check_tree(c, c.cuda(), q, sees)
+
+
+@pytest.mark.parametrize("G", [2, 40])
+@pytest.mark.parametrize("below", [8.0, 14.0, 16.0])
+def test_tree_many_small_weights_behind_a_large_one(G, below):
+    """One key e^below times the others' weights, in front of them, whose values it does not
+    share: what small weights add up to is there."""
+    T, d, L = 2, 64, 6000
+    c = ref.Cache(E4M3, 1, 1, d, 64, -(-L // 64), [L], seed=75)
+    for name in "kv":
+        c.scales[name][:] = 1.0
+    k, v = torch.zeros_like(c.cells["k"].float()), torch.ones_like(c.cells["v"].float())
+    k[int(c.table[0, 0]), 0, 5, 0] = below
+    v[int(c.table[0, 0]), 0, 5] = -1.0
+    c.cells["k"], c.cells["v"] = k.to(E4M3), v.to(E4M3)
+    q = torch.zeros(1, G, T, d)
+    q[..., 0] = 1.0
+    sees = torch.ones(1, T, T, dtype=torch.bool)
+    big, rest = math.exp(below), L - 1.0
+    want = (rest - big) / (rest + big)
+    for fp32 in (False, True):
+        o, lse = dfa.decode_tree(c.cuda(), q.to(BF16).cuda(), bref.pack(sees).cuda(), scale=1.0,
+                                 out_fp32=fp32)
+        # weights to half a step of fp16's 11 bits, or of its subnormals where the largest is
+        # 2^4 (with two terms 2^8) or more; sums cut off at 2^-23 a tile and term
+        sub = rest * 2.0 ** -25 / (2.0 ** 8 if fp32 else 2.0 ** 4) * big / (rest + big)
+        tol = (2.0 ** -22 if fp32 else 2.0 ** -11) + sub + 4 * 47 * 2.0 ** -23
+        tol += 0 if fp32 else 2.0 ** -8 * abs(want)
+        assert (o.cpu().double() - want).abs().max() <= tol, fp32
+        assert (lse.cpu().double() - math.log(rest + big)).abs().max() <= 1e-5
 
 
 def test_tree_zero_pages_and_scales_of_the_callers():
