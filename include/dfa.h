@@ -546,7 +546,8 @@ dfa_status dfa_cache_gather(const dfa_paged_cache* cache, int64_t pos0, int64_t 
  *   q [B,Hq,T,d] bf16 (strided); o [B,Hq,T,d] bf16 or fp32 (o_fp32) and
  *   lse [B,Hq,T] fp32, contiguous, apart from each other and from q (o in q's
  *   memory range is refused).  (Hq/Hkv) * T <= 1024.
- *   (From about 200 rows a head on, dfa_cache_gather and dfa_chunk_fwd are faster.)
+ *   (From about 200 rows a head on, dfa_cache_gather and dfa_chunk_fwd are faster; from
+ *   about 16 rows on dfa_decode_tree with the mask of a chain.)
  *   ws: dfa_decode_paged_workspace_size(desc, T) bytes (partials), whatever
  *   the lengths and the table.
  */
@@ -613,7 +614,8 @@ dfa_status dfa_tree_plan(const dfa_paged_cache* cache, int32_t T, const int32_t*
  *   q [B,Hq,T,d] bf16 (strided); mask [B][T][ceil(T/32)]; o [B,Hq,T,d] bf16 or fp32
  *   (o_fp32) and lse [B,Hq,T] fp32, contiguous; o and lse apart from each other and
  *   from q and mask.  (Hq/Hkv) * T <= 1024.
- *   ws: dfa_decode_tree_workspace_size(desc, T) bytes, whatever the lengths and the table.
+ *   ws: dfa_decode_tree_workspace_size(desc, T) bytes (more with o_fp32), whatever the
+ *   lengths and the table.
  */
 size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T);
 dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
