@@ -975,6 +975,15 @@ __device__ __noinline__ void mend_values(uint32_t vt, int32_t row, int32_t node,
     }
 }
 
+// A row's factor times a page's key scale.  A row of zeros over a page of zeros would have 0
+// here (2^-217), and hidden scores, which are -inf before they are scaled, would become
+// NaN: fp32's smallest normal number does as well, since a row times a key is below 2^32.
+__device__ __forceinline__ float score_factor(float factor, float scale)
+{
+    const float f = factor * scale;
+    return f < FLT_MIN ? FLT_MIN : f;
+}
+
 __device__ __forceinline__ void hide16(uint32_t (&r)[16], uint32_t seen)
 {
 #pragma unroll
@@ -1042,7 +1051,7 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[chunks(TERMS)][16],
         float2 sc = make_float2(1.f, 0.f);
         if (F8)
             sc = ti.scale[(k0 + 16 * k) >> page_log2];
-        const float fk = F8 ? factor * sc.x : factor, up = F8 ? ex2(sc.y - Dd) : 1.f;
+        const float fk = F8 ? score_factor(factor, sc.x) : factor, up = F8 ? ex2(sc.y - Dd) : 1.f;
         const uint64_t f2 = f2pack(fk, fk), up2 = f2pack(up, up);
         float y[16];
 #pragma unroll
@@ -1080,7 +1089,8 @@ __device__ __noinline__ float weights_far(uint32_t tS, uint32_t tP, const INFO& 
         tmem_ld_wait();
         tmem_reg_fence16(r);
         hide16(r, (k < 2 ? vis0 : vis1) >> (16 * (k & 1)));
-        const float fk = F8 ? factor * ti.scale[(k0 + 16 * k) >> page_log2].x : factor;
+        const float fk =
+            F8 ? score_factor(factor, ti.scale[(k0 + 16 * k) >> page_log2].x) : factor;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             // (a packed product and sum would be joined to one operation)
@@ -1247,8 +1257,9 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 for (int j = 2; j < 16; j += 2)
                     m = fmax3(m, __uint_as_float(r[k][j]), __uint_as_float(r[k][j + 1]));
                 // (rounded: N may become one of them, and is taken off them)
-                top[k] = __fmul_rn(m, F8 ? factor * ti.scale[(k0 + 16 * k) >> p.c.page_log2].x
-                                         : factor);
+                top[k] = __fmul_rn(
+                    m, F8 ? score_factor(factor, ti.scale[(k0 + 16 * k) >> p.c.page_log2].x)
+                          : factor);
             }
             const float mx = kChunks == 2 ? fmaxf(top[0], top[1])
                                           : fmaxf(fmax3(top[0], top[1], top[kChunks - 2]),
