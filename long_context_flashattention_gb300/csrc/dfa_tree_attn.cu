@@ -10,8 +10,8 @@
 // (0 for bf16 cells), so that weights fit their type whatever the scales are.  Scores far
 // from zero are rounded to fp32 before N is taken off them, as N was when it was one of
 // them: the difference is exact however large both are.  Weights are the sum's terms times
-// 2^(log2 u_j - D), where every u_j of a tile is in [2^-40, 2^40], and else powers of their
-// own.
+// 2^(log2 u_j - D), where every u_j of a tile is in [2^-40, 2^40] and D is not far below
+// that, and else powers of their own.
 //
 // What a node sees: every row before the tree, and of the tree's rows those whose bits
 // its mask has.  Only tiles that reach into the tree or over the sequence's end look at
@@ -81,8 +81,10 @@ constexpr float kNone = -FLT_MAX;         // running maximum before the first ke
 constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
                                           // taken off them (else both in one operation: N,
                                           // rounded, is then off by 2^-4 at most)
-constexpr float kNear = 40.f;             // terms times 2^(log2 u_j - D) are weights while
-                                          // |log2 u_j| is at most this
+// Terms times 2^(log2 u_j - D) are weights while |log2 u_j| is at most kNear and D at least
+// kLow (which tiny values before this tile leave behind): the factor is then at most 2^100, so
+// that it is finite, and a term that vanishes (below 2^-126) has no weight that fp16 holds.
+constexpr float kNear = 40.f, kLow = -60.f;
 constexpr float kLn2 = 0.69314718055994531f;
 // Where no sequence can be longer than so many tiles, segments are not cut and there is
 // nothing to merge.
@@ -1073,8 +1075,8 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[chunks(TERMS)][16],
     return (s0 + s1) + (s2 + s3);
 }
 
-// The same where scores are far from zero, or the tile's value scales from one another:
-// scores are rounded before N is taken off, and weights are powers of their own.
+// The same where scores are far from zero, or the tile's value scales from one another or
+// from D: scores are rounded before N is taken off, and weights are powers of their own.
 template <bool F8, Terms TERMS, typename INFO>
 __device__ __noinline__ float weights_far(uint32_t tS, uint32_t tP, const INFO& ti, int k0,
                                           int page_log2, uint32_t vis0, uint32_t vis1,
@@ -1285,8 +1287,9 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                     Dd = me - head(TERMS);
                 }
             }
-            const bool far = __any_sync(0xffffffffu, valid && fabsf(N) >= kFar && N != kNone) ||
-                             (F8 && (flags & kWideTile));
+            const bool away = (fabsf(N) >= kFar && N != kNone) || (F8 && Dd < kLow);
+            const bool far =
+                __any_sync(0xffffffffu, valid && away) || (F8 && (flags & kWideTile));
             if (__builtin_expect(far, 0))
                 l += weights_far<F8, TERMS>(tR, tP, ti, k0, p.c.page_log2, vis[0], vis[1], factor,
                                             N, Dd, second);
