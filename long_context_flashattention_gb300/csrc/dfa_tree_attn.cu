@@ -60,9 +60,10 @@ namespace tree {
 constexpr int kTile = kTreeTile;
 constexpr int kRing = 8;                  // tiles whose scales are kept
 constexpr int kRuns = 2;                  // segments that are announced ahead
-// N rises when a term exceeds 2^kGrow: no sum comes near fp32's end, and for bf16 weights,
-// which have that range, a rise costs a pass over O.
-constexpr float kGrow = 60.f;
+// N rises when a term exceeds 2^grow.  For bf16 weights, which are the terms and which values
+// up to 2^120 over the number of rows are multiplied by, that costs a pass over O; 8-bit
+// cells have D for their weights, and terms as large as that come nowhere near fp32's end.
+constexpr float grow(bool f8) { return f8 ? 60.f : 8.f; }
 // fp16 weights: D is set `head` below the largest exponent, and set anew, with a pass over
 // O, when a weight exceeds 2^kTop.  Between the two is room for larger weights to come;
 // `head` is what small ones behind a large one have left: half a step of fp16's subnormals
@@ -1268,7 +1269,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                                                   top[kChunks - 1]);
             // N up to the largest score, D up to the largest exponent, O with them
             float f = 1.f;
-            bool rise = valid && mx - N > kGrow;
+            bool rise = valid && mx - N > grow(F8);
             if (rise) {
                 f = ex2(N - mx);
                 l *= f;
