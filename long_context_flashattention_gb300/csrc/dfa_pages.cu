@@ -34,10 +34,14 @@ __device__ __forceinline__ bool pages_held(const PoolView& p, int32_t b, int32_t
     return false;
 }
 
+// (A page without holders keeps its count: at -1 it would not be free, and with its next
+// holder it would.)
 __device__ __forceinline__ void release(const PoolView& p, int32_t b, int32_t id)
 {
-    if (pool_page(p, b, id) && atomicSub(p.refs + id, 1) <= 0)
+    if (pool_page(p, b, id) && atomicSub(p.refs + id, 1) <= 0) {
+        atomicAdd(p.refs + id, 1);
         cache_fault(p.status, kSiteRefs, b);
+    }
 }
 
 // ---------------------------------------------------------------------------
