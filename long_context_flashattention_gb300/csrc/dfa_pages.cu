@@ -420,11 +420,11 @@ __global__ void __launch_bounds__(256) trim_kernel(const __grid_constant__ PoolV
     int32_t held;
     if (!pages_held(p, b, held))
         return;
-    if (len < 0) {
+    if (len < 0 || len > (int64_t)p.max_pages << p.page_log2) {
         cache_fault(p.status, kSiteSeqLen, b);
         return;
     }
-    const int32_t need = (int32_t)(((int64_t)len + (1 << p.page_log2) - 1) >> p.page_log2);
+    const int32_t need = (len + (1 << p.page_log2) - 1) >> p.page_log2;
     for (int32_t e = need + lane; e < held; e += 32)
         release(p, b, p.table[(int64_t)b * p.max_pages + e]);
     __syncwarp();

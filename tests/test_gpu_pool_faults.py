@@ -70,3 +70,16 @@ def test_releases_of_one_page_by_many_stop_at_nothing():
     dfa.pages_trim(pool)
     reported(pool)
     assert int(pool.refs.abs().sum()) == 0 and int(pool.held.sum()) == 0
+
+
+@pytest.mark.parametrize("n", [65, 66, 2 ** 31 - 1, -1, -2 ** 31])
+def test_trim_reports_a_length(n):
+    pool, model = fresh()
+    before = [x.clone() for x in (pool.block_table, pool.held, pool.refs)]
+    pool.seq_lens[1] = n
+    dfa.pages_trim(pool)
+    reported(pool)
+    assert all(torch.equal(a, b) for a, b in zip(before, (pool.block_table, pool.held, pool.refs)))
+    pool.seq_lens[1] = 64                       # all that a sequence can have: no fault
+    dfa.pages_trim(pool)
+    dfa.stream_status(pool.status)
