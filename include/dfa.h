@@ -672,7 +672,8 @@ size_t dfa_pages_workspace_size(const dfa_page_pool* pool);
  * its pages, which both then hold, and its length.  src[b] = b: stays; -1: becomes empty.
  * (Beams that go on from others, a prompt's samples, sequences that end.)  Entries of the
  * table behind a sequence's pages are left as they were.
- *   src [B] (device); another number is reported and its sequence stays.
+ *   src [B] (device); another number, or that of a sequence whose pages or length cannot
+ *   be, is reported and its sequence stays.
  *   ws: dfa_pages_workspace_size(pool) bytes.
  */
 dfa_status dfa_pages_fork(const dfa_page_pool* pool, const int32_t* src, void* ws,

@@ -60,6 +60,10 @@ __device__ __forceinline__ void fork_gather(const ForkParams& p, int32_t b, int3
     else if (src >= 0) {
         ok = pages_held(p.p, src, held);
         len = p.p.seq_lens[src];
+        if (len < 0 || len > (int64_t)p.p.max_pages << p.p.page_log2) {
+            cache_fault(p.p.status, kSiteSeqLen, src);
+            ok = false;
+        }
     }
     if (i == 0) {
         p.held[b] = ok ? held : -1;  // -1: stays as it is

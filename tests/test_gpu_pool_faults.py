@@ -83,3 +83,24 @@ def test_trim_reports_a_length(n):
     pool.seq_lens[1] = 64                       # all that a sequence can have: no fault
     dfa.pages_trim(pool)
     dfa.stream_status(pool.status)
+
+
+@pytest.mark.parametrize("B,width", [(3, 4), (40, 4), (3, 1100)])      # one launch, or two
+@pytest.mark.parametrize("n", [-1, -2 ** 31, 65, 2 ** 31 - 1])
+def test_fork_reports_the_length_of_a_source(B, width, n):
+    pool, model = new_pool(B, width, 3 * B, 16)
+    lens = [20] * B
+    pool.seq_lens.copy_(i32(lens))
+    model.lens = lens
+    reserve(pool, model, lens, 20)
+    if n == 65:
+        n = 16 * width + 1
+    pool.seq_lens[1] = n
+    model.lens[1] = n
+    dfa.pages_fork(pool, i32([1, 1] + list(range(2, B))))
+    reported(pool)
+    same(pool, model)                           # sequence 0 stays
+    dfa.pages_fork(pool, i32([0, 0] + list(range(2, B))))
+    model.fork([0, 0] + list(range(2, B)))      # a good one takes the other's place
+    same(pool, model)
+    dfa.stream_status(pool.status)
