@@ -87,45 +87,54 @@ struct PagedWs {
     }
 };
 
-dfa_status append(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,
-                  const int32_t* new_lens, const int32_t* positions, const void* k,
-                  const int64_t* k_strides, const void* v, const int64_t* v_strides, int32_t Hq,
-                  const void* q, const int64_t* q_strides, void* q_out,
-                  const int64_t* q_out_strides, void* ws, size_t ws_bytes, void* stream)
+// What errors call a call and its tensors.
+struct AppendNames {
+    const char *call, *k, *v, *q, *q_out, *queries;
+};
+constexpr AppendNames kAppend = {
+    "dfa_cache_append",    "dfa_cache_append: k",     "dfa_cache_append: v",
+    "dfa_cache_append: q", "dfa_cache_append: q_out", "dfa_cache_append: q and q_out"};
+constexpr AppendNames kAppendAt = {
+    "dfa_cache_append_at",    "dfa_cache_append_at: k",     "dfa_cache_append_at: v",
+    "dfa_cache_append_at: q", "dfa_cache_append_at: q_out", "dfa_cache_append_at: q and q_out"};
+
+dfa_status append(const AppendNames& names, const dfa_paged_cache* cache,
+                  const dfa_rope_spec* rope, int32_t T, const int32_t* new_lens,
+                  const int32_t* positions, const void* k, const int64_t* k_strides,
+                  const void* v, const int64_t* v_strides, int32_t Hq, const void* q,
+                  const int64_t* q_strides, void* q_out, const int64_t* q_out_strides, void* ws,
+                  size_t ws_bytes, void* stream)
 {
+    const char* call = names.call;
     AppendParams p;
     memset(&p, 0, sizeof p);
-    dfa_status s = make_cache(&p.c, cache, ws, "dfa_cache_append");
+    dfa_status s = make_cache(&p.c, cache, ws, call);
     if (s != DFA_OK)
         return s;
     const int32_t B = p.c.B, Hkv = p.c.Hkv, d = p.c.d, page = p.c.page;
     if (T < 1 || T >= (1 << 30))
-        return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_append: T must be in [1, 2^30)");
+        return set_error(DFA_ERR_INVALID_ARG, "%s: T must be in [1, 2^30)", call);
     if ((s = make_table(&p.t, rope, d)) != DFA_OK)
         return s;
-    if ((s = make_rows(&p.k, k, k_strides, B, Hkv, T, d, 2, false, "dfa_cache_append: k")) !=
-        DFA_OK)
+    if ((s = make_rows(&p.k, k, k_strides, B, Hkv, T, d, 2, false, names.k)) != DFA_OK)
         return s;
-    if ((s = make_rows(&p.v, v, v_strides, B, Hkv, T, d, 2, false, "dfa_cache_append: v")) !=
-        DFA_OK)
+    if ((s = make_rows(&p.v, v, v_strides, B, Hkv, T, d, 2, false, names.v)) != DFA_OK)
         return s;
     if (q) {
         if (!rope)
-            return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_append: queries without a rotation");
+            return set_error(DFA_ERR_INVALID_ARG, "%s: queries without a rotation", call);
         if (Hq < 1 || Hq > (1 << 20))
-            return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_append: Hq must be in [1, 2^20]");
-        if ((s = make_rows(&p.q, q, q_strides, B, Hq, T, d, 2, false, "dfa_cache_append: q")) !=
-            DFA_OK)
+            return set_error(DFA_ERR_INVALID_ARG, "%s: Hq must be in [1, 2^20]", call);
+        if ((s = make_rows(&p.q, q, q_strides, B, Hq, T, d, 2, false, names.q)) != DFA_OK)
             return s;
         if ((s = make_rows(&p.q_out, q_out, q_out_strides, B, Hq, T, d, 2, true,
-                           "dfa_cache_append: q_out")) != DFA_OK)
+                           names.q_out)) != DFA_OK)
             return s;
-        if ((s = check_apart(p.q, p.q_out, B, Hq, T, d, 2, "dfa_cache_append: q and q_out")) !=
-            DFA_OK)
+        if ((s = check_apart(p.q, p.q_out, B, Hq, T, d, 2, names.queries)) != DFA_OK)
             return s;
         p.Hq = Hq;
     }
-    if ((s = check_ws(ws, ws_bytes, kStatusBytes, "dfa_cache_append")) != DFA_OK)
+    if ((s = check_ws(ws, ws_bytes, kStatusBytes, call)) != DFA_OK)
         return s;
     p.new_lens = new_lens;
     p.positions = positions;
@@ -133,9 +142,8 @@ dfa_status append(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32
     // T rows touch at most this many pages, and never more than a sequence has
     p.pages = std::min(p.c.max_pages, (int32_t)(((int64_t)T + page - 2) / page + 1));
     if ((int64_t)B * T * (p.Hq + 2 * Hkv) >= kMaxBlocks)
-        return set_error(DFA_ERR_UNSUPPORTED, "dfa_cache_append: B * T * heads above 2^31");
-    return launch_status(launch_cache_append(p, num_sms(), (cudaStream_t)stream),
-                         "dfa_cache_append");
+        return set_error(DFA_ERR_UNSUPPORTED, "%s: B * T * heads above 2^31", call);
+    return launch_status(launch_cache_append(p, num_sms(), (cudaStream_t)stream), call);
 }
 
 }  // namespace
@@ -217,8 +225,8 @@ dfa_status dfa_cache_append(const dfa_paged_cache* cache, const dfa_rope_spec* r
                             const int64_t* q_strides, void* q_out, const int64_t* q_out_strides,
                             void* ws, size_t ws_bytes, void* stream)
 {
-    return append(cache, rope, T, new_lens, nullptr, k, k_strides, v, v_strides, Hq, q, q_strides,
-                  q_out, q_out_strides, ws, ws_bytes, stream);
+    return append(kAppend, cache, rope, T, new_lens, nullptr, k, k_strides, v, v_strides, Hq, q,
+                  q_strides, q_out, q_out_strides, ws, ws_bytes, stream);
 }
 
 dfa_status dfa_cache_append_at(const dfa_paged_cache* cache, const dfa_rope_spec* rope, int32_t T,
@@ -230,7 +238,7 @@ dfa_status dfa_cache_append_at(const dfa_paged_cache* cache, const dfa_rope_spec
 {
     if (!positions || !rope)
         return set_error(DFA_ERR_INVALID_ARG, "dfa_cache_append_at: positions or rope is NULL");
-    return append(cache, rope, T, new_lens, positions, k, k_strides, v, v_strides, Hq, q,
+    return append(kAppendAt, cache, rope, T, new_lens, positions, k, k_strides, v, v_strides, Hq, q,
                   q_strides, q_out, q_out_strides, ws, ws_bytes, stream);
 }
 
