@@ -141,7 +141,7 @@ dfa_status append(const AppendNames& names, const dfa_paged_cache* cache,
     p.T = T;
     // T rows touch at most this many pages, and never more than a sequence has
     p.pages = std::min(p.c.max_pages, (int32_t)(((int64_t)T + page - 2) / page + 1));
-    if ((int64_t)B * T * (p.Hq + 2 * Hkv) >= kMaxBlocks)
+    if ((int64_t)B * T >= kMaxBlocks || (int64_t)B * T * (p.Hq + 2 * Hkv) >= kMaxBlocks)
         return set_error(DFA_ERR_UNSUPPORTED, "%s: B * T * heads above 2^31", call);
     return launch_status(launch_cache_append(p, num_sms(), (cudaStream_t)stream), call);
 }

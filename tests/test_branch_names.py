@@ -1,10 +1,11 @@
-"""CPU check: a refused call names itself."""
+"""CPU checks of append at positions: a refused call names itself, and sizes whose product
+passes 64 bits are refused."""
 import ctypes
 
 import pytest
 
 from long_context_flashattention_gb300 import dfa
-from test_branch_refusals import BASE, L, append_at, cache  # noqa: F401
+from test_branch_refusals import BASE, I3, L, append_at, cache  # noqa: F401
 
 
 @pytest.mark.parametrize("kw", [dict(pos=None), dict(spec=False), dict(T=0), dict(k=None),
@@ -31,3 +32,13 @@ def test_append_at_names_its_queries(L):  # noqa: F811
                                      BASE, None, BASE, None, Hq, q, None, out, None, BASE, 256,
                                      None) != 0
         assert b"dfa_cache_append_at" in L.dfa_last_error()
+
+
+def test_append_refuses_sizes_past_64_bits(L):  # noqa: F811
+    """2^20 sequences of 2^29 tokens and 2 * 2^14 heads: 2^64 rows."""
+    c = cache(B=1 << 20, Hkv=1 << 14)
+    spec = dfa.rope_spec(64)
+    rows = (BASE, I3(0, 0, 0), BASE, I3(0, 0, 0), 0, None, None, None, None, BASE, 256, None)
+    assert L.dfa_cache_append(ctypes.byref(c), None, 1 << 29, None, *rows) == 2
+    assert L.dfa_cache_append_at(ctypes.byref(c), ctypes.byref(spec), 1 << 29, None, BASE,
+                                 *rows) == 2
