@@ -576,7 +576,7 @@ dfa_status dfa_cache_append_at(const dfa_paged_cache* cache, const dfa_rope_spec
  * describe no counterpart.
  *
  * A step with a drafted tree of n tokens a sequence: raise seq_lens by n,
- * dfa_pages_reserve, dfa_tree_plan; in every layer dfa_cache_append_at and
+ * dfa_pages_reserve (which may refuse: see there), dfa_tree_plan; in every layer dfa_cache_append_at and
  * dfa_decode_tree; then, when a path has been accepted, dfa_cache_compact in every
  * layer, lower seq_lens to what was kept, dfa_pages_trim.
  * ------------------------------------------------------------------------ */
@@ -691,6 +691,11 @@ dfa_status dfa_pages_fork(const dfa_page_pool* pool, const int32_t* src, void* w
  *   info [4] (device, written): number of jobs; pages taken; 1 if there were too few
  *   free pages or more than max_jobs jobs, else 0; 0.  In the former case nothing
  *   else changes, the number of jobs is 0 and it is reported (DFA_ERR_BOUNDS).
+ * After such a refusal, or where a sequence was passed over, no row may be stored or moved
+ * for it (dfa_cache_append, dfa_cache_append_at, dfa_cache_compact): entries of its row of
+ * the table may still name pages that other sequences hold, which the device cannot tell
+ * from its own.  Take seq_lens back and pass lengths of 0 (new_lens, q_lens, kept_lens),
+ * made from info[2] on the device where later calls are queued already or captured.
  *   jobs [max_jobs][2] (device), 8-byte aligned; entries from the number of jobs on are
  *   left as they were.  0 <= T, max_jobs < 2^30.
  *   ws: dfa_pages_workspace_size(pool) bytes.
