@@ -690,7 +690,8 @@ dfa_status dfa_pages_fork(const dfa_page_pool* pool, const int32_t* src, void* w
  * call on.
  *   info [4] (device, written): number of jobs; pages taken; 1 if there were too few
  *   free pages or more than max_jobs jobs, else 0; 0.  In the former case nothing
- *   else changes, the number of jobs is 0 and it is reported (DFA_ERR_BOUNDS).
+ *   else changes, the number of jobs is 0, info[1] is the number of pages that it would
+ *   have taken, and it is reported (DFA_ERR_BOUNDS).
  * After such a refusal, or where a sequence was passed over, no row may be stored or moved
  * for it (dfa_cache_append, dfa_cache_append_at, dfa_cache_compact): entries of its row of
  * the table may still name pages that other sequences hold, which the device cannot tell
