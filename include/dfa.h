@@ -615,8 +615,7 @@ dfa_status dfa_tree_plan(const dfa_paged_cache* cache, int32_t T, const int32_t*
  *   q [B,Hq,T,d] bf16 (strided); mask [B][T][ceil(T/32)]; o [B,Hq,T,d] bf16 or fp32
  *   (o_fp32) and lse [B,Hq,T] fp32, contiguous; o and lse apart from each other and
  *   from q and mask.  (Hq/Hkv) * T <= 1024.
- *   ws: dfa_decode_tree_workspace_size(desc, T) bytes (more with o_fp32), whatever the
- *   lengths and the table.
+ *   ws: dfa_decode_tree_workspace_size(desc, T) bytes, whatever the lengths and the table.
  */
 size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T);
 dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,

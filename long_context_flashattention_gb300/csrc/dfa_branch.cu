@@ -57,16 +57,16 @@ struct PoolWs {
 };
 
 // Workspace of dfa_decode_tree: status word, one record per block, two partial results
-// (references and sum, O) per block; for fp32 outputs what a block sets apart of O, twice.
+// (references and sum, O) per block, and what a block's two groups set apart of O.
 struct TreeWs {
     size_t info, ndl, o, apart, bytes;
-    TreeWs(int d, bool o_fp32)
+    explicit TreeWs(int d)
     {
         info = kStatusBytes;
         ndl = info + align256((size_t)kTreeMaxCtas * sizeof(int4));
         o = ndl + align256((size_t)2 * kTreeMaxCtas * kTreeRows * sizeof(float4));
         apart = o + align256((size_t)2 * kTreeMaxCtas * kTreeRows * d * 4);
-        bytes = apart + (o_fp32 ? apart - o : 0);
+        bytes = apart + (apart - o);
     }
 };
 
@@ -119,7 +119,7 @@ size_t dfa_decode_tree_workspace_size(const dfa_attn_desc* desc, int32_t T)
     if (!desc || T < 1 || desc->Hkv < 1 || desc->Hq < 1 || desc->Hq % desc->Hkv != 0 ||
         (desc->d != 64 && desc->d != 128) || (int64_t)(desc->Hq / desc->Hkv) * T > 1024)
         return 0;
-    return TreeWs(desc->d, desc->o_fp32).bytes;
+    return TreeWs(desc->d).bytes;
 }
 
 dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cache, int32_t T,
@@ -185,11 +185,11 @@ dfa_status dfa_decode_tree(const dfa_attn_desc* desc, const dfa_paged_cache* cac
     p.scale_log2 = scale_log2;
     p.o = o;
     p.lse = lse;
-    const TreeWs w(p.c.d, desc->o_fp32);
+    const TreeWs w(p.c.d);
     p.info = (int4*)((char*)ws + w.info);
     p.part_ndl = (float4*)((char*)ws + w.ndl);
     p.part_o = (float*)((char*)ws + w.o);
-    p.apart = desc->o_fp32 ? (float*)((char*)ws + w.apart) : nullptr;
+    p.apart = (float*)((char*)ws + w.apart);
     p.timeout_ns = kDefaultTimeoutNs;
     CUtensorMap tk, tv;
     if ((s = make_page_map(&tk, p.c, p.c.k, kTreeTile, "dfa_decode_tree: k")) != DFA_OK)

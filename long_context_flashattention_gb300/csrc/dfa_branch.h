@@ -40,7 +40,7 @@ struct TreeParams {
     // [2 CTAs][rows]: what the sum is relative to (log2), what O is beyond that, sum
     float4* part_ndl;
     float* part_o;                // [2 CTAs][d / 4][rows][4]
-    float* apart;                 // [2 CTAs][d / 4][rows][4]: O's earlier chains, or NULL
+    float* apart;                 // [2 CTAs][d / 4][rows][4]: O's earlier chains
     uint64_t timeout_ns;
 };
 

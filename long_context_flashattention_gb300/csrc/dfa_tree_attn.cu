@@ -73,11 +73,14 @@ constexpr float grow(bool f8) { return f8 ? 60.f : 8.f; }
 // head() below.
 constexpr float kTop = 15.f;
 // A product adds to O by cutting off what fp32 does not hold, which makes O smaller each
-// time, in the end by 2^-24 of it for every other product.  For fp32 outputs a sum of so many
-// tiles is set apart (in the workspace; the next begins at 0) and added at the segment's end:
-// off by 2.7e-6 in place of 3.5e-6 after 128K rows, 54 tiles a block, for 71 us in place of
-// 67; every 16 tiles 2.5e-6 and 73 us.
-constexpr int kChain = 32;
+// time, in the end by 2^-24 of it for every other product.  So a sum of so many tiles is set
+// apart (in the workspace; the next begins at 0) and added at the segment's end.  fp32
+// outputs: off by 2.7e-6 in place of 3.5e-6 after 128K rows, 54 tiles a block, for 71 us in
+// place of 67; every 16 tiles 2.5e-6 and 73 us.  bf16 outputs: a batch of contexts of 1M rows,
+// 8192 tiles a block, was smaller by up to 2.4e-3, more than rounding takes; 256 tiles leave
+// 2e-4.  (Weights in one term: a kernel with chains is 1 to 2 % slower, 4 sequences of 128 rows
+// 73.6 us against 72.0, and is taken where a sequence can have more tiles than that.)
+constexpr int kChain = 32, kLongChain = 256;
 constexpr float kNone = -FLT_MAX;         // running maximum before the first key
 constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
                                           // taken off them (else both in one operation: N,
@@ -421,10 +424,10 @@ __device__ __forceinline__ bool is_fp32(const TreeParams& p)
 }
 
 // The tile i of a segment begins a chain where i & this is 0.
-template <bool F8, Terms TERMS>
+template <bool F8, Terms TERMS, bool LONG>
 __device__ __forceinline__ int32_t chain_mask(const TreeParams& p)
 {
-    return is_fp32<F8, TERMS>(p) ? kChain - 1 : INT32_MAX;
+    return !LONG ? INT32_MAX : (is_fp32<F8, TERMS>(p) ? kChain : kLongChain) - 1;
 }
 
 // A place in a ring of SLOTS, and the phase that its barriers are in.
@@ -1168,7 +1171,7 @@ __device__ __noinline__ void take_back(uint32_t tO, const float4* apart, float f
     tmem_st_wait();
 }
 
-template <int D, bool F8, Terms TERMS>
+template <int D, bool F8, Terms TERMS, bool LONG>
 __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, uint32_t smem,
                                         const WaitCtx& wctx)
 {
@@ -1182,7 +1185,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
     const int row = by_rows(TERMS) ? rit & 63 : rit;       // ..., of the segment
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = lanes + w * 64, tO = lanes + C::kO0;  // (all of TMEM is the block's)
-    const int32_t R = p.G * p.T, chain = chain_mask<F8, TERMS>(p);
+    const int32_t R = p.G * p.T, chain = chain_mask<F8, TERMS, LONG>(p);
     float4* const apart = reinterpret_cast<float4*>(p.apart) +
                           (2 * (int64_t)blockIdx.x + w) * (kTreeRows * D / 4) + rit;
     uint32_t gt = 0, met = 0;
@@ -1322,7 +1325,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
                 if (i > chain)
                     sh.n[w][rit] *= f;
                 if (end_chain) {
-                    set_apart<D>(tO + w * D, apart, i > kChain ? sh.n[w][rit] : 0.f);
+                    set_apart<D>(tO + w * D, apart, i > chain + 1 ? sh.n[w][rit] : 0.f);
                     sh.n[w][rit] = 1.f;
                 }
             }
@@ -1500,7 +1503,8 @@ __device__ __forceinline__ void softmax(const TreeParams& p, Shared<D, F8>& sh, 
         p.info[blockIdx.x] = info;
 }
 
-template <int D, bool F8, Terms TERMS>
+// LONG: segments may have more tiles than a chain
+template <int D, bool F8, Terms TERMS, bool LONG>
 __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeParams p)
@@ -1573,11 +1577,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (threadIdx.x == 0)
             cache_fault(p.c.status, kSiteShared, blockIdx.x);
     } else if (warp < 8) {
-        softmax<D, F8, TERMS>(p, sh, base, wctx);
+        softmax<D, F8, TERMS, LONG>(p, sh, base, wctx);
     } else if (warp == 8) {
         multiply_scores<D, F8>(sh, base, wctx);
     } else if (warp == 10) {
-        multiply_values<D, F8, TERMS>(sh, base, chain_mask<F8, TERMS>(p), wctx);
+        multiply_values<D, F8, TERMS>(sh, base, chain_mask<F8, TERMS, LONG>(p), wctx);
     } else if (warp == 9) {
         produce<D, F8>(p, sh, base, tk, tv, wctx);
         if (*wctx.abort_flag) {
@@ -1686,13 +1690,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Tree
             make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
-template <int D, bool F8, Terms TERMS>
+template <int D, bool F8, Terms TERMS, bool LONG = true>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, int num_sms,
                    cudaStream_t stream)
 {
     using C = Cfg<D, F8>;
     static_assert(kSmem<D, F8> <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<D, F8, TERMS>,
+    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<D, F8, TERMS, LONG>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmem<D, F8>);
     if (e != cudaSuccess)
@@ -1707,7 +1711,8 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, TreeParams& p, 
     p.line_blocks = (int)min((int64_t)max(1, most / p.row_groups), pieces);
     const int grid = p.line_blocks * p.row_groups;
     p.segment_cost = C::segment_cost(p.G * p.T);
-    decode_tree_kernel<D, F8, TERMS><<<grid, C::kThreads, kSmem<D, F8>, stream>>>(tk, tv, p);
+    decode_tree_kernel<D, F8, TERMS, LONG>
+        <<<grid, C::kThreads, kSmem<D, F8>, stream>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.whole)
         return e;
@@ -1722,9 +1727,14 @@ cudaError_t launch_terms(const CUtensorMap& tk, const CUtensorMap& tv, TreeParam
 {
     // (see "Rounding" above, and is_fp32)
     if constexpr (F8)
-        if (!p.o_fp32)
-            return p.G * p.T > 64 ? launch<D, F8, kOne>(tk, tv, p, num_sms, stream)
-                                  : launch<D, F8, kSplit>(tk, tv, p, num_sms, stream);
+        if (!p.o_fp32) {
+            const bool many = p.G * p.T > 64;
+            if (p.c.max_pages * p.c.page > kLongChain * kTile)
+                return many ? launch<D, F8, kOne>(tk, tv, p, num_sms, stream)
+                            : launch<D, F8, kSplit>(tk, tv, p, num_sms, stream);
+            return many ? launch<D, F8, kOne, false>(tk, tv, p, num_sms, stream)
+                        : launch<D, F8, kSplit, false>(tk, tv, p, num_sms, stream);
+        }
     if (p.G * p.T > 64)
         return launch<D, F8, kColumns>(tk, tv, p, num_sms, stream);
     if constexpr (!F8)

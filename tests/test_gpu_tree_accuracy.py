@@ -1,6 +1,6 @@
-"""fp32 outputs of trees over a paged cache to the accuracy that the header gives each path:
-weights to 2^-25 (bf16 cells, up to 64 rows a head), 2^-17 (more) and 2^-22 (8 bits), and sums
-of many tiles."""
+"""Trees over a paged cache to the accuracy that the header gives each path: weights to 2^-25
+(bf16 cells with an fp32 output, up to 64 rows a head), 2^-17 and 2^-22 (8 bits; 2^-11 with a
+bf16 output), and sums of many tiles."""
 import math
 
 import pytest
@@ -120,3 +120,39 @@ def test_sums_of_thousands_of_tiles(cells, T):
     err = (got - want[:, None]).abs() / want[:, None]
     assert err.max() <= bound, (float(err.max()), bound)
     assert math.isfinite(float(err.max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cells", [BF16, E4M3])
+@pytest.mark.parametrize("T", [16, 100])
+def test_bf16_outputs_of_thousands_of_tiles(cells, T):
+    """8192 tiles to a block of values 1 and 1.125, in such numbers that their mean lies above
+    the border between two bf16 numbers by more than it may be off, for the products of 256
+    tiles, but not by what all of them would cut off."""
+    need_gpu()
+    L, B, Hkv, page = 1 << 20, 19, 8, 128
+    n = L // page
+    # weights; 4 products of 16 keys a tile (8 with two terms); the sum's 8192 steps of 2^-24 at
+    # worst; the shares of high values, rounded to a key
+    off = (2.0 ** -11 if cells is E4M3 else 2.0 ** -17) + 256 * 8 * 2.0 ** -23 + (
+        8192 * 2.0 ** -24) + 2.0 ** -16
+    mean = (1 + 8.5 * 2.0 ** -7) * (1 + off)
+    assert mean < 1 + 9 * 2.0 ** -7
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def values(m):
+        perm = torch.randperm(m, generator=g, device="cuda")
+        return torch.where(perm < math.ceil((mean - 1) * 8 * m), 1.125, 1.0)
+    # a page's first key has a larger weight than the others, which are then below 1, with
+    # as many bits as their type has; high values are as many among those as among all
+    k0 = torch.full((n, page), -1.0, device="cuda")
+    v = values(L).view(n, page)
+    k0[:, 0], v[:, 0] = 0.0, values(n)
+    c = cache_of(cells, k0.flatten(), v.flatten(), Hkv, page, B)
+    q = torch.zeros(B, Hkv, T, 64, dtype=BF16)
+    q[..., 0] = queries(T)
+    # (nodes that see one another, so that all rows count)
+    mask = torch.full((B, T, -(-T // 32)), -1, dtype=torch.int32, device="cuda")
+    o, _ = dfa.decode_tree(c, q.cuda(), mask, scale=1.0)
+    dfa.stream_status(c.status)
+    assert (o.float() == 1 + 9 * 2.0 ** -7).all(), float(o.float().min())
