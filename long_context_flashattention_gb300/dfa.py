@@ -1004,9 +1004,11 @@ class PagePool:
         B, max_pages = block_table.shape
         if (held is None) != (refs is None) or (refs is None) == (npages is None):
             raise ValueError("give held and refs, or npages")
+        made = ()
         if refs is None:
             held = torch.zeros(B, dtype=torch.int32, device=dev)
             refs = torch.zeros(npages, dtype=torch.int32, device=dev)
+            made = held, refs
         if refs.dim() != 1:
             raise ValueError("refs must be [npages]")
         self.device, self.B, self.page, self.npages = dev, B, page, refs.shape[0]
@@ -1024,6 +1026,7 @@ class PagePool:
         self._own_ref = ctypes.byref(self._own)
         self._need = max(256, int(lib().dfa_pages_workspace_size(self._ref)))
         self._scratch = torch.empty(self._need, dtype=torch.uint8, device=dev)
+        self._made = (*made, self.status, self._scratch)  # (else the caller's)
         self._raw = (torch.cuda.current_stream(dev).cuda_stream if dev.type == "cuda" else None)
 
     def __setattr__(self, name, value):
@@ -1040,9 +1043,11 @@ def _pool_ws(ws, nbytes, pool, stream, raw):
     """A call's workspace, and the pool as the call sees it: errors go to the caller's
     workspace, without one to the pool's status.  (The pool's calls run one at a time: what
     they need beside their arguments is the pool's.)"""
+    if stream is not None or raw != pool._raw:
+        at = stream or torch.cuda.current_stream(pool.device)
+        for t in pool._made:  # the pool may go before the call has run
+            t.record_stream(at)
     if ws is None:
-        if stream is not None or raw != pool._raw:
-            pool._scratch.record_stream(stream or torch.cuda.current_stream(pool.device))
         return pool._scratch, pool._own_ref
     return _ws(ws, nbytes, pool, stream)
 
