@@ -610,7 +610,7 @@ dfa_status dfa_tree_plan(const dfa_paged_cache* cache, int32_t T, const int32_t*
  * 2^120 over the number of a sequence's rows (from there on sums may be infinite).
  * Accuracy: as attention in fp32, weights rounded to 2^-17 (bf16 cells; to 2^-25 with an
  * fp32 output and at most 64 rows a head) or 2^-22 (E4M3; to 2^-11 with a bf16 output),
- * small ones of E4M3 to 2^-33 (2^-29) of the row's largest contribution.
+ * small ones of E4M3 to 2^-33 (2^-29) of the row's largest weight times value scale.
  * desc supplies B, Hq, Hkv, d, scale, o_fp32 (ndocs must be 0; causal is not looked at).
  *   q [B,Hq,T,d] bf16 (strided); mask [B][T][ceil(T/32)]; o [B,Hq,T,d] bf16 or fp32
  *   (o_fp32) and lse [B,Hq,T] fp32, contiguous; o and lse apart from each other and

@@ -14,9 +14,9 @@ constexpr int kSiteParent = 103;  // of DFA_ERR_BOUNDS in DevStatus::where
 // sees, and in its own group's word the former.  A warp takes four nodes, a lane a word;
 // of node t only words up to t / 32 are kept.
 //
-// Bound by the output for many deep trees (256 of 1024 nodes, 34 MB: 15 us; one doubling
-// of whole rows per step took 107), by the chain of loads for small ones (64 of up to 60
-// nodes: 2.5 us).
+// Bound by the output and by the groups' order for many deep trees (256 of 1024 nodes, 34 MB:
+// 15.5 us, other trees each time 17; one doubling of whole rows per step took 107), by the
+// chain of loads for small ones (64 of up to 60 nodes: 2.5 us).
 __global__ void __launch_bounds__(256) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
 {
     extern __shared__ uint32_t sees[];            // group g: 32 nodes of g + 1 words

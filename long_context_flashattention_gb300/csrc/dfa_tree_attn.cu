@@ -29,11 +29,15 @@
 // S has two buffers (three for d = 64): the next tile's scores are there when a tile's
 // softmax ends.
 //
-// Bound: bf16 cells by HBM up to some 64 rows a head (64 ragged sequences up to 8K 186 us,
-// 5.9 TB/s; 7.4 between start and tail), then by the softmax (128K rows, 128 rows a head,
-// d 64: 70 us, where HBM takes 40); 8-bit cells of d = 128 by shared memory, whose 224 KB a
-// tile (arriving, converted, read by the products) take 1800 of 2000 to 2150 clk (8
-// sequences up to 16K, 240 rows a head: 99.5 us; HBM takes 23, the products 38).
+// Bound: bf16 cells by HBM (64 ragged sequences up to 8K 182 us, 6.0 TB/s; 4 sequences up to
+// 32K, 128 rows a head 70 us, 73 % of DRAM's peak with start and tail); those of d = 64 with
+// more than 64 rows a head, which have half the bytes for the same softmax, by each group's
+// way from scores to weights (128K rows 72 us, where HBM takes 40: half of the issue slots, half
+// of DRAM's peak and a third of the tensor pipe's cycles are used).  8-bit cells of d = 128
+// by shared memory, whose 224 KB a tile (arriving, converted, read by the products) take 1800
+// of 2000 to 2150 clk: 42 % of its pipe's cycles are loads and stores and 30 % the products',
+// start and tail among them (8 sequences up to 16K, 240 rows a head: 96 us; HBM takes 23, the
+// products 38).
 //
 // Work: (sequence, head, row group) segments form one line, cut by cost over a grid of
 // one block an SM: a block's range covers whole segments, whose result it writes, and up
