@@ -576,9 +576,9 @@ dfa_status dfa_cache_append_at(const dfa_paged_cache* cache, const dfa_rope_spec
  * describe no counterpart.
  *
  * A step with a drafted tree of n tokens a sequence: raise seq_lens by n,
- * dfa_pages_reserve (which may refuse: see there), dfa_tree_plan; in every layer dfa_cache_append_at and
- * dfa_decode_tree; then, when a path has been accepted, dfa_cache_compact in every
- * layer, lower seq_lens to what was kept, dfa_pages_trim.
+ * dfa_pages_reserve (which may refuse: see there), dfa_tree_plan; in every layer
+ * dfa_cache_append_at and dfa_decode_tree; then, when a path has been accepted,
+ * dfa_cache_compact in every layer, lower seq_lens to what was kept, dfa_pages_trim.
  * ------------------------------------------------------------------------ */
 
 /*

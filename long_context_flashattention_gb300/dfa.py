@@ -1079,9 +1079,9 @@ def pages_reserve(pool: PagePool, T, new_lens=None, jobs=None, info=None, ws=Non
     info [4]) for cache_copy, to be called for every layer; info holds the number of jobs,
     the pages taken, and whether the call was refused for want of pages or of room in
     jobs, in which case it has changed nothing (the pages are then those that it would have
-    taken).  Then no row may be stored or moved: the
-    table may still name pages that other sequences hold.  Take seq_lens back by
-    T * info[2] and give the calls of the step (1 - info[2]) times their lengths."""
+    taken).  Then no row may be stored or moved: the table may still name pages that other
+    sequences hold.  Take seq_lens back by T * info[2] and give the calls of the step
+    (1 - info[2]) times their lengths."""
     dev = pool.device
     raw = _raw_stream(dev, stream)
     if jobs is None:
