@@ -65,8 +65,9 @@ constexpr int kTile = kTreeTile;
 constexpr int kRing = 8;                  // tiles whose scales are kept
 constexpr int kRuns = 2;                  // segments that are announced ahead
 // N rises when a term exceeds 2^grow.  For bf16 weights, which are the terms and which values
-// up to 2^120 over the number of rows are multiplied by, that costs a pass over O; 8-bit
-// cells have D for their weights, and terms as large as that come nowhere near fp32's end.
+// up to 2^120 over the number of rows are multiplied by, that costs a pass over O (128K rows
+// 71.7 us; with 60, which values above 2^68 do not bear, 70.6).  8-bit cells have D for their
+// weights, and terms of 2^60 come nowhere near fp32's end.
 constexpr float grow(bool f8) { return f8 ? 60.f : 8.f; }
 // fp16 weights: D is set `head` below the largest exponent, and set anew, with a pass over
 // O, when a weight exceeds 2^kTop.  Between the two is room for larger weights to come;
@@ -82,8 +83,9 @@ constexpr float kTop = 15.f;
 // outputs: off by 2.7e-6 in place of 3.5e-6 after 128K rows, 54 tiles a block, for 71 us in
 // place of 67; every 16 tiles 2.5e-6 and 73 us.  bf16 outputs: a batch of contexts of 1M rows,
 // 8192 tiles a block, was smaller by up to 2.4e-3, more than rounding takes; 256 tiles leave
-// 2e-4.  (Weights in one term: a kernel with chains is 1 to 2 % slower, 4 sequences of 128 rows
-// 73.6 us against 72.0, and is taken where a sequence can have more tiles than that.)
+// less than 3e-4, of which fp16 weights have their part.  (Weights in one term: a kernel with
+// chains is 1 to 2 % slower, 4 sequences of 128 rows 73.6 us against 72.0, and is taken where
+// a sequence can have more tiles than that.)
 constexpr int kChain = 32, kLongChain = 256;
 constexpr float kNone = -FLT_MAX;         // running maximum before the first key
 constexpr float kFar = 1048576.f;         // scores as far from zero are rounded before N is
